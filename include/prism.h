@@ -256,6 +256,141 @@ prism_status prism_step_noalloc(const prism_desc* desc, const void* q, const voi
                                 const void* conv, float* S, void* conv_state, void* o,
                                 hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Query / key normalisation with rotary positions
+ * ------------------------------------------------------------------------
+ * For every token and head, with x a row of d values (of q or of k):
+ *   r = (c sum_i x_i^2 + eps)^(-1/2),  c = 1 (PRISM_NORM_L2) or 1/d (PRISM_NORM_RMS)
+ *   y_i = x_i r w_i                    (w = wq or wk; NULL: ones)
+ * and the first `rot` values of y turned in pairs by the token's position:
+ *   (a, b) -> (a cos - b sin, b cos + a sin),  angle_i = 2 pi p turns[i] 2^-64,
+ * pair i being (i, i + rot/2), or (2i, 2i + 1) with `interleaved`; the other
+ * values pass.  turns[i] is the pair's frequency as an integer: turns per
+ * position in units of 2^-64 (inv_freq / (2 pi) * 2^64, rounded).  The phase
+ * p turns[i] mod 2^64 is formed exactly in integers, so the angle is as exact
+ * at position 10^9 as at 1, with no table.  The arithmetic is fp32; each
+ * output is rounded once to the storage type.  The outputs are what
+ * prism_forward and prism_linear_attention take as q and k.               */
+typedef enum {
+  PRISM_NORM_L2 = 0,
+  PRISM_NORM_RMS = 1
+} prism_norm;
+
+/* Steps between consecutive batch entries, tokens and heads of a token
+ * tensor, in elements (the last dimension is contiguous).                 */
+typedef struct {
+  long long batch, token, head;
+} prism_strides;
+
+/*   B, T       batch and tokens (>= 0; with B * T = 0 nothing is read)
+ *   Hq, Hk     query and key heads (Hq >= 1, Hk >= 0; with Hk = 0 the key
+ *              pointers are ignored)
+ *   d          head dimension, a multiple of 8, 8 <= d <= 256
+ *   rot        values of each head that are rotated: 0 or a multiple of 8,
+ *              at most d; for 0, positions and turns are ignored
+ *   eps        added under the root, finite and >= 0
+ *   q, k       strides of the inputs; qo, ko: of the outputs (forward) or of
+ *              their gradients (backward); dq, dk: of the input gradients
+ *              (backward).  Multiples of 4 elements, magnitude < 2^40.      */
+typedef struct {
+  int B, T, Hq, Hk, d, rot;
+  prism_dtype dtype;
+  int norm;          /* a prism_norm value */
+  int interleaved;   /* 0: pairs (i, i + rot/2), 1: pairs (2i, 2i + 1) */
+  float eps;
+  prism_strides q, k, qo, ko, dq, dk;
+} prism_qk_norm_desc;
+
+/* Forward.  q [B,T,Hq,d], k [B,T,Hk,d], qo, ko: dt, strided; wq, wk [d] dt or
+ * NULL; positions [B,T] int32, contiguous (negative positions turn backwards);
+ * turns [rot/2] int64.  qo may be q and ko may be k (same strides). */
+prism_status prism_qk_norm(const prism_qk_norm_desc* desc, const void* q, const void* k,
+                           const void* wq, const void* wk, const int* positions,
+                           const long long* turns, void* qo, void* ko, hipStream_t stream);
+
+/* Backward: gradients of <dqo, qo> + <dko, ko> from the forward's inputs (no
+ * intermediate is kept).  With g = dy turned back by the angle and h = g w:
+ *   dx = r h - c r^3 x (x . h),   dw = sum over tokens and heads of g x r.
+ * dq, dk: dt, strided, written; dq may be dqo and dk may be dko.  dwq, dwk
+ * [d] f32: written when wq / wk is given (required then, NULL otherwise).
+ * The weight gradients are summed in a fixed order.  workspace:
+ * prism_qk_norm_backward_workspace() bytes, 256-byte aligned (may be NULL
+ * where that is 0: no weights). */
+prism_status prism_qk_norm_backward_workspace(const prism_qk_norm_desc* desc, int weights,
+                                              size_t* bytes);
+prism_status prism_qk_norm_backward(const prism_qk_norm_desc* desc, const void* q, const void* k,
+                                    const void* wq, const void* wk, const int* positions,
+                                    const long long* turns, const void* dqo, const void* dko,
+                                    void* dq, void* dk, float* dwq, float* dwk, void* workspace,
+                                    size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Linear attention with a decay for each head
+ * ------------------------------------------------------------------------
+ *   S_t = exp(g_t) S_{t-1} + v_t k_t^T,   o_t = scale S_t q_t
+ * g is the log of the decay (f32): one number for each head, or one for each
+ * token and head.  g = -inf (any g < -150, where exp underflows) forgets the
+ * past.  The state has prism_forward's layout, [B, H, dv, dk] f32.
+ * H query heads share Hk key / value heads: head h reads k, v of head
+ * h / (H / Hk).  Chunks of tokens go through the matrix cores, with the state
+ * between them carried in fp32; in bf16 every product that adds to the state
+ * (and, for the gradient of g, every product) takes its scaled operand in
+ * three bf16 pieces, so that f32 results keep f32 accuracy.
+ *
+ *   B, H, Hk   sequences (>= 0), query heads, key / value heads (H % Hk = 0)
+ *   T          tokens of each sequence (>= 0); packed: the longest length
+ *   dk, dv     head dimensions, multiples of 16, 16 .. 128
+ *   scale      finite
+ *   packed_tokens  with cu_seqlens: rows N of the token tensors (the packed
+ *              batches of prism_forward, sanitised the same way)
+ *   q, k, v, o strides of q, k, v and of o / dO: multiples of 16 bytes, >= 0,
+ *              a token step of at most 2^22 elements.  (packed: batch ignored)
+ *   g          strides of g and dg in floats (>= 0); one decay for each head:
+ *              batch = token = 0 (then dg is summed over batch and tokens)  */
+typedef struct {
+  int B, T, H, Hk, dk, dv;
+  prism_dtype dtype;
+  float scale;
+  int packed_tokens;
+  prism_strides q, k, v, o, g;
+} prism_linear_attention_desc;
+
+/* Workspace of the forward (backward = 0) or backward (1) pass, packed or
+ * dense batch; with dg: of the backward pass that also gives dg. */
+prism_status prism_linear_attention_workspace(const prism_linear_attention_desc* desc,
+                                              int backward, int dg, size_t* bytes);
+
+/* Whole sequences.  q [B,T,H,dk], k [B,T,Hk,dk], v [B,T,Hk,dv], o [B,T,H,dv]
+ * dt, strided ([N,..] with cu_seqlens, B + 1 int32 offsets on the device);
+ * S0 may be NULL (zeros); ST may be NULL, or S0 itself (updated in place).
+ * A sequence of no tokens gives ST = S0.  A value that is not finite may
+ * reach every row of its own sequence, never another sequence's. */
+prism_status prism_linear_attention(const prism_linear_attention_desc* desc, const void* q,
+                                    const void* k, const void* v, const float* g,
+                                    const float* S0, const int* cu_seqlens, void* o, float* ST,
+                                    void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Gradients of <dO, o> + <dST, ST> from the forward's inputs.  dST may be
+ * NULL (zeros).  dq [B,T,H,dk], dk [B,T,Hk,dk], dv [B,T,Hk,dv] dt,
+ * contiguous; dg f32 (NULL: not wanted; zero where g < -104, whose decay is
+ * zero), dS0 f32 (NULL: not wanted).  Written, not accumulated; packed rows
+ * outside every (clamped) sequence are unspecified. */
+prism_status prism_linear_attention_backward(const prism_linear_attention_desc* desc,
+                                             const void* q, const void* k, const void* v,
+                                             const float* g, const float* S0,
+                                             const int* cu_seqlens, const void* dO,
+                                             const float* dST, void* dq, void* dk, void* dv,
+                                             float* dg, float* dS0, void* workspace,
+                                             size_t workspace_bytes, hipStream_t stream);
+
+/* The recurrence token by token, for the desc->T tokens of each sequence
+ * (T = 1: a decode step): S is read as S_0, S_T goes to S_out (S_out = S:
+ * in place).  T = 0 copies the state. */
+prism_status prism_linear_attention_step(const prism_linear_attention_desc* desc, const void* q,
+                                         const void* k, const void* v, const float* g,
+                                         const float* S, float* S_out, void* o,
+                                         hipStream_t stream);
+
 /* Human-readable name of a status code (static string). */
 const char* prism_status_string(prism_status status);
 

@@ -20,6 +20,8 @@ LIB = os.path.join(HERE, "libprism.so")
 
 # slowest first, so the parallel compile finishes early
 SOURCES = [
+    "linattn_bf16.hip",
+    "linattn_f32.hip",
     "chunk_bwd_solve.hip",
     "chunk_bwd_pairs.hip",
     "chunk_bwd_state.hip",
@@ -34,9 +36,12 @@ SOURCES = [
     "state.hip",
     "step.hip",
     "refine_bwd.hip",
+    "qk_norm.hip",
+    "linattn.hip",
     "noalloc.hip",
     "chunk_bwd.hip",
     "prism_api.cpp",
+    "operators_api.cpp",
 ]
 
 ARCH = "gfx950"

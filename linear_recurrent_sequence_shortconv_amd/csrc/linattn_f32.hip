@@ -1,0 +1,6 @@
+// Chunked linear attention, f32 storage (kernel in linattn_kernel.h).
+#include "linattn_inst.h"
+
+namespace prism {
+template hipError_t launch_la_pass<float>(const LaArgs<float>&, int, bool, bool, hipStream_t);
+}  // namespace prism

@@ -1,0 +1,27 @@
+// Instances of the chunk kernel by operand size (included by one source per
+// storage type).
+#pragma once
+
+#include "linattn_kernel.h"
+
+namespace prism {
+
+// chunk length: 64 tokens; 32 for fp32 rows of 128 (the tiles' LDS)
+template <typename E, int DA> constexpr int la_ch() { return sizeof(E) == 4 && DA == 128 ? 32 : 64; }
+
+template <typename E, int DA, int NV>
+hipError_t la_pass_da(const LaArgs<E>& a, bool outputs, bool precise, hipStream_t s) {
+  constexpr int CH = la_ch<E, DA>();
+  if (!outputs) return la_launch<E, DA, NV, CH, false, false>(a, s);
+  if (precise) return la_launch<E, DA, NV, CH, true, true>(a, s);
+  return la_launch<E, DA, NV, CH, false, true>(a, s);
+}
+
+template <typename E>
+hipError_t launch_la_pass(const LaArgs<E>& a, int dim, bool outputs, bool precise, hipStream_t s) {
+  if (dim <= 32) return la_pass_da<E, 32, 32>(a, outputs, precise, s);
+  if (dim <= 64) return la_pass_da<E, 64, 64>(a, outputs, precise, s);
+  return la_pass_da<E, 128, 64>(a, outputs, precise, s);
+}
+
+}  // namespace prism

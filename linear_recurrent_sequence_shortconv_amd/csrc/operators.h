@@ -1,0 +1,130 @@
+// Host-side declarations of the query / key normalisation and of the linear
+// attention, shared by the C-ABI layer (operators_api.cpp) and the kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+
+namespace prism {
+
+typedef __bf16 bf16;
+
+struct Strides {
+  long b, t, h;   // elements between batch entries, tokens, heads
+};
+
+// ---------------------------------------------------------------- qk_norm
+// One launch covers the query and the key heads: heads 0 .. Hq - 1 are q,
+// Hq .. Hq + Hk - 1 are k.
+struct QkNormArgs {
+  int B, T, Hq, Hk, d, rot;
+  float c, eps;                  // r = (c sum x^2 + eps)^(-1/2)
+  int interleaved;
+  const void *xq, *xk;           // inputs
+  const void *wq, *wk;           // weights (nullptr: ones)
+  const int* pos;                // [B, T] (nullptr: no rotation)
+  const long long* turns;        // [rot / 2]
+  const void *gq, *gk;           // output gradients (backward)
+  void *yq, *yk;                 // outputs (forward) or input gradients (backward)
+  Strides sxq, sxk, sgq, sgk, syq, syk;
+  float *part, *dwq, *dwk;       // weight-gradient partials and results (backward)
+};
+template <typename E> hipError_t launch_qk_norm(const QkNormArgs& a, hipStream_t s);
+template <typename E> hipError_t launch_qk_norm_bwd(const QkNormArgs& a, hipStream_t s);
+size_t qk_norm_part_bytes(int d);   // room for the weight-gradient partials
+
+// ------------------------------------------------------- linear attention
+// Every pass over a sequence is one form: with operand rows A_t, B_t (da
+// values) and C_t (dc values), cumulative log decays G_t and a state X [da][dc],
+//   forward:  out_t = s_in sum_{i<=t} e^{G_t-G_i} (A_t.B_i) C_i + s_row e^{G_t} A_t X0
+//   reverse:  out_t = s_in sum_{i>=t} e^{G_i-G_t} (A_t.B_i) C_i + s_row e^{G_T-G_t} A_t X0
+// and the state after the pass is e^{G_T} X0 + s_upd sum_i e^{G_T-G_i} B_i C_i^T
+// (reverse: e^{G_i}).  (q, k, v) forward gives o; (dO, v, k) forward dq;
+// (v, dO, q) reverse dk; (k, q, dO) reverse dv.
+template <typename E>
+struct LaRole {
+  const E *a, *b, *c;
+  Strides sa, sb, sc;
+  int ga, gb, gc;          // query heads per head of a, b, c
+  E* out;                  // strided by so, or
+  float* out32;            // fp32, strided by so (one row for each query head)
+  Strides so;
+  const E* e;              // rows dotted with out (fp32, before rounding), or nullptr
+  Strides se;
+  int ge;
+  float* edot;             // [B * H][parts][T] partial dots
+  int da, dc, rev;
+  float s_in, s_row, s_upd;
+  const float* X0;         // [B, H, dv, dk] entering state (nullptr: zeros)
+  float* fin;              // the same, leaving (nullptr: not wanted)
+  float* seg;              // [B * H][nseg][dv * dk] states of the segments (nseg > 1)
+  float* segdec;           // [B * H][nseg] decay over a segment (nseg > 1)
+  int xa, xc;              // element steps of X's two indexes in those arrays
+};
+constexpr int LA_ROLES = 3;
+// A sequence is cut into nseg segments of `seglen` tokens (a whole number of
+// chunks), worked on side by side.
+template <typename E>
+struct LaArgs {
+  int B, T, H, nseg, seglen, nslice, nroles;
+  int DD;                  // dv * dk
+  const int* cu;           // sanitised offsets of a packed batch, or nullptr
+  const float* g;
+  Strides sg;
+  LaRole<E> r[LA_ROLES];
+};
+// Tokens per chunk, and columns of C per workgroup, for operands of `dim`
+// (= max(dk, dv)) values.
+int la_chunk(bool f32, int dim);
+int la_slice(int dim);
+// Partial row dots written for each token.
+int la_edot_parts(bool f32, int dim, int dc);
+// outputs = false: the segments' own states only (role.seg, role.segdec).
+// precise: bf16 operands of every product in three pieces.
+template <typename E>
+hipError_t launch_la_pass(const LaArgs<E>& a, int dim, bool outputs, bool precise, hipStream_t s);
+
+// Segment states in place: own states -> states entering each segment.
+struct LaJoin {
+  int B, T, H, nseg, seglen, DD;
+  const int* cu;
+  float* seg[2];           // forward, reverse (nullptr: absent)
+  const float* dec[2];
+  const float* X0[2];
+};
+hipError_t launch_la_join(const LaJoin& a, hipStream_t s);
+
+// dg from the row dots: dg_t = sum_{i >= t} (q_i.dq_i - k_i.dk_i) + <dS, S> at
+// the segment's end.
+struct LaDecay {
+  int B, T, H, nseg, seglen, DD, pq, pk;
+  const int* cu;
+  const float* g;
+  Strides sg;
+  const float *eq, *ek;            // [B * H][pq or pk][T]
+  const float *segf, *segr;        // entering states, forward and reverse (nseg > 1)
+  const float *ST, *dST;           // final state and its gradient (nullptr: zero)
+  float* dg;                       // strided like g, or, for one decay a head,
+  float* tmp;                      // [B * H][T], then summed into dg [H]
+};
+hipError_t launch_la_decay(const LaDecay& a, hipStream_t s);
+
+// out[.., h', :] = sum over the grp query heads of h' of part [.., H, d] (fp32)
+template <typename E>
+hipError_t launch_la_group_sum(const float* part, E* out, long rows, int Hk, int grp, int d,
+                               hipStream_t s);
+
+template <typename E>
+struct LaStepArgs {
+  int B, T, H, dk, dv, grp;
+  float scale;
+  const E *q, *k, *v;
+  Strides sq, sk, sv, so, sg;
+  const float* g;
+  const float* S;
+  float* S_out;
+  E* o;
+};
+template <typename E> hipError_t launch_la_step(const LaStepArgs<E>& a, hipStream_t s);
+
+}  // namespace prism

@@ -16,16 +16,12 @@
 #include <vector>
 
 #include "../../include/prism.h"
+#include "api_common.h"
 #include "prism_internal.h"
 
 namespace {
 
 thread_local std::string g_err;
-
-prism_status fail(prism_status st, const std::string& msg) {
-  g_err = msg;
-  return st;
-}
 
 // ---------------------------------------------------------------- timing
 struct TimedLaunch {
@@ -36,7 +32,18 @@ bool g_timing = false;
 std::vector<TimedLaunch> g_launches;
 std::vector<hipEvent_t> g_pool;
 
-hipEvent_t pool_event() {
+}  // namespace
+
+namespace prism {
+
+prism_status fail(prism_status st, const std::string& msg) {
+  g_err = msg;
+  return st;
+}
+
+bool timing_on() { return g_timing; }
+
+hipEvent_t timing_event() {
   if (!g_pool.empty()) {
     hipEvent_t e = g_pool.back();
     g_pool.pop_back();
@@ -47,30 +54,16 @@ hipEvent_t pool_event() {
   return e;
 }
 
-template <typename F>
-hipError_t timed(const char* name, hipStream_t s, F&& f) {
-  if (!g_timing) return f();
-  hipEvent_t a = pool_event(), b = pool_event();
-  if (a) (void)hipEventRecord(a, s);
-  hipError_t err = f();
-  if (b) (void)hipEventRecord(b, s);
-  if (a && b) g_launches.push_back({name, a, b});
-  return err;
-}
+void timing_add(const char* name, hipEvent_t a, hipEvent_t b) { g_launches.push_back({name, a, b}); }
 
-// ---------------------------------------------------------------- layout
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+}  // namespace prism
 
-struct Carve {
-  size_t off = 0;
-  char* base = nullptr;
-  template <typename P>
-  P* take(size_t bytes) {
-    P* p = base ? reinterpret_cast<P*>(base + off) : nullptr;
-    off += align256(bytes);
-    return p;
-  }
-};
+namespace {
+
+using prism::Carve;
+using prism::check_buffer;
+using prism::check_ptr;
+using prism::fail;
 
 template <typename E>
 struct FwdWs {
@@ -173,13 +166,6 @@ prism_status check_desc(const prism_desc* desc, prism::Dims* out) {
   return PRISM_OK;
 }
 
-prism_status check_ptr(const void* p, const char* name, bool required) {
-  if (!p) return required ? fail(PRISM_ERR_NULL, std::string(name) + " is NULL") : PRISM_OK;
-  if (reinterpret_cast<uintptr_t>(p) & 15u)
-    return fail(PRISM_ERR_ALIGN, std::string(name) + " is not 16-byte aligned");
-  return PRISM_OK;
-}
-
 // Packed batches: the offsets must be a 4-byte aligned device array and the
 // packed tensors' row count N must be given; the offsets themselves are read
 // on the device only, where a sanitising pass clamps them into [0, N] before
@@ -193,19 +179,6 @@ prism_status check_cu(const int* cu, const prism_desc* desc, prism::Dims* d) {
   d->N = cu ? desc->packed_tokens : 0;
   return PRISM_OK;
 }
-
-#define CHECK_PTR(p, req)                              \
-  do {                                                 \
-    prism_status st_ = check_ptr((p), #p, (req));      \
-    if (st_ != PRISM_OK) return st_;                   \
-  } while (0)
-
-#define HIP_TRY(name, stream, expr)                                                   \
-  do {                                                                               \
-    hipError_t e_ = timed((name), (stream), [&]() { return (expr); });               \
-    if (e_ != hipSuccess)                                                            \
-      return fail(PRISM_ERR_HIP, std::string(name) + ": " + hipGetErrorString(e_));   \
-  } while (0)
 
 template <typename E>
 struct BwdWs {
@@ -549,16 +522,6 @@ prism_status prism_saved_bytes(const prism_desc* desc, size_t* bytes) {
 }  // extern "C"
 
 namespace {
-
-prism_status check_buffer(const void* p, size_t have, size_t need, const char* what) {
-  if (!p) return fail(PRISM_ERR_WORKSPACE, std::string(what) + " is NULL");
-  if (reinterpret_cast<uintptr_t>(p) & 255u)
-    return fail(PRISM_ERR_ALIGN, std::string(what) + " is not 256-byte aligned");
-  if (have < need)
-    return fail(PRISM_ERR_WORKSPACE, std::string(what) + " has " + std::to_string(have) +
-                                         " bytes, needs " + std::to_string(need));
-  return PRISM_OK;
-}
 
 prism_status forward_entry(const prism_desc* desc, const void* q, const void* k, const void* v,
                            const float* alpha, const float* beta, const void* Wk, const void* Wp,

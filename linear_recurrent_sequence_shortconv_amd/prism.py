@@ -6,6 +6,7 @@ the current stream.  There is no fallback: if the library is missing or a
 call fails, a RuntimeError is raised.
 """
 import ctypes
+import math
 import os
 
 import torch
@@ -22,7 +23,10 @@ EXPORTS = ("prism_forward_workspace", "prism_backward_workspace",
            "prism_forward_train_workspace", "prism_backward_train_workspace", "prism_forward",
            "prism_backward", "prism_saved_bytes", "prism_forward_train", "prism_backward_train",
            "prism_step_workspace", "prism_step", "prism_step_noalloc", "prism_status_string", "prism_last_error", "prism_timing_begin",
-           "prism_timing_end")
+           "prism_timing_end",
+           "prism_qk_norm", "prism_qk_norm_backward_workspace", "prism_qk_norm_backward",
+           "prism_linear_attention_workspace", "prism_linear_attention",
+           "prism_linear_attention_backward", "prism_linear_attention_step")
 
 
 class Desc(ctypes.Structure):
@@ -31,6 +35,27 @@ class Desc(ctypes.Structure):
                 ("chunk", ctypes.c_int), ("conv_width", ctypes.c_int), ("dtype", ctypes.c_int),
                 ("activation", ctypes.c_int), ("conv_offset", ctypes.c_int),
                 ("packed_tokens", ctypes.c_int)]
+
+
+class Strides(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_longlong), ("token", ctypes.c_longlong),
+                ("head", ctypes.c_longlong)]
+
+
+class QkNormDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("Hq", ctypes.c_int),
+                ("Hk", ctypes.c_int), ("d", ctypes.c_int), ("rot", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("norm", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("eps", ctypes.c_float), ("q", Strides), ("k", Strides), ("qo", Strides),
+                ("ko", Strides), ("dq", Strides), ("dk", Strides)]
+
+
+class LinearAttentionDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int),
+                ("Hk", ctypes.c_int), ("dk", ctypes.c_int), ("dv", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("scale", ctypes.c_float),
+                ("packed_tokens", ctypes.c_int), ("q", Strides), ("k", Strides), ("v", Strides),
+                ("o", Strides), ("g", Strides)]
 
 
 _lib = None
@@ -69,6 +94,18 @@ def lib():
                   "prism_backward", "prism_saved_bytes", "prism_forward_train",
                   "prism_backward_train", "prism_step_workspace", "prism_step",
                   "prism_step_noalloc"):
+            getattr(L, f).restype = ctypes.c_int
+        qd, ld, size = (ctypes.POINTER(QkNormDesc), ctypes.POINTER(LinearAttentionDesc),
+                        ctypes.c_size_t)
+        L.prism_qk_norm.argtypes = [qd] + [_P] * 9
+        L.prism_qk_norm_backward_workspace.argtypes = [qd, ctypes.c_int, ctypes.POINTER(size)]
+        L.prism_qk_norm_backward.argtypes = [qd] + [_P] * 13 + [size, _P]
+        L.prism_linear_attention_workspace.argtypes = [ld, ctypes.c_int, ctypes.c_int,
+                                                       ctypes.POINTER(size)]
+        L.prism_linear_attention.argtypes = [ld] + [_P] * 9 + [size, _P]
+        L.prism_linear_attention_backward.argtypes = [ld] + [_P] * 14 + [size, _P]
+        L.prism_linear_attention_step.argtypes = [ld] + [_P] * 8
+        for f in EXPORTS[-7:]:
             getattr(L, f).restype = ctypes.c_int
         L.prism_status_string.argtypes = [ctypes.c_int]
         L.prism_status_string.restype = ctypes.c_char_p
@@ -394,6 +431,275 @@ def step(q, k, v, alpha, beta, Wk=None, Wp=None, wbeta=None, conv=None, S=None, 
                             _ptr(beta), _ptr(Wk), _ptr(Wp), _ptr(wbeta), _ptr(conv), _ptr(S),
                             _ptr(conv_state), _ptr(o), _ptr(workspace),
                             ctypes.c_size_t(workspace.numel()), ctypes.c_void_p(stream)))
+    return o
+
+
+# --------------------------------------------------------------------------
+# query / key normalisation with rotary positions
+# --------------------------------------------------------------------------
+NORMS = {"l2": 0, "rms": 1}
+
+
+def rope_turns(rot, base=10000.0, inv_freq=None, device="cuda"):
+    """Frequencies of a rotation of `rot` values as qk_norm takes them: an int64
+    tensor [rot/2] of turns per position in units of 2^-64.  inv_freq (radians
+    per position, a sequence or tensor of rot/2 numbers) replaces
+    base^(-2i/rot)."""
+    if inv_freq is None:
+        inv_freq = [base ** (-2.0 * i / rot) for i in range(rot // 2)]
+    freq = [float(f) for f in inv_freq]
+    if len(freq) != rot // 2:
+        raise ValueError(f"inv_freq: expected {rot // 2} numbers, got {len(freq)}")
+    turns = [round(f / (2.0 * math.pi) * 2.0 ** 64) % (1 << 64) for f in freq]
+    return torch.tensor([t - (1 << 64) if t >= 1 << 63 else t for t in turns], dtype=torch.int64,
+                        device=device)
+
+
+def _steps(t, name):
+    """(batch, token, head) steps of a token tensor [B,T,H,d] or [N,H,d] whose
+    last dimension is contiguous; 0 for a dimension of one entry."""
+    s, n = t.stride(), t.shape
+    if s[-1] != 1 and n[-1] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if len(n) == 4:
+        return Strides(s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0, s[2] if n[2] > 1 else 0)
+    return Strides(0, s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0)
+
+
+def _like(t, name, dtype, device, shape):
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: expected device {device}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _qk_desc(q, k, wq, wk, positions, turns, norm, eps, interleaved):
+    if norm not in NORMS:
+        raise ValueError(f"norm must be one of {sorted(NORMS)}, got {norm!r}")
+    if q.dim() not in (3, 4):
+        raise ValueError(f"q: expected [B, T, H, d] or [N, H, d], got shape {tuple(q.shape)}")
+    code, dev, lead, d = _dtype_code(q), q.device, q.shape[:-2], q.shape[-1]
+    B, T = lead if len(lead) == 2 else (1, lead[0])
+    Hk = 0
+    if k is not None:
+        if k.dim() != q.dim():
+            raise ValueError(f"k: expected {q.dim()} dimensions, got shape {tuple(k.shape)}")
+        Hk = k.shape[-2]
+        _like(k, "k", q.dtype, dev, lead + (Hk, d))
+    elif wk is not None:
+        raise ValueError("wk without k")
+    for name, w in (("wq", wq), ("wk", wk)):
+        if w is not None:
+            _like(w, name, q.dtype, dev, (d,))
+            if not w.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+    rot = 0
+    if (positions is None) != (turns is None):
+        raise ValueError("positions and turns go together")
+    if positions is not None:
+        _like(positions, "positions", torch.int32, dev, lead)
+        if turns.dtype != torch.int64 or turns.device != dev or turns.dim() != 1:
+            raise ValueError("turns must be a 1-D int64 tensor on q's device")
+        if not (positions.is_contiguous() and turns.is_contiguous()):
+            raise ValueError("positions and turns must be contiguous")
+        rot = 2 * turns.shape[0]
+    desc = QkNormDesc(B, T, q.shape[-2], Hk, d, rot, code, NORMS[norm], int(interleaved), eps)
+    desc.q = _steps(q, "q")
+    if k is not None:
+        desc.k = _steps(k, "k")
+    return desc
+
+
+def _out(t, out, name):
+    if out is None:
+        return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    _like(out, name, t.dtype, t.device, t.shape)
+    return out
+
+
+def qk_norm(q, k=None, wq=None, wk=None, positions=None, turns=None, norm="l2", eps=1e-6,
+            interleaved=False, q_out=None, k_out=None):
+    """Queries and keys normalised for each head, weighted and rotated by
+    position (prism_qk_norm).  Returns (q_out, k_out).
+
+    q [B,T,Hq,d] (or [N,Hq,d]) and k [B,T,Hk,d] in bf16 or fp32, views of a
+    fused projection allowed (contiguous last dimension); k may be None.
+    norm: "l2" (x / |x|) or "rms" (x / root mean square); wq, wk [d] or None.
+    positions (int32, [B,T] or [N]) with turns (rope_turns) rotates the first
+    2 * len(turns) values of each head, in pairs (i, i + rot/2), or (2i, 2i+1)
+    when interleaved.  q_out, k_out: where the results go (new contiguous
+    tensors by default; q and k themselves: in place)."""
+    desc = _qk_desc(q, k, wq, wk, positions, turns, norm, eps, interleaved)
+    _on_gpu(q)
+    q_out = _out(q, q_out, "q_out")
+    desc.qo = _steps(q_out, "q_out")
+    if k is not None:
+        k_out = _out(k, k_out, "k_out")
+        desc.ko = _steps(k_out, "k_out")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    stream = torch.cuda.current_stream(q.device).cuda_stream
+    _check(lib().prism_qk_norm(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk),
+                               _ptr(positions), _ptr(turns), _ptr(q_out), _ptr(k_out), stream))
+    return q_out, k_out
+
+
+def qk_norm_backward(q, k, dq_out, dk_out, wq=None, wk=None, positions=None, turns=None,
+                     norm="l2", eps=1e-6, interleaved=False, dq=None, dk=None, workspace=None):
+    """Gradients of <dq_out, q_out> + <dk_out, k_out> of qk_norm on the same
+    inputs.  Returns a dict: dq, dk (input type; into dq, dk when given), and
+    dwq, dwk (fp32 [d]) for the weights given."""
+    desc = _qk_desc(q, k, wq, wk, positions, turns, norm, eps, interleaved)
+    _like(dq_out, "dq_out", q.dtype, q.device, q.shape)
+    desc.qo = _steps(dq_out, "dq_out")
+    if k is not None:
+        _like(dk_out, "dk_out", k.dtype, k.device, k.shape)
+        desc.ko = _steps(dk_out, "dk_out")
+    _on_gpu(q)
+    out = {"dq": _out(q, dq, "dq")}
+    desc.dq = _steps(out["dq"], "dq")
+    if k is not None:
+        out["dk"] = _out(k, dk, "dk")
+        desc.dk = _steps(out["dk"], "dk")
+    for name, w in (("dwq", wq), ("dwk", wk)):
+        if w is not None:
+            out[name] = torch.empty(w.shape, dtype=torch.float32, device=q.device)
+    if workspace is None and (wq is not None or wk is not None):
+        n = ctypes.c_size_t(0)
+        _check(lib().prism_qk_norm_backward_workspace(ctypes.byref(desc), 1, ctypes.byref(n)))
+        workspace = _workspace(n.value, q.device)[1]
+    stream = torch.cuda.current_stream(q.device).cuda_stream
+    _check(lib().prism_qk_norm_backward(
+        ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(positions), _ptr(turns),
+        _ptr(dq_out), _ptr(dk_out), _ptr(out["dq"]), _ptr(out.get("dk")), _ptr(out.get("dwq")),
+        _ptr(out.get("dwk")), _ptr(workspace), 0 if workspace is None else workspace.numel(),
+        stream))
+    return out
+
+
+# --------------------------------------------------------------------------
+# linear attention with a decay for each head
+# --------------------------------------------------------------------------
+def _la_desc(q, k, v, g, states, scale, cu_seqlens, max_seqlen):
+    """Descriptor of linear attention on q [B,T,H,dk] or, packed, [N,H,dk],
+    after checking every operand's type, device and shape."""
+    code, dev, lead = _dtype_code(q), q.device, q.shape[:-2]
+    N = 0
+    if cu_seqlens is None:
+        if q.dim() != 4:
+            raise ValueError(f"q: expected [B, T, H, dk], got shape {tuple(q.shape)}")
+        B, T = lead
+    else:
+        if max_seqlen is None:
+            raise ValueError("max_seqlen is required with cu_seqlens")
+        _req_cu(cu_seqlens, q)
+        B, T, N = cu_seqlens.numel() - 1, int(max_seqlen), lead[0]
+    if k.dim() != q.dim() or v.dim() != q.dim():
+        raise ValueError(f"k and v: expected {q.dim()} dimensions, got shapes {tuple(k.shape)}, "
+                         f"{tuple(v.shape)}")
+    H, dk, Hk, dv = q.shape[-2], q.shape[-1], k.shape[-2], v.shape[-1]
+    _like(k, "k", q.dtype, dev, lead + (Hk, dk))
+    _like(v, "v", q.dtype, dev, lead + (Hk, dv))
+    if g.dim() == 1:
+        _like(g, "g", torch.float32, dev, (H,))
+        steps = Strides(0, 0, 1)
+    else:
+        _like(g, "g", torch.float32, dev, lead + (H,))
+        steps = Strides(T * H if N == 0 else 0, H, 1)
+    if not g.is_contiguous():
+        raise ValueError("g must be contiguous")
+    for name, S in states:
+        if S is not None:
+            _like(S, name, torch.float32, dev, (B, H, dv, dk))
+            if not S.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+    desc = LinearAttentionDesc(B, T, H, Hk, dk, dv, code, scale, N)
+    desc.q, desc.k, desc.v, desc.g = _steps(q, "q"), _steps(k, "k"), _steps(v, "v"), steps
+    return desc
+
+
+def linear_attention_workspace_bytes(desc, backward=False, need_dg=False):
+    n = ctypes.c_size_t(0)
+    _check(lib().prism_linear_attention_workspace(ctypes.byref(desc), int(backward), int(need_dg),
+                                                  ctypes.byref(n)))
+    return n.value
+
+
+def linear_attention(q, k, v, g, S0=None, scale=1.0, cu_seqlens=None, max_seqlen=None, o=None,
+                     ST=None, workspace=None):
+    """Linear attention with a decay for each head (prism_linear_attention):
+    S_t = exp(g_t) S_{t-1} + v_t k_t^T, o_t = scale S_t q_t.  Returns (o, S_T).
+
+    q [B,T,H,dk], k [B,T,Hk,dk], v [B,T,Hk,dv] in bf16 or fp32 (views of a
+    fused projection allowed), H a multiple of Hk; dk, dv multiples of 16 up to
+    128.  g fp32: [H], or [B,T,H] for a decay of each token.  S0 [B,H,dv,dk]
+    fp32 or None.  cu_seqlens (int32 [B+1]) with max_seqlen packs sequences:
+    token tensors [N,..], g [N,H] or [H].  o, ST: where the results go (new
+    tensors by default; ST may be S0)."""
+    desc = _la_desc(q, k, v, g, (("S0", S0), ("ST", ST)), scale, cu_seqlens, max_seqlen)
+    _on_gpu(q)
+    shape = q.shape[:-1] + (desc.dv,)
+    if o is None:
+        o = torch.empty(shape, dtype=q.dtype, device=q.device)
+    else:
+        _like(o, "o", q.dtype, q.device, shape)
+    desc.o = _steps(o, "o")
+    if ST is None:
+        ST = torch.empty((desc.B, desc.H, desc.dv, desc.dk), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = _workspace(linear_attention_workspace_bytes(desc), q.device)[1]
+    stream = torch.cuda.current_stream(q.device).cuda_stream
+    _check(lib().prism_linear_attention(
+        ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S0), _ptr(cu_seqlens),
+        _ptr(o), _ptr(ST), _ptr(workspace), workspace.numel(), stream))
+    return o, ST
+
+
+def linear_attention_backward(q, k, v, g, dO, S0=None, dST=None, scale=1.0, need_dS0=False,
+                              need_dg=False, cu_seqlens=None, max_seqlen=None, workspace=None):
+    """Gradients of <dO, o> + <dST, S_T> of linear_attention on the same
+    inputs.  Returns a dict: dq, dk, dv (input type), dg (fp32, g's shape) when
+    need_dg, dS0 (fp32) when need_dS0."""
+    desc = _la_desc(q, k, v, g, (("S0", S0), ("dST", dST)), scale, cu_seqlens, max_seqlen)
+    _like(dO, "dO", q.dtype, q.device, q.shape[:-1] + (desc.dv,))
+    desc.o = _steps(dO, "dO")
+    _on_gpu(q)
+    out = {n: torch.empty(t.shape, dtype=t.dtype, device=t.device)
+           for n, t in (("dq", q), ("dk", k), ("dv", v))}
+    if need_dg:
+        out["dg"] = torch.empty(g.shape, dtype=torch.float32, device=q.device)
+    if need_dS0:
+        out["dS0"] = torch.empty((desc.B, desc.H, desc.dv, desc.dk), dtype=torch.float32,
+                                 device=q.device)
+    if workspace is None:
+        workspace = _workspace(linear_attention_workspace_bytes(desc, True, need_dg), q.device)[1]
+    stream = torch.cuda.current_stream(q.device).cuda_stream
+    _check(lib().prism_linear_attention_backward(
+        ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S0), _ptr(cu_seqlens),
+        _ptr(dO), _ptr(dST), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
+        _ptr(out.get("dg")), _ptr(out.get("dS0")), _ptr(workspace), workspace.numel(), stream))
+    return out
+
+
+def linear_attention_step(q, k, v, g, S, S_out=None, scale=1.0, o=None):
+    """The recurrence of linear_attention token by token over the T tokens of
+    each sequence (prism_linear_attention_step); T = 1 is a decode step.  The
+    state S [B,H,dv,dk] fp32 is read; S_T goes to S_out, or into S itself when
+    S_out is None.  Returns o [B,T,H,dv]."""
+    desc = _la_desc(q, k, v, g, (("S", S), ("S_out", S_out)), scale, None, None)
+    _on_gpu(q)
+    shape = q.shape[:-1] + (desc.dv,)
+    if o is None:
+        o = torch.empty(shape, dtype=q.dtype, device=q.device)
+    else:
+        _like(o, "o", q.dtype, q.device, shape)
+    desc.o = _steps(o, "o")
+    stream = torch.cuda.current_stream(q.device).cuda_stream
+    _check(lib().prism_linear_attention_step(
+        ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S),
+        _ptr(S if S_out is None else S_out), _ptr(o), stream))
     return o
 
 
