@@ -9,14 +9,6 @@
 namespace prism {
 
 int la_chunk(bool f32, int dim) { return f32 && dim > 64 ? 32 : 64; }
-int la_slice(int dim) { return dim <= 32 ? 32 : 64; }
-int la_edot_parts(bool f32, int dim, int dc) {
-  const int nv = la_slice(dim), ns = (dc + nv - 1) / nv;
-  // waves along the columns of the transposed output tile (NV x chunk)
-  const int wm = nv == 32 ? Tiling<32, 64, 4>::WM
-                          : (la_chunk(f32, dim) == 32 ? Tiling<64, 32, 4>::WM : Tiling<64, 64, 4>::WM);
-  return ns * wm;
-}
 
 namespace {
 
@@ -81,8 +73,8 @@ __global__ __launch_bounds__(256) void la_decay_kernel(const LaDecay a) {
     const int t = hi - 1 - tid;
     double x = 0.0;
     if (t >= 0) {
-      for (int p = 0; p < a.pq; ++p) x += (double)a.eq[((long)bh * a.pq + p) * a.T + s0 + t];
-      for (int p = 0; p < a.pk; ++p) x -= (double)a.ek[((long)bh * a.pk + p) * a.T + s0 + t];
+      for (int p = 0; p < LA_PARTS; ++p) x += (double)a.eq[((long)bh * LA_PARTS + p) * a.T + s0 + t];
+      for (int p = 0; p < LA_PARTS; ++p) x -= (double)a.ek[((long)bh * LA_PARTS + p) * a.T + s0 + t];
     }
     sm[tid] = x;
     __syncthreads();

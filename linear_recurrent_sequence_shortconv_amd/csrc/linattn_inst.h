@@ -9,19 +9,19 @@ namespace prism {
 // chunk length: 64 tokens; 32 for fp32 rows of 128 (the tiles' LDS)
 template <typename E, int DA> constexpr int la_ch() { return sizeof(E) == 4 && DA == 128 ? 32 : 64; }
 
-template <typename E, int DA, int NV>
+template <typename E, int DA, int NCT>
 hipError_t la_pass_da(const LaArgs<E>& a, bool outputs, bool precise, hipStream_t s) {
   constexpr int CH = la_ch<E, DA>();
-  if (!outputs) return la_launch<E, DA, NV, CH, false, false>(a, s);
-  if (precise) return la_launch<E, DA, NV, CH, true, true>(a, s);
-  return la_launch<E, DA, NV, CH, false, true>(a, s);
+  if (!outputs) return la_launch<E, DA, NCT, CH, false, false>(a, s);
+  if (precise) return la_launch<E, DA, NCT, CH, true, true>(a, s);
+  return la_launch<E, DA, NCT, CH, false, true>(a, s);
 }
 
 template <typename E>
 hipError_t launch_la_pass(const LaArgs<E>& a, int dim, bool outputs, bool precise, hipStream_t s) {
-  if (dim <= 32) return la_pass_da<E, 32, 32>(a, outputs, precise, s);
-  if (dim <= 64) return la_pass_da<E, 64, 64>(a, outputs, precise, s);
-  return la_pass_da<E, 128, 64>(a, outputs, precise, s);
+  if (dim <= 32) return la_pass_da<E, 32, 1>(a, outputs, precise, s);
+  if (dim <= 64) return la_pass_da<E, 64, 1>(a, outputs, precise, s);
+  return la_pass_da<E, 128, 2>(a, outputs, precise, s);
 }
 
 }  // namespace prism

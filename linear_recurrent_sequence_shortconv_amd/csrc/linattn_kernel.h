@@ -5,11 +5,17 @@
 //   X'  = 2^{G_C} X + s_upd B^T (2^{G_C - G} o C)
 // (reverse: i >= t, Gamma_ti = 2^(G_i - G_t), 2^{G_C - G_t} and 2^{G_i}).
 //
-// One workgroup carries a slice of NV columns of X in fp32 accumulators over
-// its segment's chunks: the tiles of A, B, C are fetched one chunk ahead in
-// registers and staged in LDS, out is formed transposed (a lane then holds
-// four consecutive values of one token, stored as one piece), and X goes back
-// to LDS once a chunk as the operand of the next readout.
+// One workgroup of four waves carries X over its segment's chunks; a wave owns
+// 16 NCT of its columns (all DA rows) in fp32 accumulators.  The tiles of A, B
+// and C are fetched one chunk ahead in registers and staged in LDS, the only
+// data the waves share: with a column of out^T and of X in one wave, what one
+// product leaves in accumulators is the next product's operand in the same
+// lanes, so neither X nor Gamma o A B^T passes through LDS.  An accumulator
+// tile holds rows 4 g + r (g = lane / 16) of one column, a k-contiguous operand
+// 8 consecutive k (bf16) of one row at 8 g; the 32 rows of two tiles are
+// therefore assigned to them as 8 g + r and 8 g + 4 + r (the row order of a
+// product's left operand is free).  Each wave forms the scores for itself:
+// 12 of 16 tiles (32-token halves; a half needs itself and the ones before it).
 //
 // Operand rounding (bf16): A, B, C are the inputs themselves.  2^{G_C-G} C, fp32,
 // enters the state's sum as three bf16 pieces (the state is an fp32 result: one
@@ -18,6 +24,8 @@
 // rounding adds), or, with PR, taken in three pieces as well (the gradient of
 // g is a difference of large sums of q . dq and k . dk).
 #pragma once
+
+#include <type_traits>
 
 #include "operators.h"
 #include "prism_common.h"
@@ -48,74 +56,122 @@ struct LaTile {
                   ((unsigned)r * (unsigned)stride + (unsigned)c) * (unsigned)sizeof(E));
     }
   }
-  __device__ inline uint4 get(int p, int r, int c) const {
-    uint4 w = v[p];
-    asm volatile("" : "+v"(w.x), "+v"(w.y), "+v"(w.z), "+v"(w.w));
-    return (r < nv && c < nc) ? w : uint4{0u, 0u, 0u, 0u};
-  }
-  template <typename F>
-  __device__ inline void each(int tid, F&& f) const {
+  // (the fill is a uniform branch of its own: most chunks are whole)
+  __device__ inline void store(E* s, int ld, int tid) {
+    if (nv < ROWS || nc < COLS) {
+#pragma unroll
+      for (int p = 0; p < PER; ++p) {
+        const int u = tid + p * LA_NT;
+        const bool in = u / VPR < nv && (u % VPR) * VN < nc;
+        v[p].x = in ? v[p].x : 0u;
+        v[p].y = in ? v[p].y : 0u;
+        v[p].z = in ? v[p].z : 0u;
+        v[p].w = in ? v[p].w : 0u;
+      }
+    }
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
       const int u = tid + p * LA_NT;
-      const int r = u / VPR, c = (u % VPR) * VN;
-      if (NU % LA_NT == 0 || u < NU) f(r, c, get(p, r, c));
+      if (NU % LA_NT == 0 || u < NU) st16(s + (u / VPR) * ld + (u % VPR) * VN, v[p]);
     }
   }
-  __device__ inline void store(E* s, int ld, int tid) const {
-    each(tid, [&](int r, int c, const uint4& w) { st16(s + r * ld + c, w); });
-  }
 };
 
-// x as NS pieces of type E: p[0] + p[1] + .. = x to NS times E's precision
-template <typename E, int NS>
-__device__ inline void pieces(float x, E (&p)[NS]) {
+// 16-byte operands: KV values of one row at KV (lane / 16), so one instruction
+// (bf16) or four (fp32) contract KG values.
+template <typename E> struct La16;
+template <> struct La16<bf16> {
+  static constexpr int KV = 8, KG = 32, UPG = 2;
+  typedef bf16x8 frag;
+  __device__ static inline f32x4 mma(const frag& a, const frag& b, const f32x4& c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+  // row of an accumulator tile (u-th of its group) -> index in the group
+  __device__ static inline int row(int u, int p) { return 8 * (p >> 2) + 4 * u + (p & 3); }
+  // first of the four indexes that lane group g holds of tile u
+  __device__ static inline int first(int u, int g) { return 8 * g + 4 * u; }
+  // (index row(u, lane & 15), k at k0 + 8 g) of a tile stored [k][index]
+  __device__ static inline frag trans(const bf16* p, int ld, int i0, int u, int k0, int lane, bool mapped) {
+    const int j = lane & 15;
+    const bf16* a = p + (k0 + 8 * (lane >> 4) + (j >> 2)) * ld + i0 + (mapped ? 8 * (j & 3) + 4 * u : 4 * (j & 3));
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(a));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(a + 4 * ld));
+    const short __attribute__((ext_vector_type(8))) w = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    frag f;
+    __builtin_memcpy(&f, &w, 16);
+    return f;
+  }
+};
+template <> struct La16<float> {
+  static constexpr int KV = 4, KG = 16, UPG = 1;
+  typedef f32x4 frag;
+  __device__ static inline f32x4 mma(const frag& a, const frag& b, f32x4 c) {
 #pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    p[i] = to_t<E>(x);
-    x -= to_f(p[i]);
+    for (int r = 0; r < 4; ++r) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], b[r], c, 0, 0, 0);
+    return c;
   }
-}
-
-template <typename E, int DA, int NV, int CH, bool PR, bool OUT>
-struct LaShape {
-  static constexpr bool HALF = sizeof(E) == 2;
-  static constexpr int NSU = HALF ? 3 : 1;              // pieces of the state's summand
-  static constexpr int NSX = HALF && PR ? 3 : 1;        // of X in the readout
-  static constexpr int NSP = HALF && PR ? 3 : 1;        // of Gamma o A B^T
-  static constexpr int LA = ldpad_min<E>(DA), LC = ldpad_min<E>(NV), LP = ldpad_min<E>(CH);
-  struct Lds {
-    alignas(16) E b[CH * LA];
-    alignas(16) E cs[NSU][CH * LC];
-    float gh[2][CH], gl[2][CH], ra[2][CH], rc[2][CH], gc[2];
-    // (only where outputs are formed)
-    alignas(16) E a[OUT ? CH * LA : 8];
-    alignas(16) E c[OUT ? CH * LC : 8];
-    alignas(16) E p[OUT ? NSP : 1][OUT ? CH * LP : 8];
-    alignas(16) E x[OUT ? NSX : 1][OUT ? NV * LA : 8];
-  };
+  __device__ static inline int row(int, int p) { return p; }
+  __device__ static inline int first(int, int g) { return 4 * g; }
+  __device__ static inline frag trans(const float* p, int ld, int i0, int, int k0, int lane, bool) {
+    const float* a = p + (k0 + 4 * (lane >> 4)) * ld + i0 + (lane & 15);
+    return frag{a[0], a[ld], a[2 * ld], a[3 * ld]};
+  }
 };
+
+// x[0 .. KV) as NS operands whose sum is x to NS times E's precision
+template <int NS>
+__device__ inline void la_pieces(const float (&x)[8], bf16x8 (&f)[NS]) {
+  float y[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) y[j] = x[j];
+#pragma unroll
+  for (int k = 0; k < NS; ++k)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      f[k][j] = (bf16)y[j];
+      if (k + 1 < NS) y[j] -= (float)f[k][j];
+    }
+}
+template <int NS>
+__device__ inline void la_pieces(const float (&x)[4], f32x4 (&f)[NS]) {
+  static_assert(NS == 1, "fp32 is one piece");
+  f[0] = f32x4{x[0], x[1], x[2], x[3]};
+}
 
 // log2 decay of a token; below -150 (exp underflows well before) it counts as
 // -150: infinite values would leave inf - inf between two tokens behind them.
 __device__ inline double la_log2(float g) { return (double)(g < -150.f ? -150.f : g) * 1.4426950408889634; }
 
-template <typename E, int DA, int NV, int CH, bool PR, bool OUT>
-__global__ __launch_bounds__(LA_NT) void la_pass_kernel(const LaArgs<E> args) {
-  typedef LaShape<E, DA, NV, CH, PR, OUT> SH;
-  constexpr int LA = SH::LA, LC = SH::LC, LP = SH::LP;
-  __shared__ typename SH::Lds S;
+template <typename E, int DA, int NCT, int CH, bool PR, bool OUT>
+__global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args) {
+  typedef La16<E> M;
+  typedef typename M::frag frag;
+  constexpr bool HALF = sizeof(E) == 2;
+  constexpr int NV = 64 * NCT;                    // columns of X
+  constexpr int KG = M::KG, KV = M::KV, UPG = M::UPG;
+  constexpr int AT = DA / 16, AG = DA / KG;       // tiles and groups of X's rows
+  constexpr int TG = CH / KG;                     // groups of the chunk's tokens
+  constexpr int GPH = 32 / KG;                    // groups of a half of 32 tokens
+  constexpr int NSU = HALF ? 3 : 1;               // pieces of the state's summand
+  constexpr int NSX = HALF && PR ? 3 : 1;         // of X and of Gamma o A B^T in out
+  constexpr int LA = ldpad<E>(DA), LC = ldpad<E>(NV);
+  static_assert(CH == 32 || CH == 64, "halves of 32 tokens");
+  __shared__ __attribute__((aligned(16))) E sb[CH * LA];
+  __shared__ __attribute__((aligned(16))) E sc_[CH * LC];
+  __shared__ __attribute__((aligned(16))) E sa[OUT ? CH * LA : 8];
+  // per token: signed cumulative decays (two floats), row and column factors,
+  // factor to the middle of the chunk; double buffered with the chunks
+  __shared__ __attribute__((aligned(16))) float sgh[2][CH], sgl[2][CH], sra[2][CH], srt[2][CH], smid[2][CH];
+  __shared__ float sgc[2];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l16 = lane & 15, gq = lane >> 4;
 
   int id = xcd_swizzle((int)blockIdx.x, (int)gridDim.x);
-  const int slice = id % args.nslice;
-  id /= args.nslice;
   const LaRole<E>& R = args.r[id % args.nroles];
   id /= args.nroles;
   const int seg = id % args.nseg, bh = id / args.nseg;
   const int b = bh / args.H, h = bh % args.H;
-  const int c0 = slice * NV, nc = min(NV, R.dc - c0);
-  if (nc <= 0) return;
+  const int nc = R.dc;
   const bool rev = R.rev != 0;
 
   // the segment's tokens
@@ -131,36 +187,42 @@ __global__ __launch_bounds__(LA_NT) void la_pass_kernel(const LaArgs<E> args) {
   };
   const E* pa = OUT ? at(R.a, R.sa, R.ga) : nullptr;
   const E* pb = at(R.b, R.sb, R.gb);
-  const E* pc = at(R.c, R.sc, R.gc) + c0;
+  const E* pc = at(R.c, R.sc, R.gc);
   const float* pg = args.g + ((args.cu ? 0 : b * args.sg.b) + row0 * args.sg.t + h * args.sg.h);
 
-  // X: columns c0 .. c0 + NV - 1 of the entering state
-  Acc<DA, NV, LA_NW> X;
-  X.zero();
-  auto state_at = [&](int a, int c) { return (long)a * R.xa + (long)(c0 + c) * R.xc; };
-  auto state_load = [&](const float* src) {
-    for_tiles_ij(X, wave, lane, [&](int i, int j, int a0, int c, const f32x4&) {
-      if (a0 < R.da && c < nc) {
-        f32x4 w;
-        if (R.xa == 1) {
-          w = *reinterpret_cast<const f32x4*>(src + state_at(a0, c));
-        } else {
+  // X: tile (i, j) holds rows KG (i / UPG) + first(i % UPG, g) + r, column cw + 16 j + l16
+  const int cw = wave * 16 * NCT;
+  f32x4 X[AT][NCT];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) w[r] = src[state_at(a0 + r, c)];
-        }
-        X.v[i][j] = w;
+  for (int i = 0; i < AT; ++i)
+#pragma unroll
+    for (int j = 0; j < NCT; ++j) X[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto state_each = [&](auto&& f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < AT; ++i)
+#pragma unroll
+      for (int j = 0; j < NCT; ++j) {
+        const int a0 = KG * (i / UPG) + M::first(i % UPG, gq), c = cw + 16 * j + l16;
+        if (a0 < R.da && c < nc) f(X[i][j], (long)a0 * R.xa + (long)c * R.xc);
+      }
+  };
+  auto state_load = [&](const float* src) __attribute__((always_inline)) {
+    state_each([&](f32x4& x, long o) __attribute__((always_inline)) {
+      if (R.xa == 1) {
+        x = *reinterpret_cast<const f32x4*>(src + o);
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] = src[o + (long)r * R.xa];
       }
     });
   };
-  auto state_store = [&](float* dst) {
-    for_tiles(X, wave, lane, [&](int a0, int c, const f32x4& w) {
-      if (a0 < R.da && c < nc) {
-        if (R.xa == 1) {
-          *reinterpret_cast<f32x4*>(dst + state_at(a0, c)) = w;
-        } else {
+  auto state_store = [&](float* dst) __attribute__((always_inline)) {
+    state_each([&](f32x4& x, long o) __attribute__((always_inline)) {
+      if (R.xa == 1) {
+        *reinterpret_cast<f32x4*>(dst + o) = x;
+      } else {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) dst[state_at(a0 + r, c)] = w[r];
-        }
+        for (int r = 0; r < 4; ++r) dst[o + (long)r * R.xa] = x[r];
       }
     });
   };
@@ -171,51 +233,54 @@ __global__ __launch_bounds__(LA_NT) void la_pass_kernel(const LaArgs<E> args) {
     else if (R.X0)
       state_load(R.X0 + (long)bh * args.DD);
   }
-  auto state_to_lds = [&]() {
-    for_tiles(X, wave, lane, [&](int a0, int c, const f32x4& w) {
-      E pc4[4][SH::NSX];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) pieces(w[r], pc4[r]);
-#pragma unroll
-      for (int k = 0; k < SH::NSX; ++k) {
-        const E x4[4] = {pc4[0][k], pc4[1][k], pc4[2][k], pc4[3][k]};
-        st4(&S.x[k][c * LA + a0], x4);
-      }
-    });
-  };
+
+  // what the loop uses of the arguments, in registers
+  const int sgn = rev ? -1 : 1;
+  const float s_in = R.s_in;
+  const bool wide = R.out32 != nullptr, dots = PR && R.e != nullptr;
+  const int ot = (int)R.so.t, et = (int)R.se.t;
+  const long o0 = (args.cu ? 0 : b * R.so.b) + row0 * R.so.t + h * R.so.h + cw + 4 * gq;
+  E* const po = R.out + o0;
+  float* const po32 = R.out32 + o0;
+  const E* const pe =
+      R.e + ((args.cu ? 0 : b * R.se.b) + row0 * R.se.t + (long)(h / R.ge) * R.se.h + cw + 4 * gq);
+  float* const pd = R.edot + ((long)bh * LA_NW + wave) * args.T + s0;
 
   const int nch = (len + CH - 1) / CH;
   auto first_of = [&](int it) { return (rev ? nch - 1 - it : it) * CH; };
-  LaTile<E, CH, DA> ta, tb;
+  LaTile<E, OUT ? CH : 16, DA> ta;
+  LaTile<E, CH, DA> tb;
   LaTile<E, CH, NV> tc;
   float gv = 0.f;
-  auto fetch = [&](int t0) {
+  auto fetch = [&](int t0) __attribute__((always_inline)) {
     const int nv = min(CH, len - t0);
-    if (OUT) ta.load(pa + (long)t0 * R.sa.t, R.sa.t, nv, R.da, tid);
-    tb.load(pb + (long)t0 * R.sb.t, R.sb.t, nv, R.da, tid);
-    tc.load(pc + (long)t0 * R.sc.t, R.sc.t, nv, nc, tid);
     if (wave == 0) gv = pg[(long)(t0 + min(lane, nv - 1)) * args.sg.t];
+    tb.load(pb + (long)t0 * R.sb.t, R.sb.t, nv, R.da, tid);
+    if (OUT) ta.load(pa + (long)t0 * R.sa.t, R.sa.t, nv, R.da, tid);
+    tc.load(pc + (long)t0 * R.sc.t, R.sc.t, nv, nc, tid);
   };
   // cumulative decays of a chunk of nv tokens (wave 0; tokens past the chunk
   // decay by nothing), and the factors of its rows
   double total = 0.0;
-  auto scan = [&](int buf, int nv) {
+  auto scan = [&](int buf, int nv) __attribute__((always_inline)) {
     double x = lane < nv ? la_log2(gv) : 0.0;
 #pragma unroll
     for (int o = 1; o < CH; o <<= 1) {
       const double y = __shfl_up(x, o);
       if (lane >= o) x += y;
     }
-    const double tot = __shfl(x, CH - 1);
+    const double tot = __shfl(x, CH - 1), mid = __shfl(x, 31);
     if (lane < CH) {
-      const float hi = (float)x;
-      S.gh[buf][lane] = hi;
-      S.gl[buf][lane] = (float)(x - (double)hi);
+      const double y = rev ? -x : x;
+      const float hi = (float)y;
+      sgh[buf][lane] = hi;
+      sgl[buf][lane] = (float)(y - (double)hi);
       const float from = __builtin_amdgcn_exp2f((float)x), to = __builtin_amdgcn_exp2f((float)(tot - x));
-      S.ra[buf][lane] = R.s_row * (rev ? to : from);
-      S.rc[buf][lane] = R.s_upd * (rev ? from : to);
+      sra[buf][lane] = R.s_row * (rev ? to : from);
+      srt[buf][lane] = R.s_upd * (rev ? from : to);
+      smid[buf][lane] = __builtin_amdgcn_exp2f((float)(lane < 32 ? mid - x : x - mid));
     }
-    if (lane == 0) S.gc[buf] = __builtin_amdgcn_exp2f((float)tot);
+    if (lane == 0) sgc[buf] = __builtin_amdgcn_exp2f((float)tot);
     total += tot;
   };
 
@@ -223,121 +288,181 @@ __global__ __launch_bounds__(LA_NT) void la_pass_kernel(const LaArgs<E> args) {
     fetch(first_of(0));
     if (wave == 0) scan(0, min(CH, len - first_of(0)));
   }
-  if (OUT && nch > 0) state_to_lds();
-  __syncthreads();
 
   for (int it = 0; it < nch; ++it) {
     const int buf = it & 1, t0 = first_of(it), nv = min(CH, len - t0);
-    // tiles of this chunk to LDS
-    if (OUT) {
-      ta.store(S.a, LA, tid);
-      tc.store(S.c, LC, tid);
-    }
-    tb.store(S.b, LA, tid);
-    tc.each(tid, [&](int r, int c, const uint4& w) {
-      const E* x = reinterpret_cast<const E*>(&w);
-      constexpr int VN = LaTile<E, CH, NV>::VN;
-      const float f = S.rc[buf][r];
-      E q[SH::NSU][VN];
-#pragma unroll
-      for (int j = 0; j < VN; ++j) {
-        E pcs[SH::NSU];
-        pieces(to_f(x[j]) * f, pcs);
-#pragma unroll
-        for (int k = 0; k < SH::NSU; ++k) q[k][j] = pcs[k];
-      }
-#pragma unroll
-      for (int k = 0; k < SH::NSU; ++k) {
-        uint4 y;
-        __builtin_memcpy(&y, q[k], 16);
-        st16(&S.cs[k][r * LC + c], y);
-      }
-    });
+    tb.store(sb, LA, tid);
+    if constexpr (OUT) ta.store(sa, LA, tid);
+    tc.store(sc_, LC, tid);
     __syncthreads();
     const int tn = first_of(min(it + 1, nch - 1));   // (past the end: the last chunk again)
     fetch(tn);
 
-    Acc<NV, CH, LA_NW> acc;
     if constexpr (OUT) {
-      // transposed: rows i (or c), columns t
-      Acc<CH, CH, LA_NW> sc;
-      sc.zero();
-      gemm_acc<E, CH, CH, DA, LA_NW, true, true>(sc, S.b, LA, S.a, LA, wave, lane);
-      acc.zero();
+      // out of the 32 tokens of one half: th its index, BIG: with the other
+      // half's tokens behind its own
+      auto half = [&](int th, auto big) __attribute__((always_inline)) {
+        constexpr bool BIG = decltype(big)::value;
+        constexpr int NH = BIG ? 2 : 1;   // halves of i: own, other
+        f32x4 p[NH][2][2];                // [half][tile of i][tile of t]
+        f32x4 acc[NCT][2];
 #pragma unroll
-      for (int k = 0; k < SH::NSX; ++k)
-        gemm_acc<E, NV, CH, DA, LA_NW, true, true>(acc, S.x[k], LA, S.a, LA, wave, lane);
-      for_tiles(sc, wave, lane, [&](int i0, int t, const f32x4& w) {
-        const float th = S.gh[buf][t], tl = S.gl[buf][t];
-        E pc4[4][SH::NSP];
+        for (int j = 0; j < 2; ++j) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int i = i0 + r;
-          const float dif = (th - S.gh[buf][i]) + (tl - S.gl[buf][i]);
-          const float e = __builtin_amdgcn_exp2f(rev ? -dif : dif);
-          pieces((rev ? i >= t : i <= t) ? R.s_in * e * w[r] : 0.f, pc4[r]);
+          for (int x = 0; x < NH; ++x) p[x][0][j] = p[x][1][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < NCT; ++c) acc[c][j] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
+        const E* a0 = sa + (32 * th + l16) * LA + KV * gq;
+        const int ih[2] = {th, 1 - th};
 #pragma unroll
-        for (int k = 0; k < SH::NSP; ++k) {
-          const E x4[4] = {pc4[0][k], pc4[1][k], pc4[2][k], pc4[3][k]};
-          st4(&S.p[k][t * LP + i0], x4);
-        }
-      });
-      for_tiles_ij(acc, wave, lane, [&](int i, int j, int, int t, const f32x4&) {
-        const float f = S.ra[buf][t];
+        for (int k = 0; k < AG; ++k) {
+          frag fa[2];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc.v[i][j][r] *= f;
-      });
-    }
-    if (wave == 0 && it + 1 < nch) scan(buf ^ 1, min(CH, len - tn));
-    if (OUT) __syncthreads();
-
-    if constexpr (OUT) {
+          for (int j = 0; j < 2; ++j) fa[j] = *reinterpret_cast<const frag*>(a0 + 16 * j * LA + KG * k);
 #pragma unroll
-      for (int k = 0; k < SH::NSP; ++k)
-        gemm_acc<E, NV, CH, CH, LA_NW, false, true>(acc, S.c, LC, S.p[k], LP, wave, lane);
-      // out, and its dots with the rows of e
-      typedef Tiling<NV, CH, LA_NW> TL;
-      float dot[TL::RN];
+          for (int x = 0; x < NH; ++x)
 #pragma unroll
-      for (int j = 0; j < TL::RN; ++j) dot[j] = 0.f;
-      for_tiles_ij(acc, wave, lane, [&](int, int j, int cl, int t, const f32x4& w) {
-        if (t < nv && cl < nc) {
-          const long tok = row0 + t0 + t;
-          const long o = (args.cu ? 0 : b * R.so.b) + tok * R.so.t + h * R.so.h + c0 + cl;
-          if (R.out32)
-            st_f4(R.out32 + o, w);
-          else
-            st_f4(R.out + o, w);
-          if (PR && R.e) {
-            const f32x4 x = raw4_to_f(ld_raw4(
-                R.e + ((args.cu ? 0 : b * R.se.b) + tok * R.se.t + (long)(h / R.ge) * R.se.h + c0 + cl)));
-            dot[j] += (w[0] * x[0] + w[1] * x[1]) + (w[2] * x[2] + w[3] * x[3]);
+            for (int i = 0; i < 2; ++i) {
+              const int row = 32 * ih[x] + KG * (i / UPG) + M::row(i % UPG, l16);
+              const frag fb = *reinterpret_cast<const frag*>(sb + row * LA + KV * gq + KG * k);
+#pragma unroll
+              for (int j = 0; j < 2; ++j) p[x][i][j] = M::mma(fb, fa[j], p[x][i][j]);
+            }
+#pragma unroll
+          for (int c = 0; c < NCT; ++c) {
+            float x[KV];
+#pragma unroll
+            for (int u = 0; u < UPG; ++u)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) x[4 * u + r] = X[UPG * k + u][c][r];
+            frag fx[NSX];
+            la_pieces(x, fx);
+#pragma unroll
+            for (int s = 0; s < NSX; ++s)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) acc[c][j] = M::mma(fx[s], fa[j], acc[c][j]);
           }
         }
-      });
-      if (PR && R.e && TL::active(wave)) {
-        const int part = slice * TL::WM + wave / TL::WN;
-        const int parts = (R.dc + NV - 1) / NV * TL::WM;
+        // readout factors; Gamma and the mask
+        frag fp[NH][GPH][2][NSX];
 #pragma unroll
-        for (int j = 0; j < TL::RN; ++j) {
-          dot[j] += __shfl_xor(dot[j], 16);
-          dot[j] += __shfl_xor(dot[j], 32);
-          const int t = TL::n0(wave) + 16 * j + (lane & 15);
-          if (lane < 16 && t < nv) R.edot[((long)bh * parts + part) * args.T + s0 + t0 + t] = dot[j];
+        for (int j = 0; j < 2; ++j) {
+          const int t = 32 * th + 16 * j + l16;
+          const float f = sra[buf][t], hi = sgh[buf][t], lo = sgl[buf][t], md = s_in * smid[buf][t];
+#pragma unroll
+          for (int c = 0; c < NCT; ++c) acc[c][j] *= f;
+#pragma unroll
+          for (int x = 0; x < NH; ++x) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int i0 = 32 * ih[x] + KG * (i / UPG) + M::first(i % UPG, gq);
+              if (x == 0) {
+                const f32x4 ghi = *reinterpret_cast<const f32x4*>(&sgh[buf][i0]);
+                const f32x4 glo = *reinterpret_cast<const f32x4*>(&sgl[buf][i0]);
+                const int ahead = sgn * (t - i0);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                  float dif = hi - ghi[r];
+                  if (!HALF || PR) dif += lo - glo[r];
+                  // (masked: 2^-inf; a select of the exponent keeps this free of branches)
+                  dif = ahead >= sgn * r ? dif : -__builtin_inff();
+                  p[x][i][j][r] *= s_in * __builtin_amdgcn_exp2f(dif);
+                }
+              } else {
+                const f32x4 m = *reinterpret_cast<const f32x4*>(&smid[buf][i0]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) p[x][i][j][r] *= md * m[r];
+              }
+            }
+#pragma unroll
+            for (int q = 0; q < GPH; ++q) {
+              float y[KV];
+#pragma unroll
+              for (int u = 0; u < UPG; ++u)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) y[4 * u + r] = p[x][q * UPG + u][j][r];
+              la_pieces(y, fp[x][q][j]);
+            }
+          }
         }
+#pragma unroll
+        for (int x = 0; x < NH; ++x)
+#pragma unroll
+          for (int q = 0; q < GPH; ++q)
+#pragma unroll
+            for (int c = 0; c < NCT; ++c) {
+              const frag fc = M::trans(sc_, LC, cw + 16 * c, 0, 32 * ih[x] + KG * q, lane, false);
+#pragma unroll
+              for (int s = 0; s < NSX; ++s)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc[c][j] = M::mma(fc, fp[x][q][j][s], acc[c][j]);
+            }
+        // out, and its dots with the rows of e
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int t = 32 * th + 16 * j + l16;
+          float dot = 0.f;
+#pragma unroll
+          for (int c = 0; c < NCT; ++c) {
+            if (t < nv && cw + 16 * c + 4 * gq < nc) {
+              const long o = (long)(t0 + t) * ot + 16 * c;
+              if (wide)
+                st_f4(po32 + o, acc[c][j]);
+              else
+                st_f4(po + o, acc[c][j]);
+              if (dots) {
+                const f32x4 x = raw4_to_f(ld_raw4(pe + ((long)(t0 + t) * et + 16 * c)));
+                dot += (acc[c][j][0] * x[0] + acc[c][j][1] * x[1]) + (acc[c][j][2] * x[2] + acc[c][j][3] * x[3]);
+              }
+            }
+          }
+          if (dots) {
+            dot += __shfl_xor(dot, 16);
+            dot += __shfl_xor(dot, 32);
+            if (gq == 0 && t < nv) pd[t0 + t] = dot;
+          }
+        }
+      };
+      if constexpr (CH == 64) {
+        half(rev ? 1 : 0, std::integral_constant<bool, false>());
+        half(rev ? 0 : 1, std::integral_constant<bool, true>());
+      } else {
+        half(0, std::integral_constant<bool, false>());
       }
     }
+
     // X' = 2^{G_C} X + B^T (factor o C)
-    const float gc = S.gc[buf];
-    for_tiles_ij(X, wave, lane, [&](int i, int j, int, int, const f32x4&) {
+    const float gc = sgc[buf];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) X.v[i][j][r] *= gc;
-    });
+    for (int i = 0; i < AT; ++i)
 #pragma unroll
-    for (int k = 0; k < SH::NSU; ++k)
-      gemm_acc<E, DA, NV, CH, LA_NW, false, false>(X, S.b, LA, S.cs[k], LC, wave, lane);
-    if (OUT && it + 1 < nch) state_to_lds();
+      for (int j = 0; j < NCT; ++j) X[i][j] *= gc;
+#pragma unroll
+    for (int q = 0; q < TG; ++q) {
+      frag fc[NCT][NSU];
+#pragma unroll
+      for (int c = 0; c < NCT; ++c) {
+        const frag raw = M::trans(sc_, LC, cw + 16 * c, 0, KG * q, lane, false);
+        float x[KV];
+#pragma unroll
+        for (int v = 0; v < KV; v += 4) {
+          const f32x4 f = *reinterpret_cast<const f32x4*>(&srt[buf][KG * q + KV * gq + v]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) x[v + r] = f[r] * to_f(raw[v + r]);
+        }
+        la_pieces(x, fc[c]);
+      }
+#pragma unroll
+      for (int i = 0; i < AT; ++i) {
+        const frag fb = M::trans(sb, LA, HALF ? KG * (i / UPG) : 16 * i, i % UPG, KG * q, lane, true);
+#pragma unroll
+        for (int s = 0; s < NSU; ++s)
+#pragma unroll
+          for (int c = 0; c < NCT; ++c) X[i][c] = M::mma(fb, fc[c][s], X[i][c]);
+      }
+    }
+    if (wave == 0 && it + 1 < nch) scan(buf ^ 1, min(CH, len - tn));
     __syncthreads();
   }
 
@@ -345,15 +470,15 @@ __global__ __launch_bounds__(LA_NT) void la_pass_kernel(const LaArgs<E> args) {
     if (last && R.fin) state_store(R.fin + (long)bh * args.DD);
   } else {
     state_store(R.seg + segoff);
-    if (tid == 0 && slice == 0) R.segdec[(long)bh * args.nseg + seg] = __builtin_amdgcn_exp2f((float)total);
+    if (tid == 0) R.segdec[(long)bh * args.nseg + seg] = __builtin_amdgcn_exp2f((float)total);
   }
 }
 
-// Launch of one instance; DA and NV by the operands' size.
-template <typename E, int DA, int NV, int CH, bool PR, bool OUT>
+// Launch of one instance; DA and NCT by the operands' size.
+template <typename E, int DA, int NCT, int CH, bool PR, bool OUT>
 hipError_t la_launch(const LaArgs<E>& a, hipStream_t s) {
-  const unsigned grid = (unsigned)((long)a.B * a.H * a.nseg * a.nroles * a.nslice);
-  hipLaunchKernelGGL((la_pass_kernel<E, DA, NV, CH, PR, OUT>), dim3(grid), dim3(LA_NT), 0, s, a);
+  const unsigned grid = (unsigned)((long)a.B * a.H * a.nseg * a.nroles);
+  hipLaunchKernelGGL((la_pass_kernel<E, DA, NCT, CH, PR, OUT>), dim3(grid), dim3(LA_NT), 0, s, a);
   return hipGetLastError();
 }
 

@@ -52,7 +52,7 @@ struct LaRole {
   const E* e;              // rows dotted with out (fp32, before rounding), or nullptr
   Strides se;
   int ge;
-  float* edot;             // [B * H][parts][T] partial dots
+  float* edot;             // [B * H][LA_PARTS][T] partial dots
   int da, dc, rev;
   float s_in, s_row, s_upd;
   const float* X0;         // [B, H, dv, dk] entering state (nullptr: zeros)
@@ -66,19 +66,17 @@ constexpr int LA_ROLES = 3;
 // chunks), worked on side by side.
 template <typename E>
 struct LaArgs {
-  int B, T, H, nseg, seglen, nslice, nroles;
+  int B, T, H, nseg, seglen, nroles;
   int DD;                  // dv * dk
   const int* cu;           // sanitised offsets of a packed batch, or nullptr
   const float* g;
   Strides sg;
   LaRole<E> r[LA_ROLES];
 };
-// Tokens per chunk, and columns of C per workgroup, for operands of `dim`
-// (= max(dk, dv)) values.
+// Tokens per chunk for operands of `dim` (= max(dk, dv)) values.
 int la_chunk(bool f32, int dim);
-int la_slice(int dim);
-// Partial row dots written for each token.
-int la_edot_parts(bool f32, int dim, int dc);
+// Partial row dots written for each token (one a wave).
+constexpr int LA_PARTS = 4;
 // outputs = false: the segments' own states only (role.seg, role.segdec).
 // precise: bf16 operands of every product in three pieces.
 template <typename E>
@@ -97,11 +95,11 @@ hipError_t launch_la_join(const LaJoin& a, hipStream_t s);
 // dg from the row dots: dg_t = sum_{i >= t} (q_i.dq_i - k_i.dk_i) + <dS, S> at
 // the segment's end.
 struct LaDecay {
-  int B, T, H, nseg, seglen, DD, pq, pk;
+  int B, T, H, nseg, seglen, DD;
   const int* cu;
   const float* g;
   Strides sg;
-  const float *eq, *ek;            // [B * H][pq or pk][T]
+  const float *eq, *ek;            // [B * H][LA_PARTS][T]
   const float *segf, *segr;        // entering states, forward and reverse (nseg > 1)
   const float *ST, *dST;           // final state and its gradient (nullptr: zero)
   float* dg;                       // strided like g, or, for one decay a head,

@@ -228,15 +228,8 @@ void plan_segments(const prism_linear_attention_desc& d, int wide, LaPlan* p) {
   p->nseg = (int)(chunks > 0 ? (chunks + per - 1) / per : 1);
 }
 
-int slices(int dim, int dc) {
-  const int nv = prism::la_slice(dim);
-  return (dc + nv - 1) / nv;
-}
-
-void plan_forward(const prism_linear_attention_desc& d, LaPlan* p) { plan_segments(d, slices(p->dim, d.dv), p); }
-void plan_backward(const prism_linear_attention_desc& d, LaPlan* p) {
-  plan_segments(d, 2 * slices(p->dim, d.dk) + slices(p->dim, d.dv), p);
-}
+void plan_forward(const prism_linear_attention_desc& d, LaPlan* p) { plan_segments(d, 1, p); }
+void plan_backward(const prism_linear_attention_desc& d, LaPlan* p) { plan_segments(d, 3, p); }
 
 struct LaFwdWs {
   int* cu;
@@ -272,9 +265,8 @@ LaBwdWs carve_la_bwd(const prism_linear_attention_desc& d, const LaPlan& p, bool
     w.dvp = cv.take<float>((size_t)p.rows * d.H * d.dv * 4);
   }
   if (dg) {
-    const size_t parts = (size_t)prism::la_edot_parts(p.f32, p.dim, d.dk);
-    w.eq = cv.take<float>(p.bh * parts * d.T * 4);
-    w.ek = cv.take<float>(p.bh * parts * d.T * 4);
+    w.eq = cv.take<float>(p.bh * prism::LA_PARTS * d.T * 4);
+    w.ek = cv.take<float>(p.bh * prism::LA_PARTS * d.T * 4);
     w.ST = cv.take<float>(p.bh * p.DD * 4);
     w.tmp = cv.take<float>(p.bh * d.T * 4);
   }
@@ -357,7 +349,6 @@ prism_status la_forward(const prism_linear_attention_desc& d, const LaPlan& p, c
   r.segdec = w.dec;
   a.r[0] = r;
   a.nroles = 1;
-  a.nslice = slices(p.dim, d.dv);
   if (p.nseg > 1) {
     HIP_TRY("la_states", s, prism::launch_la_pass<E>(a, p.dim, false, false, s));
     prism::LaJoin j = {};
@@ -421,13 +412,11 @@ prism_status la_backward(const prism_linear_attention_desc& d, const LaPlan& p, 
   rv.X0 = dST;
   rv.seg = w.segr;
   prism::LaArgs<E> a = la_args<E>(d, p, cu, g);
-  const int nk = slices(p.dim, d.dk), nv = slices(p.dim, d.dv);
   if (p.nseg > 1 && d.B > 0) {
     prism::LaArgs<E> b = a;
     b.r[0] = rq;
     b.r[1] = rk;
     b.nroles = 2;
-    b.nslice = nk;
     HIP_TRY("la_states", s, prism::launch_la_pass<E>(b, p.dim, false, false, s));
     prism::LaJoin j = {};
     j.B = d.B;
@@ -458,18 +447,15 @@ prism_status la_backward(const prism_linear_attention_desc& d, const LaPlan& p, 
     a.r[0] = rq;
     a.r[1] = rk;
     a.nroles = 2;
-    a.nslice = nk;
     HIP_TRY("la_bwd_qk", s, prism::launch_la_pass<E>(a, p.dim, true, true, s));
     a.r[0] = rv;
     a.nroles = 1;
-    a.nslice = nv;
     HIP_TRY("la_bwd_v", s, prism::launch_la_pass<E>(a, p.dim, true, false, s));
   } else if (d.B > 0) {
     a.r[0] = rq;
     a.r[1] = rk;
     a.r[2] = rv;
     a.nroles = 3;
-    a.nslice = nk > nv ? nk : nv;
     HIP_TRY("la_bwd", s, prism::launch_la_pass<E>(a, p.dim, true, false, s));
   }
   if (dg) {
@@ -480,7 +466,6 @@ prism_status la_backward(const prism_linear_attention_desc& d, const LaPlan& p, 
     x.nseg = p.nseg;
     x.seglen = p.seglen;
     x.DD = (int)p.DD;
-    x.pq = x.pk = prism::la_edot_parts(p.f32, p.dim, d.dk);
     x.cu = cu;
     x.g = g;
     x.sg = strides(d.g);
