@@ -8,7 +8,6 @@
 
 namespace prism {
 
-int la_chunk(bool f32, int dim) { return f32 && dim > 64 ? 32 : 64; }
 
 namespace {
 

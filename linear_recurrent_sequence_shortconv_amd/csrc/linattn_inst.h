@@ -6,15 +6,11 @@
 
 namespace prism {
 
-// chunk length: 64 tokens; 32 for fp32 rows of 128 (the tiles' LDS)
-template <typename E, int DA> constexpr int la_ch() { return sizeof(E) == 4 && DA == 128 ? 32 : 64; }
-
 template <typename E, int DA, int NCT>
 hipError_t la_pass_da(const LaArgs<E>& a, bool outputs, bool precise, hipStream_t s) {
-  constexpr int CH = la_ch<E, DA>();
-  if (!outputs) return la_launch<E, DA, NCT, CH, false, false>(a, s);
-  if (precise) return la_launch<E, DA, NCT, CH, true, true>(a, s);
-  return la_launch<E, DA, NCT, CH, false, true>(a, s);
+  if (!outputs) return la_launch<E, DA, NCT, false, false>(a, s);
+  if (precise) return la_launch<E, DA, NCT, true, true>(a, s);
+  return la_launch<E, DA, NCT, false, true>(a, s);
 }
 
 template <typename E>

@@ -1,4 +1,4 @@
-// Linear attention with a decay for each head, over chunks of CH tokens
+// Linear attention with a decay for each head, over chunks of 32 tokens
 // (LaRole in operators.h has the formula).  In a chunk entered with state X,
 // with the cumulative log2 decays G_1 .. G_C of its tokens (Gamma_ti = 2^(G_t - G_i)):
 //   out = s_in (Gamma o A B^T)_{i<=t} C + s_row 2^G o (A X)
@@ -14,8 +14,9 @@
 // tile holds rows 4 g + r (g = lane / 16) of one column, a k-contiguous operand
 // 8 consecutive k (bf16) of one row at 8 g; the 32 rows of two tiles are
 // therefore assigned to them as 8 g + r and 8 g + 4 + r (the row order of a
-// product's left operand is free).  Each wave forms the scores for itself:
-// 12 of 16 tiles (32-token halves; a half needs itself and the ones before it).
+// product's left operand is free).  Each wave forms the scores for itself.
+// The staged tiles are double buffered: one barrier a chunk.  The decays are
+// summed for 256 tokens at a time, one token a thread.
 //
 // Operand rounding (bf16): A, B, C are the inputs themselves.  2^{G_C-G} C, fp32,
 // enters the state's sum as three bf16 pieces (the state is an fp32 result: one
@@ -32,7 +33,7 @@
 
 namespace prism {
 
-constexpr int LA_NW = 4, LA_NT = LA_NW * WAVE;
+constexpr int LA_NW = LA_PARTS, LA_NT = LA_NW * WAVE;
 
 // ROWS x COLS of T in registers as 16-byte pieces; rows >= nv and columns >=
 // nc (a multiple of the piece) are zeros.  Loads read the nearest valid piece
@@ -142,27 +143,30 @@ __device__ inline void la_pieces(const float (&x)[4], f32x4 (&f)[NS]) {
 // -150: infinite values would leave inf - inf between two tokens behind them.
 __device__ inline double la_log2(float g) { return (double)(g < -150.f ? -150.f : g) * 1.4426950408889634; }
 
-template <typename E, int DA, int NCT, int CH, bool PR, bool OUT>
+template <typename E, int DA, int NCT, bool PR, bool OUT>
 __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args) {
   typedef La16<E> M;
   typedef typename M::frag frag;
+  constexpr int CH = LA_CHUNK;
   constexpr bool HALF = sizeof(E) == 2;
   constexpr int NV = 64 * NCT;                    // columns of X
   constexpr int KG = M::KG, KV = M::KV, UPG = M::UPG;
   constexpr int AT = DA / 16, AG = DA / KG;       // tiles and groups of X's rows
   constexpr int TG = CH / KG;                     // groups of the chunk's tokens
-  constexpr int GPH = 32 / KG;                    // groups of a half of 32 tokens
   constexpr int NSU = HALF ? 3 : 1;               // pieces of the state's summand
   constexpr int NSX = HALF && PR ? 3 : 1;         // of X and of Gamma o A B^T in out
   constexpr int LA = ldpad<E>(DA), LC = ldpad<E>(NV);
-  static_assert(CH == 32 || CH == 64, "halves of 32 tokens");
-  __shared__ __attribute__((aligned(16))) E sb[CH * LA];
-  __shared__ __attribute__((aligned(16))) E sc_[CH * LC];
-  __shared__ __attribute__((aligned(16))) E sa[OUT ? CH * LA : 8];
-  // per token: signed cumulative decays (two floats), row and column factors,
-  // factor to the middle of the chunk; double buffered with the chunks
-  __shared__ __attribute__((aligned(16))) float sgh[2][CH], sgl[2][CH], sra[2][CH], srt[2][CH], smid[2][CH];
-  __shared__ float sgc[2];
+  // (fp32 rows of 128 take too much LDS for two workgroups a CU with two buffers)
+  constexpr int NBUF = OUT && !HALF && DA == 128 ? 1 : 2;
+  constexpr int CPB = LA_NT / CH;                 // chunks of a batch of decays
+  __shared__ __attribute__((aligned(16))) E sb_[NBUF][CH * LA];
+  __shared__ __attribute__((aligned(16))) E sc_[NBUF][CH * LC];
+  __shared__ __attribute__((aligned(16))) E sa_[NBUF][OUT ? CH * LA : 8];
+  // per token: signed cumulative decays in its chunk (two floats), row and
+  // column factors; per chunk: its decay, also as a log.  Two batches.
+  __shared__ __attribute__((aligned(16))) float sgh[2][LA_NT], sgl[2][LA_NT], sra[2][LA_NT], srt[2][LA_NT];
+  __shared__ float sgc[2][CPB];
+  __shared__ double sgt[2][CPB];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, gq = lane >> 4;
 
@@ -251,189 +255,148 @@ __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args)
   LaTile<E, OUT ? CH : 16, DA> ta;
   LaTile<E, CH, DA> tb;
   LaTile<E, CH, NV> tc;
-  float gv = 0.f;
   auto fetch = [&](int t0) __attribute__((always_inline)) {
     const int nv = min(CH, len - t0);
-    if (wave == 0) gv = pg[(long)(t0 + min(lane, nv - 1)) * args.sg.t];
     tb.load(pb + (long)t0 * R.sb.t, R.sb.t, nv, R.da, tid);
     if (OUT) ta.load(pa + (long)t0 * R.sa.t, R.sa.t, nv, R.da, tid);
     tc.load(pc + (long)t0 * R.sc.t, R.sc.t, nv, nc, tid);
   };
-  // cumulative decays of a chunk of nv tokens (wave 0; tokens past the chunk
-  // decay by nothing), and the factors of its rows
-  double total = 0.0;
-  auto scan = [&](int buf, int nv) __attribute__((always_inline)) {
-    double x = lane < nv ? la_log2(gv) : 0.0;
+  // a thread's token in the batch of chunks from `it` on (tokens past the
+  // segment decay by nothing), its cumulative decay in its chunk, its factors
+  float gv = 0.f;
+  const int bq = tid / CH, bj = tid % CH;
+  auto batch_token = [&](int it) { return it + bq < nch ? first_of(it + bq) + bj : len; };
+  auto batch_load = [&](int it) __attribute__((always_inline)) {
+    gv = pg[(long)min(batch_token(it), len - 1) * args.sg.t];
+  };
+  auto batch_scan = [&](int it) __attribute__((always_inline)) {
+    const int buf = (it / CPB) & 1;
+    double x = batch_token(it) < len ? la_log2(gv) : 0.0;
 #pragma unroll
     for (int o = 1; o < CH; o <<= 1) {
-      const double y = __shfl_up(x, o);
-      if (lane >= o) x += y;
+      const double y = __shfl_up(x, o, CH);
+      if (bj >= o) x += y;
     }
-    const double tot = __shfl(x, CH - 1), mid = __shfl(x, 31);
-    if (lane < CH) {
-      const double y = rev ? -x : x;
-      const float hi = (float)y;
-      sgh[buf][lane] = hi;
-      sgl[buf][lane] = (float)(y - (double)hi);
-      const float from = __builtin_amdgcn_exp2f((float)x), to = __builtin_amdgcn_exp2f((float)(tot - x));
-      sra[buf][lane] = R.s_row * (rev ? to : from);
-      srt[buf][lane] = R.s_upd * (rev ? from : to);
-      smid[buf][lane] = __builtin_amdgcn_exp2f((float)(lane < 32 ? mid - x : x - mid));
+    const double tot = __shfl(x, CH - 1, CH);
+    const double y = rev ? -x : x;
+    const float hi = (float)y;
+    sgh[buf][tid] = hi;
+    sgl[buf][tid] = (float)(y - (double)hi);
+    const float from = __builtin_amdgcn_exp2f((float)x), to = __builtin_amdgcn_exp2f((float)(tot - x));
+    sra[buf][tid] = R.s_row * (rev ? to : from);
+    srt[buf][tid] = R.s_upd * (rev ? from : to);
+    if (bj == 0) {
+      sgc[buf][bq] = __builtin_amdgcn_exp2f((float)tot);
+      sgt[buf][bq] = tot;
     }
-    if (lane == 0) sgc[buf] = __builtin_amdgcn_exp2f((float)tot);
-    total += tot;
   };
 
+  double total = 0.0;
   if (nch > 0) {
     fetch(first_of(0));
-    if (wave == 0) scan(0, min(CH, len - first_of(0)));
+    batch_load(0);
   }
 
   for (int it = 0; it < nch; ++it) {
-    const int buf = it & 1, t0 = first_of(it), nv = min(CH, len - t0);
+    const int t0 = first_of(it), nv = min(CH, len - t0);
+    if (it % CPB == 0) {
+      batch_scan(it);
+      batch_load(min(it + CPB, nch - 1));
+    }
+    const int bat = (it / CPB) & 1, boff = (it % CPB) * CH;
+    const float *gh = &sgh[bat][boff], *gl = &sgl[bat][boff], *ra = &sra[bat][boff], *rt = &srt[bat][boff];
+    E *sa = sa_[it % NBUF], *sb = sb_[it % NBUF], *sc = sc_[it % NBUF];
     tb.store(sb, LA, tid);
     if constexpr (OUT) ta.store(sa, LA, tid);
-    tc.store(sc_, LC, tid);
+    tc.store(sc, LC, tid);
     __syncthreads();
-    const int tn = first_of(min(it + 1, nch - 1));   // (past the end: the last chunk again)
-    fetch(tn);
+    fetch(first_of(min(it + 1, nch - 1)));   // (past the end: the last chunk again)
 
+    f32x4 acc[NCT][2];                       // out^T, [tile of columns][tile of t]
     if constexpr (OUT) {
-      // out of the 32 tokens of one half: th its index, BIG: with the other
-      // half's tokens behind its own
-      auto half = [&](int th, auto big) __attribute__((always_inline)) {
-        constexpr bool BIG = decltype(big)::value;
-        constexpr int NH = BIG ? 2 : 1;   // halves of i: own, other
-        f32x4 p[NH][2][2];                // [half][tile of i][tile of t]
-        f32x4 acc[NCT][2];
+      f32x4 p[2][2];                         // scores^T, [tile of i][tile of t]
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < 2; ++j) {
+        p[0][j] = p[1][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int x = 0; x < NH; ++x) p[x][0][j] = p[x][1][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int c = 0; c < NCT; ++c) acc[c][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-        }
-        const E* a0 = sa + (32 * th + l16) * LA + KV * gq;
-        const int ih[2] = {th, 1 - th};
-#pragma unroll
-        for (int k = 0; k < AG; ++k) {
-          frag fa[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) fa[j] = *reinterpret_cast<const frag*>(a0 + 16 * j * LA + KG * k);
-#pragma unroll
-          for (int x = 0; x < NH; ++x)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int row = 32 * ih[x] + KG * (i / UPG) + M::row(i % UPG, l16);
-              const frag fb = *reinterpret_cast<const frag*>(sb + row * LA + KV * gq + KG * k);
-#pragma unroll
-              for (int j = 0; j < 2; ++j) p[x][i][j] = M::mma(fb, fa[j], p[x][i][j]);
-            }
-#pragma unroll
-          for (int c = 0; c < NCT; ++c) {
-            float x[KV];
-#pragma unroll
-            for (int u = 0; u < UPG; ++u)
-#pragma unroll
-              for (int r = 0; r < 4; ++r) x[4 * u + r] = X[UPG * k + u][c][r];
-            frag fx[NSX];
-            la_pieces(x, fx);
-#pragma unroll
-            for (int s = 0; s < NSX; ++s)
-#pragma unroll
-              for (int j = 0; j < 2; ++j) acc[c][j] = M::mma(fx[s], fa[j], acc[c][j]);
-          }
-        }
-        // readout factors; Gamma and the mask
-        frag fp[NH][GPH][2][NSX];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int t = 32 * th + 16 * j + l16;
-          const float f = sra[buf][t], hi = sgh[buf][t], lo = sgl[buf][t], md = s_in * smid[buf][t];
-#pragma unroll
-          for (int c = 0; c < NCT; ++c) acc[c][j] *= f;
-#pragma unroll
-          for (int x = 0; x < NH; ++x) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int i0 = 32 * ih[x] + KG * (i / UPG) + M::first(i % UPG, gq);
-              if (x == 0) {
-                const f32x4 ghi = *reinterpret_cast<const f32x4*>(&sgh[buf][i0]);
-                const f32x4 glo = *reinterpret_cast<const f32x4*>(&sgl[buf][i0]);
-                const int ahead = sgn * (t - i0);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                  float dif = hi - ghi[r];
-                  if (!HALF || PR) dif += lo - glo[r];
-                  // (masked: 2^-inf; a select of the exponent keeps this free of branches)
-                  dif = ahead >= sgn * r ? dif : -__builtin_inff();
-                  p[x][i][j][r] *= s_in * __builtin_amdgcn_exp2f(dif);
-                }
-              } else {
-                const f32x4 m = *reinterpret_cast<const f32x4*>(&smid[buf][i0]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) p[x][i][j][r] *= md * m[r];
-              }
-            }
-#pragma unroll
-            for (int q = 0; q < GPH; ++q) {
-              float y[KV];
-#pragma unroll
-              for (int u = 0; u < UPG; ++u)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) y[4 * u + r] = p[x][q * UPG + u][j][r];
-              la_pieces(y, fp[x][q][j]);
-            }
-          }
-        }
-#pragma unroll
-        for (int x = 0; x < NH; ++x)
-#pragma unroll
-          for (int q = 0; q < GPH; ++q)
-#pragma unroll
-            for (int c = 0; c < NCT; ++c) {
-              const frag fc = M::trans(sc_, LC, cw + 16 * c, 0, 32 * ih[x] + KG * q, lane, false);
-#pragma unroll
-              for (int s = 0; s < NSX; ++s)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) acc[c][j] = M::mma(fc, fp[x][q][j][s], acc[c][j]);
-            }
-        // out, and its dots with the rows of e
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int t = 32 * th + 16 * j + l16;
-          float dot = 0.f;
-#pragma unroll
-          for (int c = 0; c < NCT; ++c) {
-            if (t < nv && cw + 16 * c + 4 * gq < nc) {
-              const long o = (long)(t0 + t) * ot + 16 * c;
-              if (wide)
-                st_f4(po32 + o, acc[c][j]);
-              else
-                st_f4(po + o, acc[c][j]);
-              if (dots) {
-                const f32x4 x = raw4_to_f(ld_raw4(pe + ((long)(t0 + t) * et + 16 * c)));
-                dot += (acc[c][j][0] * x[0] + acc[c][j][1] * x[1]) + (acc[c][j][2] * x[2] + acc[c][j][3] * x[3]);
-              }
-            }
-          }
-          if (dots) {
-            dot += __shfl_xor(dot, 16);
-            dot += __shfl_xor(dot, 32);
-            if (gq == 0 && t < nv) pd[t0 + t] = dot;
-          }
-        }
-      };
-      if constexpr (CH == 64) {
-        half(rev ? 1 : 0, std::integral_constant<bool, false>());
-        half(rev ? 0 : 1, std::integral_constant<bool, true>());
-      } else {
-        half(0, std::integral_constant<bool, false>());
+        for (int c = 0; c < NCT; ++c) acc[c][j] = f32x4{0.f, 0.f, 0.f, 0.f};
       }
+#pragma unroll
+      for (int k = 0; k < AG; ++k) {
+        frag fa[2], fb[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          fa[j] = *reinterpret_cast<const frag*>(sa + (16 * j + l16) * LA + KV * gq + KG * k);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          fb[i] = *reinterpret_cast<const frag*>(sb + (KG * (i / UPG) + M::row(i % UPG, l16)) * LA + KV * gq + KG * k);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) p[i][j] = M::mma(fb[i], fa[j], p[i][j]);
+#pragma unroll
+        for (int c = 0; c < NCT; ++c) {
+          float x[KV];
+#pragma unroll
+          for (int u = 0; u < UPG; ++u)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[4 * u + r] = X[UPG * k + u][c][r];
+          frag fx[NSX];
+          la_pieces(x, fx);
+#pragma unroll
+          for (int s = 0; s < NSX; ++s)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) acc[c][j] = M::mma(fx[s], fa[j], acc[c][j]);
+        }
+      }
+      // readout factors; Gamma and the mask
+      frag fp[TG][2][NSX];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int t = 16 * j + l16;
+        const float f = ra[t], hi = gh[t], lo = gl[t];
+#pragma unroll
+        for (int c = 0; c < NCT; ++c) acc[c][j] *= f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int i0 = KG * (i / UPG) + M::first(i % UPG, gq);
+          const f32x4 ghi = *reinterpret_cast<const f32x4*>(gh + i0);
+          const f32x4 glo = *reinterpret_cast<const f32x4*>(gl + i0);
+          const int ahead = sgn * (t - i0);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            float dif = hi - ghi[r];
+            if (!HALF || PR) dif += lo - glo[r];
+            // (masked: 2^-inf; a select of the exponent keeps this free of branches)
+            dif = ahead >= sgn * r ? dif : -__builtin_inff();
+            p[i][j][r] *= s_in * __builtin_amdgcn_exp2f(dif);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < TG; ++q) {
+          float y[KV];
+#pragma unroll
+          for (int u = 0; u < UPG; ++u)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) y[4 * u + r] = p[q * UPG + u][j][r];
+          la_pieces(y, fp[q][j]);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < TG; ++q)
+#pragma unroll
+        for (int c = 0; c < NCT; ++c) {
+          const frag fc = M::trans(sc, LC, cw + 16 * c, 0, KG * q, lane, false);
+#pragma unroll
+          for (int s = 0; s < NSX; ++s)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) acc[c][j] = M::mma(fc, fp[q][j][s], acc[c][j]);
+        }
     }
 
     // X' = 2^{G_C} X + B^T (factor o C)
-    const float gc = sgc[buf];
+    const float gc = sgc[bat][it % CPB];
+    if (!OUT) total += sgt[bat][it % CPB];
 #pragma unroll
     for (int i = 0; i < AT; ++i)
 #pragma unroll
@@ -443,11 +406,11 @@ __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args)
       frag fc[NCT][NSU];
 #pragma unroll
       for (int c = 0; c < NCT; ++c) {
-        const frag raw = M::trans(sc_, LC, cw + 16 * c, 0, KG * q, lane, false);
+        const frag raw = M::trans(sc, LC, cw + 16 * c, 0, KG * q, lane, false);
         float x[KV];
 #pragma unroll
         for (int v = 0; v < KV; v += 4) {
-          const f32x4 f = *reinterpret_cast<const f32x4*>(&srt[buf][KG * q + KV * gq + v]);
+          const f32x4 f = *reinterpret_cast<const f32x4*>(rt + KG * q + KV * gq + v);
 #pragma unroll
           for (int r = 0; r < 4; ++r) x[v + r] = f[r] * to_f(raw[v + r]);
         }
@@ -462,8 +425,35 @@ __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args)
           for (int c = 0; c < NCT; ++c) X[i][c] = M::mma(fb, fc[c][s], X[i][c]);
       }
     }
-    if (wave == 0 && it + 1 < nch) scan(buf ^ 1, min(CH, len - tn));
-    __syncthreads();
+
+    // out, and its dots with the rows of e
+    if constexpr (OUT) {
+      auto out_each = [&](auto&& f) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int c = 0; c < NCT; ++c)
+            if (16 * j + l16 < nv && cw + 16 * c + 4 * gq < nc) f(j, c, (long)(t0 + 16 * j + l16));
+      };
+      if (wide)
+        out_each([&](int j, int c, long t) { st_f4(po32 + t * ot + 16 * c, acc[c][j]); });
+      else
+        out_each([&](int j, int c, long t) { st_f4(po + t * ot + 16 * c, acc[c][j]); });
+      if (dots) {
+        float dot[2] = {0.f, 0.f};
+        out_each([&](int j, int c, long t) {
+          const f32x4 x = raw4_to_f(ld_raw4(pe + t * et + 16 * c));
+          dot[j] += (acc[c][j][0] * x[0] + acc[c][j][1] * x[1]) + (acc[c][j][2] * x[2] + acc[c][j][3] * x[3]);
+        });
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          dot[j] += __shfl_xor(dot[j], 16);
+          dot[j] += __shfl_xor(dot[j], 32);
+          if (gq == 0 && 16 * j + l16 < nv) pd[t0 + 16 * j + l16] = dot[j];
+        }
+      }
+    }
+    if (NBUF == 1) __syncthreads();
   }
 
   if (OUT) {
@@ -475,10 +465,10 @@ __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args)
 }
 
 // Launch of one instance; DA and NCT by the operands' size.
-template <typename E, int DA, int NCT, int CH, bool PR, bool OUT>
+template <typename E, int DA, int NCT, bool PR, bool OUT>
 hipError_t la_launch(const LaArgs<E>& a, hipStream_t s) {
   const unsigned grid = (unsigned)((long)a.B * a.H * a.nseg * a.nroles);
-  hipLaunchKernelGGL((la_pass_kernel<E, DA, NCT, CH, PR, OUT>), dim3(grid), dim3(LA_NT), 0, s, a);
+  hipLaunchKernelGGL((la_pass_kernel<E, DA, NCT, PR, OUT>), dim3(grid), dim3(LA_NT), 0, s, a);
   return hipGetLastError();
 }
 

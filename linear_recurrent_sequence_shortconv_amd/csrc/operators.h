@@ -73,8 +73,7 @@ struct LaArgs {
   Strides sg;
   LaRole<E> r[LA_ROLES];
 };
-// Tokens per chunk for operands of `dim` (= max(dk, dv)) values.
-int la_chunk(bool f32, int dim);
+constexpr int LA_CHUNK = 32;   // tokens per chunk
 // Partial row dots written for each token (one a wave).
 constexpr int LA_PARTS = 4;
 // outputs = false: the segments' own states only (role.seg, role.segdec).

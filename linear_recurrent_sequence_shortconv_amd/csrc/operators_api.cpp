@@ -216,7 +216,7 @@ prism_status check_la(const prism_linear_attention_desc* desc, bool packed, LaPl
 // Segments a sequence is cut into: enough that the passes fill the chip
 // (`wide` workgroups of the pass for each (b, h)), none under 256 tokens.
 void plan_segments(const prism_linear_attention_desc& d, int wide, LaPlan* p) {
-  const int ch = prism::la_chunk(p->f32, p->dim);
+  const int ch = prism::LA_CHUNK;
   const long have = (long)p->bh * wide, want = 512;
   long nseg = have > 0 ? (want + have - 1) / have : 1;
   const long most = (d.T + 255) / 256;
