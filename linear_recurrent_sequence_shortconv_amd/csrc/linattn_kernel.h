@@ -1,16 +1,24 @@
 // Linear attention with a decay for each head, over chunks of 32 tokens
-// (LaRole in operators.h has the formula).  In a chunk entered with state X,
-// with the cumulative log2 decays G_1 .. G_C of its tokens (Gamma_ti = 2^(G_t - G_i)):
-//   out = s_in (Gamma o A B^T)_{i<=t} C + s_row 2^G o (A X)
-//   X'  = 2^{G_C} X + s_upd B^T (2^{G_C - G} o C)
-// (reverse: i >= t, Gamma_ti = 2^(G_i - G_t), 2^{G_C - G_t} and 2^{G_i}).
+// (LaRole in operators.h has the formula).  With u_t the log2 decay from the
+// chunk's entry to token t in the direction of the pass (forward: G_t, the sum
+// of the decays up to t; reverse: G_C - G_t), a chunk entered with state X gives
+//   out_t = s_row 2^{u_t} A_t (X + s_upd sum_{i <= t} 2^{-u_i} B_i C_i^T)
+//   X'    = 2^{G_C} (X + s_upd sum_i 2^{-u_i} B_i C_i^T)
+// (reverse: i >= t; s_row s_upd = s_in).  X is kept without the decay: with F
+// the log2 decay since X was last brought up to date, the registers hold
+// 2^{-F} X, rows are read out with 2^{F + u_t} and added with 2^{-(F + u_i)},
+// so that a chunk costs no pass over X and no decay between pairs of tokens.
+// That holds while F + u stays within +-80; X is brought up to date (F = 0)
+// every 256 tokens, or when a chunk would leave this range, and a chunk that
+// leaves it by itself (a decay by 2^-80 within 32 tokens, a reset) takes the form with
+// Gamma_ti = 2^{u_t - u_i} on each pair and 2^{G_C - u_i} on each added row.
 //
 // One workgroup of four waves carries X over its segment's chunks; a wave owns
 // 16 NCT of its columns (all DA rows) in fp32 accumulators.  The tiles of A, B
 // and C are fetched one chunk ahead in registers and staged in LDS, the only
 // data the waves share: with a column of out^T and of X in one wave, what one
 // product leaves in accumulators is the next product's operand in the same
-// lanes, so neither X nor Gamma o A B^T passes through LDS.  An accumulator
+// lanes, so neither X nor the scores pass through LDS.  An accumulator
 // tile holds rows 4 g + r (g = lane / 16) of one column, a k-contiguous operand
 // 8 consecutive k (bf16) of one row at 8 g; the 32 rows of two tiles are
 // therefore assigned to them as 8 g + r and 8 g + 4 + r (the row order of a
@@ -18,9 +26,9 @@
 // The staged tiles are double buffered: one barrier a chunk.  The decays are
 // summed for 256 tokens at a time, one token a thread.
 //
-// Operand rounding (bf16): A, B, C are the inputs themselves.  2^{G_C-G} C, fp32,
+// Operand rounding (bf16): A, B, C are the inputs themselves.  2^{-(F+u)} C, fp32,
 // enters the state's sum as three bf16 pieces (the state is an fp32 result: one
-// piece would leave it 2e-3 off).  Gamma o A B^T and the copy of X in the
+// piece would leave it 2e-3 off).  The scaled scores and the copy of X in the
 // readout are rounded once to bf16 (out is bf16: each adds what the final
 // rounding adds), or, with PR, taken in three pieces as well (the gradient of
 // g is a difference of large sums of q . dq and k . dk).
@@ -45,17 +53,24 @@ struct LaTile {
   static constexpr int NU = ROWS * VPR;
   static constexpr int PER = (NU + LA_NT - 1) / LA_NT;
   uint4 v[PER];
+  unsigned row[PER], col[PER];   // byte offsets
+  unsigned step;
   int nv, nc;
-  __device__ inline void load(const E* g, long stride, int nvalid, int ncols, int tid) {
-    nv = nvalid;
+  __device__ inline void place(long stride, int ncols, int tid) {
     nc = ncols;
+    step = (unsigned)stride * (unsigned)sizeof(E);
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
       const int u = min(tid + p * LA_NT, NU - 1);
-      const int r = min(u / VPR, nv - 1), c = min((u % VPR) * VN, nc - VN);
-      v[p] = ld16(reinterpret_cast<const char*>(g) +
-                  ((unsigned)r * (unsigned)stride + (unsigned)c) * (unsigned)sizeof(E));
+      row[p] = (unsigned)(u / VPR) * step;
+      col[p] = (unsigned)min((u % VPR) * VN, nc - VN) * (unsigned)sizeof(E);
     }
+  }
+  __device__ inline void load(const E* g, int nvalid) {
+    nv = nvalid;
+    const unsigned end = (unsigned)(nvalid - 1) * step;
+#pragma unroll
+    for (int p = 0; p < PER; ++p) v[p] = ld16(reinterpret_cast<const char*>(g) + (min(row[p], end) + col[p]));
   }
   // (the fill is a uniform branch of its own: most chunks are whole)
   __device__ inline void store(E* s, int ld, int tid) {
@@ -139,9 +154,56 @@ __device__ inline void la_pieces(const float (&x)[4], f32x4 (&f)[NS]) {
   f[0] = f32x4{x[0], x[1], x[2], x[3]};
 }
 
+// Four values at element `at` of a buffer from a wave-uniform address; nothing
+// is written where the byte offset passes the buffer's 2^31 - 1 bytes, as that
+// of LA_NOWHERE does (a chunk's own are under 32 rows of 2^22 elements).
+constexpr unsigned LA_NOWHERE = 0x60000000u;   // (2 and 4 times it, mod 2^32, are 2^31 or more)
+__device__ inline __amdgpu_buffer_rsrc_t la_buffer(void* p) {
+  return __builtin_amdgcn_make_buffer_rsrc(p, 0, 0x7fffffff, 0x00020000);
+}
+__device__ inline void la_store4(__amdgpu_buffer_rsrc_t p, unsigned at, const f32x4& x, float) {
+  typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), p, at * 4u, 0, 0);
+}
+__device__ inline void la_store4(__amdgpu_buffer_rsrc_t p, unsigned at, const f32x4& x, bf16) {
+  typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+  const bf16 b[4] = {(bf16)x[0], (bf16)x[1], (bf16)x[2], (bf16)x[3]};
+  u32x2 w;
+  __builtin_memcpy(&w, b, 8);
+  __builtin_amdgcn_raw_buffer_store_b64(w, p, at * 2u, 0, 0);
+}
+
 // log2 decay of a token; below -150 (exp underflows well before) it counts as
 // -150: infinite values would leave inf - inf between two tokens behind them.
 __device__ inline double la_log2(float g) { return (double)(g < -150.f ? -150.f : g) * 1.4426950408889634; }
+
+// log2 range of the factors kept without the decay: their products with each
+// other and with the data stay finite in fp32.
+constexpr double LA_RANGE = 80.0;
+
+// Inclusive prefix sum over each 32 lanes: shifts within rows of 16 lanes, then
+// the first row's sum to the second (lane 15 to the row behind it).
+template <int CTRL, int ROWS>
+__device__ inline double la_dpp(double x) {
+  const long long b = __builtin_bit_cast(long long, x);
+  const unsigned lo = __builtin_amdgcn_update_dpp(0, (int)b, CTRL, ROWS, 0xf, ROWS == 0xf);
+  const unsigned hi = __builtin_amdgcn_update_dpp(0, (int)(b >> 32), CTRL, ROWS, 0xf, ROWS == 0xf);
+  return __builtin_bit_cast(double, (long long)(((unsigned long long)hi << 32) | lo));
+}
+__device__ inline double la_scan32(double x) {
+  x += la_dpp<0x111, 0xf>(x);
+  x += la_dpp<0x112, 0xf>(x);
+  x += la_dpp<0x114, 0xf>(x);
+  x += la_dpp<0x118, 0xf>(x);
+  x += la_dpp<0x142, 0xa>(x);
+  return x;
+}
+// Sum over each 32 lanes, in the last of them
+__device__ inline float la_sum32(float x) {
+  x = row16_sum(x);
+  const int b = __builtin_bit_cast(int, x);
+  return x + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, b, 0x142, 0xa, 0xf, false));
+}
 
 template <typename E, int DA, int NCT, bool PR, bool OUT>
 __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args) {
@@ -162,11 +224,14 @@ __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args)
   __shared__ __attribute__((aligned(16))) E sb_[NBUF][CH * LA];
   __shared__ __attribute__((aligned(16))) E sc_[NBUF][CH * LC];
   __shared__ __attribute__((aligned(16))) E sa_[NBUF][OUT ? CH * LA : 8];
-  // per token: signed cumulative decays in its chunk (two floats), row and
-  // column factors; per chunk: its decay, also as a log.  Two batches.
-  __shared__ __attribute__((aligned(16))) float sgh[2][LA_NT], sgl[2][LA_NT], sra[2][LA_NT], srt[2][LA_NT];
-  __shared__ float sgc[2][CPB];
-  __shared__ double sgt[2][CPB];
+  // per token: u (two floats), readout and update factors; per chunk: factors of
+  // X before its readout and before its update, and whether it takes the form
+  // with Gamma.  Two batches.
+  __shared__ __attribute__((aligned(16))) float suh[2][LA_NT], sul[2][LA_NT], sra[2][LA_NT], srt[2][LA_NT];
+  __shared__ float sm0[2][CPB], sm1[2][CPB];
+  __shared__ int strong[2][CPB];
+  __shared__ double stot[CPB];
+  __shared__ float spos[CPB];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, gq = lane >> 4;
 
@@ -239,31 +304,43 @@ __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args)
   }
 
   // what the loop uses of the arguments, in registers
-  const int sgn = rev ? -1 : 1;
   const float s_in = R.s_in;
   const bool wide = R.out32 != nullptr, dots = PR && R.e != nullptr;
-  const int ot = (int)R.so.t, et = (int)R.se.t;
-  const long o0 = (args.cu ? 0 : b * R.so.b) + row0 * R.so.t + h * R.so.h + cw + 4 * gq;
-  E* const po = R.out + o0;
-  float* const po32 = R.out32 + o0;
-  const E* const pe =
-      R.e + ((args.cu ? 0 : b * R.se.b) + row0 * R.se.t + (long)(h / R.ge) * R.se.h + cw + 4 * gq);
+  const long ot = R.so.t, et = R.se.t;
+  const long o0 = (args.cu ? 0 : b * R.so.b) + row0 * ot + h * R.so.h;
+  const long e0 = (args.cu ? 0 : b * R.se.b) + row0 * et + (long)(h / R.ge) * R.se.h;
   float* const pd = R.edot + ((long)bh * LA_NW + wave) * args.T + s0;
+  // the lane's place in a chunk's output and e rows (elements)
+  unsigned ol[2], el[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    ol[j] = (unsigned)(16 * j + l16) * (unsigned)ot + (unsigned)(cw + 4 * gq);
+    el[j] = (unsigned)(16 * j + l16) * (unsigned)et + (unsigned)(cw + 4 * gq);
+  }
+  // masked scores: bits kept of each value of p[i][j] (its i against its t)
+  auto keep = [&](int i, int j, int r) {
+    const int ii = KG * (i / UPG) + M::first(i % UPG, gq) + r, t = 16 * j + l16;
+    return rev ? ii >= t : ii <= t;
+  };
 
   const int nch = (len + CH - 1) / CH;
   auto first_of = [&](int it) { return (rev ? nch - 1 - it : it) * CH; };
   LaTile<E, OUT ? CH : 16, DA> ta;
   LaTile<E, CH, DA> tb;
   LaTile<E, CH, NV> tc;
+  if (OUT) ta.place(R.sa.t, R.da, tid);
+  tb.place(R.sb.t, R.da, tid);
+  tc.place(R.sc.t, nc, tid);
   auto fetch = [&](int t0) __attribute__((always_inline)) {
     const int nv = min(CH, len - t0);
-    tb.load(pb + (long)t0 * R.sb.t, R.sb.t, nv, R.da, tid);
-    if (OUT) ta.load(pa + (long)t0 * R.sa.t, R.sa.t, nv, R.da, tid);
-    tc.load(pc + (long)t0 * R.sc.t, R.sc.t, nv, nc, tid);
+    tb.load(pb + (long)t0 * R.sb.t, nv);
+    if (OUT) ta.load(pa + (long)t0 * R.sa.t, nv);
+    tc.load(pc + (long)t0 * R.sc.t, nv);
   };
   // a thread's token in the batch of chunks from `it` on (tokens past the
-  // segment decay by nothing), its cumulative decay in its chunk, its factors
+  // segment decay by nothing), and its factors
   float gv = 0.f;
+  double F = 0.0, total = 0.0;
   const int bq = tid / CH, bj = tid % CH;
   auto batch_token = [&](int it) { return it + bq < nch ? first_of(it + bq) + bj : len; };
   auto batch_load = [&](int it) __attribute__((always_inline)) {
@@ -272,30 +349,85 @@ __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args)
   auto batch_scan = [&](int it) __attribute__((always_inline)) {
     const int buf = (it / CPB) & 1;
     double x = batch_token(it) < len ? la_log2(gv) : 0.0;
-#pragma unroll
-    for (int o = 1; o < CH; o <<= 1) {
-      const double y = __shfl_up(x, o, CH);
-      if (bj >= o) x += y;
-    }
+    float pos = (float)fmax(x, 0.0);
+    x = la_scan32(x);
+    pos = la_sum32(pos);
     const double tot = __shfl(x, CH - 1, CH);
-    const double y = rev ? -x : x;
-    const float hi = (float)y;
-    sgh[buf][tid] = hi;
-    sgl[buf][tid] = (float)(y - (double)hi);
-    const float from = __builtin_amdgcn_exp2f((float)x), to = __builtin_amdgcn_exp2f((float)(tot - x));
-    sra[buf][tid] = R.s_row * (rev ? to : from);
-    srt[buf][tid] = R.s_upd * (rev ? from : to);
+    const double u = rev ? tot - x : x;
+    if (bj == CH - 1) {
+      stot[bq] = tot;
+      spos[bq] = pos;
+    }
+    __syncthreads();
+    // Every batch starts with X up to date.  u of a chunk lies between its sum
+    // less its positive part and its positive part.
+    double f = 0.0, sum = 0.0;
+    float up = 0.f;
+#pragma unroll
+    for (int q = 0; q < CPB; ++q) {
+      const double t = stot[q];
+      if (q < bq) f += t;
+      sum += t;
+      up += spos[q];
+    }
+    double m0 = bq == 0 ? F : 0.0, m1 = 0.0;   // log2 factors of X at this thread's chunk
+    bool st = false;
+    total += sum;
+    if (up <= LA_RANGE && sum - up >= -LA_RANGE) {
+      F = sum;
+    } else {
+      // chunk after chunk (every thread alike).  (A NaN takes the strong form,
+      // which spreads it as the recurrence would.)
+#pragma unroll 1
+      for (int q = 0; q < CPB; ++q) {
+        const double t = stot[q], hi = spos[q], lo = t - hi;
+        double pre = 0.0, post = 0.0;
+        bool s = false;
+        if (q == 0 || !(F + lo >= -LA_RANGE && F + hi <= LA_RANGE)) {
+          pre = F;
+          F = 0.0;
+          s = !(lo >= -LA_RANGE && hi <= LA_RANGE);
+          if (s) post = t;
+        }
+        if (q == bq) {
+          f = F;
+          m0 = pre;
+          m1 = post;
+          st = s;
+        }
+        if (!s) F += t;
+      }
+    }
+    const float uh = (float)u;
+    suh[buf][tid] = uh;
+    sul[buf][tid] = (float)(u - (double)uh);
+    sra[buf][tid] = R.s_row * __builtin_amdgcn_exp2f((float)(f + u));
+    srt[buf][tid] = R.s_upd * __builtin_amdgcn_exp2f((float)((st ? tot : -f) - u));
     if (bj == 0) {
-      sgc[buf][bq] = __builtin_amdgcn_exp2f((float)tot);
-      sgt[buf][bq] = tot;
+      sm0[buf][bq] = __builtin_amdgcn_exp2f((float)m0);
+      sm1[buf][bq] = __builtin_amdgcn_exp2f((float)m1);
+      strong[buf][bq] = st;
+    }
+  };
+  auto state_scale = [&](float m) __attribute__((always_inline)) {
+    if (m != 1.f) {
+#pragma unroll
+      for (int i = 0; i < AT; ++i)
+#pragma unroll
+        for (int j = 0; j < NCT; ++j) X[i][j] *= m;
     }
   };
 
-  double total = 0.0;
   if (nch > 0) {
     fetch(first_of(0));
     batch_load(0);
   }
+  // X here, not at its first use in the loop: a wait there for loads from
+  // before the loop would in every chunk wait for the stores of the one before
+#pragma unroll
+  for (int i = 0; i < AT; ++i)
+#pragma unroll
+    for (int j = 0; j < NCT; ++j) asm volatile("" : "+v"(X[i][j]));
 
   for (int it = 0; it < nch; ++it) {
     const int t0 = first_of(it), nv = min(CH, len - t0);
@@ -304,13 +436,15 @@ __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args)
       batch_load(min(it + CPB, nch - 1));
     }
     const int bat = (it / CPB) & 1, boff = (it % CPB) * CH;
-    const float *gh = &sgh[bat][boff], *gl = &sgl[bat][boff], *ra = &sra[bat][boff], *rt = &srt[bat][boff];
+    const float *uh = &suh[bat][boff], *ul = &sul[bat][boff], *ra = &sra[bat][boff], *rt = &srt[bat][boff];
     E *sa = sa_[it % NBUF], *sb = sb_[it % NBUF], *sc = sc_[it % NBUF];
     tb.store(sb, LA, tid);
     if constexpr (OUT) ta.store(sa, LA, tid);
     tc.store(sc, LC, tid);
     __syncthreads();
     fetch(first_of(min(it + 1, nch - 1)));   // (past the end: the last chunk again)
+    const bool st = __builtin_amdgcn_readfirstlane(strong[bat][it % CPB]) != 0;
+    state_scale(sm0[bat][it % CPB]);
 
     f32x4 acc[NCT][2];                       // out^T, [tile of columns][tile of t]
     if constexpr (OUT) {
@@ -321,19 +455,26 @@ __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args)
 #pragma unroll
         for (int c = 0; c < NCT; ++c) acc[c][j] = f32x4{0.f, 0.f, 0.f, 0.f};
       }
+      // (every operand requested before the first product: read as they are
+      // used, each group of products would wait out an LDS access)
+      frag fa[AG][2], fb[AG][2];
 #pragma unroll
       for (int k = 0; k < AG; ++k) {
-        frag fa[2], fb[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          fa[j] = *reinterpret_cast<const frag*>(sa + (16 * j + l16) * LA + KV * gq + KG * k);
+          fa[k][j] = *reinterpret_cast<const frag*>(sa + (16 * j + l16) * LA + KV * gq + KG * k);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          fb[i] = *reinterpret_cast<const frag*>(sb + (KG * (i / UPG) + M::row(i % UPG, l16)) * LA + KV * gq + KG * k);
+          fb[k][i] =
+              *reinterpret_cast<const frag*>(sb + (KG * (i / UPG) + M::row(i % UPG, l16)) * LA + KV * gq + KG * k);
+      }
+      if (HALF) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int k = 0; k < AG; ++k) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) p[i][j] = M::mma(fb[i], fa[j], p[i][j]);
+          for (int j = 0; j < 2; ++j) p[i][j] = M::mma(fb[k][i], fa[k][j], p[i][j]);
 #pragma unroll
         for (int c = 0; c < NCT; ++c) {
           float x[KV];
@@ -346,42 +487,50 @@ __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args)
 #pragma unroll
           for (int s = 0; s < NSX; ++s)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) acc[c][j] = M::mma(fx[s], fa[j], acc[c][j]);
+            for (int j = 0; j < 2; ++j) acc[c][j] = M::mma(fx[s], fa[k][j], acc[c][j]);
         }
       }
-      // readout factors; Gamma and the mask
-      frag fp[TG][2][NSX];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int t = 16 * j + l16;
-        const float f = ra[t], hi = gh[t], lo = gl[t];
-#pragma unroll
-        for (int c = 0; c < NCT; ++c) acc[c][j] *= f;
+      // factors of the added rows (or Gamma), the mask, operands
+      float fin[2];
+      if (!st) {
+        fin[0] = ra[l16];
+        fin[1] = ra[16 + l16];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int i0 = KG * (i / UPG) + M::first(i % UPG, gq);
-          const f32x4 ghi = *reinterpret_cast<const f32x4*>(gh + i0);
-          const f32x4 glo = *reinterpret_cast<const f32x4*>(gl + i0);
-          const int ahead = sgn * (t - i0);
+          const f32x4 f = *reinterpret_cast<const f32x4*>(rt + KG * (i / UPG) + M::first(i % UPG, gq));
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            float dif = hi - ghi[r];
-            if (!HALF || PR) dif += lo - glo[r];
-            // (masked: 2^-inf; a select of the exponent keeps this free of branches)
-            dif = ahead >= sgn * r ? dif : -__builtin_inff();
-            p[i][j][r] *= s_in * __builtin_amdgcn_exp2f(dif);
+          for (int j = 0; j < 2; ++j) p[i][j] *= f;
+        }
+      } else {
+        fin[0] = fin[1] = 1.f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float f = ra[16 * j + l16], hi = uh[16 * j + l16], lo = ul[16 * j + l16];
+#pragma unroll
+          for (int c = 0; c < NCT; ++c) acc[c][j] *= f;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int i0 = KG * (i / UPG) + M::first(i % UPG, gq);
+            const f32x4 vh = *reinterpret_cast<const f32x4*>(uh + i0), vl = *reinterpret_cast<const f32x4*>(ul + i0);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              p[i][j][r] *= s_in * __builtin_amdgcn_exp2f((hi - vh[r]) + (lo - vl[r]));
           }
         }
+      }
+      frag fp[TG][2][NSX];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int q = 0; q < TG; ++q) {
           float y[KV];
 #pragma unroll
           for (int u = 0; u < UPG; ++u)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) y[4 * u + r] = p[q * UPG + u][j][r];
+            for (int r = 0; r < 4; ++r)
+              y[4 * u + r] = keep(q * UPG + u, j, r) ? p[q * UPG + u][j][r] : 0.f;
           la_pieces(y, fp[q][j]);
         }
-      }
 #pragma unroll
       for (int q = 0; q < TG; ++q)
 #pragma unroll
@@ -392,59 +541,79 @@ __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args)
 #pragma unroll
             for (int j = 0; j < 2; ++j) acc[c][j] = M::mma(fc, fp[q][j][s], acc[c][j]);
         }
+#pragma unroll
+      for (int c = 0; c < NCT; ++c)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[c][j] *= fin[j];
     }
 
-    // X' = 2^{G_C} X + B^T (factor o C)
-    const float gc = sgc[bat][it % CPB];
-    if (!OUT) total += sgt[bat][it % CPB];
-#pragma unroll
-    for (int i = 0; i < AT; ++i)
-#pragma unroll
-      for (int j = 0; j < NCT; ++j) X[i][j] *= gc;
+    // the chunk's rows into X
+    state_scale(sm1[bat][it % CPB]);
 #pragma unroll
     for (int q = 0; q < TG; ++q) {
-      frag fc[NCT][NSU];
+      frag raw[NCT], fc[NCT][NSU], fb[HALF ? AT : 1];
+#pragma unroll
+      for (int c = 0; c < NCT; ++c) raw[c] = M::trans(sc, LC, cw + 16 * c, 0, KG * q, lane, false);
+      f32x4 f[KV / 4];
+#pragma unroll
+      for (int v = 0; v < KV / 4; ++v) f[v] = *reinterpret_cast<const f32x4*>(rt + KG * q + KV * gq + 4 * v);
+      if (HALF) {
+#pragma unroll
+        for (int i = 0; i < AT; ++i) fb[HALF ? i : 0] = M::trans(sb, LA, KG * (i / UPG), i % UPG, KG * q, lane, true);
+        __builtin_amdgcn_sched_barrier(0);
+      }
 #pragma unroll
       for (int c = 0; c < NCT; ++c) {
-        const frag raw = M::trans(sc, LC, cw + 16 * c, 0, KG * q, lane, false);
         float x[KV];
 #pragma unroll
-        for (int v = 0; v < KV; v += 4) {
-          const f32x4 f = *reinterpret_cast<const f32x4*>(rt + KG * q + KV * gq + v);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) x[v + r] = f[r] * to_f(raw[v + r]);
-        }
+        for (int v = 0; v < KV; ++v) x[v] = f[v / 4][v % 4] * to_f(raw[c][v]);
         la_pieces(x, fc[c]);
       }
 #pragma unroll
       for (int i = 0; i < AT; ++i) {
-        const frag fb = M::trans(sb, LA, HALF ? KG * (i / UPG) : 16 * i, i % UPG, KG * q, lane, true);
+        if (!HALF) fb[0] = M::trans(sb, LA, 16 * i, 0, KG * q, lane, true);
 #pragma unroll
         for (int s = 0; s < NSU; ++s)
 #pragma unroll
-          for (int c = 0; c < NCT; ++c) X[i][c] = M::mma(fb, fc[c][s], X[i][c]);
+          for (int c = 0; c < NCT; ++c) X[i][c] = M::mma(fb[HALF ? i : 0], fc[c][s], X[i][c]);
       }
     }
 
     // out, and its dots with the rows of e
     if constexpr (OUT) {
-      auto out_each = [&](auto&& f) __attribute__((always_inline)) {
+      // (buffer stores, whose out-of-range lanes write nothing: a branch around
+      // a store hides their number from the wait for the next tiles' loads,
+      // which would then wait for the stores as well)
+      unsigned os[2][NCT];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int c = 0; c < NCT; ++c)
+          os[j][c] = (16 * j + l16 < nv && cw + 16 * c + 4 * gq < nc) ? ol[j] + 16 * c : LA_NOWHERE;
+      if (wide) {
+        const auto po = la_buffer(R.out32 + (o0 + t0 * ot));
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int c = 0; c < NCT; ++c) la_store4(po, os[j][c], acc[c][j], 0.f);
+      } else {
+        const auto po = la_buffer(R.out + (o0 + t0 * ot));
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int c = 0; c < NCT; ++c) la_store4(po, os[j][c], acc[c][j], E(0.f));
+      }
+      if (dots) {
+        const E* const pe = R.e + (e0 + t0 * et);
+        float dot[2] = {0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int c = 0; c < NCT; ++c)
-            if (16 * j + l16 < nv && cw + 16 * c + 4 * gq < nc) f(j, c, (long)(t0 + 16 * j + l16));
-      };
-      if (wide)
-        out_each([&](int j, int c, long t) { st_f4(po32 + t * ot + 16 * c, acc[c][j]); });
-      else
-        out_each([&](int j, int c, long t) { st_f4(po + t * ot + 16 * c, acc[c][j]); });
-      if (dots) {
-        float dot[2] = {0.f, 0.f};
-        out_each([&](int j, int c, long t) {
-          const f32x4 x = raw4_to_f(ld_raw4(pe + t * et + 16 * c));
-          dot[j] += (acc[c][j][0] * x[0] + acc[c][j][1] * x[1]) + (acc[c][j][2] * x[2] + acc[c][j][3] * x[3]);
-        });
+            if (16 * j + l16 < nv && cw + 16 * c + 4 * gq < nc) {
+              const f32x4 x = raw4_to_f(ld_raw4(pe + (el[j] + 16 * c)));
+              dot[j] += (acc[c][j][0] * x[0] + acc[c][j][1] * x[1]) + (acc[c][j][2] * x[2] + acc[c][j][3] * x[3]);
+            }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           dot[j] += __shfl_xor(dot[j], 16);
@@ -456,6 +625,7 @@ __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args)
     if (NBUF == 1) __syncthreads();
   }
 
+  state_scale(__builtin_amdgcn_exp2f((float)F));
   if (OUT) {
     if (last && R.fin) state_store(R.fin + (long)bh * args.DD);
   } else {
