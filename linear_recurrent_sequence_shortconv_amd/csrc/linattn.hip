@@ -12,30 +12,41 @@ namespace prism {
 namespace {
 
 // ------------------------------------------------------------ segment join
-// One thread carries one element of the state over the segments:
+// One thread carries four elements of the state over the segments:
 // forward X_{s+1} = decay_s X_s + own_s, reverse the other way round.  The
 // last segment of a pass has no own state (nothing enters after it).
 __global__ __launch_bounds__(256) void la_join_kernel(const LaJoin a) {
-  const int per = (a.DD + 255) / 256;
+  const int per = (a.DD + 1023) / 1024;
   int id = blockIdx.x;
   const int blk = id % per;
   id /= per;
-  const int dir = id % 2, bh = id / 2;
-  if (!a.seg[dir]) return;
-  const int e = blk * 256 + threadIdx.x;
-  if (e >= a.DD) return;
+  const int dir = a.seg[1] ? id % 2 : 0, bh = a.seg[1] ? id / 2 : id;
+  const int e = blk * 1024 + 4 * threadIdx.x;
+  if (e >= a.DD) return;   // (DD is a multiple of 256)
   const int n = seq_len(a.cu, bh / a.H, a.T);
   const int used = max(1, (n + a.seglen - 1) / a.seglen);
   float* seg = a.seg[dir] + (long)bh * a.nseg * a.DD + e;
   const float* dec = a.dec[dir] + (long)bh * a.nseg;
-  float x = a.X0[dir] ? a.X0[dir][(long)bh * a.DD + e] : 0.f;
-  for (int i = 0; i < used - 1; ++i) {
-    const int s = dir ? used - 1 - i : i;
-    const float own = seg[(long)s * a.DD];
-    seg[(long)s * a.DD] = x;
-    x = fmaf(dec[s], x, own);
+  auto at = [&](int x) { return reinterpret_cast<f32x4*>(seg + (long)x * a.DD); };
+  f32x4 x = a.X0[dir] ? *reinterpret_cast<const f32x4*>(a.X0[dir] + (long)bh * a.DD + e) : f32x4{0.f, 0.f, 0.f, 0.f};
+  constexpr int U = 8;   // own states requested together
+  for (int i0 = 0; i0 < used - 1; i0 += U) {
+    f32x4 own[U];
+    float d[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = min(i0 + u, used - 2), s = dir ? used - 1 - i : i;
+      own[u] = *at(s);
+      d[u] = dec[s];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + u < used - 1) {
+        *at(dir ? used - 1 - (i0 + u) : i0 + u) = x;
+        x = x * d[u] + own[u];
+      }
   }
-  seg[(long)(dir ? 0 : used - 1) * a.DD] = x;
+  *at(dir ? 0 : used - 1) = x;
 }
 
 // ---------------------------------------------------------- decay gradient
@@ -43,57 +54,97 @@ __global__ __launch_bounds__(256) void la_join_kernel(const LaJoin a) {
 // q.dq - k.dk (in fp64: differences of long sums), 256 tokens at a time from
 // the end.
 __global__ __launch_bounds__(256) void la_decay_kernel(const LaDecay a) {
-  __shared__ double sm[256];
+  __shared__ double sm[8];
   const int tid = threadIdx.x;
   const int seg = blockIdx.x % a.nseg, bh = blockIdx.x / a.nseg;
   const int b = bh / a.H, h = bh % a.H;
   const int n = seq_len(a.cu, b, a.T);
   const int s0 = seg * a.seglen, len = min(n - s0, a.seglen);
   if (len <= 0) return;
+  // S and dS at the segment's end: the caller's after the last token, else the
+  // states that enter the next segment and (in reverse) this one
   const bool last = s0 + len == n;
-  const float* R = last ? (a.dST ? a.dST + (long)bh * a.DD : nullptr)
-                        : a.segr + ((long)bh * a.nseg + seg) * a.DD;
-  const float* X = last ? (a.dST ? a.ST + (long)bh * a.DD : nullptr)
-                        : a.segf + ((long)bh * a.nseg + seg + 1) * a.DD;
+  const int used = (n + a.seglen - 1) / a.seglen;
+  const long o = (long)bh * a.DD;
+  auto entering = [&](const float* own, const float* dec, const float* X0, int from, int to, int step, int e) {
+    f32x4 x = X0 ? *reinterpret_cast<const f32x4*>(X0 + o + e) : f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = from; i != to; i += step)
+      x = x * dec[(long)bh * a.nseg + i] + *reinterpret_cast<const f32x4*>(own + ((long)bh * a.nseg + i) * a.DD + e);
+    return x;
+  };
+  auto joined = [&](const float* seg_, int i, int e) {
+    return *reinterpret_cast<const f32x4*>(seg_ + ((long)bh * a.nseg + i) * a.DD + e);
+  };
   double s = 0.0;
-  if (R)
-    for (int e = tid; e < a.DD; e += 256) s += (double)R[e] * (double)X[e];
-  sm[tid] = s;
+  if (!last || a.dST)
+    for (int e = 4 * tid; e < a.DD; e += 1024) {
+      f32x4 r, x;
+      if (last) {
+        r = *reinterpret_cast<const f32x4*>(a.dST + o + e);
+        x = *reinterpret_cast<const f32x4*>(a.ST + o + e);
+      } else if (a.joined) {
+        r = joined(a.segr, seg, e);
+        x = joined(a.segf, seg + 1, e);
+      } else {
+        r = entering(a.segr, a.decr, a.dST, used - 1, seg, -1, e);
+        x = entering(a.segf, a.decf, a.S0, 0, seg + 1, 1, e);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s += (double)r[k] * (double)x[k];
+    }
+  const int lane = tid & 63, wave = tid >> 6;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+  if (lane == 0) sm[wave] = s;
   __syncthreads();
-  for (int o = 128; o > 0; o >>= 1) {
-    if (tid < o) sm[tid] += sm[tid + o];
-    __syncthreads();
-  }
-  double carry = sm[0];
-  __syncthreads();
+  double carry = (sm[0] + sm[1]) + (sm[2] + sm[3]);
   const long row0 = a.cu ? (long)a.cu[b] + s0 : s0;
+  const float* eq = a.eq + (long)bh * LA_PARTS * a.T + s0;
+  const float* ek = a.ek + (long)bh * LA_PARTS * a.T + s0;
+  const float* pg = a.g + ((a.cu ? 0 : b * a.sg.b) + row0 * a.sg.t + h * a.sg.h);
+  // thread tid holds token hi - 1 - tid (a prefix sum over the threads); the
+  // next block's values are requested before this one's are summed
+  float q[LA_PARTS], k[LA_PARTS], gv = 0.f;
+  auto load = [&](int hi) __attribute__((always_inline)) {
+    const int t = max(hi - 1 - tid, 0);
+#pragma unroll
+    for (int p = 0; p < LA_PARTS; ++p) {
+      q[p] = eq[(long)p * a.T + t];
+      k[p] = ek[(long)p * a.T + t];
+    }
+    gv = pg[(long)t * a.sg.t];
+  };
+  load(len);
+  int buf = 4;
   for (int hi = len; hi > 0; hi -= 256) {
-    // thread tid holds token hi - 1 - tid; a prefix sum over the threads
     const int t = hi - 1 - tid;
     double x = 0.0;
-    if (t >= 0) {
-      for (int p = 0; p < LA_PARTS; ++p) x += (double)a.eq[((long)bh * LA_PARTS + p) * a.T + s0 + t];
-      for (int p = 0; p < LA_PARTS; ++p) x -= (double)a.ek[((long)bh * LA_PARTS + p) * a.T + s0 + t];
+#pragma unroll
+    for (int p = 0; p < LA_PARTS; ++p) x += (double)q[p] - (double)k[p];
+    if (t < 0) x = 0.0;
+    const float g = gv;
+    load(max(hi - 256, 1));
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const double y = __shfl_up(x, o);
+      if (lane >= o) x += y;
     }
-    sm[tid] = x;
+    if (lane == 63) sm[buf + wave] = x;
     __syncthreads();
-    for (int o = 1; o < 256; o <<= 1) {
-      const double y = tid >= o ? sm[tid - o] : 0.0;
-      __syncthreads();
-      x += y;
-      sm[tid] = x;
-      __syncthreads();
+    double before = carry;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      if (w < wave) before += sm[buf + w];
+      carry += sm[buf + w];
     }
+    buf ^= 4;   // (the other four sums: one barrier a block)
     if (t >= 0) {
-      const long at = (a.cu ? 0 : b * a.sg.b) + (row0 + t) * a.sg.t + h * a.sg.h;
-      const float d = a.g[at] < -104.f ? 0.f : (float)(carry + x);
+      const float d = g < -104.f ? 0.f : (float)(before + x);
       if (a.tmp)
         a.tmp[(long)bh * a.T + s0 + t] = d;
       else
-        a.dg[at] = d;
+        a.dg[(a.cu ? 0 : b * a.sg.b) + (row0 + t) * a.sg.t + h * a.sg.h] = d;
     }
-    carry += sm[255];
-    __syncthreads();
   }
 }
 
@@ -118,15 +169,19 @@ __global__ __launch_bounds__(256) void la_decay_head_kernel(const LaDecay a) {
 
 // ---------------------------------------------------------------- group sum
 template <typename E>
-__global__ __launch_bounds__(256) void la_group_kernel(const float* __restrict__ part, E* __restrict__ out,
-                                                       long n4, int grp, int d4) {
-  for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < n4; i += (long)gridDim.x * 256) {
+__global__ __launch_bounds__(256) void la_group_kernel(const float* __restrict__ dkp, const float* __restrict__ dvp,
+                                                       E* __restrict__ dk, E* __restrict__ dv, long nk4, long n4,
+                                                       int grp, int dk4, int dv4) {
+  for (long j = (long)blockIdx.x * 256 + threadIdx.x; j < n4; j += (long)gridDim.x * 256) {
+    const bool keys = j < nk4;
+    const long i = keys ? j : j - nk4;
+    const int d4 = keys ? dk4 : dv4;
     const long row = i / d4;
     const int c = (int)(i - row * d4);
-    const float* p = part + (row * grp * d4 + c) * 4;
+    const float* p = (keys ? dkp : dvp) + (row * grp * d4 + c) * 4;
     f32x4 s = *reinterpret_cast<const f32x4*>(p);
     for (int k = 1; k < grp; ++k) s += *reinterpret_cast<const f32x4*>(p + (long)k * d4 * 4);
-    st_f4(out + i * 4, s);
+    st_f4((keys ? dk : dv) + i * 4, s);
   }
 }
 
@@ -199,7 +254,7 @@ hipError_t step_lk(const LaStepArgs<E>& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_la_join(const LaJoin& a, hipStream_t s) {
-  const unsigned grid = (unsigned)((long)a.B * a.H * 2 * ((a.DD + 255) / 256));
+  const unsigned grid = (unsigned)((long)a.B * a.H * (a.seg[1] ? 2 : 1) * ((a.DD + 1023) / 1024));
   hipLaunchKernelGGL(la_join_kernel, dim3(grid), dim3(256), 0, s, a);
   return hipGetLastError();
 }
@@ -216,12 +271,13 @@ hipError_t launch_la_decay(const LaDecay& a, hipStream_t s) {
 }
 
 template <typename E>
-hipError_t launch_la_group_sum(const float* part, E* out, long rows, int Hk, int grp, int d, hipStream_t s) {
-  const long n4 = rows * Hk * (d / 4);
+hipError_t launch_la_group_sum(const float* dkp, const float* dvp, E* dk, E* dv, long rows, int Hk, int grp, int dimk,
+                               int dimv, hipStream_t s) {
+  const long nk4 = rows * Hk * (dimk / 4), n4 = nk4 + rows * Hk * (dimv / 4);
   if (n4 == 0) return hipSuccess;
   const long want = (n4 + 255) / 256;
-  hipLaunchKernelGGL((la_group_kernel<E>), dim3((unsigned)(want < 8192 ? want : 8192)), dim3(256), 0, s, part, out,
-                     n4, grp, d / 4);
+  hipLaunchKernelGGL((la_group_kernel<E>), dim3((unsigned)(want < 8192 ? want : 8192)), dim3(256), 0, s, dkp, dvp, dk,
+                     dv, nk4, n4, grp, dimk / 4, dimv / 4);
   return hipGetLastError();
 }
 
@@ -233,8 +289,10 @@ hipError_t launch_la_step(const LaStepArgs<E>& a, hipStream_t s) {
   return step_lk<E, 32>(a, s);
 }
 
-template hipError_t launch_la_group_sum<bf16>(const float*, bf16*, long, int, int, int, hipStream_t);
-template hipError_t launch_la_group_sum<float>(const float*, float*, long, int, int, int, hipStream_t);
+template hipError_t launch_la_group_sum<bf16>(const float*, const float*, bf16*, bf16*, long, int, int, int, int,
+                                              hipStream_t);
+template hipError_t launch_la_group_sum<float>(const float*, const float*, float*, float*, long, int, int, int, int,
+                                               hipStream_t);
 template hipError_t launch_la_step<bf16>(const LaStepArgs<bf16>&, hipStream_t);
 template hipError_t launch_la_step<float>(const LaStepArgs<float>&, hipStream_t);
 

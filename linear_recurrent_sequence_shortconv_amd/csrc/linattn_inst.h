@@ -7,17 +7,21 @@
 namespace prism {
 
 template <typename E, int DA, int NCT>
-hipError_t la_pass_da(const LaArgs<E>& a, bool outputs, bool precise, hipStream_t s) {
-  if (!outputs) return la_launch<E, DA, NCT, false, false>(a, s);
+hipError_t la_pass_da(const LaArgs<E>& a, bool precise, hipStream_t s) {
   if (precise) return la_launch<E, DA, NCT, true, true>(a, s);
   return la_launch<E, DA, NCT, false, true>(a, s);
 }
 
 template <typename E>
 hipError_t launch_la_pass(const LaArgs<E>& a, int dim, bool outputs, bool precise, hipStream_t s) {
-  if (dim <= 32) return la_pass_da<E, 32, 1>(a, outputs, precise, s);
-  if (dim <= 64) return la_pass_da<E, 64, 1>(a, outputs, precise, s);
-  return la_pass_da<E, 128, 2>(a, outputs, precise, s);
+  if (!outputs) {
+    if (dim <= 32) return la_launch<E, 32, 1, false, false>(a, s);
+    if (dim <= 64) return la_launch<E, 64, 1, false, false>(a, s);
+    return la_launch<E, 128, 2, false, false>(a, s);
+  }
+  if (dim <= 32) return la_pass_da<E, 32, 1>(a, precise, s);
+  if (dim <= 64) return la_pass_da<E, 64, 1>(a, precise, s);
+  return la_pass_da<E, 128, 2>(a, precise, s);
 }
 
 }  // namespace prism

@@ -137,16 +137,24 @@ template <> struct La16<float> {
 // x[0 .. KV) as NS operands whose sum is x to NS times E's precision
 template <int NS>
 __device__ inline void la_pieces(const float (&x)[8], bf16x8 (&f)[NS]) {
-  float y[8];
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
 #pragma unroll
-  for (int j = 0; j < 8; ++j) y[j] = x[j];
+  for (int j = 0; j < 8; j += 2) {
+    float a = x[j], b = x[j + 1];
 #pragma unroll
-  for (int k = 0; k < NS; ++k)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      f[k][j] = (bf16)y[j];
-      if (k + 1 < NS) y[j] -= (float)f[k][j];
+    for (int k = 0; k < NS; ++k) {
+      // (a pair is rounded by one instruction and taken apart by two)
+      const bf16x2 w = __builtin_convertvector((f32x2{a, b}), bf16x2);
+      f[k][j] = w[0];
+      f[k][j + 1] = w[1];
+      if (k + 1 < NS) {
+        const unsigned u = __builtin_bit_cast(unsigned, w);
+        a -= __uint_as_float(u << 16);
+        b -= __uint_as_float(u & 0xffff0000u);
+      }
     }
+  }
 }
 template <int NS>
 __device__ inline void la_pieces(const float (&x)[4], f32x4 (&f)[NS]) {
@@ -297,10 +305,25 @@ __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args)
   };
   const long segoff = ((long)bh * args.nseg + seg) * args.DD;
   if (OUT) {
-    if (args.nseg > 1)
+    if (args.nseg > 1 && args.joined) {
       state_load(R.seg + segoff);
-    else if (R.X0)
-      state_load(R.X0 + (long)bh * args.DD);
+    } else {
+      if (R.X0) state_load(R.X0 + (long)bh * args.DD);
+      // the segments before this one (in the pass's direction), by their own states
+      for (int i = 0; i < (rev ? used - 1 - seg : seg); ++i) {
+        const long s = (long)bh * args.nseg + (rev ? used - 1 - i : i);
+        const float dec = R.segdec[s];
+        const float* src = R.seg + s * args.DD;
+        state_each([&](f32x4& x, long o) __attribute__((always_inline)) {
+          if (R.xa == 1) {
+            x = x * dec + *reinterpret_cast<const f32x4*>(src + o);
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] = fmaf(x[r], dec, src[o + (long)r * R.xa]);
+          }
+        });
+      }
+    }
   }
 
   // what the loop uses of the arguments, in registers

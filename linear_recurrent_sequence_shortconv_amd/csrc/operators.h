@@ -67,6 +67,7 @@ constexpr int LA_ROLES = 3;
 template <typename E>
 struct LaArgs {
   int B, T, H, nseg, seglen, nroles;
+  int joined;              // role.seg holds entering states, not the segments' own
   int DD;                  // dv * dk
   const int* cu;           // sanitised offsets of a packed batch, or nullptr
   const float* g;
@@ -99,17 +100,19 @@ struct LaDecay {
   const float* g;
   Strides sg;
   const float *eq, *ek;            // [B * H][LA_PARTS][T]
-  const float *segf, *segr;        // entering states, forward and reverse (nseg > 1)
-  const float *ST, *dST;           // final state and its gradient (nullptr: zero)
+  const float *segf, *segr;        // states of the segments, forward and reverse (nseg > 1):
+  const float *decf, *decr;        // entering (joined), or their own with their decays
+  int joined;
+  const float *S0, *ST, *dST;      // first, last state and the latter's gradient (nullptr: zero)
   float* dg;                       // strided like g, or, for one decay a head,
   float* tmp;                      // [B * H][T], then summed into dg [H]
 };
 hipError_t launch_la_decay(const LaDecay& a, hipStream_t s);
 
-// out[.., h', :] = sum over the grp query heads of h' of part [.., H, d] (fp32)
+// dk, dv [.., Hk, d] = sums over the grp query heads of each of the fp32 partials [.., H, d]
 template <typename E>
-hipError_t launch_la_group_sum(const float* part, E* out, long rows, int Hk, int grp, int d,
-                               hipStream_t s);
+hipError_t launch_la_group_sum(const float* dkp, const float* dvp, E* dk, E* dv, long rows, int Hk, int grp, int dimk,
+                               int dimv, hipStream_t s);
 
 template <typename E>
 struct LaStepArgs {

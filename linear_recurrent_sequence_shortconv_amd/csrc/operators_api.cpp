@@ -213,23 +213,52 @@ prism_status check_la(const prism_linear_attention_desc* desc, bool packed, LaPl
   return PRISM_OK;
 }
 
-// Segments a sequence is cut into: enough that the passes fill the chip
-// (`wide` workgroups of the pass for each (b, h)), none under 256 tokens.
-void plan_segments(const prism_linear_attention_desc& d, int wide, LaPlan* p) {
-  const int ch = prism::LA_CHUNK;
-  const long have = (long)p->bh * wide, want = 512;
-  long nseg = have > 0 ? (want + have - 1) / have : 1;
-  const long most = (d.T + 255) / 256;
-  if (nseg > most) nseg = most;
-  if (nseg < 1) nseg = 1;
-  const long chunks = ((long)d.T + ch - 1) / ch;
-  const long per = chunks > 0 ? (chunks + nseg - 1) / nseg : 1;
-  p->seglen = (int)(per * ch);
+// Up to this many segments a workgroup forms its entering state from the own
+// states of the segments before it; more are joined by a kernel of its own.
+constexpr int LA_SELF_JOIN = 4;
+
+// Segments a sequence is cut into.  A launch runs B H workgroups for each of
+// its passes and each segment, 512 of them at once (two a CU); more than one
+// segment also needs the states at their starts, from `sources` further passes
+// of half the work over all but one segment.  Taken is the count with the
+// least cost in the time of one chunk on a full chip (4 us in bf16 at d = 128),
+// as measured there: a workgroup costs 2.5 chunks beside its own (2 where it
+// forms states alone), a round of at most one workgroup a CU goes by 0.6 of
+// the time for each chunk, fp32 takes twice and the decays' gradient 1.6 times
+// as long.  8 x 2048 tokens, 16 heads, forward: 4 segments 123 us, 3 138, 2 146.
+enum LaWork { LA_FORWARD, LA_BACKWARD, LA_BACKWARD_DG };
+void plan_segments(const prism_linear_attention_desc& d, LaWork work, LaPlan* p) {
+  const long chunks = ((long)d.T + prism::LA_CHUNK - 1) / prism::LA_CHUNK;
+  const long most = chunks / 4 < 64 ? chunks / 4 : 64;
+  const double bh = (double)p->bh, unit = p->f32 ? 2.0 : 1.0;
+  auto rounds = [&](double groups, double each, double fixed) {
+    const double full = std::floor(groups / 512), rest = groups - 512 * full;
+    each *= unit;
+    return full * (each + fixed) + (rest == 0 ? 0.0 : rest <= 256 ? 0.6 * each + fixed : each + fixed);
+  };
+  long best = 1;
+  double least = 0.0;
+  for (long n = 1; n <= (most > 1 ? most : 1); ++n) {
+    const double per = chunks > 0 ? (double)((chunks + n - 1) / n) : 1.0;
+    double cost = work == LA_FORWARD    ? rounds(bh * n, per, 2.5)
+                  : work == LA_BACKWARD ? rounds(bh * 3 * n, per, 2.5)
+                                        : rounds(bh * 2 * n, 1.6 * per, 2.5) + rounds(bh * n, per, 2.5);
+    if (n > 1) cost += rounds(bh * (work == LA_FORWARD ? 1 : 2) * (n - 1), 0.5 * per, 2.0);
+    if (n > LA_SELF_JOIN) cost += 2.0;
+    if (n == 1 || cost < least) {
+      best = n;
+      least = cost;
+    }
+  }
+  const long per = chunks > 0 ? (chunks + best - 1) / best : 1;
+  p->seglen = (int)(per * prism::LA_CHUNK);
   p->nseg = (int)(chunks > 0 ? (chunks + per - 1) / per : 1);
 }
 
-void plan_forward(const prism_linear_attention_desc& d, LaPlan* p) { plan_segments(d, 1, p); }
-void plan_backward(const prism_linear_attention_desc& d, LaPlan* p) { plan_segments(d, 3, p); }
+void plan_forward(const prism_linear_attention_desc& d, LaPlan* p) { plan_segments(d, LA_FORWARD, p); }
+void plan_backward(const prism_linear_attention_desc& d, bool dg, LaPlan* p) {
+  plan_segments(d, dg ? LA_BACKWARD_DG : LA_BACKWARD, p);
+}
 
 struct LaFwdWs {
   int* cu;
@@ -349,8 +378,8 @@ prism_status la_forward(const prism_linear_attention_desc& d, const LaPlan& p, c
   r.segdec = w.dec;
   a.r[0] = r;
   a.nroles = 1;
-  if (p.nseg > 1) {
-    HIP_TRY("la_states", s, prism::launch_la_pass<E>(a, p.dim, false, false, s));
+  if (p.nseg > 1) HIP_TRY("la_states", s, prism::launch_la_pass<E>(a, p.dim, false, false, s));
+  if (p.nseg > LA_SELF_JOIN) {
     prism::LaJoin j = {};
     j.B = d.B;
     j.T = d.T;
@@ -363,6 +392,7 @@ prism_status la_forward(const prism_linear_attention_desc& d, const LaPlan& p, c
     j.dec[0] = w.dec;
     j.X0[0] = S0;
     HIP_TRY("la_join", s, prism::launch_la_join(j, s));
+    a.joined = 1;
   }
   HIP_TRY("la_fwd", s, prism::launch_la_pass<E>(a, p.dim, true, false, s));
   return PRISM_OK;
@@ -411,6 +441,7 @@ prism_status la_backward(const prism_linear_attention_desc& d, const LaPlan& p, 
   rv.so = flat(d.H, d.dv);
   rv.X0 = dST;
   rv.seg = w.segr;
+  rv.segdec = w.decr;
   prism::LaArgs<E> a = la_args<E>(d, p, cu, g);
   if (p.nseg > 1 && d.B > 0) {
     prism::LaArgs<E> b = a;
@@ -418,6 +449,8 @@ prism_status la_backward(const prism_linear_attention_desc& d, const LaPlan& p, 
     b.r[1] = rk;
     b.nroles = 2;
     HIP_TRY("la_states", s, prism::launch_la_pass<E>(b, p.dim, false, false, s));
+  }
+  if (p.nseg > LA_SELF_JOIN && d.B > 0) {
     prism::LaJoin j = {};
     j.B = d.B;
     j.T = d.T;
@@ -433,6 +466,7 @@ prism_status la_backward(const prism_linear_attention_desc& d, const LaPlan& p, 
     j.X0[0] = S0;
     j.X0[1] = dST;
     HIP_TRY("la_join", s, prism::launch_la_join(j, s));
+    a.joined = 1;
   }
   if (d.B > 0 && dg) {
     rq.e = q;
@@ -473,16 +507,19 @@ prism_status la_backward(const prism_linear_attention_desc& d, const LaPlan& p, 
     x.ek = w.ek;
     x.segf = w.segf;
     x.segr = w.segr;
+    x.decf = w.decf;
+    x.decr = w.decr;
+    x.joined = a.joined;
+    x.S0 = S0;
     x.ST = w.ST;
     x.dST = dST;
     x.dg = dg;
     x.tmp = d.g.batch == 0 && d.g.token == 0 ? w.tmp : nullptr;
     HIP_TRY("la_decay", s, prism::launch_la_decay(x, s));
   }
-  if (p.grp > 1) {
-    HIP_TRY("la_group", s, prism::launch_la_group_sum<E>(w.dkp, dk, p.rows, d.Hk, p.grp, d.dk, s));
-    HIP_TRY("la_group", s, prism::launch_la_group_sum<E>(w.dvp, dv, p.rows, d.Hk, p.grp, d.dv, s));
-  }
+  if (p.grp > 1)
+    HIP_TRY("la_group", s,
+            prism::launch_la_group_sum<E>(w.dkp, w.dvp, dk, dv, p.rows, d.Hk, p.grp, d.dk, d.dv, s));
   return PRISM_OK;
 }
 
@@ -530,7 +567,7 @@ prism_status prism_linear_attention_workspace(const prism_linear_attention_desc*
     if (desc->packed_tokens > p.rows) p.rows = desc->packed_tokens;
     Carve cv;
     if (backward) {
-      plan_backward(*desc, &p);
+      plan_backward(*desc, dg != 0, &p);
       carve_la_bwd(*desc, p, dg != 0, cv);
     } else {
       plan_forward(*desc, &p);
@@ -597,7 +634,7 @@ prism_status prism_linear_attention_backward(const prism_linear_attention_desc* 
     if (reinterpret_cast<uintptr_t>(dg) & 3u) return fail(PRISM_ERR_ALIGN, "dg is not 4-byte aligned");
     CHECK_PTR(dS0, false);
     if (desc->B == 0 && !dg) return PRISM_OK;
-    plan_backward(*desc, &p);
+    plan_backward(*desc, dg != 0, &p);
     Carve cv;
     carve_la_bwd(*desc, p, dg != nullptr, cv);
     st = check_buffer(workspace, workspace_bytes, cv.off, "workspace");
