@@ -356,7 +356,8 @@ typedef struct {
 } prism_linear_attention_desc;
 
 /* Workspace of the forward (backward = 0) or backward (1) pass, packed or
- * dense batch; with dg: of the backward pass that also gives dg. */
+ * dense batch; with dg: of the backward pass that also gives dg.  The
+ * workspace is 256-byte aligned, and may be NULL where 0 bytes are needed. */
 prism_status prism_linear_attention_workspace(const prism_linear_attention_desc* desc,
                                               int backward, int dg, size_t* bytes);
 

@@ -21,9 +21,12 @@ __global__ __launch_bounds__(256) void la_join_kernel(const LaJoin a) {
   const int blk = id % per;
   id /= per;
   const int dir = a.seg[1] ? id % 2 : 0, bh = a.seg[1] ? id / 2 : id;
+  __shared__ int sm[4];
+  long first = 0;
+  int n = a.T;
+  if (a.cu) la_sequence(a.cu, a.N, a.T, bh / a.H, threadIdx.x, sm, first, n);
   const int e = blk * 1024 + 4 * threadIdx.x;
   if (e >= a.DD) return;   // (DD is a multiple of 256)
-  const int n = seq_len(a.cu, bh / a.H, a.T);
   const int used = max(1, (n + a.seglen - 1) / a.seglen);
   float* seg = a.seg[dir] + (long)bh * a.nseg * a.DD + e;
   const float* dec = a.dec[dir] + (long)bh * a.nseg;
@@ -58,7 +61,10 @@ __global__ __launch_bounds__(256) void la_decay_kernel(const LaDecay a) {
   const int tid = threadIdx.x;
   const int seg = blockIdx.x % a.nseg, bh = blockIdx.x / a.nseg;
   const int b = bh / a.H, h = bh % a.H;
-  const int n = seq_len(a.cu, b, a.T);
+  __shared__ int sq[4];
+  long first = 0;
+  int n = a.T;
+  if (a.cu) la_sequence(a.cu, a.N, a.T, b, tid, sq, first, n);
   const int s0 = seg * a.seglen, len = min(n - s0, a.seglen);
   if (len <= 0) return;
   // S and dS at the segment's end: the caller's after the last token, else the
@@ -98,7 +104,7 @@ __global__ __launch_bounds__(256) void la_decay_kernel(const LaDecay a) {
   if (lane == 0) sm[wave] = s;
   __syncthreads();
   double carry = (sm[0] + sm[1]) + (sm[2] + sm[3]);
-  const long row0 = a.cu ? (long)a.cu[b] + s0 : s0;
+  const long row0 = first + s0;
   const float* eq = a.eq + (long)bh * LA_PARTS * a.T + s0;
   const float* ek = a.ek + (long)bh * LA_PARTS * a.T + s0;
   const float* pg = a.g + ((a.cu ? 0 : b * a.sg.b) + row0 * a.sg.t + h * a.sg.h);
@@ -153,8 +159,14 @@ __global__ __launch_bounds__(256) void la_decay_head_kernel(const LaDecay a) {
   __shared__ double sm[256];
   const int tid = threadIdx.x, h = blockIdx.x;
   double s = 0.0;
+  int m = a.cu ? min(max(a.cu[0], 0), a.N) : 0;   // (the clamped offsets, as la_sequence has them)
   for (int b = 0; b < a.B; ++b) {
-    const int n = seq_len(a.cu, b, a.T);
+    int n = a.T;
+    if (a.cu) {
+      const int end = max(m, min(a.cu[b + 1], a.N));
+      n = min(end - m, a.T);
+      m = end;
+    }
     const float* x = a.tmp + ((long)b * a.H + h) * a.T;
     for (int t = tid; t < n; t += 256) s += (double)x[t];
   }

@@ -252,13 +252,16 @@ __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args)
   const bool rev = R.rev != 0;
 
   // the segment's tokens
-  const int n = seq_len(args.cu, b, args.T);
+  __shared__ int sseq[LA_NW];
+  long first = 0;
+  int n = args.T;
+  if (args.cu) la_sequence(args.cu, args.N, args.T, b, tid, sseq, first, n);
   const int used = max(1, (n + args.seglen - 1) / args.seglen);   // segments with tokens (or one)
   if (seg >= used) return;
   const int s0 = seg * args.seglen, len = min(n - s0, args.seglen);
   const bool last = rev ? seg == 0 : seg == used - 1;   // of the pass: its state leaves
   if (!OUT && last) return;                             // nothing enters after it
-  const long row0 = args.cu ? (long)args.cu[b] + s0 : s0;
+  const long row0 = first + s0;
   auto at = [&](const E* p, const Strides& s, int grp) {
     return p + ((args.cu ? 0 : b * s.b) + row0 * s.t + (long)(h / grp) * s.h);
   };

@@ -41,6 +41,24 @@ size_t qk_norm_part_bytes(int d);   // room for the weight-gradient partials
 // and the state after the pass is e^{G_T} X0 + s_upd sum_i e^{G_T-G_i} B_i C_i^T
 // (reverse: e^{G_i}).  (q, k, v) forward gives o; (dO, v, k) forward dq;
 // (v, dO, q) reverse dk; (k, q, dO) reverse dv.
+// Rows of sequence b of a packed batch, from the caller's offsets: c'_i = max_{j <= i} clamp(cu[j], 0, N)
+// in place of cu[i], and at most T rows, so that every sequence lies inside the N rows and no two overlap
+// whatever the offsets are.  Called by all 256 threads of a workgroup; sm: four ints of LDS.
+#ifdef __HIPCC__
+__device__ inline void la_sequence(const int* cu, int N, int T, int b, int tid, int* sm, long& first, int& n) {
+  int m = 0;
+  for (int j = tid; j <= b; j += 256) m = max(m, min(cu[j], N));
+  const int end = min(cu[b + 1], N);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = max(m, __shfl_xor(m, o));
+  if ((tid & 63) == 0) sm[tid >> 6] = m;
+  __syncthreads();
+  m = __builtin_amdgcn_readfirstlane(max(max(sm[0], sm[1]), max(sm[2], sm[3])));
+  first = m;
+  n = __builtin_amdgcn_readfirstlane(min(max(end - m, 0), T));
+}
+#endif
+
 template <typename E>
 struct LaRole {
   const E *a, *b, *c;
@@ -69,7 +87,8 @@ struct LaArgs {
   int B, T, H, nseg, seglen, nroles;
   int joined;              // role.seg holds entering states, not the segments' own
   int DD;                  // dv * dk
-  const int* cu;           // sanitised offsets of a packed batch, or nullptr
+  const int* cu;           // offsets of a packed batch of N rows, or nullptr
+  int N;
   const float* g;
   Strides sg;
   LaRole<E> r[LA_ROLES];
@@ -86,6 +105,7 @@ hipError_t launch_la_pass(const LaArgs<E>& a, int dim, bool outputs, bool precis
 struct LaJoin {
   int B, T, H, nseg, seglen, DD;
   const int* cu;
+  int N;
   float* seg[2];           // forward, reverse (nullptr: absent)
   const float* dec[2];
   const float* X0[2];
@@ -97,6 +117,7 @@ hipError_t launch_la_join(const LaJoin& a, hipStream_t s);
 struct LaDecay {
   int B, T, H, nseg, seglen, DD;
   const int* cu;
+  int N;
   const float* g;
   Strides sg;
   const float *eq, *ek;            // [B * H][LA_PARTS][T]

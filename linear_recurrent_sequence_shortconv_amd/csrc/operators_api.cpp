@@ -8,7 +8,6 @@
 
 #include "api_common.h"
 #include "operators.h"
-#include "prism_internal.h"
 
 namespace {
 
@@ -261,12 +260,10 @@ void plan_backward(const prism_linear_attention_desc& d, bool dg, LaPlan* p) {
 }
 
 struct LaFwdWs {
-  int* cu;
   float *seg, *dec;
 };
 LaFwdWs carve_la_fwd(const prism_linear_attention_desc& d, const LaPlan& p, Carve& cv) {
   LaFwdWs w = {};
-  w.cu = cv.take<int>(((size_t)d.B + 1) * 4);
   if (p.nseg > 1) {
     w.seg = cv.take<float>(p.bh * p.nseg * p.DD * 4);
     w.dec = cv.take<float>(p.bh * p.nseg * 4);
@@ -275,14 +272,12 @@ LaFwdWs carve_la_fwd(const prism_linear_attention_desc& d, const LaPlan& p, Carv
 }
 
 struct LaBwdWs {
-  int* cu;
   float *segf, *segr, *decf, *decr;
   float *dkp, *dvp;              // per query head (shared keys and values)
   float *eq, *ek, *ST, *tmp;     // decay gradient
 };
 LaBwdWs carve_la_bwd(const prism_linear_attention_desc& d, const LaPlan& p, bool dg, Carve& cv) {
   LaBwdWs w = {};
-  w.cu = cv.take<int>(((size_t)d.B + 1) * 4);
   if (p.nseg > 1) {
     w.segf = cv.take<float>(p.bh * p.nseg * p.DD * 4);
     w.segr = cv.take<float>(p.bh * p.nseg * p.DD * 4);
@@ -307,16 +302,6 @@ prism_status check_offsets(const int* cu) {
   return PRISM_OK;
 }
 
-prism_status sanitize(const prism_linear_attention_desc& d, const int* cu, int* out, hipStream_t s) {
-  prism::Dims x = {};
-  x.B = d.B;
-  x.T = d.T;
-  x.cu = cu;
-  x.N = d.packed_tokens;
-  HIP_TRY("cu_sanitize", s, prism::launch_cu_sanitize(x, out, s));
-  return PRISM_OK;
-}
-
 template <typename E>
 prism::LaArgs<E> la_args(const prism_linear_attention_desc& d, const LaPlan& p, const int* cu, const float* g) {
   prism::LaArgs<E> a = {};
@@ -327,6 +312,7 @@ prism::LaArgs<E> la_args(const prism_linear_attention_desc& d, const LaPlan& p, 
   a.seglen = p.seglen;
   a.DD = (int)p.DD;
   a.cu = cu;
+  a.N = d.packed_tokens;
   a.g = g;
   a.sg = strides(d.g);
   return a;
@@ -361,11 +347,6 @@ prism_status la_forward(const prism_linear_attention_desc& d, const LaPlan& p, c
   Carve cv;
   cv.base = static_cast<char*>(ws);
   const LaFwdWs w = carve_la_fwd(d, p, cv);
-  if (cu) {
-    const prism_status st = sanitize(d, cu, w.cu, s);
-    if (st != PRISM_OK) return st;
-    cu = w.cu;
-  }
   prism::LaArgs<E> a = la_args<E>(d, p, cu, g);
   prism::LaRole<E> r =
       la_role<E>(q, strides(d.q), 1, k, strides(d.k), p.grp, v, strides(d.v), p.grp, d.dk, d.dv, true, d);
@@ -388,6 +369,7 @@ prism_status la_forward(const prism_linear_attention_desc& d, const LaPlan& p, c
     j.seglen = p.seglen;
     j.DD = (int)p.DD;
     j.cu = cu;
+    j.N = d.packed_tokens;
     j.seg[0] = w.seg;
     j.dec[0] = w.dec;
     j.X0[0] = S0;
@@ -405,12 +387,6 @@ prism_status la_backward(const prism_linear_attention_desc& d, const LaPlan& p, 
   Carve cv;
   cv.base = static_cast<char*>(ws);
   const LaBwdWs w = carve_la_bwd(d, p, dg != nullptr, cv);
-  const int* cu_in = cu;
-  if (cu_in) {
-    const prism_status st = sanitize(d, cu_in, w.cu, s);
-    if (st != PRISM_OK) return st;
-    cu = w.cu;
-  }
   const Strides sq = strides(d.q), sk = strides(d.k), sv = strides(d.v), so = strides(d.o);
   auto flat = [&](int H, int dim) { return Strides{(long)d.T * H * dim, (long)H * dim, (long)dim}; };
   // dq_t = scale sum_{i<=t} (dO_t . v_i) k_i: forward in time, through S
@@ -459,6 +435,7 @@ prism_status la_backward(const prism_linear_attention_desc& d, const LaPlan& p, 
     j.seglen = p.seglen;
     j.DD = (int)p.DD;
     j.cu = cu;
+    j.N = d.packed_tokens;
     j.seg[0] = w.segf;
     j.seg[1] = w.segr;
     j.dec[0] = w.decf;
@@ -501,6 +478,7 @@ prism_status la_backward(const prism_linear_attention_desc& d, const LaPlan& p, 
     x.seglen = p.seglen;
     x.DD = (int)p.DD;
     x.cu = cu;
+    x.N = d.packed_tokens;
     x.g = g;
     x.sg = strides(d.g);
     x.eq = w.eq;
@@ -599,8 +577,7 @@ prism_status prism_linear_attention(const prism_linear_attention_desc* desc, con
     plan_forward(*desc, &p);
     Carve cv;
     carve_la_fwd(*desc, p, cv);
-    st = check_buffer(workspace, workspace_bytes, cv.off, "workspace");
-    if (st != PRISM_OK) return st;
+    if (cv.off > 0 && (st = check_buffer(workspace, workspace_bytes, cv.off, "workspace")) != PRISM_OK) return st;
     if (desc->dtype == PRISM_BF16)
       return la_forward<prism::bf16>(*desc, p, (const prism::bf16*)q, (const prism::bf16*)k, (const prism::bf16*)v, g,
                                      S0, cu_seqlens, (prism::bf16*)o, ST, workspace, stream);
@@ -637,8 +614,7 @@ prism_status prism_linear_attention_backward(const prism_linear_attention_desc* 
     plan_backward(*desc, dg != 0, &p);
     Carve cv;
     carve_la_bwd(*desc, p, dg != nullptr, cv);
-    st = check_buffer(workspace, workspace_bytes, cv.off, "workspace");
-    if (st != PRISM_OK) return st;
+    if (cv.off > 0 && (st = check_buffer(workspace, workspace_bytes, cv.off, "workspace")) != PRISM_OK) return st;
     if (desc->dtype == PRISM_BF16)
       return la_backward<prism::bf16>(*desc, p, (const prism::bf16*)q, (const prism::bf16*)k, (const prism::bf16*)v, g,
                                       S0, cu_seqlens, (const prism::bf16*)dO, dST, (prism::bf16*)dq, (prism::bf16*)dk,

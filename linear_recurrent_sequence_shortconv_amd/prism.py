@@ -8,6 +8,7 @@ call fails, a RuntimeError is raised.
 import ctypes
 import math
 import os
+import struct
 
 import torch
 
@@ -95,8 +96,9 @@ def lib():
                   "prism_backward_train", "prism_step_workspace", "prism_step",
                   "prism_step_noalloc"):
             getattr(L, f).restype = ctypes.c_int
-        qd, ld, size = (ctypes.POINTER(QkNormDesc), ctypes.POINTER(LinearAttentionDesc),
-                        ctypes.c_size_t)
+        # (descriptors as bytes or structures)
+        qd = ld = _P
+        size = ctypes.c_size_t
         L.prism_qk_norm.argtypes = [qd] + [_P] * 9
         L.prism_qk_norm_backward_workspace.argtypes = [qd, ctypes.c_int, ctypes.POINTER(size)]
         L.prism_qk_norm_backward.argtypes = [qd] + [_P] * 13 + [size, _P]
@@ -462,17 +464,32 @@ def _steps(t, name):
     if s[-1] != 1 and n[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
     if len(n) == 4:
-        return Strides(s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0, s[2] if n[2] > 1 else 0)
-    return Strides(0, s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0)
+        return (s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0, s[2] if n[2] > 1 else 0)
+    return (0, s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0)
 
 
 def _like(t, name, dtype, device, shape):
-    if t.dtype != dtype:
+    """Type, device (a number, -1: host) and shape of a tensor."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: expected device {device}, got {t.device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: expected device {device}, got {t.get_device()}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+# the descriptors' bytes (QkNormDesc, LinearAttentionDesc): one pack costs a
+# fraction of filling the structures field by field, which shows in the calls
+# for single tokens
+_QK_DESC = struct.Struct("=9if18q")
+_LA_DESC = struct.Struct("=7ifi4x15q")
+assert _QK_DESC.size == ctypes.sizeof(QkNormDesc)
+assert _LA_DESC.size == ctypes.sizeof(LinearAttentionDesc)
+_NO_STEPS = (0, 0, 0)
 
 
 def _qk_desc(q, k, wq, wk, positions, turns, norm, eps, interleaved):
@@ -480,7 +497,7 @@ def _qk_desc(q, k, wq, wk, positions, turns, norm, eps, interleaved):
         raise ValueError(f"norm must be one of {sorted(NORMS)}, got {norm!r}")
     if q.dim() not in (3, 4):
         raise ValueError(f"q: expected [B, T, H, d] or [N, H, d], got shape {tuple(q.shape)}")
-    code, dev, lead, d = _dtype_code(q), q.device, q.shape[:-2], q.shape[-1]
+    code, dev, lead, d = _dtype_code(q), q.get_device(), q.shape[:-2], q.shape[-1]
     B, T = lead if len(lead) == 2 else (1, lead[0])
     Hk = 0
     if k is not None:
@@ -500,23 +517,30 @@ def _qk_desc(q, k, wq, wk, positions, turns, norm, eps, interleaved):
         raise ValueError("positions and turns go together")
     if positions is not None:
         _like(positions, "positions", torch.int32, dev, lead)
-        if turns.dtype != torch.int64 or turns.device != dev or turns.dim() != 1:
+        if turns.dtype != torch.int64 or turns.get_device() != dev or turns.dim() != 1:
             raise ValueError("turns must be a 1-D int64 tensor on q's device")
         if not (positions.is_contiguous() and turns.is_contiguous()):
             raise ValueError("positions and turns must be contiguous")
         rot = 2 * turns.shape[0]
-    desc = QkNormDesc(B, T, q.shape[-2], Hk, d, rot, code, NORMS[norm], int(interleaved), eps)
-    desc.q = _steps(q, "q")
-    if k is not None:
-        desc.k = _steps(k, "k")
-    return desc
+    return (B, T, q.shape[-2], Hk, d, rot, code, NORMS[norm], int(interleaved), eps,
+            *_steps(q, "q"), *(_NO_STEPS if k is None else _steps(k, "k")))
 
 
 def _out(t, out, name):
     if out is None:
-        return torch.empty(t.shape, dtype=t.dtype, device=t.device)
-    _like(out, name, t.dtype, t.device, t.shape)
+        return t.new_empty(t.shape)
+    _like(out, name, t.dtype, t.get_device(), t.shape)
     return out
+
+
+# the current stream's handle without the Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(device):
+    if _raw_stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream(device.index)
 
 
 def qk_norm(q, k=None, wq=None, wk=None, positions=None, turns=None, norm="l2", eps=1e-6,
@@ -534,15 +558,16 @@ def qk_norm(q, k=None, wq=None, wk=None, positions=None, turns=None, norm="l2", 
     desc = _qk_desc(q, k, wq, wk, positions, turns, norm, eps, interleaved)
     _on_gpu(q)
     q_out = _out(q, q_out, "q_out")
-    desc.qo = _steps(q_out, "q_out")
+    ko = _NO_STEPS
     if k is not None:
         k_out = _out(k, k_out, "k_out")
-        desc.ko = _steps(k_out, "k_out")
+        ko = _steps(k_out, "k_out")
     elif k_out is not None:
         raise ValueError("k_out without k")
-    stream = torch.cuda.current_stream(q.device).cuda_stream
-    _check(lib().prism_qk_norm(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk),
-                               _ptr(positions), _ptr(turns), _ptr(q_out), _ptr(k_out), stream))
+    _check(lib().prism_qk_norm(
+        _QK_DESC.pack(*desc, *_steps(q_out, "q_out"), *ko, 0, 0, 0, 0, 0, 0), _addr(q), _addr(k),
+        _addr(wq), _addr(wk), _addr(positions), _addr(turns), _addr(q_out), _addr(k_out),
+        _stream(q.device)))
     return q_out, k_out
 
 
@@ -552,30 +577,31 @@ def qk_norm_backward(q, k, dq_out, dk_out, wq=None, wk=None, positions=None, tur
     inputs.  Returns a dict: dq, dk (input type; into dq, dk when given), and
     dwq, dwk (fp32 [d]) for the weights given."""
     desc = _qk_desc(q, k, wq, wk, positions, turns, norm, eps, interleaved)
-    _like(dq_out, "dq_out", q.dtype, q.device, q.shape)
-    desc.qo = _steps(dq_out, "dq_out")
+    _like(dq_out, "dq_out", q.dtype, q.get_device(), q.shape)
     if k is not None:
-        _like(dk_out, "dk_out", k.dtype, k.device, k.shape)
-        desc.ko = _steps(dk_out, "dk_out")
+        _like(dk_out, "dk_out", k.dtype, k.get_device(), k.shape)
+    steps = (*_steps(dq_out, "dq_out"), *(_NO_STEPS if k is None else _steps(dk_out, "dk_out")))
     _on_gpu(q)
     out = {"dq": _out(q, dq, "dq")}
-    desc.dq = _steps(out["dq"], "dq")
+    steps += _steps(out["dq"], "dq")
     if k is not None:
         out["dk"] = _out(k, dk, "dk")
-        desc.dk = _steps(out["dk"], "dk")
+        steps += _steps(out["dk"], "dk")
+    else:
+        steps += _NO_STEPS
     for name, w in (("dwq", wq), ("dwk", wk)):
         if w is not None:
-            out[name] = torch.empty(w.shape, dtype=torch.float32, device=q.device)
+            out[name] = w.new_empty(w.shape, dtype=torch.float32)
+    packed = _QK_DESC.pack(*desc, *steps)
     if workspace is None and (wq is not None or wk is not None):
         n = ctypes.c_size_t(0)
-        _check(lib().prism_qk_norm_backward_workspace(ctypes.byref(desc), 1, ctypes.byref(n)))
+        _check(lib().prism_qk_norm_backward_workspace(packed, 1, ctypes.byref(n)))
         workspace = _workspace(n.value, q.device)[1]
-    stream = torch.cuda.current_stream(q.device).cuda_stream
     _check(lib().prism_qk_norm_backward(
-        ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(positions), _ptr(turns),
-        _ptr(dq_out), _ptr(dk_out), _ptr(out["dq"]), _ptr(out.get("dk")), _ptr(out.get("dwq")),
-        _ptr(out.get("dwk")), _ptr(workspace), 0 if workspace is None else workspace.numel(),
-        stream))
+        packed, _addr(q), _addr(k), _addr(wq), _addr(wk), _addr(positions), _addr(turns),
+        _addr(dq_out), _addr(dk_out), _addr(out["dq"]), _addr(out.get("dk")),
+        _addr(out.get("dwq")), _addr(out.get("dwk")), _addr(workspace),
+        0 if workspace is None else workspace.numel(), _stream(q.device)))
     return out
 
 
@@ -583,9 +609,11 @@ def qk_norm_backward(q, k, dq_out, dk_out, wq=None, wk=None, positions=None, tur
 # linear attention with a decay for each head
 # --------------------------------------------------------------------------
 def _la_desc(q, k, v, g, states, scale, cu_seqlens, max_seqlen):
-    """Descriptor of linear attention on q [B,T,H,dk] or, packed, [N,H,dk],
-    after checking every operand's type, device and shape."""
-    code, dev, lead = _dtype_code(q), q.device, q.shape[:-2]
+    """Every operand's type, device and shape checked; the descriptor's fields
+    up to the steps of v, the steps of g, and the shapes of a state and of o.
+    q is [B,T,H,dk] or, packed, [N,H,dk]."""
+    qs = q.shape
+    code, dev, lead = _dtype_code(q), q.get_device(), qs[:-2]
     N = 0
     if cu_seqlens is None:
         if q.dim() != 4:
@@ -599,15 +627,15 @@ def _la_desc(q, k, v, g, states, scale, cu_seqlens, max_seqlen):
     if k.dim() != q.dim() or v.dim() != q.dim():
         raise ValueError(f"k and v: expected {q.dim()} dimensions, got shapes {tuple(k.shape)}, "
                          f"{tuple(v.shape)}")
-    H, dk, Hk, dv = q.shape[-2], q.shape[-1], k.shape[-2], v.shape[-1]
+    H, dk, Hk, dv = qs[-2], qs[-1], k.shape[-2], v.shape[-1]
     _like(k, "k", q.dtype, dev, lead + (Hk, dk))
     _like(v, "v", q.dtype, dev, lead + (Hk, dv))
     if g.dim() == 1:
         _like(g, "g", torch.float32, dev, (H,))
-        steps = Strides(0, 0, 1)
+        steps = (0, 0, 1)
     else:
         _like(g, "g", torch.float32, dev, lead + (H,))
-        steps = Strides(T * H if N == 0 else 0, H, 1)
+        steps = (T * H if cu_seqlens is None else 0, H, 1)
     if not g.is_contiguous():
         raise ValueError("g must be contiguous")
     for name, S in states:
@@ -615,16 +643,24 @@ def _la_desc(q, k, v, g, states, scale, cu_seqlens, max_seqlen):
             _like(S, name, torch.float32, dev, (B, H, dv, dk))
             if not S.is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
-    desc = LinearAttentionDesc(B, T, H, Hk, dk, dv, code, scale, N)
-    desc.q, desc.k, desc.v, desc.g = _steps(q, "q"), _steps(k, "k"), _steps(v, "v"), steps
-    return desc
+    return ((B, T, H, Hk, dk, dv, code, scale, N, *_steps(q, "q"), *_steps(k, "k"), *_steps(v, "v")),
+            steps, (B, H, dv, dk), lead + (H, dv))
 
 
-def linear_attention_workspace_bytes(desc, backward=False, need_dg=False):
-    n = ctypes.c_size_t(0)
-    _check(lib().prism_linear_attention_workspace(ctypes.byref(desc), int(backward), int(need_dg),
-                                                  ctypes.byref(n)))
-    return n.value
+# workspace bytes by descriptor, pass and wish
+_la_bytes = {}
+
+
+def _la_workspace(packed, backward, dg, device):
+    key = (packed, backward, dg)
+    size = _la_bytes.get(key)
+    if size is None:
+        n = ctypes.c_size_t(0)
+        _check(lib().prism_linear_attention_workspace(packed, backward, dg, ctypes.byref(n)))
+        if len(_la_bytes) >= 4096:
+            _la_bytes.clear()
+        size = _la_bytes[key] = n.value
+    return _workspace(size, device)[1] if size else None
 
 
 def linear_attention(q, k, v, g, S0=None, scale=1.0, cu_seqlens=None, max_seqlen=None, o=None,
@@ -638,22 +674,22 @@ def linear_attention(q, k, v, g, S0=None, scale=1.0, cu_seqlens=None, max_seqlen
     fp32 or None.  cu_seqlens (int32 [B+1]) with max_seqlen packs sequences:
     token tensors [N,..], g [N,H] or [H].  o, ST: where the results go (new
     tensors by default; ST may be S0)."""
-    desc = _la_desc(q, k, v, g, (("S0", S0), ("ST", ST)), scale, cu_seqlens, max_seqlen)
+    desc, gs, state, shape = _la_desc(q, k, v, g, (("S0", S0), ("ST", ST)), scale, cu_seqlens,
+                                      max_seqlen)
     _on_gpu(q)
-    shape = q.shape[:-1] + (desc.dv,)
     if o is None:
-        o = torch.empty(shape, dtype=q.dtype, device=q.device)
+        o = q.new_empty(shape)
     else:
-        _like(o, "o", q.dtype, q.device, shape)
-    desc.o = _steps(o, "o")
+        _like(o, "o", q.dtype, q.get_device(), shape)
     if ST is None:
-        ST = torch.empty((desc.B, desc.H, desc.dv, desc.dk), dtype=torch.float32, device=q.device)
+        ST = g.new_empty(state)
+    packed = _LA_DESC.pack(*desc, *_steps(o, "o"), *gs)
     if workspace is None:
-        workspace = _workspace(linear_attention_workspace_bytes(desc), q.device)[1]
-    stream = torch.cuda.current_stream(q.device).cuda_stream
+        workspace = _la_workspace(packed, 0, 0, q.device)
     _check(lib().prism_linear_attention(
-        ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S0), _ptr(cu_seqlens),
-        _ptr(o), _ptr(ST), _ptr(workspace), workspace.numel(), stream))
+        packed, _addr(q), _addr(k), _addr(v), _addr(g), _addr(S0), _addr(cu_seqlens), _addr(o),
+        _addr(ST), _addr(workspace), 0 if workspace is None else workspace.numel(),
+        _stream(q.device)))
     return o, ST
 
 
@@ -662,24 +698,24 @@ def linear_attention_backward(q, k, v, g, dO, S0=None, dST=None, scale=1.0, need
     """Gradients of <dO, o> + <dST, S_T> of linear_attention on the same
     inputs.  Returns a dict: dq, dk, dv (input type), dg (fp32, g's shape) when
     need_dg, dS0 (fp32) when need_dS0."""
-    desc = _la_desc(q, k, v, g, (("S0", S0), ("dST", dST)), scale, cu_seqlens, max_seqlen)
-    _like(dO, "dO", q.dtype, q.device, q.shape[:-1] + (desc.dv,))
-    desc.o = _steps(dO, "dO")
+    desc, gs, state, shape = _la_desc(q, k, v, g, (("S0", S0), ("dST", dST)), scale, cu_seqlens,
+                                      max_seqlen)
+    _like(dO, "dO", q.dtype, q.get_device(), shape)
+    packed = _LA_DESC.pack(*desc, *_steps(dO, "dO"), *gs)
     _on_gpu(q)
-    out = {n: torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    out = {n: t.new_empty(t.shape)
            for n, t in (("dq", q), ("dk", k), ("dv", v))}
     if need_dg:
-        out["dg"] = torch.empty(g.shape, dtype=torch.float32, device=q.device)
+        out["dg"] = g.new_empty(g.shape)
     if need_dS0:
-        out["dS0"] = torch.empty((desc.B, desc.H, desc.dv, desc.dk), dtype=torch.float32,
-                                 device=q.device)
+        out["dS0"] = g.new_empty(state)
     if workspace is None:
-        workspace = _workspace(linear_attention_workspace_bytes(desc, True, need_dg), q.device)[1]
-    stream = torch.cuda.current_stream(q.device).cuda_stream
+        workspace = _la_workspace(packed, 1, int(need_dg), q.device)
     _check(lib().prism_linear_attention_backward(
-        ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S0), _ptr(cu_seqlens),
-        _ptr(dO), _ptr(dST), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
-        _ptr(out.get("dg")), _ptr(out.get("dS0")), _ptr(workspace), workspace.numel(), stream))
+        packed, _addr(q), _addr(k), _addr(v), _addr(g), _addr(S0), _addr(cu_seqlens), _addr(dO),
+        _addr(dST), _addr(out["dq"]), _addr(out["dk"]), _addr(out["dv"]), _addr(out.get("dg")),
+        _addr(out.get("dS0")), _addr(workspace), 0 if workspace is None else workspace.numel(),
+        _stream(q.device)))
     return out
 
 
@@ -688,18 +724,15 @@ def linear_attention_step(q, k, v, g, S, S_out=None, scale=1.0, o=None):
     each sequence (prism_linear_attention_step); T = 1 is a decode step.  The
     state S [B,H,dv,dk] fp32 is read; S_T goes to S_out, or into S itself when
     S_out is None.  Returns o [B,T,H,dv]."""
-    desc = _la_desc(q, k, v, g, (("S", S), ("S_out", S_out)), scale, None, None)
+    desc, gs, _, shape = _la_desc(q, k, v, g, (("S", S), ("S_out", S_out)), scale, None, None)
     _on_gpu(q)
-    shape = q.shape[:-1] + (desc.dv,)
     if o is None:
-        o = torch.empty(shape, dtype=q.dtype, device=q.device)
+        o = q.new_empty(shape)
     else:
-        _like(o, "o", q.dtype, q.device, shape)
-    desc.o = _steps(o, "o")
-    stream = torch.cuda.current_stream(q.device).cuda_stream
+        _like(o, "o", q.dtype, q.get_device(), shape)
     _check(lib().prism_linear_attention_step(
-        ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S),
-        _ptr(S if S_out is None else S_out), _ptr(o), stream))
+        _LA_DESC.pack(*desc, *_steps(o, "o"), *gs), _addr(q), _addr(k), _addr(v), _addr(g),
+        _addr(S), _addr(S if S_out is None else S_out), _addr(o), _stream(q.device)))
     return o
 
 

@@ -139,10 +139,11 @@ def test_linear_attention_pointers_and_workspace():
     assert _la(la(), cu_seqlens=ctypes.c_void_p(0x10002)) == E_ALIGN
     assert _la(la(packed_tokens=-1), cu_seqlens=FAKE) == E_SHAPE and "packed_tokens" in _err()
     n = ctypes.c_size_t(0)
+    long = lambda: la(B=1, T=5000)   # (few heads, many tokens: cut into segments, whose states need room)
     for bwd, dg, call in ((0, 0, _la), (1, 1, _la_bwd)):
-        assert L.prism_linear_attention_workspace(ctypes.byref(la()), bwd, dg, ctypes.byref(n)) == OK and n.value > 0
-        assert call(la(), nbytes=n.value - 1) == E_WS and str(n.value) in _err()
-        assert call(la(), ws=None) == E_WS and call(la(), ws=ctypes.c_void_p(0x10010)) == E_ALIGN
+        assert L.prism_linear_attention_workspace(ctypes.byref(long()), bwd, dg, ctypes.byref(n)) == OK and n.value > 0
+        assert call(long(), nbytes=n.value - 1) == E_WS and str(n.value) in _err()
+        assert call(long(), ws=None) == E_WS and call(long(), ws=ctypes.c_void_p(0x10010)) == E_ALIGN
     assert L.prism_linear_attention_workspace(ctypes.byref(la()), 0, 0, None) == E_NULL
     # an empty batch asks for nothing
     assert _la(la(B=0), q=None, k=None, v=None, g=None, o=None, ST=None, S0=None, ws=None, nbytes=0) == OK
@@ -150,7 +151,11 @@ def test_linear_attention_pointers_and_workspace():
 
 def test_workspace_covers_packed_and_dense_rows():
     """One query serves both layouts: more rows or more wishes, no less room."""
-    size = lambda D, b=True, g=False: P.linear_attention_workspace_bytes(D, b, g)
+    def size(D, backward=True, dg=False):
+        n = ctypes.c_size_t(0)
+        assert P.lib().prism_linear_attention_workspace(ctypes.byref(D), int(backward), int(dg), ctypes.byref(n)) == OK
+        return n.value
+
     assert size(la(packed_tokens=1000)) > size(la()) == size(la(packed_tokens=150))
     assert size(la(), True, True) > size(la(), True) > size(la(), False)
 
