@@ -221,7 +221,7 @@ __global__ __launch_bounds__(256) void la_step_kernel(const LaStepArgs<E> a, int
     const E* kp = a.k + (b * a.sk.b + t * a.sk.t + hk * a.sk.h) + k0;
     const E* vp = a.v + (b * a.sv.b + t * a.sv.t + hk * a.sv.h);
     const f32x4 q = raw4_to_f(ld_raw4(qp)), k = raw4_to_f(ld_raw4(kp));
-    const float e = __expf(a.g[b * a.sg.b + t * a.sg.t + h * a.sg.h]);
+    const float e = expf(a.g[b * a.sg.b + t * a.sg.t + h * a.sg.h]);
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
       const int v = v0 + i * RW;

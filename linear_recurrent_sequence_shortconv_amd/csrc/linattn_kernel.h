@@ -185,6 +185,14 @@ __device__ inline void la_store4(__amdgpu_buffer_rsrc_t p, unsigned at, const f3
 // -150: infinite values would leave inf - inf between two tokens behind them.
 __device__ inline double la_log2(float g) { return (double)(g < -150.f ? -150.f : g) * 1.4426950408889634; }
 
+// 2^e for an exponent in fp64: the whole part goes to the exponent bits, so the
+// factor is good to 2^-23 however far e is from 0 (an fp32 e of 80 is not known
+// to better than 4e-6).
+__device__ inline float la_exp2(double e) {
+  const double n = rint(e);
+  return __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f((float)(e - n)), (int)fmin(fmax(n, -400.0), 400.0));
+}
+
 // log2 range of the factors kept without the decay: their products with each
 // other and with the data stay finite in fp32.
 constexpr double LA_RANGE = 80.0;
@@ -427,11 +435,11 @@ __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args)
     const float uh = (float)u;
     suh[buf][tid] = uh;
     sul[buf][tid] = (float)(u - (double)uh);
-    sra[buf][tid] = R.s_row * __builtin_amdgcn_exp2f((float)(f + u));
-    srt[buf][tid] = R.s_upd * __builtin_amdgcn_exp2f((float)((st ? tot : -f) - u));
+    sra[buf][tid] = R.s_row * la_exp2(f + u);
+    srt[buf][tid] = R.s_upd * la_exp2((st ? tot : -f) - u);
     if (bj == 0) {
-      sm0[buf][bq] = __builtin_amdgcn_exp2f((float)m0);
-      sm1[buf][bq] = __builtin_amdgcn_exp2f((float)m1);
+      sm0[buf][bq] = la_exp2(m0);
+      sm1[buf][bq] = la_exp2(m1);
       strong[buf][bq] = st;
     }
   };
@@ -651,12 +659,12 @@ __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args)
     if (NBUF == 1) __syncthreads();
   }
 
-  state_scale(__builtin_amdgcn_exp2f((float)F));
+  state_scale(la_exp2(F));
   if (OUT) {
     if (last && R.fin) state_store(R.fin + (long)bh * args.DD);
   } else {
     state_store(R.seg + segoff);
-    if (tid == 0) R.segdec[(long)bh * args.nseg + seg] = __builtin_amdgcn_exp2f((float)total);
+    if (tid == 0) R.segdec[(long)bh * args.nseg + seg] = la_exp2(total);
   }
 }
 
