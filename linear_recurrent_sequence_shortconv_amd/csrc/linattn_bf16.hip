@@ -2,5 +2,5 @@
 #include "linattn_inst.h"
 
 namespace prism {
-template hipError_t launch_la_pass<bf16>(const LaArgs<bf16>&, int, bool, bool, hipStream_t);
+template hipError_t launch_la_pass<bf16>(const LaArgs<bf16>&, int, LaPass, hipStream_t);
 }  // namespace prism

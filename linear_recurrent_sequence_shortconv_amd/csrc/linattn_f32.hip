@@ -2,5 +2,5 @@
 #include "linattn_inst.h"
 
 namespace prism {
-template hipError_t launch_la_pass<float>(const LaArgs<float>&, int, bool, bool, hipStream_t);
+template hipError_t launch_la_pass<float>(const LaArgs<float>&, int, LaPass, hipStream_t);
 }  // namespace prism

@@ -27,8 +27,9 @@
 // summed for 256 tokens at a time, one token a thread.
 //
 // Operand rounding (bf16): A, B, C are the inputs themselves.  2^{-(F+u)} C, fp32,
-// enters the state's sum as three bf16 pieces (the state is an fp32 result: one
-// piece would leave it 2e-3 off).  The scaled scores and the copy of X in the
+// enters the state's sum as three bf16 pieces where the state is an fp32 result
+// (one piece would leave it 2e-3 off, two 3e-6), as two where only out, bf16,
+// comes of it.  The scaled scores and the copy of X in the
 // readout are rounded once to bf16 (out is bf16: each adds what the final
 // rounding adds), or, with PR, taken in three pieces as well (the gradient of
 // g is a difference of large sums of q . dq and k . dk).
@@ -221,7 +222,7 @@ __device__ inline float la_sum32(float x) {
   return x + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, b, 0x142, 0xa, 0xf, false));
 }
 
-template <typename E, int DA, int NCT, bool PR, bool OUT>
+template <typename E, int DA, int NCT, bool PR, bool OUT, int PIECES>
 __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args) {
   typedef La16<E> M;
   typedef typename M::frag frag;
@@ -231,7 +232,7 @@ __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args)
   constexpr int KG = M::KG, KV = M::KV, UPG = M::UPG;
   constexpr int AT = DA / 16, AG = DA / KG;       // tiles and groups of X's rows
   constexpr int TG = CH / KG;                     // groups of the chunk's tokens
-  constexpr int NSU = HALF ? 3 : 1;               // pieces of the state's summand
+  constexpr int NSU = HALF ? PIECES : 1;          // pieces of the state's summand
   constexpr int NSX = HALF && PR ? 3 : 1;         // of X and of Gamma o A B^T in out
   constexpr int LA = ldpad<E>(DA), LC = ldpad<E>(NV);
   // (fp32 rows of 128 take too much LDS for two workgroups a CU with two buffers)
@@ -669,10 +670,10 @@ __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args)
 }
 
 // Launch of one instance; DA and NCT by the operands' size.
-template <typename E, int DA, int NCT, bool PR, bool OUT>
+template <typename E, int DA, int NCT, bool PR, bool OUT, int PIECES>
 hipError_t la_launch(const LaArgs<E>& a, hipStream_t s) {
   const unsigned grid = (unsigned)((long)a.B * a.H * a.nseg * a.nroles);
-  hipLaunchKernelGGL((la_pass_kernel<E, DA, NCT, PR, OUT>), dim3(grid), dim3(LA_NT), 0, s, a);
+  hipLaunchKernelGGL((la_pass_kernel<E, DA, NCT, PR, OUT, PIECES>), dim3(grid), dim3(LA_NT), 0, s, a);
   return hipGetLastError();
 }
 

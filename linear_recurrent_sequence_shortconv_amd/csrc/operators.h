@@ -96,10 +96,13 @@ struct LaArgs {
 constexpr int LA_CHUNK = 32;   // tokens per chunk
 // Partial row dots written for each token (one a wave).
 constexpr int LA_PARTS = 4;
-// outputs = false: the segments' own states only (role.seg, role.segdec).
-// precise: bf16 operands of every product in three pieces.
+// What a pass computes (dim = max(dk, dv)): the segments' own states alone
+// (role.seg, role.segdec), as far as bf16 outputs or as fp32 results need them;
+// outputs; outputs and a final state (role.fin); outputs, a final state and the
+// row dots, every product's bf16 operands in three pieces.
+enum LaPass { LA_STATES, LA_STATES_FP32, LA_OUT, LA_OUT_STATE, LA_OUT_DOTS };
 template <typename E>
-hipError_t launch_la_pass(const LaArgs<E>& a, int dim, bool outputs, bool precise, hipStream_t s);
+hipError_t launch_la_pass(const LaArgs<E>& a, int dim, LaPass kind, hipStream_t s);
 
 // Segment states in place: own states -> states entering each segment.
 struct LaJoin {

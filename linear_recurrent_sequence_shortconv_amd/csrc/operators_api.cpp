@@ -359,7 +359,8 @@ prism_status la_forward(const prism_linear_attention_desc& d, const LaPlan& p, c
   r.segdec = w.dec;
   a.r[0] = r;
   a.nroles = 1;
-  if (p.nseg > 1) HIP_TRY("la_states", s, prism::launch_la_pass<E>(a, p.dim, false, false, s));
+  if (p.nseg > 1)
+    HIP_TRY("la_states", s, prism::launch_la_pass<E>(a, p.dim, ST ? prism::LA_STATES_FP32 : prism::LA_STATES, s));
   if (p.nseg > LA_SELF_JOIN) {
     prism::LaJoin j = {};
     j.B = d.B;
@@ -376,7 +377,7 @@ prism_status la_forward(const prism_linear_attention_desc& d, const LaPlan& p, c
     HIP_TRY("la_join", s, prism::launch_la_join(j, s));
     a.joined = 1;
   }
-  HIP_TRY("la_fwd", s, prism::launch_la_pass<E>(a, p.dim, true, false, s));
+  HIP_TRY("la_fwd", s, prism::launch_la_pass<E>(a, p.dim, ST ? prism::LA_OUT_STATE : prism::LA_OUT, s));
   return PRISM_OK;
 }
 
@@ -424,7 +425,8 @@ prism_status la_backward(const prism_linear_attention_desc& d, const LaPlan& p, 
     b.r[0] = rq;
     b.r[1] = rk;
     b.nroles = 2;
-    HIP_TRY("la_states", s, prism::launch_la_pass<E>(b, p.dim, false, false, s));
+    HIP_TRY("la_states", s,
+            prism::launch_la_pass<E>(b, p.dim, dg || dS0 ? prism::LA_STATES_FP32 : prism::LA_STATES, s));
   }
   if (p.nseg > LA_SELF_JOIN && d.B > 0) {
     prism::LaJoin j = {};
@@ -458,16 +460,16 @@ prism_status la_backward(const prism_linear_attention_desc& d, const LaPlan& p, 
     a.r[0] = rq;
     a.r[1] = rk;
     a.nroles = 2;
-    HIP_TRY("la_bwd_qk", s, prism::launch_la_pass<E>(a, p.dim, true, true, s));
+    HIP_TRY("la_bwd_qk", s, prism::launch_la_pass<E>(a, p.dim, prism::LA_OUT_DOTS, s));
     a.r[0] = rv;
     a.nroles = 1;
-    HIP_TRY("la_bwd_v", s, prism::launch_la_pass<E>(a, p.dim, true, false, s));
+    HIP_TRY("la_bwd_v", s, prism::launch_la_pass<E>(a, p.dim, prism::LA_OUT, s));
   } else if (d.B > 0) {
     a.r[0] = rq;
     a.r[1] = rk;
     a.r[2] = rv;
     a.nroles = 3;
-    HIP_TRY("la_bwd", s, prism::launch_la_pass<E>(a, p.dim, true, false, s));
+    HIP_TRY("la_bwd", s, prism::launch_la_pass<E>(a, p.dim, dS0 ? prism::LA_OUT_STATE : prism::LA_OUT, s));
   }
   if (dg) {
     prism::LaDecay x = {};
