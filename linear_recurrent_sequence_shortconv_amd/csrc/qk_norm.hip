@@ -105,9 +105,11 @@ __device__ inline LanePlace lane_place(int p, int d, int rot) {
 }
 
 // cos, sin of the lane's V angles.  The phase p F mod 2^64 is exact; its upper
-// 32 bits, as a signed number of 2^-31 half turns, keep the angle to 2^-24 of
-// its size (an fp32 product p * frequency would lose position's bits).
-template <int V>
+// 32 bits, as a signed number, keep the angle to 2^-24 of its size (an fp32
+// product p * frequency would lose position's bits).  For bf16 the hardware's
+// sine and cosine of turns do (absolute error about 2^-20; the outputs are
+// rounded at 2^-9); fp32 takes the library's.
+template <typename E, int V>
 __device__ inline void lane_angles(const QkNormArgs& g, long tok, const LanePlace& q, float (&cs)[V],
                                    float (&sn)[V]) {
 #pragma unroll
@@ -120,8 +122,13 @@ __device__ inline void lane_angles(const QkNormArgs& g, long tok, const LanePlac
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const unsigned long long ph = p * (unsigned long long)g.turns[q.pair + i];
-      const float f = (float)(int)(unsigned)(ph >> 32) * 0x1p-31f;
-      sincospif(f, &sn[i], &cs[i]);
+      const float f = (float)(int)(unsigned)(ph >> 32);
+      if (sizeof(E) == 2) {
+        sn[i] = __builtin_amdgcn_sinf(f * 0x1p-32f);
+        cs[i] = __builtin_amdgcn_cosf(f * 0x1p-32f);
+      } else {
+        sincospif(f * 0x1p-31f, &sn[i], &cs[i]);
+      }
     }
   }
 }
@@ -197,7 +204,7 @@ __global__ __launch_bounds__(QN_NT) void qk_norm_kernel(const QkNormArgs g, int 
         ra[u] = *reinterpret_cast<const raw*>(x + q.a);
         rb[u] = *reinterpret_cast<const raw*>(x + q.b);
       }
-      if (first) lane_angles<V>(g, tok, q, cs, sn);
+      if (first) lane_angles<E, V>(g, tok, q, cs, sn);
       first = false;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -227,95 +234,91 @@ __global__ __launch_bounds__(QN_NT) void qk_norm_kernel(const QkNormArgs g, int 
   }
 }
 
-// One pass over the rows of one of q, k in the backward kernel (see there).
+// The rows of q or of k (the first nq workgroups take q: one kind's weights and
+// sums in a workgroup's registers).  The weight gradients of a workgroup's rows
+// are summed in registers over its tokens, then over its groups (in the wave,
+// then over the waves through LDS), and written as one partial [d] for each
+// workgroup.
 template <typename E, int V, bool IL, bool DW>
-__device__ inline void bwd_rows(const QkNormArgs& g, const LanePlace& q, int G, int gi, int tg,
-                                const E* x, const E* dz, E* dx, long sx, long sg, long sy, int H,
-                                const float (&wa)[V], const float (&wb)[V], const float (&cs)[V],
-                                const float (&sn)[V], float (&da)[V], float (&db)[V]) {
+__global__ __launch_bounds__(QN_NT) void qk_norm_bwd_kernel(const QkNormArgs g, int G, int nq, int tgq, int tgk) {
   typedef VecIo<E, V> IO;
   typedef typename IO::raw raw;
-  constexpr int U = 2;
-  for (int h0 = gi; h0 < H; h0 += U * tg) {
-    raw ra[U], rb[U], rc[U], rd[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = min(h0 + u * tg, H - 1);
-      ra[u] = *reinterpret_cast<const raw*>(x + h * sx + q.a);
-      rb[u] = *reinterpret_cast<const raw*>(x + h * sx + q.b);
-      rc[u] = *reinterpret_cast<const raw*>(dz + h * sg + q.a);
-      rd[u] = *reinterpret_cast<const raw*>(dz + h * sg + q.b);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * tg;
-      float xa[V], xb[V], ga[V], gb[V];
-      IO::unpack(ra[u], xa);
-      IO::unpack(rb[u], xb);
-      IO::unpack(rc[u], ga);
-      IO::unpack(rd[u], gb);
-      turn<V, IL, -1>(ga, gb, cs, sn);
-      float ss = 0.f, xh = 0.f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        ss = fmaf(xa[i], xa[i], fmaf(xb[i], xb[i], ss));
-        xh = fmaf(xa[i] * wa[i], ga[i], fmaf(xb[i] * wb[i], gb[i], xh));
-      }
-      ss = group_sum(q.on ? ss : 0.f, G);
-      xh = group_sum(q.on ? xh : 0.f, G);
-      const float r = rsqrtf(fmaf(g.c, ss, g.eps));
-      const float m = g.c * r * r * r * xh;
-      if (h < H && q.on) {
-        float ya[V], yb[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          ya[i] = fmaf(-m, xa[i], r * wa[i] * ga[i]);
-          yb[i] = fmaf(-m, xb[i], r * wb[i] * gb[i]);
-        }
-        if (DW) {
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            da[i] = fmaf(r * xa[i], ga[i], da[i]);
-            db[i] = fmaf(r * xb[i], gb[i], db[i]);
-          }
-        }
-        *reinterpret_cast<raw*>(dx + h * sy + q.a) = IO::pack(ya);
-        *reinterpret_cast<raw*>(dx + h * sy + q.b) = IO::pack(yb);
-      }
-    }
-  }
-}
-
-// The weight gradients of a workgroup's rows are summed in registers over its
-// tokens, then over its groups (in the wave, then over the waves through LDS),
-// and written as one partial [2][d] for each workgroup.
-template <typename E, int V, bool IL, bool DW>
-__global__ __launch_bounds__(QN_NT) void qk_norm_bwd_kernel(const QkNormArgs g, int G, int tg) {
+  constexpr int U = 2;   // rows of a group in flight
+  const bool isq = (int)blockIdx.x < nq;
+  const int blk = isq ? blockIdx.x : blockIdx.x - nq, nblk = isq ? nq : gridDim.x - nq;
+  const int tg = isq ? tgq : tgk, H = isq ? g.Hq : g.Hk;
+  const void *px = isq ? g.xq : g.xk, *pz = isq ? g.gq : g.gk;
+  void* py = isq ? g.yq : g.yk;
+  const Strides sx = isq ? g.sxq : g.sxk, sg = isq ? g.sgq : g.sgk, sy = isq ? g.syq : g.syk;
   const int tid = threadIdx.x, lane = tid & (G - 1);
   const int grp = tid / G, team = grp / tg, gi = grp & (tg - 1);
   const int teams = QN_NT / (G * tg);
   const LanePlace q = lane_place<V, IL>(lane, g.d, g.rot);
   const long N = (long)g.B * g.T;
-  float wqa[V], wqb[V], wka[V], wkb[V];
-  load_w<E, V>(g.wq, q, wqa, wqb);
-  load_w<E, V>(g.wk, q, wka, wkb);
-  float d0[V], d1[V], d2[V], d3[V];
+  float wa[V], wb[V], da[V], db[V];
+  load_w<E, V>(isq ? g.wq : g.wk, q, wa, wb);
 #pragma unroll
-  for (int i = 0; i < V; ++i) d0[i] = d1[i] = d2[i] = d3[i] = 0.f;
-  for (long tok = (long)blockIdx.x * teams + team; tok < N; tok += (long)gridDim.x * teams) {
+  for (int i = 0; i < V; ++i) da[i] = db[i] = 0.f;
+  for (long tok = (long)blk * teams + team; tok < N; tok += (long)nblk * teams) {
     const int b = (int)(tok / g.T), t = (int)(tok - (long)b * g.T);
+    const E* x = static_cast<const E*>(px) + (b * sx.b + t * sx.t);
+    const E* dz = static_cast<const E*>(pz) + (b * sg.b + t * sg.t);
+    E* dx = static_cast<E*>(py) + (b * sy.b + t * sy.t);
     float cs[V], sn[V];
-    lane_angles<V>(g, tok, q, cs, sn);
-    auto at = [&](const void* p, const Strides& s) { return static_cast<const E*>(p) + (b * s.b + t * s.t); };
-    bwd_rows<E, V, IL, DW>(g, q, G, gi, tg, at(g.xq, g.sxq), at(g.gq, g.sgq),
-                           const_cast<E*>(at(g.yq, g.syq)), g.sxq.h, g.sgq.h, g.syq.h, g.Hq, wqa, wqb,
-                           cs, sn, d0, d1);
-    bwd_rows<E, V, IL, DW>(g, q, G, gi, tg, at(g.xk, g.sxk), at(g.gk, g.sgk),
-                           const_cast<E*>(at(g.yk, g.syk)), g.sxk.h, g.sgk.h, g.syk.h, g.Hk, wka, wkb,
-                           cs, sn, d2, d3);
+    bool first = true;
+    for (int h0 = gi; h0 < H; h0 += U * tg) {
+      raw ra[U], rb[U], rc[U], rd[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = min(h0 + u * tg, H - 1);
+        ra[u] = *reinterpret_cast<const raw*>(x + h * sx.h + q.a);
+        rb[u] = *reinterpret_cast<const raw*>(x + h * sx.h + q.b);
+        rc[u] = *reinterpret_cast<const raw*>(dz + h * sg.h + q.a);
+        rd[u] = *reinterpret_cast<const raw*>(dz + h * sg.h + q.b);
+      }
+      if (first) lane_angles<E, V>(g, tok, q, cs, sn);
+      first = false;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * tg;
+        float xa[V], xb[V], ga[V], gb[V];
+        IO::unpack(ra[u], xa);
+        IO::unpack(rb[u], xb);
+        IO::unpack(rc[u], ga);
+        IO::unpack(rd[u], gb);
+        turn<V, IL, -1>(ga, gb, cs, sn);
+        float ss = 0.f, xh = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          ss = fmaf(xa[i], xa[i], fmaf(xb[i], xb[i], ss));
+          xh = fmaf(xa[i] * wa[i], ga[i], fmaf(xb[i] * wb[i], gb[i], xh));
+        }
+        ss = group_sum(q.on ? ss : 0.f, G);
+        xh = group_sum(q.on ? xh : 0.f, G);
+        const float r = rsqrtf(fmaf(g.c, ss, g.eps));
+        const float m = g.c * r * r * r * xh;
+        if (h < H && q.on) {
+          float ya[V], yb[V];
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            ya[i] = fmaf(-m, xa[i], r * wa[i] * ga[i]);
+            yb[i] = fmaf(-m, xb[i], r * wb[i] * gb[i]);
+          }
+          if (DW) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              da[i] = fmaf(r * xa[i], ga[i], da[i]);
+              db[i] = fmaf(r * xb[i], gb[i], db[i]);
+            }
+          }
+          *reinterpret_cast<raw*>(dx + h * sy.h + q.a) = IO::pack(ya);
+          *reinterpret_cast<raw*>(dx + h * sy.h + q.b) = IO::pack(yb);
+        }
+      }
+    }
   }
   if constexpr (DW) {
-    __shared__ float sm[QN_NT / WAVE][4][V * 32];
+    __shared__ float sm[QN_NT / WAVE][2][V * 32];
     const int wave = tid / WAVE, wl = tid & (WAVE - 1);
     auto fold = [&](float (&v)[V], int row) {
 #pragma unroll
@@ -324,48 +327,49 @@ __global__ __launch_bounds__(QN_NT) void qk_norm_bwd_kernel(const QkNormArgs g, 
         if (wl < G) sm[wave][row][V * wl + i] = v[i];
       }
     };
-    fold(d0, 0);
-    fold(d1, 1);
-    fold(d2, 2);
-    fold(d3, 3);
+    fold(da, 0);
+    fold(db, 1);
     __syncthreads();
-    float* out = g.part + (long)blockIdx.x * 2 * g.d;
-    for (int e = tid; e < 4 * V * G; e += QN_NT) {
+    float* out = g.part + (long)blockIdx.x * g.d;
+    for (int e = tid; e < 2 * V * G; e += QN_NT) {
       const int row = e / (V * G), j = e % (V * G);
       const LanePlace w = lane_place<V, IL>(j / V, g.d, g.rot);
       float s = 0.f;
 #pragma unroll
       for (int k = 0; k < QN_NT / WAVE; ++k) s += sm[k][row][j];
-      if (w.on) out[(row >> 1) * g.d + ((row & 1) ? w.b : w.a) + j % V] = s;
+      if (w.on) out[(row ? w.b : w.a) + j % V] = s;
     }
   }
 }
 
-// Column sums of the n partial rows [2 d]: 32 columns a workgroup, 32 threads
-// on each column taking every 32nd row, joined through LDS in a fixed order.
-__global__ __launch_bounds__(1024) void qk_norm_dw_kernel(const float* __restrict__ part, int n, int d,
+// Column sums of the partial rows [d]: the first nq give dwq, the others dwk.
+// 32 columns a workgroup, 32 threads on each column taking every 32nd row,
+// joined through LDS in a fixed order.
+__global__ __launch_bounds__(1024) void qk_norm_dw_kernel(const float* __restrict__ part, int nq, int n, int d,
                                                           float* __restrict__ dwq,
                                                           float* __restrict__ dwk) {
   __shared__ float sm[32][33];
   const int c = threadIdx.x & 31, y = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + c;
+  const bool isq = blockIdx.y == 0;
+  float* out = isq ? dwq : dwk;
+  if (!out) return;
   float s = 0.f;
-  if (col < 2 * d) {
+  if (col < d) {
 #pragma unroll 8
-    for (int r = y; r < n; r += 32) s += part[(long)r * 2 * d + col];
+    for (int r = (isq ? 0 : nq) + y; r < (isq ? nq : n); r += 32) s += part[(long)r * d + col];
   }
   sm[y][c] = s;
   __syncthreads();
-  if (y == 0 && col < 2 * d) {
+  if (y == 0 && col < d) {
     float x = 0.f;
 #pragma unroll
     for (int k = 0; k < 32; ++k) x += sm[k][c];
-    float* o = col < d ? dwq : dwk;
-    if (o) o[col < d ? col : col - d] = x;
+    out[col] = x;
   }
 }
 
-constexpr int QN_PARTS = 1024;   // workgroups of the backward kernel, at most
+constexpr int QN_PARTS = 1024;   // workgroups of the backward kernel with weights, at most
 
 int pow2_at_least(int n) {
   int p = 1;
@@ -386,16 +390,16 @@ bool wide(const QkNormArgs& a, bool bwd) {
 
 // Groups a token: a wave where the tokens fill the chip with a wave each,
 // else the whole workgroup; never more than there are heads.
-int team_groups(const QkNormArgs& a, int G) {
+int team_groups(const QkNormArgs& a, int G, int H) {
   const long N = (long)a.B * a.T;
   const int most = (N >= 4096 ? WAVE : QN_NT) / G;
-  const int need = pow2_at_least(a.Hq + a.Hk);
+  const int need = pow2_at_least(H);
   return most < need ? most : need;
 }
 
 template <typename E, int V>
 hipError_t run_fwd(const QkNormArgs& a, hipStream_t s) {
-  const int G = pow2_at_least(a.d / (2 * V)), tg = team_groups(a, G), teams = QN_NT / (G * tg);
+  const int G = pow2_at_least(a.d / (2 * V)), tg = team_groups(a, G, a.Hq + a.Hk), teams = QN_NT / (G * tg);
   const long N = (long)a.B * a.T;
   long grid = (N + teams - 1) / teams;
   if (grid > (1 << 20)) grid = 1 << 20;
@@ -408,22 +412,31 @@ hipError_t run_fwd(const QkNormArgs& a, hipStream_t s) {
 
 template <typename E, int V, bool IL>
 hipError_t run_bwd(const QkNormArgs& a, hipStream_t s) {
-  const int G = pow2_at_least(a.d / (2 * V)), tg = team_groups(a, G), teams = QN_NT / (G * tg);
+  const int G = pow2_at_least(a.d / (2 * V));
   const long N = (long)a.B * a.T;
   const bool dw = a.dwq || a.dwk;
-  long grid = (N + teams - 1) / teams;
+  // workgroups for q and for k: as many as there are teams of tokens, at most
+  // `most` in the proportion of their heads
   const long most = dw ? QN_PARTS : (1 << 20);
-  if (grid > most) grid = most;
+  auto blocks = [&](int H, int tg) -> long {
+    if (H == 0 || N == 0) return 0;
+    const int teams = QN_NT / (G * tg);
+    const long want = (N + teams - 1) / teams, room = most * H / (a.Hq + a.Hk);
+    return want < room ? want : (room > 1 ? room : 1);
+  };
+  const int tgq = team_groups(a, G, a.Hq), tgk = a.Hk ? team_groups(a, G, a.Hk) : 1;
+  const long nq = blocks(a.Hq, tgq), nk = blocks(a.Hk, tgk);
   if (N > 0) {
+    const dim3 grid((unsigned)(nq + nk));
     if (dw)
-      hipLaunchKernelGGL((qk_norm_bwd_kernel<E, V, IL, true>), dim3((unsigned)grid), dim3(QN_NT), 0, s, a, G, tg);
+      hipLaunchKernelGGL((qk_norm_bwd_kernel<E, V, IL, true>), grid, dim3(QN_NT), 0, s, a, G, (int)nq, tgq, tgk);
     else
-      hipLaunchKernelGGL((qk_norm_bwd_kernel<E, V, IL, false>), dim3((unsigned)grid), dim3(QN_NT), 0, s, a, G, tg);
+      hipLaunchKernelGGL((qk_norm_bwd_kernel<E, V, IL, false>), grid, dim3(QN_NT), 0, s, a, G, (int)nq, tgq, tgk);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (dw) {
-    hipLaunchKernelGGL(qk_norm_dw_kernel, dim3((2 * a.d + 31) / 32), dim3(1024), 0, s, a.part, N > 0 ? (int)grid : 0,
+    hipLaunchKernelGGL(qk_norm_dw_kernel, dim3((a.d + 31) / 32, 2), dim3(1024), 0, s, a.part, (int)nq, (int)(nq + nk),
                        a.d, a.dwq, a.dwk);
     return hipGetLastError();
   }
@@ -432,7 +445,8 @@ hipError_t run_bwd(const QkNormArgs& a, hipStream_t s) {
 
 }  // namespace
 
-size_t qk_norm_part_bytes(int d) { return (size_t)QN_PARTS * 2 * d * sizeof(float); }
+// (with few heads of one kind its share may round up to one more)
+size_t qk_norm_part_bytes(int d) { return (size_t)(QN_PARTS + 1) * d * sizeof(float); }
 
 template <typename E>
 hipError_t launch_qk_norm(const QkNormArgs& a, hipStream_t s) {
