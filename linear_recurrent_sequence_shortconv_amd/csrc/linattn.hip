@@ -59,8 +59,12 @@ __global__ __launch_bounds__(256) void la_join_kernel(const LaJoin a) {
 __global__ __launch_bounds__(256) void la_decay_kernel(const LaDecay a) {
   __shared__ double sm[8];
   const int tid = threadIdx.x;
-  const int seg = blockIdx.x % a.nseg, bh = blockIdx.x / a.nseg;
-  const int b = bh / a.H, h = bh % a.H;
+  // (the heads of one stretch of tokens on one XCD: their values of g and dg
+  // share cache lines)
+  int id = xcd_swizzle((int)blockIdx.x, (int)gridDim.x);
+  const int h = id % a.H;
+  id /= a.H;
+  const int seg = id % a.nseg, b = id / a.nseg, bh = b * a.H + h;
   __shared__ int sq[4];
   long first = 0;
   int n = a.T;
@@ -72,32 +76,51 @@ __global__ __launch_bounds__(256) void la_decay_kernel(const LaDecay a) {
   const bool last = s0 + len == n;
   const int used = (n + a.seglen - 1) / a.seglen;
   const long o = (long)bh * a.DD;
-  auto entering = [&](const float* own, const float* dec, const float* X0, int from, int to, int step, int e) {
-    f32x4 x = X0 ? *reinterpret_cast<const f32x4*>(X0 + o + e) : f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int i = from; i != to; i += step)
-      x = x * dec[(long)bh * a.nseg + i] + *reinterpret_cast<const f32x4*>(own + ((long)bh * a.nseg + i) * a.DD + e);
-    return x;
-  };
-  auto joined = [&](const float* seg_, int i, int e) {
-    return *reinterpret_cast<const f32x4*>(seg_ + ((long)bh * a.nseg + i) * a.DD + e);
-  };
   double s = 0.0;
-  if (!last || a.dST)
-    for (int e = 4 * tid; e < a.DD; e += 1024) {
-      f32x4 r, x;
+  if (!last || a.dST) {
+    constexpr int U = 8;   // pieces of each state requested together
+    const long sg0 = (long)bh * a.nseg;
+    for (int e0 = 4 * tid; e0 < a.DD; e0 += 1024 * U) {
+      f32x4 r[U], x[U];
+      auto at = [&](int u) { return min(e0 + 1024 * u, a.DD - 4); };
+      auto load = [&](f32x4 (&y)[U], const float* p) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) y[u] = *reinterpret_cast<const f32x4*>(p + at(u));
+      };
+      // the state entering a segment, from the own states before it
+      auto enter = [&](f32x4 (&y)[U], const float* own, const float* dec, const float* X0, int from, int to, int step) {
+        if (X0) {
+          load(y, X0 + o);
+        } else {
+#pragma unroll
+          for (int u = 0; u < U; ++u) y[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+        for (int i = from; i != to; i += step) {
+          f32x4 z[U];
+          load(z, own + (sg0 + i) * a.DD);
+          const float d = dec[sg0 + i];
+#pragma unroll
+          for (int u = 0; u < U; ++u) y[u] = y[u] * d + z[u];
+        }
+      };
       if (last) {
-        r = *reinterpret_cast<const f32x4*>(a.dST + o + e);
-        x = *reinterpret_cast<const f32x4*>(a.ST + o + e);
+        load(r, a.dST + o);
+        load(x, a.ST + o);
       } else if (a.joined) {
-        r = joined(a.segr, seg, e);
-        x = joined(a.segf, seg + 1, e);
+        load(r, a.segr + (sg0 + seg) * a.DD);
+        load(x, a.segf + (sg0 + seg + 1) * a.DD);
       } else {
-        r = entering(a.segr, a.decr, a.dST, used - 1, seg, -1, e);
-        x = entering(a.segf, a.decf, a.S0, 0, seg + 1, 1, e);
+        enter(r, a.segr, a.decr, a.dST, used - 1, seg, -1);
+        enter(x, a.segf, a.decf, a.S0, 0, seg + 1, 1);
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) s += (double)r[k] * (double)x[k];
+      for (int u = 0; u < U; ++u)
+        if (e0 + 1024 * u < a.DD) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s += (double)r[u][k] * (double)x[u][k];
+        }
     }
+  }
   const int lane = tid & 63, wave = tid >> 6;
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
@@ -108,44 +131,52 @@ __global__ __launch_bounds__(256) void la_decay_kernel(const LaDecay a) {
   const float* eq = a.eq + (long)bh * LA_PARTS * a.T + s0;
   const float* ek = a.ek + (long)bh * LA_PARTS * a.T + s0;
   const float* pg = a.g + ((a.cu ? 0 : b * a.sg.b) + row0 * a.sg.t + h * a.sg.h);
-  // thread tid holds token hi - 1 - tid (a prefix sum over the threads); the
-  // next block's values are requested before this one's are summed
-  float q[LA_PARTS], k[LA_PARTS], gv = 0.f;
-  auto load = [&](int hi) __attribute__((always_inline)) {
-    const int t = max(hi - 1 - tid, 0);
-#pragma unroll
-    for (int p = 0; p < LA_PARTS; ++p) {
-      q[p] = eq[(long)p * a.T + t];
-      k[p] = ek[(long)p * a.T + t];
-    }
-    gv = pg[(long)t * a.sg.t];
-  };
-  load(len);
+  // thread tid holds the U tokens hi - 1 - U tid - r, r = 0 .. U - 1, of a block
+  // of 256 U (prefix sums over r, then over the threads)
+  constexpr int U = 4;
   int buf = 4;
-  for (int hi = len; hi > 0; hi -= 256) {
-    const int t = hi - 1 - tid;
-    double x = 0.0;
+  for (int hi = len; hi > 0; hi -= 256 * U) {
+    const int t0 = hi - 1 - U * tid;
+    float q[U][LA_PARTS], k[U][LA_PARTS], g[U];
 #pragma unroll
-    for (int p = 0; p < LA_PARTS; ++p) x += (double)q[p] - (double)k[p];
-    if (t < 0) x = 0.0;
-    const float g = gv;
-    load(max(hi - 256, 1));
+    for (int r = 0; r < U; ++r) {
+      const int t = max(t0 - r, 0);
+#pragma unroll
+      for (int p = 0; p < LA_PARTS; ++p) {
+        q[r][p] = eq[(long)p * a.T + t];
+        k[r][p] = ek[(long)p * a.T + t];
+      }
+      g[r] = pg[(long)t * a.sg.t];
+    }
+    double x[U];
+#pragma unroll
+    for (int r = 0; r < U; ++r) {
+      x[r] = 0.0;
+#pragma unroll
+      for (int p = 0; p < LA_PARTS; ++p) x[r] += (double)q[r][p] - (double)k[r][p];
+      if (t0 - r < 0) x[r] = 0.0;
+      if (r > 0) x[r] += x[r - 1];
+    }
+    double run = x[U - 1];
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-      const double y = __shfl_up(x, o);
-      if (lane >= o) x += y;
+      const double y = __shfl_up(run, o);
+      if (lane >= o) run += y;
     }
-    if (lane == 63) sm[buf + wave] = x;
+    if (lane == 63) sm[buf + wave] = run;
     __syncthreads();
-    double before = carry;
+    double before = carry + (run - x[U - 1]);
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       if (w < wave) before += sm[buf + w];
       carry += sm[buf + w];
     }
     buf ^= 4;   // (the other four sums: one barrier a block)
-    if (t >= 0) {
-      const float d = g < -104.f ? 0.f : (float)(before + x);
+#pragma unroll
+    for (int r = 0; r < U; ++r) {
+      const int t = t0 - r;
+      if (t < 0) continue;
+      const float d = g[r] < -104.f ? 0.f : (float)(before + x[r]);
       if (a.tmp)
         a.tmp[(long)bh * a.T + s0 + t] = d;
       else

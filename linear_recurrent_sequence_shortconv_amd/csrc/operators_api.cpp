@@ -228,7 +228,7 @@ constexpr int LA_SELF_JOIN = 4;
 enum LaWork { LA_FORWARD, LA_BACKWARD, LA_BACKWARD_DG };
 void plan_segments(const prism_linear_attention_desc& d, LaWork work, LaPlan* p) {
   const long chunks = ((long)d.T + prism::LA_CHUNK - 1) / prism::LA_CHUNK;
-  const long most = chunks / 4 < 64 ? chunks / 4 : 64;
+  const long most = chunks / 2 < 64 ? chunks / 2 : 64;
   const double bh = (double)p->bh, unit = p->f32 ? 2.0 : 1.0;
   auto rounds = [&](double groups, double each, double fixed) {
     const double full = std::floor(groups / 512), rest = groups - 512 * full;
