@@ -338,8 +338,9 @@ prism_status prism_qk_norm_backward(const prism_qk_norm_desc* desc, const void* 
  * three bf16 pieces, so that f32 results keep f32 accuracy.
  *
  *   B, H, Hk   sequences (>= 0), query heads, key / value heads (H % Hk = 0)
- *   T          tokens of each sequence (>= 0); packed: the longest length
- *   dk, dv     head dimensions, multiples of 16, 16 .. 128
+ *   T          tokens of each sequence (0 .. 2^30); packed: the longest length
+ *   dk, dv     head dimensions, multiples of 16, 16 .. 128; H * dk, H * dv at
+ *              most 2^22
  *   scale      finite
  *   packed_tokens  with cu_seqlens: rows N of the token tensors (the packed
  *              batches of prism_forward, sanitised the same way)
@@ -374,7 +375,7 @@ prism_status prism_linear_attention(const prism_linear_attention_desc* desc, con
 /* Gradients of <dO, o> + <dST, ST> from the forward's inputs.  dST may be
  * NULL (zeros).  dq [B,T,H,dk], dk [B,T,Hk,dk], dv [B,T,Hk,dv] dt,
  * contiguous; dg f32 (NULL: not wanted; zero where g < -104, whose decay is
- * zero), dS0 f32 (NULL: not wanted).  Written, not accumulated; packed rows
+ * zero), dS0 f32 (NULL: not wanted; not the buffer of dST or S0).  Written, not accumulated; packed rows
  * outside every (clamped) sequence are unspecified. */
 prism_status prism_linear_attention_backward(const prism_linear_attention_desc* desc,
                                              const void* q, const void* k, const void* v,

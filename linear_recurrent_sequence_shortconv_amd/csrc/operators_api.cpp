@@ -181,6 +181,11 @@ prism_status check_la(const prism_linear_attention_desc* desc, bool packed, LaPl
       return fail(PRISM_ERR_UNSUPPORTED, "dk and dv must be multiples of 16 from 16 to 128 (got " + num(d.dk) + ", " +
                                              num(d.dv) + ")");
   if (!std::isfinite(d.scale)) return fail(PRISM_ERR_SHAPE, "scale must be finite");
+  // (32-bit token arithmetic with room for a segment; 32-bit offsets in a chunk
+  // of the contiguous gradients)
+  if (d.T > (1 << 30)) return fail(PRISM_ERR_SHAPE, "T must be <= 1073741824 (got " + num(d.T) + ")");
+  if ((long long)d.H * (d.dk > d.dv ? d.dk : d.dv) > (1LL << 22))
+    return fail(PRISM_ERR_SHAPE, "H * dk and H * dv must be <= 4194304");
   if (packed && d.packed_tokens < 0) return fail(PRISM_ERR_SHAPE, "packed_tokens must be >= 0 with cu_seqlens");
   const int unit = d.dtype == PRISM_F32 ? 4 : 8;
   const struct {
@@ -361,7 +366,9 @@ prism_status la_forward(const prism_linear_attention_desc& d, const LaPlan& p, c
   a.nroles = 1;
   if (p.nseg > 1)
     HIP_TRY("la_states", s, prism::launch_la_pass<E>(a, p.dim, ST ? prism::LA_STATES_FP32 : prism::LA_STATES, s));
-  if (p.nseg > LA_SELF_JOIN) {
+  // (a state updated in place is written while other segments still start from
+  // it, so they then start from the joined copies)
+  if (p.nseg > LA_SELF_JOIN || (p.nseg > 1 && ST && ST == S0)) {
     prism::LaJoin j = {};
     j.B = d.B;
     j.T = d.T;
@@ -612,6 +619,8 @@ prism_status prism_linear_attention_backward(const prism_linear_attention_desc* 
     CHECK_PTR(dv, some);
     if (reinterpret_cast<uintptr_t>(dg) & 3u) return fail(PRISM_ERR_ALIGN, "dg is not 4-byte aligned");
     CHECK_PTR(dS0, false);
+    if (dS0 && (dS0 == dST || dS0 == S0))
+      return fail(PRISM_ERR_UNSUPPORTED, "dS0 must not be the buffer of dST or S0");
     if (desc->B == 0 && !dg) return PRISM_OK;
     plan_backward(*desc, dg != 0, &p);
     Carve cv;

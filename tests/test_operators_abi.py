@@ -99,7 +99,8 @@ def _la(D, ws=FAKE, nbytes=1 << 40, **kw):
 
 def _la_bwd(D, ws=FAKE, nbytes=1 << 40, **kw):
     names = ("q", "k", "v", "g", "S0", "cu_seqlens", "dO", "dST", "dq", "dk", "dv", "dg", "dS0")
-    p = [kw.get(n, None if n == "cu_seqlens" else FAKE) for n in names]
+    own = {"cu_seqlens": None, "dS0": ctypes.c_void_p(0x30000)}
+    p = [kw.get(n, own.get(n, FAKE)) for n in names]
     return P.lib().prism_linear_attention_backward(ctypes.byref(D), *p, ws, nbytes, None)
 
 
@@ -111,7 +112,7 @@ def _la_step(D, **kw):
 @no_gpu
 @pytest.mark.parametrize("field,value,code", [
     ("B", -1, E_SHAPE), ("T", -1, E_SHAPE), ("H", 0, E_SHAPE), ("Hk", 0, E_SHAPE), ("Hk", 3, E_SHAPE),
-    ("dk", 8, E_UNSUP), ("dk", 144, E_UNSUP), ("dv", 40, E_UNSUP), ("dtype", 3, E_UNSUP),
+    ("T", (1 << 30) + 1, E_SHAPE), ("H", 1 << 17, E_SHAPE), ("dk", 8, E_UNSUP), ("dk", 144, E_UNSUP), ("dv", 40, E_UNSUP), ("dtype", 3, E_UNSUP),
     ("scale", float("inf"), E_SHAPE), ("scale", float("nan"), E_SHAPE), ("B", 1 << 23, E_SHAPE),
     ("sq", _st(25600, 252, 64), E_ALIGN), ("sv", _st(-8, 256, 64), E_SHAPE), ("so", _st(25600, 256, 12), E_ALIGN),
     ("sk", _st(0, (1 << 22) + 8, 0), E_SHAPE), ("sg", _st(-1, 4, 1), E_SHAPE)])
@@ -135,6 +136,9 @@ def test_linear_attention_pointers_and_workspace():
     for n in ("q", "S0", "o", "ST"):
         assert _la(la(), **{n: ctypes.c_void_p(0x10008)}) == E_ALIGN and n in _err()
     assert _la(la(), g=ctypes.c_void_p(0x10002)) == E_ALIGN
+    other = ctypes.c_void_p(0x20000)   # (dS0 may not share a buffer with dST or S0)
+    for n in ("dST", "S0"):
+        assert _la_bwd(la(), **{"dST": other, "S0": other, "dS0": FAKE, n: FAKE}) == E_UNSUP and "dS0" in _err()
     assert _la_bwd(la(), dg=ctypes.c_void_p(0x10002)) == E_ALIGN
     assert _la(la(), cu_seqlens=ctypes.c_void_p(0x10002)) == E_ALIGN
     assert _la(la(packed_tokens=-1), cu_seqlens=FAKE) == E_SHAPE and "packed_tokens" in _err()
