@@ -20,9 +20,12 @@
 // product leaves in accumulators is the next product's operand in the same
 // lanes, so neither X nor the scores pass through LDS.  An accumulator
 // tile holds rows 4 g + r (g = lane / 16) of one column, a k-contiguous operand
-// 8 consecutive k (bf16) of one row at 8 g; the 32 rows of two tiles are
+// 8 consecutive k (bf16) of one row at 8 g; the 32 state rows of two tiles are
 // therefore assigned to them as 8 g + r and 8 g + 4 + r (the row order of a
-// product's left operand is free).  Each wave forms the scores for itself.
+// product's left operand is free), while tokens, which both operands of their
+// products read transposed, are contracted in the accumulators' order (in the
+// other one the scores' reads of B met in LDS banks: 4 of 10 cycles).  Each
+// wave forms the scores for itself.
 // The staged tiles are double buffered: one barrier a chunk.  The decays are
 // summed for 256 tokens at a time, one token a thread.
 //
@@ -94,8 +97,10 @@ struct LaTile {
   }
 };
 
-// 16-byte operands: KV values of one row at KV (lane / 16), so one instruction
-// (bf16) or four (fp32) contract KG values.
+// 16-byte operands: KV values of one row in each lane, so one instruction (bf16)
+// or four (fp32) contract KG values.  A group of KG tokens is contracted in the
+// order of the accumulators: lane group g has tokens 16 u + 4 g + r (u-th tile).
+// A group of KG state rows in the order of a k-contiguous operand: 8 g + j.
 template <typename E> struct La16;
 template <> struct La16<bf16> {
   static constexpr int KV = 8, KG = 32, UPG = 2;
@@ -103,16 +108,16 @@ template <> struct La16<bf16> {
   __device__ static inline f32x4 mma(const frag& a, const frag& b, const f32x4& c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
-  // row of an accumulator tile (u-th of its group) -> index in the group
-  __device__ static inline int row(int u, int p) { return 8 * (p >> 2) + 4 * u + (p & 3); }
-  // first of the four indexes that lane group g holds of tile u
+  // first of the four state rows that lane group g holds of a group's tile u
   __device__ static inline int first(int u, int g) { return 8 * g + 4 * u; }
-  // (index row(u, lane & 15), k at k0 + 8 g) of a tile stored [k][index]
-  __device__ static inline frag trans(const bf16* p, int ld, int i0, int u, int k0, int lane, bool mapped) {
+  // Column i0 + (lane & 15) of a tile stored [token][column], at the group's
+  // tokens from k0 on; STATE: column i0 + the state row of (lane & 15) in tile u.
+  template <bool STATE>
+  __device__ static inline frag trans(const bf16* p, int ld, int i0, int u, int k0, int lane) {
     const int j = lane & 15;
-    const bf16* a = p + (k0 + 8 * (lane >> 4) + (j >> 2)) * ld + i0 + (mapped ? 8 * (j & 3) + 4 * u : 4 * (j & 3));
+    const bf16* a = p + (k0 + 4 * (lane >> 4) + (j >> 2)) * ld + i0 + (STATE ? 8 * (j & 3) + 4 * u : 4 * (j & 3));
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(a));
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(a + 4 * ld));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(a + 16 * ld));
     const short __attribute__((ext_vector_type(8))) w = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     frag f;
     __builtin_memcpy(&f, &w, 16);
@@ -127,9 +132,9 @@ template <> struct La16<float> {
     for (int r = 0; r < 4; ++r) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], b[r], c, 0, 0, 0);
     return c;
   }
-  __device__ static inline int row(int, int p) { return p; }
   __device__ static inline int first(int, int g) { return 4 * g; }
-  __device__ static inline frag trans(const float* p, int ld, int i0, int, int k0, int lane, bool) {
+  template <bool STATE>
+  __device__ static inline frag trans(const float* p, int ld, int i0, int, int k0, int lane) {
     const float* a = p + (k0 + 4 * (lane >> 4)) * ld + i0 + (lane & 15);
     return frag{a[0], a[ld], a[2 * ld], a[3 * ld]};
   }
@@ -354,7 +359,7 @@ __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args)
   }
   // masked scores: bits kept of each value of p[i][j] (its i against its t)
   auto keep = [&](int i, int j, int r) {
-    const int ii = KG * (i / UPG) + M::first(i % UPG, gq) + r, t = 16 * j + l16;
+    const int ii = 16 * i + 4 * gq + r, t = 16 * j + l16;
     return rev ? ii >= t : ii <= t;
   };
 
@@ -501,7 +506,7 @@ __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           fb[k][i] =
-              *reinterpret_cast<const frag*>(sb + (KG * (i / UPG) + M::row(i % UPG, l16)) * LA + KV * gq + KG * k);
+              *reinterpret_cast<const frag*>(sb + (16 * i + l16) * LA + KV * gq + KG * k);
       }
       if (HALF) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -532,7 +537,7 @@ __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args)
         fin[1] = ra[16 + l16];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const f32x4 f = *reinterpret_cast<const f32x4*>(rt + KG * (i / UPG) + M::first(i % UPG, gq));
+          const f32x4 f = *reinterpret_cast<const f32x4*>(rt + 16 * i + 4 * gq);
 #pragma unroll
           for (int j = 0; j < 2; ++j) p[i][j] *= f;
         }
@@ -545,7 +550,7 @@ __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args)
           for (int c = 0; c < NCT; ++c) acc[c][j] *= f;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int i0 = KG * (i / UPG) + M::first(i % UPG, gq);
+            const int i0 = 16 * i + 4 * gq;
             const f32x4 vh = *reinterpret_cast<const f32x4*>(uh + i0), vl = *reinterpret_cast<const f32x4*>(ul + i0);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
@@ -570,7 +575,7 @@ __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args)
       for (int q = 0; q < TG; ++q)
 #pragma unroll
         for (int c = 0; c < NCT; ++c) {
-          const frag fc = M::trans(sc, LC, cw + 16 * c, 0, KG * q, lane, false);
+          const frag fc = M::template trans<false>(sc, LC, cw + 16 * c, 0, KG * q, lane);
 #pragma unroll
           for (int s = 0; s < NSX; ++s)
 #pragma unroll
@@ -588,13 +593,13 @@ __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args)
     for (int q = 0; q < TG; ++q) {
       frag raw[NCT], fc[NCT][NSU], fb[HALF ? AT : 1];
 #pragma unroll
-      for (int c = 0; c < NCT; ++c) raw[c] = M::trans(sc, LC, cw + 16 * c, 0, KG * q, lane, false);
+      for (int c = 0; c < NCT; ++c) raw[c] = M::template trans<false>(sc, LC, cw + 16 * c, 0, KG * q, lane);
       f32x4 f[KV / 4];
 #pragma unroll
-      for (int v = 0; v < KV / 4; ++v) f[v] = *reinterpret_cast<const f32x4*>(rt + KG * q + KV * gq + 4 * v);
+      for (int v = 0; v < KV / 4; ++v) f[v] = *reinterpret_cast<const f32x4*>(rt + KG * q + 16 * v + 4 * gq);
       if (HALF) {
 #pragma unroll
-        for (int i = 0; i < AT; ++i) fb[HALF ? i : 0] = M::trans(sb, LA, KG * (i / UPG), i % UPG, KG * q, lane, true);
+        for (int i = 0; i < AT; ++i) fb[HALF ? i : 0] = M::template trans<true>(sb, LA, KG * (i / UPG), i % UPG, KG * q, lane);
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
@@ -606,7 +611,7 @@ __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args)
       }
 #pragma unroll
       for (int i = 0; i < AT; ++i) {
-        if (!HALF) fb[0] = M::trans(sb, LA, 16 * i, 0, KG * q, lane, true);
+        if (!HALF) fb[0] = M::template trans<true>(sb, LA, 16 * i, 0, KG * q, lane);
 #pragma unroll
         for (int s = 0; s < NSU; ++s)
 #pragma unroll
