@@ -337,7 +337,8 @@ prism_status prism_qk_norm_backward(const prism_qk_norm_desc* desc, const void* 
  * (and, for the gradient of g, every product) takes its scaled operand in
  * three bf16 pieces, so that f32 results keep f32 accuracy.
  *
- *   B, H, Hk   sequences (>= 0), query heads, key / value heads (H % Hk = 0)
+ *   B, H, Hk   sequences (>= 0), query heads, key / value heads (H % Hk = 0);
+ *              B * H < 2^21
  *   T          tokens of each sequence (0 .. 2^30); packed: the longest length
  *   dk, dv     head dimensions, multiples of 16, 16 .. 128; H * dk, H * dv at
  *              most 2^22
@@ -347,7 +348,8 @@ prism_status prism_qk_norm_backward(const prism_qk_norm_desc* desc, const void* 
  *   q, k, v, o strides of q, k, v and of o / dO: multiples of 16 bytes, >= 0,
  *              a token step of at most 2^22 elements.  (packed: batch ignored)
  *   g          strides of g and dg in floats (>= 0); one decay for each head:
- *              batch = token = 0 (then dg is summed over batch and tokens)  */
+ *              batch = token = 0 (then dg is summed over batch and tokens;
+ *              other zero steps that repeat a value are refused with dg)  */
 typedef struct {
   int B, T, H, Hk, dk, dv;
   prism_dtype dtype;
@@ -375,8 +377,9 @@ prism_status prism_linear_attention(const prism_linear_attention_desc* desc, con
 /* Gradients of <dO, o> + <dST, ST> from the forward's inputs.  dST may be
  * NULL (zeros).  dq [B,T,H,dk], dk [B,T,Hk,dk], dv [B,T,Hk,dv] dt,
  * contiguous; dg f32 (NULL: not wanted; zero where g < -104, whose decay is
- * zero), dS0 f32 (NULL: not wanted; not the buffer of dST or S0).  Written, not accumulated; packed rows
- * outside every (clamped) sequence are unspecified. */
+ * zero), dS0 f32 (NULL: not wanted; not the buffer of dST or S0).  Written,
+ * not accumulated; packed rows outside every (clamped) sequence are
+ * unspecified. */
 prism_status prism_linear_attention_backward(const prism_linear_attention_desc* desc,
                                              const void* q, const void* k, const void* v,
                                              const float* g, const float* S0,

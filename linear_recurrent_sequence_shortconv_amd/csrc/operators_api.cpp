@@ -211,7 +211,8 @@ prism_status check_la(const prism_linear_attention_desc* desc, bool packed, LaPl
   p.DD = (size_t)d.dk * d.dv;
   p.nseg = 1;
   p.seglen = 0;
-  if ((double)p.bh * p.DD * 4 > 1.0e12 || (double)p.rows * d.H * p.dim > 4.0e12 || p.bh > (size_t(1) << 24))
+  // (a launch has at most 8 workgroups of 256 threads for each head: under 2^32 threads)
+  if ((double)p.bh * p.DD * 4 > 1.0e12 || (double)p.rows * d.H * p.dim > 4.0e12 || p.bh >= (size_t(1) << 21))
     return fail(PRISM_ERR_SHAPE, "problem too large");
   *out = p;
   return PRISM_OK;
@@ -619,6 +620,15 @@ prism_status prism_linear_attention_backward(const prism_linear_attention_desc* 
     CHECK_PTR(dv, some);
     if (reinterpret_cast<uintptr_t>(dg) & 3u) return fail(PRISM_ERR_ALIGN, "dg is not 4-byte aligned");
     CHECK_PTR(dS0, false);
+    if (dg && some) {
+      // dg has g's strides: a value of g that serves several tokens or heads
+      // would be written by each of them (one a head is summed)
+      const prism_strides& x = desc->g;
+      const bool head = x.batch == 0 && x.token == 0;
+      if ((x.head == 0 && desc->H > 1) || (!head && x.token == 0 && desc->T > 1) ||
+          (!head && !cu_seqlens && x.batch == 0 && desc->B > 1) || (!head && cu_seqlens && x.token == 0))
+        return fail(PRISM_ERR_UNSUPPORTED, "dg needs a g for each token and head, or one for each head");
+    }
     if (dS0 && (dS0 == dST || dS0 == S0))
       return fail(PRISM_ERR_UNSUPPORTED, "dS0 must not be the buffer of dST or S0");
     if (desc->B == 0 && !dg) return PRISM_OK;

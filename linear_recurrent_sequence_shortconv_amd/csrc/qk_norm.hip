@@ -10,8 +10,14 @@
 // of G lanes; a lane owns P = d / (2 V G) <= 1 pair of 16-byte (8-byte) vectors
 // that hold both members of V rotation pairs, so turning needs no exchange
 // between lanes and the row sums are DPP sums over the group.  The groups of a
-// team (a wave, or the whole workgroup when there are few tokens) share one
-// token: its V angles are formed once in each lane and used for all its heads.
+// team, at most a wave, share one token: its V angles are formed once in each
+// lane and used for all its heads.  (A workgroup a token took 83 us in place of
+// 48 for 8 x 2048 tokens of 16 + 16 heads, and nothing less for 64 tokens.)
+//
+// Measured, bf16, d = 128: forward, 8 x 2048 tokens of 16 + 16 heads, 268 MB,
+// 48 us, 5.6 TB/s (a copy of this size runs at 5.3 TB/s); backward with weights,
+// 16384 tokens of 16 + 4 heads, 252 MB, 50 us, 5.0 TB/s.  One token for each of
+// 64 sequences: 5 us, the launch and one memory latency.
 #include "operators.h"
 #include "prism_common.h"
 
@@ -176,7 +182,7 @@ __device__ inline void load_w(const void* w, const LanePlace& q, float (&wa)[V],
   }
 }
 
-// G lanes a row, tg groups a token (both powers of two, G * tg <= 256).
+// G lanes a row, tg groups a token (both powers of two, G * tg <= 64).
 template <typename E, int V, bool IL>
 __global__ __launch_bounds__(QN_NT) void qk_norm_kernel(const QkNormArgs g, int G, int tg) {
   typedef VecIo<E, V> IO;
@@ -368,29 +374,26 @@ int pow2_at_least(int n) {
   return p;
 }
 
-// Vectors of 8 bf16 where every row offset is a multiple of 16 bytes, else of 4.
-template <typename E>
-bool wide(const QkNormArgs& a, bool bwd) {
-  if (sizeof(E) != 2 || a.d % 16 || a.rot % 16) return false;
+// The forward pass takes vectors of 8 bf16 where every row offset is a multiple
+// of 16 bytes, else of 4 (8 x 2048 tokens, 16 + 16 heads of 128: 48 us with 8,
+// 56 with 4).  The backward pass always takes 4, for its registers (the same
+// shape: 82 us with 4, 85 with 8).
+bool wide(const QkNormArgs& a) {
+  if (a.d % 16 || a.rot % 16) return false;
   long m = a.sxq.b | a.sxq.t | a.sxq.h | a.syq.b | a.syq.t | a.syq.h;
   if (a.Hk) m |= a.sxk.b | a.sxk.t | a.sxk.h | a.syk.b | a.syk.t | a.syk.h;
-  if (bwd) m |= a.sgq.b | a.sgq.t | a.sgq.h;
-  if (bwd && a.Hk) m |= a.sgk.b | a.sgk.t | a.sgk.h;
   return m % 8 == 0;
 }
 
-// Groups a token: a wave where the tokens fill the chip with a wave each,
-// else the whole workgroup; never more than there are heads.
-int team_groups(const QkNormArgs& a, int G, int H) {
-  const long N = (long)a.B * a.T;
-  const int most = (N >= 4096 ? WAVE : QN_NT) / G;
-  const int need = pow2_at_least(H);
+// Groups a token: a wave's, never more than there are heads.
+int team_groups(int G, int H) {
+  const int most = WAVE / G, need = pow2_at_least(H);
   return most < need ? most : need;
 }
 
 template <typename E, int V>
 hipError_t run_fwd(const QkNormArgs& a, hipStream_t s) {
-  const int G = pow2_at_least(a.d / (2 * V)), tg = team_groups(a, G, a.Hq + a.Hk), teams = QN_NT / (G * tg);
+  const int G = pow2_at_least(a.d / (2 * V)), tg = team_groups(G, a.Hq + a.Hk), teams = QN_NT / (G * tg);
   const long N = (long)a.B * a.T;
   long grid = (N + teams - 1) / teams;
   if (grid > (1 << 20)) grid = 1 << 20;
@@ -401,8 +404,9 @@ hipError_t run_fwd(const QkNormArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename E, int V, bool IL>
+template <typename E, bool IL>
 hipError_t run_bwd(const QkNormArgs& a, hipStream_t s) {
+  constexpr int V = 4;
   const int G = pow2_at_least(a.d / (2 * V));
   const long N = (long)a.B * a.T;
   const bool dw = a.dwq || a.dwk;
@@ -415,7 +419,7 @@ hipError_t run_bwd(const QkNormArgs& a, hipStream_t s) {
     const long want = (N + teams - 1) / teams, room = most * H / (a.Hq + a.Hk);
     return want < room ? want : (room > 1 ? room : 1);
   };
-  const int tgq = team_groups(a, G, a.Hq), tgk = a.Hk ? team_groups(a, G, a.Hk) : 1;
+  const int tgq = team_groups(G, a.Hq), tgk = a.Hk ? team_groups(G, a.Hk) : 1;
   const long nq = blocks(a.Hq, tgq), nk = blocks(a.Hk, tgk);
   if (N > 0) {
     const dim3 grid((unsigned)(nq + nk));
@@ -442,16 +446,13 @@ size_t qk_norm_part_bytes(int d) { return (size_t)(QN_PARTS + 1) * d * sizeof(fl
 template <typename E>
 hipError_t launch_qk_norm(const QkNormArgs& a, hipStream_t s) {
   if constexpr (sizeof(E) == 2) {
-    if (wide<E>(a, false)) return run_fwd<E, 8>(a, s);
+    if (wide(a)) return run_fwd<E, 8>(a, s);
   }
   return run_fwd<E, 4>(a, s);
 }
 template <typename E>
 hipError_t launch_qk_norm_bwd(const QkNormArgs& a, hipStream_t s) {
-  if constexpr (sizeof(E) == 2) {
-    if (wide<E>(a, true)) return a.interleaved ? run_bwd<E, 8, true>(a, s) : run_bwd<E, 8, false>(a, s);
-  }
-  return a.interleaved ? run_bwd<E, 4, true>(a, s) : run_bwd<E, 4, false>(a, s);
+  return a.interleaved ? run_bwd<E, true>(a, s) : run_bwd<E, false>(a, s);
 }
 template hipError_t launch_qk_norm<bf16>(const QkNormArgs&, hipStream_t);
 template hipError_t launch_qk_norm<float>(const QkNormArgs&, hipStream_t);

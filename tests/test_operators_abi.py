@@ -220,3 +220,22 @@ def test_turns():
     assert t.tolist() == [-(1 << 62), 1 << 62]     # three quarters of a turn: minus one quarter
     with pytest.raises(ValueError):
         P.rope_turns(8, inv_freq=[1.0], device="cpu")
+
+
+@no_gpu
+def test_decay_gradient_of_a_repeated_decay():
+    # a value of g that serves several tokens, heads or sequences has no place of its own in dg
+    for sg in (_st(0, 4, 1), _st(400, 0, 1), _st(400, 4, 0), _st(0, 0, 0)):
+        assert _la_bwd(la(sg=sg)) == E_UNSUP and "dg" in _err(), sg
+        # without dg the call is fine so far: it stops at the workspace
+        assert _la_bwd(la(sg=sg), dg=None, ws=None) != E_UNSUP, sg
+    # one sequence, one token, one head repeat nothing
+    for kw in (dict(B=1, sg=_st(0, 4, 1)), dict(T=1, sg=_st(4, 0, 1))):
+        assert _la_bwd(la(**kw), ws=None) != E_UNSUP, kw
+
+
+@no_gpu
+def test_heads_in_flight():
+    # 2^21 heads of all sequences would pass a launch's threads
+    D = la(B=1 << 19, H=4, Hk=4, dk=16, dv=16, T=1)
+    assert _la_step(D) == E_SHAPE and _la(D) == E_SHAPE
