@@ -571,6 +571,10 @@ def qk_norm(q, k=None, wq=None, wk=None, positions=None, turns=None, norm="l2", 
     return q_out, k_out
 
 
+# workspace bytes of the backward pass by descriptor
+_qk_bytes = {}
+
+
 def qk_norm_backward(q, k, dq_out, dk_out, wq=None, wk=None, positions=None, turns=None,
                      norm="l2", eps=1e-6, interleaved=False, dq=None, dk=None, workspace=None):
     """Gradients of <dq_out, q_out> + <dk_out, k_out> of qk_norm on the same
@@ -594,9 +598,14 @@ def qk_norm_backward(q, k, dq_out, dk_out, wq=None, wk=None, positions=None, tur
             out[name] = w.new_empty(w.shape, dtype=torch.float32)
     packed = _QK_DESC.pack(*desc, *steps)
     if workspace is None and (wq is not None or wk is not None):
-        n = ctypes.c_size_t(0)
-        _check(lib().prism_qk_norm_backward_workspace(packed, 1, ctypes.byref(n)))
-        workspace = _workspace(n.value, q.device)[1]
+        size = _qk_bytes.get(packed)
+        if size is None:
+            n = ctypes.c_size_t(0)
+            _check(lib().prism_qk_norm_backward_workspace(packed, 1, ctypes.byref(n)))
+            if len(_qk_bytes) >= 4096:
+                _qk_bytes.clear()
+            size = _qk_bytes[packed] = n.value
+        workspace = _workspace(size, q.device)[1]
     _check(lib().prism_qk_norm_backward(
         packed, _addr(q), _addr(k), _addr(wq), _addr(wk), _addr(positions), _addr(turns),
         _addr(dq_out), _addr(dk_out), _addr(out["dq"]), _addr(out.get("dk")),
