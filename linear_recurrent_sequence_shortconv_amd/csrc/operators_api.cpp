@@ -221,8 +221,11 @@ prism_status check_la(const prism_linear_attention_desc* desc, bool packed, LaPl
 // Up to this many segments a workgroup forms its entering state from the own
 // states of the segments before it; more are joined by a kernel of its own.
 // 8 x 2048 tokens, 16 heads, forward: by itself 129, 121 and 151 us with 2, 4
-// and 6 segments, joined 136, 124 and 144.
-constexpr int LA_SELF_JOIN = 4;
+// and 6 segments, joined 136, 124 and 144.  The decays' gradient uses each of these
+// states in three launches: the same tokens, by itself 358, 446 and 406 us with 2,
+// 3 and 4, joined 367, 422 and 392; 2 x 333 tokens, 3 heads in fp32 71, 58 and
+// 52, joined 71, 55 and 47.
+constexpr int LA_SELF_JOIN = 4, LA_SELF_JOIN_DG = 2;
 
 // Segments a sequence is cut into.  A launch runs B H workgroups for each of
 // its passes and each segment, 512 of them at once (two a CU); more than one
@@ -442,7 +445,7 @@ prism_status la_backward(const prism_linear_attention_desc& d, const LaPlan& p, 
     HIP_TRY("la_states", s,
             prism::launch_la_pass<E>(b, p.dim, dg || dS0 ? prism::LA_STATES_FP32 : prism::LA_STATES, s));
   }
-  if (p.nseg > LA_SELF_JOIN && d.B > 0) {
+  if (p.nseg > (dg ? LA_SELF_JOIN_DG : LA_SELF_JOIN) && d.B > 0) {
     prism::LaJoin j = {};
     j.B = d.B;
     j.T = d.T;
