@@ -162,6 +162,7 @@ prism_status qk_backward(const prism_qk_norm_desc* desc, const void* q, const vo
 struct LaPlan {
   int dim, grp, nseg, seglen;
   bool f32;
+  bool one;        // dv in the launch of dq and dk that also gives the row dots
   long rows;       // token rows of the tensors
   size_t bh, DD;
 };
@@ -211,6 +212,7 @@ prism_status check_la(const prism_linear_attention_desc* desc, bool packed, LaPl
   p.DD = (size_t)d.dk * d.dv;
   p.nseg = 1;
   p.seglen = 0;
+  p.one = false;
   // (a launch has at most 8 workgroups of 256 threads for each head: under 2^32 threads)
   if ((double)p.bh * p.DD * 4 > 1.0e12 || (double)p.rows * d.H * p.dim > 4.0e12 || p.bh >= (size_t(1) << 21))
     return fail(PRISM_ERR_SHAPE, "problem too large");
@@ -267,6 +269,11 @@ void plan_segments(const prism_linear_attention_desc& d, LaWork work, LaPlan* p)
   const long per = chunks > 0 ? (chunks + best - 1) / best : 1;
   p->seglen = (int)(per * prism::LA_CHUNK);
   p->nseg = (int)(chunks > 0 ? (chunks + per - 1) / per : 1);
+  // (dv takes 1.3 times as long in the kernel with the row dots as in its own, but
+  // where all workgroups run at once it costs no launch after the other two:
+  // 8 x 128 tokens, 16 heads, 384 workgroups, 32 us in place of 39, 2 x 333 in fp32,
+  // 72, 33 in place of 48; 2 x 4096 tokens, 16 heads, 227 in place of 196)
+  p->one = p->bh * p->nseg * 3 <= 512;
 }
 
 void plan_forward(const prism_linear_attention_desc& d, LaPlan* p) { plan_segments(d, LA_FORWARD, p); }
@@ -476,11 +483,14 @@ prism_status la_backward(const prism_linear_attention_desc& d, const LaPlan& p, 
     rk.edot = w.ek;
     a.r[0] = rq;
     a.r[1] = rk;
-    a.nroles = 2;
+    a.r[2] = rv;
+    a.nroles = p.one ? 3 : 2;
     HIP_TRY("la_bwd_qk", s, prism::launch_la_pass<E>(a, p.dim, prism::LA_OUT_DOTS, s));
-    a.r[0] = rv;
-    a.nroles = 1;
-    HIP_TRY("la_bwd_v", s, prism::launch_la_pass<E>(a, p.dim, prism::LA_OUT, s));
+    if (!p.one) {
+      a.r[0] = rv;
+      a.nroles = 1;
+      HIP_TRY("la_bwd_v", s, prism::launch_la_pass<E>(a, p.dim, prism::LA_OUT, s));
+    }
   } else if (d.B > 0) {
     a.r[0] = rq;
     a.r[1] = rk;
