@@ -242,13 +242,14 @@ constexpr int LA_SELF_JOIN = 4, LA_SELF_JOIN_DG = 2;
 // tokens with 1, 4, 8, 16 and 32: 1089, 441, 228, 131 and 114 (32 taken); a
 // backward pass of 2 x 4096 tokens, 16 heads on 4, with 1, 2, 4, 5 and 8: 305,
 // 253, 183, 170 and 169 (5 taken).
+constexpr int LA_AT_ONCE = 512;   // workgroups
 enum LaWork { LA_FORWARD, LA_BACKWARD, LA_BACKWARD_DG };
 void plan_segments(const prism_linear_attention_desc& d, LaWork work, LaPlan* p) {
   const long chunks = ((long)d.T + prism::LA_CHUNK - 1) / prism::LA_CHUNK;
   const long most = chunks / 2 < 64 ? chunks / 2 : 64;
   const double bh = (double)p->bh, unit = p->f32 ? 2.0 : 1.0;
   auto rounds = [&](double groups, double each, double fixed) {
-    const double full = std::floor(groups / 512), rest = groups - 512 * full;
+    const double full = std::floor(groups / LA_AT_ONCE), rest = groups - LA_AT_ONCE * full;
     each *= unit;
     return full * (each + fixed) + (rest == 0 ? 0.0 : rest <= 256 ? 0.6 * each + fixed : each + fixed);
   };
@@ -258,7 +259,8 @@ void plan_segments(const prism_linear_attention_desc& d, LaWork work, LaPlan* p)
     const double per = chunks > 0 ? (double)((chunks + n - 1) / n) : 1.0;
     double cost = work == LA_FORWARD    ? rounds(bh * n, per, 2.5)
                   : work == LA_BACKWARD ? rounds(bh * 3 * n, per, 2.5)
-                                        : rounds(bh * 2 * n, 1.6 * per, 2.5) + rounds(bh * n, per, 2.5);
+                  : bh * 3 * n <= LA_AT_ONCE ? rounds(bh * 3 * n, 1.6 * per, 2.5)
+                                             : rounds(bh * 2 * n, 1.6 * per, 2.5) + rounds(bh * n, per, 2.5);
     if (n > 1) cost += rounds(bh * (work == LA_FORWARD ? 1 : 2) * (n - 1), 0.5 * per, 2.0);
     if (n > LA_SELF_JOIN) cost += 2.0;
     if (n == 1 || cost < least) {
@@ -273,7 +275,7 @@ void plan_segments(const prism_linear_attention_desc& d, LaWork work, LaPlan* p)
   // where all workgroups run at once it costs no launch after the other two:
   // 8 x 128 tokens, 16 heads, 384 workgroups, 32 us in place of 39, 2 x 333 in fp32,
   // 72, 33 in place of 48; 2 x 4096 tokens, 16 heads, 227 in place of 196)
-  p->one = p->bh * p->nseg * 3 <= 512;
+  p->one = p->bh * p->nseg * 3 <= (size_t)LA_AT_ONCE;
 }
 
 void plan_forward(const prism_linear_attention_desc& d, LaPlan* p) { plan_segments(d, LA_FORWARD, p); }
