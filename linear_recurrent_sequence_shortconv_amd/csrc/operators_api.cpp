@@ -226,7 +226,7 @@ prism_status check_la(const prism_linear_attention_desc* desc, bool packed, LaPl
 // and 6 segments, joined 136, 124 and 144.  The decays' gradient uses each of these
 // states in three launches: the same tokens, by itself 358, 446 and 406 us with 2,
 // 3 and 4, joined 367, 422 and 392; 2 x 333 tokens, 3 heads in fp32 71, 58 and
-// 52, joined 71, 55 and 47.
+// 52, joined 71, 55 and 47 (dv in a launch of its own throughout).
 constexpr int LA_SELF_JOIN = 4, LA_SELF_JOIN_DG = 2;
 
 // Segments a sequence is cut into.  A launch runs B H workgroups for each of
@@ -234,8 +234,9 @@ constexpr int LA_SELF_JOIN = 4, LA_SELF_JOIN_DG = 2;
 // segment also needs the states at their starts, from `sources` further passes
 // of half the work over all but one segment.  Taken is the count with the
 // least cost in the time of one chunk on a full chip (4 us in bf16 at d = 128),
-// as measured there: a workgroup costs 2.5 chunks beside its own (2 where it
-// forms states alone), a round of at most one workgroup a CU goes by 0.6 of
+// as measured there: a workgroup costs 2.5 chunks beside its own (4 where it
+// forms states alone, with their join: 8 x 512 tokens, 16 heads 44 us in one segment,
+// 56 in the four that 2 would give), a round of at most one workgroup a CU goes by 0.6 of
 // the time for each chunk, fp32 takes twice and the decays' gradient 1.6 times
 // as long.  8 x 2048 tokens, 16 heads, forward, with 1, 2, 3, 4, 5 and 8
 // segments: 146, 130, 127, 122, 133 and 151 us (4 taken); one sequence of 16384
@@ -261,7 +262,7 @@ void plan_segments(const prism_linear_attention_desc& d, LaWork work, LaPlan* p)
                   : work == LA_BACKWARD ? rounds(bh * 3 * n, per, 2.5)
                   : bh * 3 * n <= LA_AT_ONCE ? rounds(bh * 3 * n, 1.6 * per, 2.5)
                                              : rounds(bh * 2 * n, 1.6 * per, 2.5) + rounds(bh * n, per, 2.5);
-    if (n > 1) cost += rounds(bh * (work == LA_FORWARD ? 1 : 2) * (n - 1), 0.5 * per, 2.0);
+    if (n > 1) cost += rounds(bh * (work == LA_FORWARD ? 1 : 2) * (n - 1), 0.5 * per, 4.0);
     if (n > LA_SELF_JOIN) cost += 2.0;
     if (n == 1 || cost < least) {
       best = n;
