@@ -179,7 +179,7 @@ __global__ __launch_bounds__(256) void la_decay_kernel(const LaDecay a) {
       const int t = t0 - r;
       if (t < 0) continue;
       const float d = g[r] < -104.f ? 0.f : (float)(before + x[r]);
-      if (a.tmp)
+      if (a.per_head)
         a.tmp[(long)bh * a.T + s0 + t] = d;
       else
         a.dg[(a.cu ? 0 : b * a.sg.b) + (row0 + t) * a.sg.t + h * a.sg.h] = d;
@@ -307,7 +307,7 @@ hipError_t launch_la_decay(const LaDecay& a, hipStream_t s) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (!a.tmp) return hipSuccess;
+  if (!a.per_head) return hipSuccess;
   hipLaunchKernelGGL(la_decay_head_kernel, dim3(a.H), dim3(256), 0, s, a);
   return hipGetLastError();
 }

@@ -128,8 +128,9 @@ struct LaDecay {
   const float *decf, *decr;        // entering (joined), or their own with their decays
   int joined;
   const float *S0, *ST, *dST;      // first, last state and the latter's gradient (nullptr: zero)
-  float* dg;                       // strided like g, or, for one decay a head,
-  float* tmp;                      // [B * H][T], then summed into dg [H]
+  int per_head;                    // dg is one sum a head (over no sequences: zero)
+  float* dg;                       // strided like g, or [H] (strided like its heads), summed from
+  float* tmp;                      // [B * H][T]
 };
 hipError_t launch_la_decay(const LaDecay& a, hipStream_t s);
 

@@ -524,7 +524,8 @@ prism_status la_backward(const prism_linear_attention_desc& d, const LaPlan& p, 
     x.ST = w.ST;
     x.dST = dST;
     x.dg = dg;
-    x.tmp = d.g.batch == 0 && d.g.token == 0 ? w.tmp : nullptr;
+    x.per_head = d.g.batch == 0 && d.g.token == 0;
+    x.tmp = w.tmp;
     HIP_TRY("la_decay", s, prism::launch_la_decay(x, s));
   }
   if (p.grp > 1)
