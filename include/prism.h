@@ -360,9 +360,14 @@ typedef struct {
 
 /* Workspace of the forward (backward = 0) or backward (1) pass, packed or
  * dense batch; with dg: of the backward pass that also gives dg.  The
- * workspace is 256-byte aligned, and may be NULL where 0 bytes are needed. */
+ * workspace is 256-byte aligned, and may be NULL where 0 bytes are needed.
+ * The first query serves both layouts, with room for the larger of B * T and
+ * packed_tokens rows; the second the calls with cu_seqlens alone, with room
+ * for packed_tokens rows (where lengths differ, far fewer than B * T). */
 prism_status prism_linear_attention_workspace(const prism_linear_attention_desc* desc,
                                               int backward, int dg, size_t* bytes);
+prism_status prism_linear_attention_packed_workspace(const prism_linear_attention_desc* desc,
+                                                     int backward, int dg, size_t* bytes);
 
 /* Whole sequences.  q [B,T,H,dk], k [B,T,Hk,dk], v [B,T,Hk,dv], o [B,T,H,dv]
  * dt, strided ([N,..] with cu_seqlens, B + 1 int32 offsets on the device);

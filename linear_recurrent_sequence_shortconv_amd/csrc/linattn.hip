@@ -130,8 +130,9 @@ __global__ __launch_bounds__(256) void la_decay_kernel(const LaDecay a) {
   __syncthreads();
   double carry = (sm[0] + sm[1]) + (sm[2] + sm[3]);
   const long row0 = first + s0;
-  const float* eq = a.eq + (long)bh * LA_PARTS * a.T + s0;
-  const float* ek = a.ek + (long)bh * LA_PARTS * a.T + s0;
+  const long at0 = (a.cu ? 0 : (long)b * a.T) + row0;   // the segment's first row of all rows
+  const float* eq = a.eq + (long)h * LA_PARTS * a.rows + at0;
+  const float* ek = a.ek + (long)h * LA_PARTS * a.rows + at0;
   const float* pg = a.g + ((a.cu ? 0 : b * a.sg.b) + row0 * a.sg.t + h * a.sg.h);
   // thread tid holds the U tokens hi - 1 - U tid - r, r = 0 .. U - 1, of a block
   // of 256 U (prefix sums over r, then over the threads)
@@ -145,8 +146,8 @@ __global__ __launch_bounds__(256) void la_decay_kernel(const LaDecay a) {
       const int t = max(t0 - r, 0);
 #pragma unroll
       for (int p = 0; p < LA_PARTS; ++p) {
-        q[r][p] = eq[(long)p * a.T + t];
-        k[r][p] = ek[(long)p * a.T + t];
+        q[r][p] = eq[p * a.rows + t];
+        k[r][p] = ek[p * a.rows + t];
       }
       g[r] = pg[(long)t * a.sg.t];
     }
@@ -180,7 +181,7 @@ __global__ __launch_bounds__(256) void la_decay_kernel(const LaDecay a) {
       if (t < 0) continue;
       const float d = g[r] < -104.f ? 0.f : (float)(before + x[r]);
       if (a.per_head)
-        a.tmp[(long)bh * a.T + s0 + t] = d;
+        a.tmp[(long)h * a.rows + at0 + t] = d;
       else
         a.dg[(a.cu ? 0 : b * a.sg.b) + (row0 + t) * a.sg.t + h * a.sg.h] = d;
     }
@@ -195,12 +196,14 @@ __global__ __launch_bounds__(256) void la_decay_head_kernel(const LaDecay a) {
   int m = a.cu ? min(max(a.cu[0], 0), a.N) : 0;   // (the clamped offsets, as la_sequence has them)
   for (int b = 0; b < a.B; ++b) {
     int n = a.T;
+    long first = (long)b * a.T;
     if (a.cu) {
       const int end = max(m, min(a.cu[b + 1], a.N));
+      first = m;
       n = min(end - m, a.T);
       m = end;
     }
-    const float* x = a.tmp + ((long)b * a.H + h) * a.T;
+    const float* x = a.tmp + (long)h * a.rows + first;
     for (int t = tid; t < n; t += 256) s += (double)x[t];
   }
   sm[tid] = s;

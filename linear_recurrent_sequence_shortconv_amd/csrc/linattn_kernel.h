@@ -363,7 +363,7 @@ __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args)
   const long ot = R.so.t, et = R.se.t;
   const long o0 = (args.cu ? 0 : b * R.so.b) + row0 * ot + h * R.so.h;
   const long e0 = (args.cu ? 0 : b * R.se.b) + row0 * et + (long)(h / R.ge) * R.se.h;
-  float* const pd = R.edot + ((long)bh * LA_NW + wave) * args.T + s0;
+  float* const pd = R.edot + ((long)h * LA_NW + wave) * args.rows + ((args.cu ? 0 : (long)b * args.T) + row0);
   // the lane's place in a chunk's output and e rows (elements)
   unsigned ol[2], el[2];
 #pragma unroll

@@ -70,7 +70,7 @@ struct LaRole {
   const E* e;              // rows dotted with out (fp32, before rounding), or nullptr
   Strides se;
   int ge;
-  float* edot;             // [B * H][LA_PARTS][T] partial dots
+  float* edot;             // [H][LA_PARTS][rows] partial dots
   int da, dc, rev;
   float s_in, s_row, s_upd;
   const float* X0;         // [B, H, dv, dk] entering state (nullptr: zeros)
@@ -89,6 +89,7 @@ struct LaArgs {
   int DD;                  // dv * dk
   const int* cu;           // offsets of a packed batch of N rows, or nullptr
   int N;
+  long rows;               // N, or B * T
   const float* g;
   Strides sg;
   LaRole<E> r[LA_ROLES];
@@ -121,16 +122,17 @@ struct LaDecay {
   int B, T, H, nseg, seglen, DD;
   const int* cu;
   int N;
+  long rows;                       // N, or B * T
   const float* g;
   Strides sg;
-  const float *eq, *ek;            // [B * H][LA_PARTS][T]
+  const float *eq, *ek;            // [H][LA_PARTS][rows]
   const float *segf, *segr;        // states of the segments, forward and reverse (nseg > 1):
   const float *decf, *decr;        // entering (joined), or their own with their decays
   int joined;
   const float *S0, *ST, *dST;      // first, last state and the latter's gradient (nullptr: zero)
   int per_head;                    // dg is one sum a head (over no sequences: zero)
   float* dg;                       // strided like g, or [H] (strided like its heads), summed from
-  float* tmp;                      // [B * H][T]
+  float* tmp;                      // [H][rows]
 };
 hipError_t launch_la_decay(const LaDecay& a, hipStream_t s);
 

@@ -314,10 +314,10 @@ LaBwdWs carve_la_bwd(const prism_linear_attention_desc& d, const LaPlan& p, bool
     w.dvp = cv.take<float>((size_t)p.rows * d.H * d.dv * 4);
   }
   if (dg) {
-    w.eq = cv.take<float>(p.bh * prism::LA_PARTS * d.T * 4);
-    w.ek = cv.take<float>(p.bh * prism::LA_PARTS * d.T * 4);
+    w.eq = cv.take<float>((size_t)p.rows * d.H * prism::LA_PARTS * 4);
+    w.ek = cv.take<float>((size_t)p.rows * d.H * prism::LA_PARTS * 4);
     w.ST = cv.take<float>(p.bh * p.DD * 4);
-    w.tmp = cv.take<float>(p.bh * d.T * 4);
+    w.tmp = cv.take<float>((size_t)p.rows * d.H * 4);
   }
   return w;
 }
@@ -338,6 +338,7 @@ prism::LaArgs<E> la_args(const prism_linear_attention_desc& d, const LaPlan& p, 
   a.DD = (int)p.DD;
   a.cu = cu;
   a.N = d.packed_tokens;
+  a.rows = p.rows;
   a.g = g;
   a.sg = strides(d.g);
   return a;
@@ -511,6 +512,7 @@ prism_status la_backward(const prism_linear_attention_desc& d, const LaPlan& p, 
     x.DD = (int)p.DD;
     x.cu = cu;
     x.N = d.packed_tokens;
+    x.rows = p.rows;
     x.g = g;
     x.sg = strides(d.g);
     x.eq = w.eq;
@@ -535,6 +537,27 @@ prism_status la_backward(const prism_linear_attention_desc& d, const LaPlan& p, 
 }
 
 bool has_tokens(const LaPlan& p) { return p.rows > 0; }
+
+// Workspace of calls with cu_seqlens (packed), or of either layout: as many
+// rows as the larger of the two has.
+prism_status la_workspace(const prism_linear_attention_desc* desc, bool packed, bool backward, bool dg, size_t* bytes) {
+  if (!bytes) return fail(PRISM_ERR_NULL, "bytes is NULL");
+  *bytes = 0;
+  LaPlan p;
+  const prism_status st = check_la(desc, packed, &p);
+  if (st != PRISM_OK) return st;
+  if (desc->packed_tokens > p.rows) p.rows = desc->packed_tokens;
+  Carve cv;
+  if (backward) {
+    plan_backward(*desc, dg, &p);
+    carve_la_bwd(*desc, p, dg, cv);
+  } else {
+    plan_forward(*desc, &p);
+    carve_la_fwd(*desc, p, cv);
+  }
+  *bytes = cv.off;
+  return PRISM_OK;
+}
 
 }  // namespace
 
@@ -568,25 +591,12 @@ prism_status prism_qk_norm_backward(const prism_qk_norm_desc* desc, const void* 
 
 prism_status prism_linear_attention_workspace(const prism_linear_attention_desc* desc, int backward, int dg,
                                               size_t* bytes) {
-  return prism::guarded([&] {
-    if (!bytes) return fail(PRISM_ERR_NULL, "bytes is NULL");
-    *bytes = 0;
-    LaPlan p;
-    const prism_status st = check_la(desc, false, &p);
-    if (st != PRISM_OK) return st;
-    // the query serves both layouts: as many rows as the larger has
-    if (desc->packed_tokens > p.rows) p.rows = desc->packed_tokens;
-    Carve cv;
-    if (backward) {
-      plan_backward(*desc, dg != 0, &p);
-      carve_la_bwd(*desc, p, dg != 0, cv);
-    } else {
-      plan_forward(*desc, &p);
-      carve_la_fwd(*desc, p, cv);
-    }
-    *bytes = cv.off;
-    return PRISM_OK;
-  });
+  return prism::guarded([&] { return la_workspace(desc, false, backward != 0, dg != 0, bytes); });
+}
+
+prism_status prism_linear_attention_packed_workspace(const prism_linear_attention_desc* desc, int backward, int dg,
+                                                     size_t* bytes) {
+  return prism::guarded([&] { return la_workspace(desc, true, backward != 0, dg != 0, bytes); });
 }
 
 prism_status prism_linear_attention(const prism_linear_attention_desc* desc, const void* q, const void* k,

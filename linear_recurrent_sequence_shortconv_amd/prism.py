@@ -26,7 +26,8 @@ EXPORTS = ("prism_forward_workspace", "prism_backward_workspace",
            "prism_step_workspace", "prism_step", "prism_step_noalloc", "prism_status_string", "prism_last_error", "prism_timing_begin",
            "prism_timing_end",
            "prism_qk_norm", "prism_qk_norm_backward_workspace", "prism_qk_norm_backward",
-           "prism_linear_attention_workspace", "prism_linear_attention",
+           "prism_linear_attention_workspace", "prism_linear_attention_packed_workspace",
+           "prism_linear_attention",
            "prism_linear_attention_backward", "prism_linear_attention_step")
 
 
@@ -102,12 +103,13 @@ def lib():
         L.prism_qk_norm.argtypes = [qd] + [_P] * 9
         L.prism_qk_norm_backward_workspace.argtypes = [qd, ctypes.c_int, ctypes.POINTER(size)]
         L.prism_qk_norm_backward.argtypes = [qd] + [_P] * 13 + [size, _P]
-        L.prism_linear_attention_workspace.argtypes = [ld, ctypes.c_int, ctypes.c_int,
-                                                       ctypes.POINTER(size)]
+        for query in (L.prism_linear_attention_workspace,
+                      L.prism_linear_attention_packed_workspace):
+            query.argtypes = [ld, ctypes.c_int, ctypes.c_int, ctypes.POINTER(size)]
         L.prism_linear_attention.argtypes = [ld] + [_P] * 9 + [size, _P]
         L.prism_linear_attention_backward.argtypes = [ld] + [_P] * 14 + [size, _P]
         L.prism_linear_attention_step.argtypes = [ld] + [_P] * 8
-        for f in EXPORTS[-7:]:
+        for f in EXPORTS[-8:]:
             getattr(L, f).restype = ctypes.c_int
         L.prism_status_string.argtypes = [ctypes.c_int]
         L.prism_status_string.restype = ctypes.c_char_p
@@ -656,16 +658,18 @@ def _la_desc(q, k, v, g, states, scale, cu_seqlens, max_seqlen):
             steps, (B, H, dv, dk), lead + (H, dv))
 
 
-# workspace bytes by descriptor, pass and wish
+# workspace bytes by descriptor, layout, pass and wish
 _la_bytes = {}
 
 
-def _la_workspace(packed, backward, dg, device):
-    key = (packed, backward, dg)
+def _la_workspace(desc, packed, backward, dg, device):
+    key = (desc, packed, backward, dg)
     size = _la_bytes.get(key)
     if size is None:
         n = ctypes.c_size_t(0)
-        _check(lib().prism_linear_attention_workspace(packed, backward, dg, ctypes.byref(n)))
+        query = (lib().prism_linear_attention_packed_workspace if packed
+                 else lib().prism_linear_attention_workspace)
+        _check(query(desc, backward, dg, ctypes.byref(n)))
         if len(_la_bytes) >= 4096:
             _la_bytes.clear()
         size = _la_bytes[key] = n.value
@@ -694,7 +698,7 @@ def linear_attention(q, k, v, g, S0=None, scale=1.0, cu_seqlens=None, max_seqlen
         ST = g.new_empty(state)
     packed = _LA_DESC.pack(*desc, *_steps(o, "o"), *gs)
     if workspace is None:
-        workspace = _la_workspace(packed, 0, 0, q.device)
+        workspace = _la_workspace(packed, cu_seqlens is not None, 0, 0, q.device)
     _check(lib().prism_linear_attention(
         packed, _addr(q), _addr(k), _addr(v), _addr(g), _addr(S0), _addr(cu_seqlens), _addr(o),
         _addr(ST), _addr(workspace), 0 if workspace is None else workspace.numel(),
@@ -719,7 +723,7 @@ def linear_attention_backward(q, k, v, g, dO, S0=None, dST=None, scale=1.0, need
     if need_dS0:
         out["dS0"] = g.new_empty(state)
     if workspace is None:
-        workspace = _la_workspace(packed, 1, int(need_dg), q.device)
+        workspace = _la_workspace(packed, cu_seqlens is not None, 1, int(need_dg), q.device)
     _check(lib().prism_linear_attention_backward(
         packed, _addr(q), _addr(k), _addr(v), _addr(g), _addr(S0), _addr(cu_seqlens), _addr(dO),
         _addr(dST), _addr(out["dq"]), _addr(out["dk"]), _addr(out["dv"]), _addr(out.get("dg")),

@@ -37,3 +37,47 @@ def test_dg_of_one_decay_a_head_without_sequences(packed):
         None, ptr(dg), None, None, 0, ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
     torch.cuda.synchronize()
     assert st == 0 and dg.tolist() == [0.0] * 4
+
+
+# -------------------------------------------------------------------- paths
+def _launches(f):
+    """What f launches: name -> count."""
+    with P().KernelTimer() as t:
+        f()
+    return {n: c for n, (_, c) in t.result.items()}
+
+
+@pytest.mark.parametrize("dt,Hk", [(BF, 1), (F, 2)])
+def test_packed_over_segments(dt, Hk):
+    """One long sequence (several segments) between short and empty ones."""
+    lens = [3, 700, 0, 33, 1]
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    x = LA._draw(dt, (int(cu[-1]),), len(lens), 2, Hk, 64, 48, "token", seed=35)
+    packed = {"cu_seqlens": torch.tensor(cu, dtype=torch.int32, device="cuda"), "max_seqlen": 700}
+    print(f"\n[packed over segments {dt}]", flush=True)
+    assert "la_states" in _launches(lambda: LA._run(x, 1.0, **packed))
+    got, plain = LA._run(x, 1.0, **packed)
+    want = LA._oracle(x, [(int(a), int(b)) for a, b in zip(cu[:-1], cu[1:])], 1.0)
+    LA._check(got, want, dt, LA.ALL)
+    LA._check(plain, want, dt, ("dq", "dk", "dv", "dS0"))
+
+
+def test_packed_workspace_follows_the_rows():
+    """Backward of a packed batch with one long and many short sequences takes
+    memory for its rows, not for as many rows as the longest has in every
+    sequence."""
+    lens = [8192] + [64] * 63
+    N, H, Hk, d = sum(lens), 8, 2, 64
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    x = LA._draw(BF, (N,), len(lens), H, Hk, d, d, "token", seed=37, states=False)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    P().linear_attention_backward(x["q"], x["k"], x["v"], x["g"], x["dO"], cu_seqlens=cu, max_seqlen=8192, need_dg=True)
+    torch.cuda.synchronize()
+    used = torch.cuda.max_memory_allocated() - before
+    # gradients (bf16 and dg), fp32 partials of dk and dv, nine floats a row and
+    # head, states of the segments (at most 64 each way) and ST
+    rows = N * H * (2 * 2 * d + 4 + 2 * 4 * d + 4 * 9)
+    states = len(lens) * H * d * d * 4
+    assert used < 1.1 * rows + 5 * states, (used, rows, states)

@@ -239,3 +239,30 @@ def test_heads_in_flight():
     # 2^21 heads of all sequences would pass a launch's threads
     D = la(B=1 << 19, H=4, Hk=4, dk=16, dv=16, T=1)
     assert _la_step(D) == E_SHAPE and _la(D) == E_SHAPE
+
+
+@no_gpu
+def test_packed_workspace_follows_the_rows():
+    """The query for packed batches asks for what their rows need, whatever the
+    longest length is, and what the call then requires."""
+    def size(D, backward=True, dg=True):
+        n = ctypes.c_size_t(0)
+        assert P.lib().prism_linear_attention_packed_workspace(ctypes.byref(D), int(backward), int(dg),
+                                                               ctypes.byref(n)) == OK, _err()
+        return n.value
+
+    B, H, N, d = 64, 16, 41984, 128
+    D = la(B=B, T=16384, H=H, Hk=4, dk=d, dv=d, packed_tokens=N)
+    # fp32 dk and dv of each query head; row dots and dg, nine floats; the last state
+    need = N * H * (2 * d * 4 + 9 * 4) + B * H * d * d * 4
+    assert need <= size(D) < need + 8 * 256
+    assert size(D, True, False) < size(D)
+    n = size(D)
+    assert _la_bwd(D, nbytes=n - 1, cu_seqlens=FAKE) == E_WS and str(n) in _err()
+    # a batch whose padded form would be too large
+    D = la(B=4096, T=1 << 20, H=16, Hk=16, packed_tokens=1 << 20)
+    assert P.lib().prism_linear_attention_workspace(ctypes.byref(D), 1, 0, ctypes.byref(ctypes.c_size_t(0))) == E_SHAPE
+    assert size(D) > 0
+    assert P.lib().prism_linear_attention_packed_workspace(ctypes.byref(la()), 1, 1, None) == E_NULL
+    assert P.lib().prism_linear_attention_packed_workspace(ctypes.byref(la(packed_tokens=-1)), 1, 1,
+                                                           ctypes.byref(ctypes.c_size_t(0))) == E_SHAPE
