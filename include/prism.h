@@ -309,8 +309,8 @@ prism_status prism_qk_norm(const prism_qk_norm_desc* desc, const void* q, const 
                            const long long* turns, void* qo, void* ko, hipStream_t stream);
 
 /* Backward: gradients of <dqo, qo> + <dko, ko> from the forward's inputs (no
- * intermediate is kept).  With g = dy turned back by the angle and h = g w:
- *   dx = r h - c r^3 x (x . h),   dw = sum over tokens and heads of g x r.
+ * intermediate is kept).  With g = dy turned back by the angle, h = g w and
+ * u = r x:  dx = r (h - c u (u . h)),   dw = sum over tokens and heads of g u.
  * dq, dk: dt, strided, written; dq may be dqo and dk may be dko.  dwq, dwk
  * [d] f32: written when wq / wk is given (required then, NULL otherwise).
  * The weight gradients are summed in a fixed order.  workspace:

@@ -2,8 +2,10 @@
 // its backward pass.  For a row x of d values (one token, one head):
 //   r = (c sum x^2 + eps)^(-1/2),  y = r x w,  z = y with its first `rot`
 //   values turned in pairs by angle_i = 2 pi p F_i 2^-64,
-// and, with dy = dz turned back and h = dy w,
-//   dx = r h - c r^3 x (x . h),  dw = sum over rows of dy x r.
+// and, with dy = dz turned back, h = dy w and u = r x,
+//   dx = r (h - c u (u . h)),  dw = sum over rows of dy u
+// (by u, of size 1: r^3 would leave fp32's range for rows shorter than 1e-13 or
+// longer than 1e13, whose gradients are well within it).
 //
 // Memory bound: a row is read once and written once (backward: x and dz read,
 // dx written), everything else stays in registers.  A row belongs to a group
@@ -294,19 +296,17 @@ __global__ __launch_bounds__(QN_NT) void qk_norm_bwd_kernel(const QkNormArgs g, 
       ss = group_sum(q.on ? ss : 0.f, G);
       xh = group_sum(q.on ? xh : 0.f, G);
       const float r = rsqrtf(fmaf(g.c, ss, g.eps));
-      const float m = g.c * r * r * r * xh;
+      const float m = g.c * (r * xh);   // c u.h
       if (q.on) {
         float ya[V], yb[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          ya[i] = fmaf(-m, xa[i], r * wa[i] * ga[i]);
-          yb[i] = fmaf(-m, xb[i], r * wb[i] * gb[i]);
-        }
-        if (DW) {
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            da[i] = fmaf(r * xa[i], ga[i], da[i]);
-            db[i] = fmaf(r * xb[i], gb[i], db[i]);
+          const float ua = r * xa[i], ub = r * xb[i];
+          ya[i] = r * fmaf(-m, ua, wa[i] * ga[i]);
+          yb[i] = r * fmaf(-m, ub, wb[i] * gb[i]);
+          if (DW) {
+            da[i] = fmaf(ua, ga[i], da[i]);
+            db[i] = fmaf(ub, gb[i], db[i]);
           }
         }
         *reinterpret_cast<raw*>(dx + h * sy.h + q.a) = IO::pack(ya);

@@ -81,3 +81,25 @@ def test_packed_workspace_follows_the_rows():
     rows = N * H * (2 * 2 * d + 4 + 2 * 4 * d + 4 * 9)
     states = len(lens) * H * d * d * 4
     assert used < 1.1 * rows + 5 * states, (used, rows, states)
+
+
+# --------------------------------------------------------------------- norm
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("size", [2.0 ** -50, 2.0 ** 50])
+def test_norm_backward_of_small_and_large_rows(dt, size):
+    """Without eps, rows of any length whose squares fp32 holds: the gradient is
+    that of the unit row over the length."""
+    gen = torch.Generator(device="cuda").manual_seed(38)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    q, k, dq, dk = (r(2, 5, 3, 64) for _ in range(4))
+    q, k, dq, dk = (q * size).to(dt), (k * size).to(dt), dq.to(dt), dk.to(dt)
+    pos = torch.arange(10, dtype=torch.int32, device="cuda").view(2, 5)
+    turns = P().rope_turns(64)
+    w = (1 + 0.2 * r(64)).to(dt)
+    g = P().qk_norm_backward(q, k, dq, dk, wq=w, positions=pos, turns=turns, eps=0.0)
+    n = lambda t: t.double().cpu().numpy()
+    for x, dz, ww, name in ((q, dq, w, "q"), (k, dk, None, "k")):
+        dx, dw = O.norm_backward(n(x), None if ww is None else n(ww), n(dz), pos.cpu().numpy(), turns.tolist(), "l2", 0.0, False)
+        assert O.rel2(n(g["d" + name]), dx) < {BF: 2.1e-3, F: 1e-5}[dt]
+        if ww is not None:
+            assert O.rel2(n(g["dwq"]), dw) < 1e-5
