@@ -336,6 +336,9 @@ prism_status prism_qk_norm_backward(const prism_qk_norm_desc* desc, const void* 
  * between them carried in fp32; in bf16 every product that adds to the state
  * (and, for the gradient of g, every product) takes its scaled operand in
  * three bf16 pieces, so that f32 results keep f32 accuracy.
+ * Sums of products (S, q . k v, S q, and the backward pass's own) below 2^76
+ * (7e22) in magnitude never overflow on the way; larger ones may, although
+ * their definition is still within fp32 (the step has no such limit).
  *
  *   B, H, Hk   sequences (>= 0), query heads, key / value heads (H % Hk = 0);
  *              B * H < 2^21

@@ -8,9 +8,10 @@
 // the log2 decay since X was last brought up to date, the registers hold
 // 2^{-F} X, rows are read out with 2^{F + u_t} and added with 2^{-(F + u_i)},
 // so that a chunk costs no pass over X and no decay between pairs of tokens.
-// That holds while F + u stays within +-80; X is brought up to date (F = 0)
-// every 256 tokens, or when a chunk would leave this range, and a chunk that
-// leaves it by itself (a decay by 2^-80 within 32 tokens, a reset) takes the form with
+// That holds while F + u stays within +-48; X is brought up to date (F = 0)
+// every 256 tokens, 128 where 256 leave this range, or when a chunk would leave
+// it, and a chunk that leaves it by itself (a decay by 2^-48 within 32 tokens, a
+// reset) takes the form with
 // Gamma_ti = 2^{u_t - u_i} on each pair and 2^{G_C - u_i} on each added row.
 //
 // One workgroup of four waves carries X over its segment's chunks; a wave owns
@@ -213,9 +214,12 @@ __device__ inline float la_exp2(double e) {
   return __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f((float)(e - n)), (int)fmin(fmax(n, -400.0), 400.0));
 }
 
-// log2 range of the factors kept without the decay: their products with each
-// other and with the data stay finite in fp32.
-constexpr double LA_RANGE = 80.0;
+// log2 range of the factors kept without the decay.  They enlarge sums of
+// products by up to 2^48, so that those below 2^76 stay finite in fp32.  (With 80
+// a v k^T of 2^48 overflows; 8 x 2048 tokens, 16 heads of 128, learned decays of a
+// gate near 0.86, backward: 355 us with 80, 359 with 48, 368 with 40 and no halves
+// of a batch; of a gate near 0.5: 371 with 80, 377 with 48.)
+constexpr double LA_RANGE = 48.0;
 
 // Inclusive prefix sum over each 32 lanes: shifts within rows of 16 lanes, then
 // the first row's sum to the second (lane 15 to the row behind it).
@@ -415,20 +419,27 @@ __global__ __launch_bounds__(LA_NT, 2) void la_pass_kernel(const LaArgs<E> args)
     __syncthreads();
     // Every batch starts with X up to date.  u of a chunk lies between its sum
     // less its positive part and its positive part.
-    double f = 0.0, sum = 0.0;
-    float up = 0.f;
+    constexpr int HB = CPB / 2;
+    double f = 0.0, sums[2] = {0.0, 0.0};   // of each half of the batch
+    float ups[2] = {0.f, 0.f};
 #pragma unroll
     for (int q = 0; q < CPB; ++q) {
       const double t = stot[q];
       if (q < bq) f += t;
-      sum += t;
-      up += spos[q];
+      sums[q / HB] += t;
+      ups[q / HB] += spos[q];
     }
+    auto within = [](double sum, float up) { return up <= LA_RANGE && sum - up >= -LA_RANGE; };
+    const double sum = sums[0] + sums[1];
     double m0 = bq == 0 ? F : 0.0, m1 = 0.0;   // log2 factors of X at this thread's chunk
     bool st = false;
     total += sum;
-    if (up <= LA_RANGE && sum - up >= -LA_RANGE) {
+    if (within(sum, ups[0] + ups[1])) {
       F = sum;
+    } else if (within(sums[0], ups[0]) && within(sums[1], ups[1])) {
+      if (bq == HB) m0 = sums[0];
+      if (bq >= HB) f -= sums[0];
+      F = sums[1];
     } else {
       // chunk after chunk (every thread alike).  (A NaN takes the strong form,
       // which spreads it as the recurrence would.)

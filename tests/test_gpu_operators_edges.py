@@ -39,6 +39,40 @@ def test_dg_of_one_decay_a_head_without_sequences(packed):
     assert st == 0 and dg.tolist() == [0.0] * 4
 
 
+# --------------------------------------------------------------- magnitudes
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("decay", ["slow", "token", "fast", "growth"])
+def test_large_magnitudes(dt, decay):
+    """Keys and values of 2^36: every product of the formulas is below 2^80, and
+    so far from the end of fp32 that no result overflows."""
+    print(f"\n[large {dt} {decay}]", flush=True)
+    x = LA._draw(dt, (1, 300), 1, 2, 2, 64, 64, "token", seed=31)
+    x["k"], x["v"] = x["k"] * 2.0 ** 36, x["v"] * 2.0 ** 36
+    x["S0"], x["dST"] = x["S0"] * 2.0 ** 72, x["dST"]
+    if decay != "token":
+        lo, hi = {"slow": (-0.2, -0.2), "fast": (-1.6, -0.8), "growth": (-0.02, 0.06)}[decay]
+        x["g"] = lo + (hi - lo) * torch.rand(1, 300, 2, device="cuda", generator=torch.Generator("cuda").manual_seed(1))
+    got, plain = LA._run(x, 1.0)
+    want = LA._oracle(x, [(0, 300)], 1.0)
+    LA._check(got, want, dt, LA.ALL)
+    LA._check(plain, want, dt, ("dq", "dk", "dv", "dS0"))
+
+
+@pytest.mark.parametrize("dt", [BF, F])
+def test_growth(dt):
+    """Positive log decays: the state grows by 2^70 over a batch of decays, and
+    decay and growth alternate."""
+    print(f"\n[growth {dt}]", flush=True)
+    x = LA._draw(dt, (1, 300), 1, 2, 2, 64, 64, "token", seed=32)
+    u = torch.rand(1, 300, device="cuda", generator=torch.Generator("cuda").manual_seed(2))
+    x["g"][:, :, 0] = 0.1 + 0.2 * u
+    x["g"][:, :, 1] = 4.0 * (u - 0.5)
+    got, plain = LA._run(x, 1.0)
+    want = LA._oracle(x, [(0, 300)], 1.0)
+    LA._check(got, want, dt, LA.ALL)
+    LA._check(plain, want, dt, ("dq", "dk", "dv", "dS0"))
+
+
 # -------------------------------------------------------------------- paths
 def _launches(f):
     """What f launches: name -> count."""
