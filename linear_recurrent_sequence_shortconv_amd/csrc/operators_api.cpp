@@ -359,6 +359,7 @@ prism::LaRole<E> la_role(const E* a, Strides sa, int ga, const E* b, Strides sb,
   r.ga = ga;
   r.gb = gb;
   r.gc = gc;
+  r.ge = 1;
   r.da = da;
   r.dc = dc;
   r.xa = keys_first ? 1 : d.dk;
