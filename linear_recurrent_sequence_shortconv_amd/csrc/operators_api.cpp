@@ -231,18 +231,23 @@ constexpr int LA_SELF_JOIN = 4, LA_SELF_JOIN_DG = 2;
 
 // Segments a sequence is cut into.  A launch runs B H workgroups for each of
 // its passes and each segment, 512 of them at once (two a CU); more than one
-// segment also needs the states at their starts, from `sources` further passes
-// of half the work over all but one segment.  Taken is the count with the
+// segment also needs the states at their starts, from a further pass (backward:
+// two) of half the work over all but one segment.  Taken is the count with the
 // least cost in the time of one chunk on a full chip (4 us in bf16 at d = 128),
 // as measured there: a workgroup costs 2.5 chunks beside its own (4 where it
-// forms states alone, with their join: 8 x 512 tokens, 16 heads 44 us in one segment,
-// 56 in the four that 2 would give), a round of at most one workgroup a CU goes by 0.6 of
-// the time for each chunk, fp32 takes twice and the decays' gradient 1.6 times
-// as long.  8 x 2048 tokens, 16 heads, forward, with 1, 2, 3, 4, 5 and 8
-// segments: 146, 130, 127, 122, 133 and 151 us (4 taken); one sequence of 16384
-// tokens with 1, 4, 8, 16 and 32: 1089, 441, 228, 131 and 114 (32 taken); a
-// backward pass of 2 x 4096 tokens, 16 heads on 4, with 1, 2, 4, 5 and 8: 305,
-// 253, 183, 170 and 169 (5 taken).
+// forms states alone, with their join: 8 x 512 tokens, 16 heads 44 us in one
+// segment, 56 in the four that 2 would give), a round of at most one workgroup a
+// CU goes by 0.6 of the time for each chunk, fp32 takes twice and the decays'
+// gradient 1.6 times as long.  The join's launch is priced from 5 segments on,
+// with the decays' gradient too, whose join of 3 or 4 takes the place of work in
+// three launches: priced from 3 on, a backward pass with dg, 16 heads of 128,
+// takes 109 in place of 87 us for 3 x 700 tokens, 48 in place of 45 for 1 x 256
+// (one segment chosen) and 82 in place of 88 for 2 x 1024 (5 in place of 4).
+// 8 x 2048 tokens, 16 heads, forward, with 1, 2, 3, 4, 5 and 8 segments: 146, 130,
+// 127, 122, 133 and 151 us (4 taken); one sequence of 16384 tokens with 1, 4, 8,
+// 16 and 32: 1089, 441, 228, 131 and 114 (32 taken); a backward pass of 2 x 4096
+// tokens, 16 heads on 4, with 1, 2, 4, 5 and 8: 305, 253, 183, 170 and 169 (5
+// taken).
 constexpr int LA_AT_ONCE = 512;   // workgroups
 enum LaWork { LA_FORWARD, LA_BACKWARD, LA_BACKWARD_DG };
 void plan_segments(const prism_linear_attention_desc& d, LaWork work, LaPlan* p) {
