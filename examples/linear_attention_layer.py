@@ -66,7 +66,7 @@ class Layer:
         """One step of gradient descent on mean (y - target)^2.  Returns the loss."""
         _, q, k, v = self._project(x)
         qn, kn = P.qk_norm(q, k, positions=positions, **self._norm())
-        o, _ = P.linear_attention(qn, kn, v, self.g, scale=self.scale)
+        o, _ = P.linear_attention(qn, kn, v, self.g, scale=self.scale, need_state=False)
         y = (o.flatten(-2) @ self.w_out).float()
         dy = (2.0 / y.numel()) * (y - target)
         dyh = dy.to(x.dtype)

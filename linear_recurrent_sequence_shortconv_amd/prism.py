@@ -677,9 +677,11 @@ def _la_workspace(desc, packed, backward, dg, device):
 
 
 def linear_attention(q, k, v, g, S0=None, scale=1.0, cu_seqlens=None, max_seqlen=None, o=None,
-                     ST=None, workspace=None):
+                     ST=None, workspace=None, need_state=True):
     """Linear attention with a decay for each head (prism_linear_attention):
-    S_t = exp(g_t) S_{t-1} + v_t k_t^T, o_t = scale S_t q_t.  Returns (o, S_T).
+    S_t = exp(g_t) S_{t-1} + v_t k_t^T, o_t = scale S_t q_t.  Returns (o, S_T),
+    or (o, None) with need_state false: the last state is then neither kept to
+    fp32 accuracy nor written.
 
     q [B,T,H,dk], k [B,T,Hk,dk], v [B,T,Hk,dv] in bf16 or fp32 (views of a
     fused projection allowed), H a multiple of Hk; dk, dv multiples of 16 up to
@@ -687,6 +689,8 @@ def linear_attention(q, k, v, g, S0=None, scale=1.0, cu_seqlens=None, max_seqlen
     fp32 or None.  cu_seqlens (int32 [B+1]) with max_seqlen packs sequences:
     token tensors [N,..], g [N,H] or [H].  o, ST: where the results go (new
     tensors by default; ST may be S0)."""
+    if ST is not None and not need_state:
+        raise ValueError("ST given, but need_state is false")
     desc, gs, state, shape = _la_desc(q, k, v, g, (("S0", S0), ("ST", ST)), scale, cu_seqlens,
                                       max_seqlen)
     _on_gpu(q)
@@ -694,7 +698,7 @@ def linear_attention(q, k, v, g, S0=None, scale=1.0, cu_seqlens=None, max_seqlen
         o = q.new_empty(shape)
     else:
         _like(o, "o", q.dtype, q.get_device(), shape)
-    if ST is None:
+    if ST is None and need_state:
         ST = g.new_empty(state)
     packed = _LA_DESC.pack(*desc, *_steps(o, "o"), *gs)
     if workspace is None:

@@ -96,6 +96,20 @@ def test_packed_over_segments(dt, Hk):
     LA._check(plain, want, dt, ("dq", "dk", "dv", "dS0"))
 
 
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("T,H", [(90, 2), (577, 2), (1100, 2)])
+def test_without_states_in_or_out(dt, T, H):
+    """No final state and no state gradient wanted: in one, four and more segments."""
+    x = LA._draw(dt, (1, T), 1, H, H, 64, 64, "token", seed=36, states=False)
+    want = LA._oracle(x, [(0, T)], 0.7)
+    print(f"\n[no states {dt} {T}]", flush=True)
+    o, ST = P().linear_attention(x["q"], x["k"], x["v"], x["g"], scale=0.7, need_state=False)
+    assert ST is None
+    g = P().linear_attention_backward(x["q"], x["k"], x["v"], x["g"], x["dO"], scale=0.7)
+    assert set(g) == {"dq", "dk", "dv"}
+    LA._check({"o": o, **g}, want, dt, ("o", "dq", "dk", "dv"))
+
+
 def test_packed_workspace_follows_the_rows():
     """Backward of a packed batch with one long and many short sequences takes
     memory for its rows, not for as many rows as the longest has in every

@@ -266,3 +266,11 @@ def test_packed_workspace_follows_the_rows():
     assert P.lib().prism_linear_attention_packed_workspace(ctypes.byref(la()), 1, 1, None) == E_NULL
     assert P.lib().prism_linear_attention_packed_workspace(ctypes.byref(la(packed_tokens=-1)), 1, 1,
                                                            ctypes.byref(ctypes.c_size_t(0))) == E_SHAPE
+
+
+def test_binding_refuses_a_state_that_is_not_needed():
+    q, k, v, g = _t(2, 5, 4, 64), _t(2, 5, 2, 64), _t(2, 5, 2, 32), _t(4, dt=torch.float32)
+    with pytest.raises(ValueError, match="need_state"):
+        P.linear_attention(q, k, v, g, ST=_t(2, 4, 32, 64, dt=torch.float32), need_state=False)
+    with pytest.raises(ValueError, match="GPU"):
+        P.linear_attention(q, k, v, g, need_state=False)
