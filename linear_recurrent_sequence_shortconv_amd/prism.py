@@ -585,7 +585,11 @@ def qk_norm_backward(q, k, dq_out, dk_out, wq=None, wk=None, positions=None, tur
     desc = _qk_desc(q, k, wq, wk, positions, turns, norm, eps, interleaved)
     _like(dq_out, "dq_out", q.dtype, q.get_device(), q.shape)
     if k is not None:
+        if dk_out is None:
+            raise ValueError("dk_out is required with k")
         _like(dk_out, "dk_out", k.dtype, k.get_device(), k.shape)
+    elif dk_out is not None or dk is not None:
+        raise ValueError("dk_out or dk without k")
     steps = (*_steps(dq_out, "dq_out"), *(_NO_STEPS if k is None else _steps(dk_out, "dk_out")))
     _on_gpu(q)
     out = {"dq": _out(q, dq, "dq")}

@@ -274,3 +274,12 @@ def test_binding_refuses_a_state_that_is_not_needed():
         P.linear_attention(q, k, v, g, ST=_t(2, 4, 32, 64, dt=torch.float32), need_state=False)
     with pytest.raises(ValueError, match="GPU"):
         P.linear_attention(q, k, v, g, need_state=False)
+
+
+def test_binding_wants_key_gradients_with_keys():
+    q, k = _t(2, 3, 4, 64), _t(2, 3, 2, 64)
+    with pytest.raises(ValueError, match="dk_out is required with k"):
+        P.qk_norm_backward(q, k, q, None)
+    for kw in ({"dk_out": k}, {"dk_out": None, "dk": k}):
+        with pytest.raises(ValueError, match="without k"):
+            P.qk_norm_backward(q, None, q, **kw)
