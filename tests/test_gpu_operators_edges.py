@@ -73,12 +73,62 @@ def test_growth(dt):
     LA._check(plain, want, dt, ("dq", "dk", "dv", "dS0"))
 
 
+@pytest.mark.parametrize("value", [float("inf"), -float("inf")])
+def test_infinite_tokens_stay_in_their_sequence(value):
+    cu = torch.tensor([0, 70, 100], dtype=torch.int32, device="cuda")
+    x = LA._draw(BF, (100,), 2, 2, 2, 64, 64, "token", seed=21)
+    clean, _ = LA._run(x, 1.0, cu_seqlens=cu, max_seqlen=70)
+    for n in ("q", "k", "v", "dO"):
+        x[n][70:] = value
+    got, _ = LA._run(x, 1.0, cu_seqlens=cu, max_seqlen=70)
+    for n in ("o", "dq", "dk", "dv", "dg"):
+        assert torch.equal(got[n][:70], clean[n][:70]), n
+    assert torch.equal(got["ST"][0], clean["ST"][0]) and torch.equal(got["dS0"][0], clean["dS0"][0])
+
+
 # -------------------------------------------------------------------- paths
 def _launches(f):
     """What f launches: name -> count."""
     with P().KernelTimer() as t:
         f()
     return {n: c for n, (_, c) in t.result.items()}
+
+
+@pytest.mark.parametrize("dt,B,T,H,Hk,nseg", [(BF, 1, 1100, 128, 128, 2), (F, 1, 1100, 128, 64, 2),
+                                              (BF, 2, 1100, 128, 128, 1), (F, 1, 1100, 256, 256, 1)])
+def test_many_heads_with_dg(dt, B, T, H, Hk, nseg):
+    """As many heads as a training batch has in flight: dv in a launch of its
+    own, two segments whose entering states every pass (and the decay gradient)
+    forms by itself, or one segment longer than 1024 tokens, of which the last
+    chunk is cut."""
+    print(f"\n[many heads {dt} {B} {T} {H} {Hk}]", flush=True)
+    x = LA._draw(dt, (B, T), B, H, Hk, 16, 16, "token", seed=33)
+    run = lambda: P().linear_attention_backward(x["q"], x["k"], x["v"], x["g"], x["dO"], S0=x["S0"], dST=x["dST"],
+                                                scale=0.5, need_dS0=True, need_dg=True)
+    did = _launches(run)
+    assert "la_bwd_v" in did and "la_join" not in did and ("la_states" in did) == (nseg > 1), did
+    want = LA._oracle(x, [(b * T, (b + 1) * T) for b in range(B)], 0.5)
+    LA._check(run(), want, dt, ("dq", "dk", "dv", "dg", "dS0"))
+
+
+@pytest.mark.parametrize("T,H,join", [(577, 2, False), (700, 1, True)])
+def test_state_in_place_over_segments(T, H, join):
+    """A state updated in place is written while other segments still start from
+    it: they then start from joined copies, also where few segments would
+    otherwise form their entering states from it by themselves."""
+    x = LA._draw(BF, (1, T), 1, H, H, 64, 64, "token", seed=34)
+    want = LA._oracle(x, [(0, T)], 1.0)
+    run = lambda S, ST: P().linear_attention(x["q"], x["k"], x["v"], x["g"], S0=S, ST=ST)
+    out, S = torch.empty_like(x["S0"]), x["S0"].clone()
+    did = _launches(lambda: run(x["S0"], out))
+    assert "la_states" in did and ("la_join" in did) == join, did
+    o, _ = run(x["S0"], out)
+    LA._check({"o": o, "ST": out}, want, BF, ("o", "ST"))
+    did = _launches(lambda: run(S, S))
+    assert "la_join" in did, did
+    S = x["S0"].clone()
+    o, _ = run(S, S)
+    LA._check({"o": o, "ST": S}, want, BF, ("o", "ST"))
 
 
 @pytest.mark.parametrize("dt,Hk", [(BF, 1), (F, 2)])
