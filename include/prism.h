@@ -268,9 +268,11 @@ prism_status prism_step_noalloc(const prism_desc* desc, const void* q, const voi
  * values pass.  turns[i] is the pair's frequency as an integer: turns per
  * position in units of 2^-64 (inv_freq / (2 pi) * 2^64, rounded).  The phase
  * p turns[i] mod 2^64 is formed exactly in integers, so the angle is as exact
- * at position 10^9 as at 1, with no table.  The arithmetic is fp32; each
- * output is rounded once to the storage type.  The outputs are what
- * prism_forward and prism_linear_attention take as q and k.               */
+ * at position 10^9 as at 1, with no table.  The arithmetic is fp32 (the sum of
+ * squares too: rows of values beyond about 2^58, or without eps below about
+ * 2^-58, leave its range); each output is rounded once to the storage type.
+ * The outputs are what prism_forward and prism_linear_attention take as q
+ * and k.                                                                   */
 typedef enum {
   PRISM_NORM_L2 = 0,
   PRISM_NORM_RMS = 1
@@ -333,9 +335,12 @@ prism_status prism_qk_norm_backward(const prism_qk_norm_desc* desc, const void* 
  * past.  The state has prism_forward's layout, [B, H, dv, dk] f32.
  * H query heads share Hk key / value heads: head h reads k, v of head
  * h / (H / Hk).  Chunks of tokens go through the matrix cores, with the state
- * between them carried in fp32; in bf16 every product that adds to the state
- * (and, for the gradient of g, every product) takes its scaled operand in
- * three bf16 pieces, so that f32 results keep f32 accuracy.
+ * between them carried in fp32.  In bf16, what a product adds to the state is
+ * taken in three bf16 pieces where ST, dS0 or dg is wanted, so that these f32
+ * results keep f32 accuracy, and in two where all results are bf16; the scaled
+ * scores and the copy of the state that is read out are rounded once to bf16
+ * (for dq and dk with dg: three pieces).  A bf16 o, dq, dk or dv is then off by
+ * 2.4e-3 (2-norm, random values), where its own rounding alone gives 1.7e-3.
  * Sums of products (S, q . k v, S q, and the backward pass's own) below 2^76
  * (7e22) in magnitude never overflow on the way; larger ones may, although
  * their definition is still within fp32 (the step has no such limit).
@@ -385,9 +390,11 @@ prism_status prism_linear_attention(const prism_linear_attention_desc* desc, con
 /* Gradients of <dO, o> + <dST, ST> from the forward's inputs.  dST may be
  * NULL (zeros).  dq [B,T,H,dk], dk [B,T,Hk,dk], dv [B,T,Hk,dv] dt,
  * contiguous; dg f32 (NULL: not wanted; zero where g < -104, whose decay is
- * zero), dS0 f32 (NULL: not wanted; not the buffer of dST or S0).  Written,
- * not accumulated; packed rows outside every (clamped) sequence are
- * unspecified. */
+ * zero; it is formed as a difference of sums over the tokens behind, good to
+ * f32 against those sums: a dg_t far smaller than they are, as where exp(g_t)
+ * is small, keeps fewer digits or none), dS0 f32 (NULL: not wanted; not the
+ * buffer of dST or S0).  Written, not accumulated; packed rows outside every
+ * (clamped) sequence are unspecified. */
 prism_status prism_linear_attention_backward(const prism_linear_attention_desc* desc,
                                              const void* q, const void* k, const void* v,
                                              const float* g, const float* S0,
@@ -398,7 +405,8 @@ prism_status prism_linear_attention_backward(const prism_linear_attention_desc* 
 
 /* The recurrence token by token, for the desc->T tokens of each sequence
  * (T = 1: a decode step): S is read as S_0, S_T goes to S_out (S_out = S:
- * in place).  T = 0 copies the state. */
+ * in place).  T = 0 copies the state.  (Here as above, other outputs overlap
+ * neither inputs nor one another.) */
 prism_status prism_linear_attention_step(const prism_linear_attention_desc* desc, const void* q,
                                          const void* k, const void* v, const float* g,
                                          const float* S, float* S_out, void* o,

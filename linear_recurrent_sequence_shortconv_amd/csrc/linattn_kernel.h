@@ -35,7 +35,7 @@
 // scores and readout take 1700, their product with C 630, the update of X 2000,
 // the rest waits for loads, LDS stores, barrier and decays; matrix units are
 // busy 25 %, the vector ALU 30 to 40 %, LDS 24 %.  8 x 2048 tokens, 16 heads of
-// 128: 80 us for out (4 reads and writes of 67 MB; 3.4 TB/s), 38 for the states
+// 128: 83 us for out (4 reads and writes of 67 MB; 3.2 TB/s), 36 for the states
 // before it; with its dots (a gradient and the rows for dg) 118 each.
 // The sizes taken: chunks of 32 tokens (64: 88 us where 32 took 82: more
 // products, fewer workgroups a CU), 32 columns of X a wave and four waves (eight

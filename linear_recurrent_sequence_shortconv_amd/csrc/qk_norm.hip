@@ -113,8 +113,9 @@ __device__ inline LanePlace lane_place(int p, int d, int rot) {
 }
 
 // cos, sin of the lane's V angles.  The phase p F mod 2^64 is exact; its upper
-// 32 bits, as a signed number, keep the angle to 2^-24 of its size (an fp32
-// product p * frequency would lose position's bits).  For bf16 the hardware's
+// 32 bits, as a signed number rounded to fp32, keep the angle to 2^-32 of a turn
+// and 2^-24 of its size (an fp32 product p * frequency would lose position's
+// bits).  For bf16 the hardware's
 // sine and cosine of turns do (absolute error about 2^-20; the outputs are
 // rounded at 2^-9); fp32 takes the library's.
 template <typename E, int V>
