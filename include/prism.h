@@ -23,7 +23,7 @@
  * Conventions common to every entry point
  * ---------------------------------------
  * - All tensor pointers are DEVICE pointers, contiguous, row-major, 16-byte
- *   aligned.  The caller owns every buffer, including the workspace.  The
+ *   aligned (the later sections name what they take beside that).  The caller owns every buffer, including the workspace.  The
  *   library allocates no device memory and keeps no pointer after a call.
  * - Work is enqueued asynchronously on `stream`; nothing synchronises the
  *   host.  Buffers must stay alive until the stream has finished the work.
@@ -66,7 +66,8 @@ typedef enum {
  * ablation without the nonlinearity). */
 typedef enum {
   PRISM_ACT_GELU = 0,
-  PRISM_ACT_IDENTITY = 1
+  PRISM_ACT_IDENTITY = 1,
+  PRISM_ACT_SILU = 2       /* z sigmoid(z), of prism_short_conv alone */
 } prism_activation;
 
 /* Problem descriptor.
@@ -80,8 +81,8 @@ typedef enum {
  *              accepted (the last chunk may be partial)
  *   conv_width ShortConv width; must be 4
  *   dtype      storage type of the dtype-typed tensors (see prism_dtype)
- *   activation refinement step activation, a prism_activation value
- *              (0 = GELU, the method's step)
+ *   activation refinement step activation, PRISM_ACT_GELU (0, the method's
+ *              step) or PRISM_ACT_IDENTITY
  *   conv_offset ShortConv tap offset: 0 = tap j multiplies v_{t-j} (the
  *              current token and the three before it), 1 = tap j multiplies
  *              v_{t-1-j} (strictly past tokens, the ones the state S_{t-1}
@@ -275,7 +276,8 @@ prism_status prism_step_noalloc(const prism_desc* desc, const void* q, const voi
  * and k.                                                                   */
 typedef enum {
   PRISM_NORM_L2 = 0,
-  PRISM_NORM_RMS = 1
+  PRISM_NORM_RMS = 1,
+  PRISM_NORM_LAYER = 2     /* mean and deviation, of prism_layer_norm alone */
 } prism_norm;
 
 /* Steps between consecutive batch entries, tokens and heads of a token
@@ -297,7 +299,7 @@ typedef struct {
 typedef struct {
   int B, T, Hq, Hk, d, rot;
   prism_dtype dtype;
-  int norm;          /* a prism_norm value */
+  int norm;          /* PRISM_NORM_L2 or PRISM_NORM_RMS */
   int interleaved;   /* 0: pairs (i, i + rot/2), 1: pairs (2i, 2i + 1) */
   float eps;
   prism_strides q, k, qo, ko, dq, dk;
@@ -410,6 +412,175 @@ prism_status prism_linear_attention_backward(const prism_linear_attention_desc* 
 prism_status prism_linear_attention_step(const prism_linear_attention_desc* desc, const void* q,
                                          const void* k, const void* v, const float* g,
                                          const float* S, float* S_out, void* o,
+                                         hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Layer norm with the residual sum in front
+ * ------------------------------------------------------------------------
+ * For every row of D values (the width of the model, or of one head's output),
+ *   s = x + residual,  m = mean(s)           (PRISM_NORM_RMS: m = 0)
+ *   r = (mean((s - m)^2) + eps)^(-1/2),  y = (s - m) r w + b,  h = s.
+ * The arithmetic is fp32; y is formed from the sum before it is rounded to the
+ * storage type, which h then is.  Squares of deviations have to be within
+ * fp32's range (deviations below about 2^60).
+ *
+ * In this section and the following two, token tensors start at any multiple of
+ * their element's size, and so do their rows; 16-byte rows are read faster.
+ *
+ *   B, T, H    rows: B * T * H of them, each >= 0, at most 2^30 in all
+ *   D          values of a row, 1 .. 16384
+ *   norm       PRISM_NORM_LAYER or PRISM_NORM_RMS
+ *   eps        finite and >= 0
+ *   x, r, y, h strides; r: of the residual (backward: of dh), y: of y (backward:
+ *              of dy), h: of h (backward: of dx).  Magnitude < 2^40; a result's
+ *              are not 0 where there is more than one entry.                 */
+typedef struct {
+  int B, T, H, D;
+  prism_dtype dtype;
+  int norm;
+  float eps;
+  prism_strides x, r, y, h;
+} prism_layer_norm_desc;
+
+/* Forward.  x, residual, y, h [B,T,H,D] dt, strided; w, b [D] dt or NULL (ones,
+ * zeros).  residual may be NULL (s = x; h is then NULL too); h may be NULL (the
+ * sum is not wanted).  y and h may each be x or residual, with its strides. */
+prism_status prism_layer_norm(const prism_layer_norm_desc* desc, const void* x,
+                              const void* residual, const void* w, const void* b, void* y, void* h,
+                              hipStream_t stream);
+
+/* Backward, from x, the rows that were normalised (h where there was a
+ * residual): with u = (x - m) r and g = dy w,
+ *   dx = r (g - mean(g) - u mean(g u)) + dh   (PRISM_NORM_RMS: without mean(g))
+ *   dw = sum over rows of dy u,  db = sum over rows of dy.
+ * dh, the gradient that reaches the sum by itself, may be NULL (zero); dx, dt,
+ * is the gradient of x and of the residual alike, and may be dy, dh or x.
+ * dw, db [D] f32: NULL where not wanted; summed in a fixed order.  workspace:
+ * prism_layer_norm_backward_workspace() bytes (weights: whether dw or db is
+ * wanted), 256-byte aligned (may be NULL where that is 0). */
+prism_status prism_layer_norm_backward_workspace(const prism_layer_norm_desc* desc, int weights,
+                                                 size_t* bytes);
+prism_status prism_layer_norm_backward(const prism_layer_norm_desc* desc, const void* x,
+                                       const void* w, const void* dy, const void* dh, void* dx,
+                                       float* dw, float* db, void* workspace,
+                                       size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Short convolution
+ * ------------------------------------------------------------------------
+ * The depthwise causal convolution by itself (the layer's anchor has it on v):
+ * for every channel,
+ *   z_t = b + sum_{j < K} w[c, j] x_{t-j},  y_t = z_t (PRISM_ACT_IDENTITY) or
+ *   z_t sigmoid(z_t) (PRISM_ACT_SILU),
+ * x_{-1}, x_{-2}, .. from hist.  The arithmetic is fp32, y rounded once.
+ *
+ *   B, T, D    sequences, tokens (each >= 0, B * T <= 2^30), channels (1 ..
+ *              4194304; B * D < 2^31)
+ *   K          taps, 2 .. 4
+ *   activation PRISM_ACT_IDENTITY or PRISM_ACT_SILU
+ *   packed_tokens  with cu_seqlens: rows N of the token tensors (T is then not
+ *              used).  Offsets as in prism_forward's packed batches, clamped the
+ *              same way; a sequence is as long as they say, and rows of no
+ *              sequence stay as they are.
+ *   x, y, dx   strides (batch and token; head is not used) of x, of y (backward:
+ *              of dy) and, backward, of dx, as in prism_layer_norm_desc      */
+typedef struct {
+  int B, T, D, K;
+  prism_dtype dtype;
+  int activation;
+  int packed_tokens;
+  prism_strides x, y, dx;
+} prism_short_conv_desc;
+
+/* Forward.  x, y [B,T,D] ([N,D] with cu_seqlens) dt, strided; w [D,K] dt, tap j
+ * multiplying x_{t-j}; b [D] dt or NULL; hist [B,K-1,D] dt, the tokens before the
+ * sequence, oldest first, or NULL (zeros); hist_out (may be NULL) receives the
+ * last K - 1 tokens for the next call, from hist or zeros where the sequence is
+ * shorter, and may be hist itself.  y overlaps no input. */
+prism_status prism_short_conv(const prism_short_conv_desc* desc, const void* x, const void* w,
+                              const void* b, const void* hist, const int* cu_seqlens, void* y,
+                              void* hist_out, hipStream_t stream);
+
+/* Backward: gradients of <dy, y> from the forward's inputs (hist as the forward
+ * read it).  dx dt, strided; dw [D,K] f32; db [D] f32 or NULL; dhist [B,K-1,D] f32
+ * or NULL (add it to the last rows of the gradient of the call before).  Written,
+ * not accumulated; the sums over tokens in a fixed order.  workspace:
+ * prism_short_conv_backward_workspace() bytes (packed: whether cu_seqlens is
+ * given), 256-byte aligned.  No output overlaps an input. */
+prism_status prism_short_conv_backward_workspace(const prism_short_conv_desc* desc, int packed,
+                                                 size_t* bytes);
+prism_status prism_short_conv_backward(const prism_short_conv_desc* desc, const void* x,
+                                       const void* w, const void* b, const void* hist,
+                                       const int* cu_seqlens, const void* dy, void* dx, float* dw,
+                                       float* db, float* dhist, void* workspace,
+                                       size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Gated recurrence
+ * ------------------------------------------------------------------------
+ * A state of one value a channel: h_t = a_t h_{t-1} + u_t with the gates formed
+ * in the same pass.  With s = sigmoid(i), or 1 without i,
+ *   PRISM_GATE_LOG      a = exp(f),                  u = s x
+ *   PRISM_GATE_SIGMOID  a = sigmoid(f),              u = (1 - a) s x
+ *   PRISM_GATE_POWER    a = exp(-lam sigmoid(f)),    u = sqrt(1 - a^2) s x
+ * lam [D] f32, >= 0.  Gates, state and sums are fp32 (1 - a and 1 - a^2 to their
+ * own size); h is rounded once.  A value that is not finite may reach every later
+ * token of its sequence and channel, never another's.
+ *
+ *   B, T, D    as in prism_short_conv_desc
+ *   gate       a prism_gate value
+ *   packed_tokens  as in prism_short_conv_desc
+ *   x, f, i, h strides (batch and token) of the inputs and of h; dh, dx, df, di:
+ *              backward, as in prism_layer_norm_desc                         */
+typedef enum {
+  PRISM_GATE_LOG = 0,
+  PRISM_GATE_SIGMOID = 1,
+  PRISM_GATE_POWER = 2
+} prism_gate;
+typedef struct {
+  int B, T, D;
+  prism_dtype dtype;
+  int gate;
+  int packed_tokens;
+  prism_strides x, f, i, h, dh, dx, df, di;
+} prism_gated_recurrence_desc;
+
+/* Workspace of the forward (backward = 0) or backward (1) pass, of a packed
+ * batch or a dense one; 256-byte aligned, may be NULL where 0 bytes are needed.
+ * Passes in flight at the same time need one each. */
+prism_status prism_gated_recurrence_workspace(const prism_gated_recurrence_desc* desc, int packed,
+                                              int backward, size_t* bytes);
+
+/* Whole sequences.  x, f, i, h [B,T,D] ([N,D] with cu_seqlens) dt, strided; i may
+ * be NULL; lam is NULL but with PRISM_GATE_POWER.  h0 [B,D] f32, the state before
+ * the sequence, may be NULL (zeros); hT [B,D] f32, the state after it, may be NULL,
+ * or h0 itself.  A sequence of no tokens gives hT = h0. */
+prism_status prism_gated_recurrence(const prism_gated_recurrence_desc* desc, const void* x,
+                                    const void* f, const void* i, const float* lam,
+                                    const float* h0, const int* cu_seqlens, void* h, float* hT,
+                                    void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Gradients of <dh, h> + <dhT, hT> from the forward's inputs and its output h,
+ * which is read as h_{t-1} (in bf16 as rounded: df and dlam then carry its
+ * rounding, of at most 2^-9 of each h_{t-1}).  dhT [B,D] f32 may be NULL (zero).
+ * dx, df, di dt, strided (di: NULL without i); dlam [D] f32, NULL but with
+ * PRISM_GATE_POWER, summed in a fixed order; dh0 [B,D] f32 or NULL (may be dhT).
+ * Where lam sigmoid(f) = 0 the root's infinite slope is taken as 0.  Written, not
+ * accumulated. */
+prism_status prism_gated_recurrence_backward(const prism_gated_recurrence_desc* desc,
+                                             const void* x, const void* f, const void* i,
+                                             const float* lam, const float* h0,
+                                             const int* cu_seqlens, const void* h, const void* dh,
+                                             const float* dhT, void* dx, void* df, void* di,
+                                             float* dlam, float* dh0, void* workspace,
+                                             size_t workspace_bytes, hipStream_t stream);
+
+/* Token by token for the T tokens of each dense sequence (T = 1: a decode step):
+ * state [B,D] f32 is read, the state after the tokens goes to state_out (state
+ * itself: in place). */
+prism_status prism_gated_recurrence_step(const prism_gated_recurrence_desc* desc, const void* x,
+                                         const void* f, const void* i, const float* lam,
+                                         const float* state, float* state_out, void* h,
                                          hipStream_t stream);
 
 /* Human-readable name of a status code (static string). */

@@ -36,12 +36,17 @@ SOURCES = [
     "state.hip",
     "step.hip",
     "refine_bwd.hip",
+    "recurrence.hip",
+    "layer_norm.hip",
+    "short_conv.hip",
     "qk_norm.hip",
     "linattn.hip",
     "noalloc.hip",
     "chunk_bwd.hip",
     "prism_api.cpp",
     "operators_api.cpp",
+    "block_ops.hip",
+    "block_ops_api.cpp",
 ]
 
 ARCH = "gfx950"

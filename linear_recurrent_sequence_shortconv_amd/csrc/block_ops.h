@@ -1,0 +1,124 @@
+// Host-side declarations of the operators of a recurrent block (layer norm,
+// short convolution, gated recurrence), shared by the C-ABI layer
+// (block_ops_api.cpp) and the kernels.
+#pragma once
+
+#include "operators.h"
+
+namespace prism {
+
+// Element steps of a token tensor [B, T, D] (packed: [N, D], batch unused).
+struct TokenSteps {
+  long b, t;
+};
+
+// --------------------------------------------------------------- layer norm
+struct LayerNormArgs {
+  long rows;               // B * T * H rows of D values
+  int T, H, D;
+  int center;              // 1: mean and deviation, 0: root mean square
+  float eps;
+  const void *x, *r, *w, *b;
+  void *y, *h;             // forward: results; h nullptr: the sum is not wanted
+  Strides sx, sr, sy, sh;  // backward: sr of dh, sy of dy, sh of dx
+  const void *dy, *dh;
+  void* dx;
+  float *part, *dw, *db;   // weight-gradient partials and results (nullptr: not wanted)
+};
+template <typename E> hipError_t launch_layer_norm(const LayerNormArgs& a, hipStream_t s);
+template <typename E> hipError_t launch_layer_norm_bwd(const LayerNormArgs& a, hipStream_t s);
+size_t layer_norm_part_bytes(int D);   // room for the weight-gradient partials
+constexpr int LN_MAX_D = 16384;
+
+// -------------------------------------------------------- short convolution
+struct ShortConvArgs {
+  int B, T, D, K;
+  int rows;                // N, or B * T
+  int silu;
+  const int* cu;           // offsets of a packed batch, or nullptr
+  const void *x, *w, *b, *hist;
+  void *y, *hist_out;
+  TokenSteps sx, sy, sd;   // of x, of y / dy, of dx
+  const void* dy;
+  void* dx;
+  float *part, *dw, *db, *dhist;
+};
+template <typename E> hipError_t launch_short_conv(const ShortConvArgs& a, hipStream_t s);
+template <typename E> hipError_t launch_short_conv_bwd(const ShortConvArgs& a, hipStream_t s);
+size_t short_conv_part_bytes(int rows, int D, int K);
+
+// --------------------------------------------------------- gated recurrence
+enum Gate { GATE_LOG, GATE_SIGMOID, GATE_POWER };
+struct RecurrenceArgs {
+  int B, T, D;
+  int rows;                // N, or B * T
+  int gate;
+  const int* cu;
+  const void *x, *f, *i;   // i nullptr: an open input gate
+  const float *lam, *h0;
+  void* h;
+  float* hT;
+  TokenSteps sx, sf, si, sh;
+  // backward
+  const void* dh;
+  const float* dhT;
+  void *dx, *df, *di;
+  float *dh0, *dlam, *part;
+  TokenSteps sdh, sdx, sdf, sdi;
+};
+template <typename E> hipError_t launch_recurrence(const RecurrenceArgs& a, hipStream_t s);
+template <typename E> hipError_t launch_recurrence_bwd(const RecurrenceArgs& a, hipStream_t s);
+size_t recurrence_part_bytes(int B, int D);
+
+// ---------------------------------------------------------------- sequences
+// dst[b] = src[b] (nullptr: zeros), n 4- or 2-byte values each, for every
+// sequence without tokens, which no row of the passes belongs to.
+hipError_t launch_empty_sequences(const int* cu, int B, int rows, int T, void* dst, const void* src, int n, int size,
+                                  hipStream_t s);
+// out[e] = sum over p of part[p][e], e < n, in a fixed order; with K > 0 the
+// columns are [K][n / K] and go to out[c * K + j].
+hipError_t launch_column_sums(const float* part, int parts, long stride, int n, int K, float* out, hipStream_t s);
+
+#ifdef __HIPCC__
+// The sequence that holds row `row` of a batch: rows start .. end - 1 of
+// sequence b; b < 0 or b >= B: rows of no sequence.  Packed batches take the
+// caller's offsets as c'_i = max_{j <= i} min(max(cu[j], 0), rows), so that the
+// sequences lie inside the tensors and do not overlap whatever the offsets are.
+struct Sequence {
+  int b, start, end;
+};
+// Called by whole waves with one row each.
+__device__ inline Sequence find_sequence(const int* cu, int B, int T, int rows, int row) {
+  Sequence q;
+  if (!cu) {
+    q.b = row / T;
+    q.start = q.b * T;
+    q.end = q.start + T;
+    return q;
+  }
+  const int lane = threadIdx.x & 63;
+  int before = 0;   // largest offset not behind the row
+  for (int j0 = 0; j0 <= B; j0 += 64) {
+    const int j = j0 + lane;
+    const int c = j <= B ? min(max(cu[j], 0), rows) : 0;
+    const unsigned long long behind = __ballot(c > row);
+    const int first = behind ? __builtin_ctzll(behind) : 64;
+    int m = lane < first ? c : 0;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) m = max(m, __shfl_xor(m, o));
+    before = max(before, m);
+    if (behind) {
+      q.b = __builtin_amdgcn_readfirstlane(j0 + first - 1);
+      q.start = __builtin_amdgcn_readfirstlane(before);
+      q.end = __builtin_amdgcn_readlane(c, first);
+      return q;
+    }
+  }
+  q.b = B;
+  q.start = __builtin_amdgcn_readfirstlane(before);
+  q.end = rows;
+  return q;
+}
+#endif
+
+}  // namespace prism

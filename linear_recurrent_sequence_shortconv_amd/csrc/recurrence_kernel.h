@@ -1,0 +1,104 @@
+// Gates of the gated recurrence h_t = a_t h_{t-1} + u_t, value by value, and
+// their derivatives.  With s = sigma(i), or 1,
+//   log      a = e^f,                 u = s x
+//   sigmoid  a = sigma(f),            u = (1 - a) s x
+//   power    a = e^(-lam sigma(f)),   u = (1 - a^2)^(1/2) s x
+// u = c s x throughout, with c = 1, 1 - a, or (1 - a^2)^(1/2).
+#pragma once
+
+#include "block_ops.h"
+#include "vec_io.h"
+
+namespace prism {
+
+// Exponential, reciprocal and root: of bf16 inputs by the hardware's (1 ulp
+// each; the exponential's argument adds 2^-24 of its size), of fp32 inputs by
+// the library's.
+template <typename E> __device__ inline float gate_exp(float x) {
+  if constexpr (sizeof(E) == 2) return __expf(x);
+  return expf(x);
+}
+template <typename E> __device__ inline float gate_rcp(float x) {
+  if constexpr (sizeof(E) == 2) return __builtin_amdgcn_rcpf(x);
+  return 1.f / x;
+}
+template <typename E> __device__ inline float gate_sqrt(float x) {
+  if constexpr (sizeof(E) == 2) return __builtin_amdgcn_sqrtf(x);
+  return sqrtf(x);
+}
+
+// sigma(z) and 1 - sigma(z), each to its own size (1 - p of a p near 1 would
+// keep few digits).
+template <typename E>
+__device__ inline void sigmoid_pair(float z, float& p, float& q) {
+  const float e = gate_exp<E>(-z);
+  p = gate_rcp<E>(1.f + e);
+  q = e > 1.f ? 1.f - p : e * p;
+}
+
+// 1 - e^-z for z >= 0: below 1/4 by its series (1 - a^2 of an a near 1 would
+// keep few digits; the first term left out is below 2^-24 of the sum), else from
+// aa = e^-z.
+__device__ inline float one_minus_exp(float z, float aa) {
+  float s = fmaf(z, -1.f / 6.f, 1.f);
+  s = fmaf(z * (-1.f / 5.f), s, 1.f);
+  s = fmaf(z * (-1.f / 4.f), s, 1.f);
+  s = fmaf(z * (-1.f / 3.f), s, 1.f);
+  s = fmaf(z * (-1.f / 2.f), s, 1.f);
+  return z < 0.25f ? z * s : 1.f - aa;
+}
+
+// a and c.
+template <typename E, int G>
+__device__ inline void gate_values(float f, float lam, float& a, float& c) {
+  if constexpr (G == GATE_LOG) {
+    a = gate_exp<E>(f);
+    c = 1.f;
+  } else if constexpr (G == GATE_SIGMOID) {
+    sigmoid_pair<E>(f, a, c);
+  } else {
+    const float y = lam * gate_rcp<E>(1.f + gate_exp<E>(-f));
+    a = gate_exp<E>(-y);
+    c = gate_sqrt<E>(one_minus_exp(2.f * y, a * a));
+  }
+}
+template <typename E, int G, bool INP>
+__device__ inline void gate_inputs(float x, float f, float i, float lam, float& a, float& u) {
+  float c;
+  gate_values<E, G>(f, lam, a, c);
+  u = G == GATE_LOG ? x : c * x;
+  if (INP) u *= gate_rcp<E>(1.f + gate_exp<E>(-i));
+}
+
+// Gradients of a token's inputs from g, that of h_t, and h_{t-1}; dl: its part
+// of the gradient of lam.  At lam sigma(f) = 0, where the root's slope is
+// infinite, its part is left out.
+template <typename E, int G, bool INP>
+__device__ inline void gate_gradients(float x, float f, float i, float lam, float before, float g, float& dx, float& df,
+                                      float& di, float& dl) {
+  float s = 1.f, t = 0.f;
+  if (INP) sigmoid_pair<E>(i, s, t);
+  float p, q, a, c;
+  dl = 0.f;
+  if constexpr (G == GATE_LOG) {
+    a = gate_exp<E>(f);
+    c = 1.f;
+    df = g * a * before;
+  } else if constexpr (G == GATE_SIGMOID) {
+    sigmoid_pair<E>(f, a, c);
+    df = g * (before - s * x) * a * c;
+  } else {
+    sigmoid_pair<E>(f, p, q);
+    const float y = lam * p;
+    a = gate_exp<E>(-y);
+    c = gate_sqrt<E>(one_minus_exp(2.f * y, a * a));
+    const float slope = c > 0.f ? a * gate_rcp<E>(c) : 0.f;
+    const float d = g * a * (before - slope * s * x);   // of log a
+    dl = -p * d;
+    df = lam * q * dl;
+  }
+  dx = g * c * s;
+  di = INP ? dx * x * t : 0.f;
+}
+
+}  // namespace prism

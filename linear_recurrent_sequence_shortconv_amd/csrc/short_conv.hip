@@ -1,0 +1,351 @@
+// Depthwise causal convolution over the last K tokens with its activation, and
+// its backward pass.  Channel by channel,
+//   z_t = bias + sum_{j < K} w_j x_{t-j},  y_t = z_t, or z_t sigma(z_t) (silu),
+// with the K - 1 tokens before the sequence from `hist` (nullptr: zeros), and,
+// with g_t = dy_t act'(z_t) (z formed again from x),
+//   dx_t = sum_j w_j g_{t+j},  dw_j = sum_t g_t x_{t-j},  dbias = sum_t g_t,
+// the dx of the tokens before the sequence being dhist.
+//
+// Memory bound: a wave walks a strip of tokens with V channels a lane, so that
+// each value is read once but for the K - 1 rows in front of a strip (backward:
+// behind it too), which the wave next to it reads at the same time.  The rows
+// before the current one, and in the backward pass the g before it, stay in
+// registers.
+#include "block_ops.h"
+#include "vec_io.h"
+
+namespace prism {
+
+namespace {
+
+constexpr int SC_WAVES = 4;
+
+// sigma, for bf16 results by the hardware's exponential and reciprocal (1 ulp
+// each; the argument's rounding adds 2^-24 of its size).
+template <typename E>
+__device__ inline float sigma(float z) {
+  if constexpr (sizeof(E) == 2) return __builtin_amdgcn_rcpf(1.f + __expf(-z));
+  return 1.f / (1.f + expf(-z));
+}
+
+template <typename E, int V>
+__device__ inline void load_row(const E* p, float (&x)[V]) {
+  typedef typename VecIo<E, V>::raw raw;
+  VecIo<E, V>::unpack(*reinterpret_cast<const raw*>(p), x);
+}
+
+// Row e - start of a sequence, or of the rows before it.
+template <typename E, int V, int K>
+__device__ inline void load_past(const ShortConvArgs& a, const E* x, int b, int t, int c, float (&v)[V]) {
+  if (t >= 0) {
+    load_row<E, V>(x + t * a.sx.t + c, v);
+  } else if (a.hist) {
+    load_row<E, V>(static_cast<const E*>(a.hist) + ((long)b * (K - 1) + K - 1 + t) * a.D + c, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = 0.f;
+  }
+}
+
+// The lane's taps, w [D][K].
+template <typename E, int V, int K>
+__device__ inline void load_taps(const void* w, int c, float (&t)[K][V]) {
+  typedef typename VecIo<E, V>::raw raw;
+  E e[V * K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const raw r = *reinterpret_cast<const raw*>(static_cast<const E*>(w) + (long)c * K + k * V);
+    __builtin_memcpy(e + k * V, &r, sizeof(raw));
+  }
+#pragma unroll
+  for (int j = 0; j < K; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) t[j][i] = to_f(e[i * K + j]);
+}
+
+// A workgroup's waves take neighbouring strips of the same channels.
+struct Place {
+  int strip, c;
+  bool on;
+};
+template <int V>
+__device__ inline Place place_of(int D, int cw) {
+  Place p;
+  const int blk = blockIdx.x / cw;
+  p.strip = __builtin_amdgcn_readfirstlane(blk * SC_WAVES + threadIdx.x / WAVE);
+  p.c = ((blockIdx.x % cw) * WAVE + (threadIdx.x & (WAVE - 1))) * V;
+  p.on = p.c < D;
+  if (!p.on) p.c = 0;
+  return p;
+}
+
+template <typename E>
+__device__ inline const E* sequence_base(const void* p, const TokenSteps& s, const int* cu, const Sequence& q) {
+  return static_cast<const E*>(p) + (cu ? q.start * s.t : q.b * s.b);
+}
+
+// The first K - 1 tokens of a sequence, which read hist, belong to the strip of
+// its first token, whose wave also writes hist_out: hist may be updated in place.
+template <typename E, int V, int K>
+__global__ __launch_bounds__(SC_WAVES * WAVE) void short_conv_kernel(const ShortConvArgs a, int cw, int S) {
+  typedef VecIo<E, V> IO;
+  typedef typename IO::raw raw;
+  constexpr int U = 8;
+  const Place p = place_of<V>(a.D, cw);
+  const int lo = p.strip * S, hi = min(lo + S, a.rows);
+  if (lo >= a.rows) return;
+  float w[K][V], bias[V];
+  load_taps<E, V, K>(a.w, p.c, w);
+  if (a.b) {
+    load_row<E, V>(static_cast<const E*>(a.b) + p.c, bias);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) bias[i] = 0.f;
+  }
+  int row = lo;
+  while (row < hi) {
+    const Sequence q = find_sequence(a.cu, a.B, a.T, a.rows, row);
+    if (q.b < 0 || q.b >= a.B) {
+      row = q.end;
+      continue;
+    }
+    const bool mine = q.start >= lo;
+    if (!mine) row = max(row, min(q.start + K - 1, q.end));
+    const int stop = max(min(q.end, hi), mine ? min(q.end, q.start + K - 1) : 0);
+    if (row >= stop) {
+      row = max(row, stop);
+      continue;
+    }
+    const E* x = sequence_base<E>(a.x, a.sx, a.cu, q);
+    E* y = const_cast<E*>(sequence_base<E>(a.y, a.sy, a.cu, q));
+    float past[K - 1][V];   // past[j]: row - 1 - j
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) load_past<E, V, K>(a, x, q.b, row - q.start - 1 - j, p.c, past[j]);
+    if (mine && a.hist_out) {
+      float last[K - 1][V];
+      const int n = q.end - q.start;
+#pragma unroll
+      for (int m = 0; m < K - 1; ++m) load_past<E, V, K>(a, x, q.b, n - (K - 1) + m, p.c, last[m]);
+#pragma unroll
+      for (int m = 0; m < K - 1; ++m)
+        if (p.on)
+          *reinterpret_cast<raw*>(static_cast<E*>(a.hist_out) + ((long)q.b * (K - 1) + m) * a.D + p.c) =
+              IO::pack(last[m]);
+    }
+    for (; row < stop; row += U) {
+      raw in[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        in[u] = *reinterpret_cast<const raw*>(x + (long)(min(row + u, stop - 1) - q.start) * a.sx.t + p.c);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float now[V], z[V];
+        IO::unpack(in[u], now);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          z[i] = fmaf(w[0][i], now[i], bias[i]);
+#pragma unroll
+          for (int j = 1; j < K; ++j) z[i] = fmaf(w[j][i], past[j - 1][i], z[i]);
+          if (a.silu) z[i] *= sigma<E>(z[i]);
+#pragma unroll
+          for (int j = K - 2; j > 0; --j) past[j][i] = past[j - 1][i];
+          past[0][i] = now[i];
+        }
+        if (row + u < stop && p.on)
+          *reinterpret_cast<raw*>(y + (long)(row + u - q.start) * a.sy.t + p.c) = IO::pack(z);
+      }
+    }
+    row = stop;
+  }
+}
+
+// Rows lo .. hi - 1 of dx come from g up to K - 1 rows further; the sums over
+// tokens take the g of lo .. hi - 1 alone.  The waves' sums are joined through
+// LDS one after the other, and leave as one partial [K + 1][D] a workgroup.
+template <typename E, int V, int K>
+__global__ __launch_bounds__(SC_WAVES * WAVE) void short_conv_bwd_kernel(const ShortConvArgs a, int cw, int S) {
+  typedef VecIo<E, V> IO;
+  typedef typename IO::raw raw;
+  constexpr int U = 4;
+  __shared__ float sm[(K + 1) * V][WAVE];
+  const Place p = place_of<V>(a.D, cw);
+  const int lo = min(p.strip * S, a.rows), hi = min(lo + S, a.rows);
+  float w[K][V], bias[V], dw[K + 1][V];
+  load_taps<E, V, K>(a.w, p.c, w);
+  if (a.b) {
+    load_row<E, V>(static_cast<const E*>(a.b) + p.c, bias);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) bias[i] = 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j <= K; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) dw[j][i] = 0.f;
+  int at = lo;
+  while (at < hi) {
+    const Sequence q = find_sequence(a.cu, a.B, a.T, a.rows, at);
+    if (q.b < 0 || q.b >= a.B) {
+      at = q.end;
+      continue;
+    }
+    const E* x = sequence_base<E>(a.x, a.sx, a.cu, q);
+    const E* dy = sequence_base<E>(a.dy, a.sy, a.cu, q);
+    E* dx = const_cast<E*>(sequence_base<E>(a.dx, a.sd, a.cu, q));
+    const int own = min(q.end, hi), stop = own + K - 1;   // rows of g, zero from q.end on
+    float past[K - 1][V], gp[K - 1][V];
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+      load_past<E, V, K>(a, x, q.b, at - q.start - 1 - j, p.c, past[j]);
+#pragma unroll
+      for (int i = 0; i < V; ++i) gp[j][i] = 0.f;
+    }
+    for (int row = at; row < stop; row += U) {
+      raw in[U], gr[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const long t = min(row + u, q.end - 1) - q.start;
+        in[u] = *reinterpret_cast<const raw*>(x + t * a.sx.t + p.c);
+        gr[u] = *reinterpret_cast<const raw*>(dy + t * a.sy.t + p.c);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int r = row + u;
+        float now[V], g[V], out[V];
+        IO::unpack(in[u], now);
+        IO::unpack(gr[u], g);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          if (a.silu) {
+            float z = fmaf(w[0][i], now[i], bias[i]);
+#pragma unroll
+            for (int j = 1; j < K; ++j) z = fmaf(w[j][i], past[j - 1][i], z);
+            const float s = sigma<E>(z);
+            g[i] *= s * fmaf(z, 1.f - s, 1.f);
+          }
+          if (r >= q.end) g[i] = 0.f;
+          if (r < own) {
+            dw[0][i] = fmaf(g[i], now[i], dw[0][i]);
+#pragma unroll
+            for (int j = 1; j < K; ++j) dw[j][i] = fmaf(g[i], past[j - 1][i], dw[j][i]);
+            dw[K][i] += g[i];
+          }
+          // dx of row r - (K - 1)
+          out[i] = w[K - 1][i] * g[i];
+#pragma unroll
+          for (int j = 0; j < K - 1; ++j) out[i] = fmaf(w[K - 2 - j][i], gp[j][i], out[i]);
+#pragma unroll
+          for (int j = K - 2; j > 0; --j) {
+            past[j][i] = past[j - 1][i];
+            gp[j][i] = gp[j - 1][i];
+          }
+          past[0][i] = now[i];
+          gp[0][i] = g[i];
+        }
+        const int e = r - (K - 1);
+        if (r < stop && p.on) {
+          if (e >= at) {
+            *reinterpret_cast<raw*>(dx + (long)(e - q.start) * a.sd.t + p.c) = IO::pack(out);
+          } else if (at == q.start && a.dhist) {
+            float* d = a.dhist + ((long)q.b * (K - 1) + (r - q.start)) * a.D + p.c;
+#pragma unroll
+            for (int i = 0; i < V; ++i) d[i] = out[i];
+          }
+        }
+      }
+    }
+    at = own;
+  }
+  const int wave = threadIdx.x / WAVE, lane = threadIdx.x & (WAVE - 1);
+  for (int k = 0; k < SC_WAVES; ++k) {
+    __syncthreads();
+    if (wave != k) continue;
+#pragma unroll
+    for (int j = 0; j <= K; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float& s = sm[j * V + i][lane];
+        s = k ? s + dw[j][i] : dw[j][i];
+        if (k == SC_WAVES - 1 && p.on) a.part[((long)(blockIdx.x / cw) * (K + 1) + j) * a.D + p.c + i] = s;
+      }
+  }
+}
+
+// Tokens a strip: 32, fewer (to 4) where that leaves under two waves a SIMD of
+// 4 channels a lane.
+int strip_tokens(int rows, int D) {
+  const long waves = (D + 255) / 256;
+  int S = 32;
+  while (S > 4 && (rows + S - 1L) / S * waves < 2048) S /= 2;
+  return S;
+}
+int parts_of(int rows, int S) { return (int)((rows + S * SC_WAVES - 1L) / (S * SC_WAVES)); }
+
+// (a dense sequence of at most 8 tokens is a strip of its own, with others where
+// a launch would have 2^32 threads)
+template <typename E, int V, int K>
+hipError_t run_fwd(const ShortConvArgs& a, hipStream_t s) {
+  const long cw = (a.D + WAVE * V - 1) / (WAVE * V);
+  int S = !a.cu && a.T <= 8 ? a.T : strip_tokens(a.rows, a.D);
+  while (cw * parts_of(a.rows, S) >= (1L << 23)) S *= 2;
+  hipLaunchKernelGGL((short_conv_kernel<E, V, K>), dim3((unsigned)(cw * parts_of(a.rows, S))), dim3(SC_WAVES * WAVE), 0,
+                     s, a, (int)cw, S);
+  return hipGetLastError();
+}
+template <typename E, int V, int K>
+hipError_t run_bwd(const ShortConvArgs& a, hipStream_t s) {
+  const int cw = (a.D + WAVE * V - 1) / (WAVE * V), S = strip_tokens(a.rows, a.D), parts = parts_of(a.rows, S);
+  if (parts > 0) {
+    hipLaunchKernelGGL((short_conv_bwd_kernel<E, V, K>), dim3((unsigned)cw * parts), dim3(SC_WAVES * WAVE), 0, s, a, cw,
+                       S);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const long stride = (long)(K + 1) * a.D;
+  const hipError_t e = launch_column_sums(a.part, parts, stride, K * a.D, K, a.dw, s);
+  if (e != hipSuccess || !a.db) return e;
+  return launch_column_sums(a.part + (long)K * a.D, parts, stride, a.D, 0, a.db, s);
+}
+
+// Channels a lane: 16 bytes of them where every row starts at a multiple of 16
+// bytes and a wave's 64 lanes find enough channels, else 8 bytes, else one.
+template <typename E, bool BWD, int K>
+hipError_t run_k(const ShortConvArgs& a, hipStream_t s) {
+  uintptr_t p = (uintptr_t)a.x | (uintptr_t)a.w | (uintptr_t)a.b | (uintptr_t)a.hist | (uintptr_t)a.y |
+                (uintptr_t)a.hist_out | (uintptr_t)a.dy | (uintptr_t)a.dx;
+  long m = a.D | a.sx.b | a.sx.t | a.sy.b | a.sy.t;
+  if (BWD) m |= a.sd.b | a.sd.t;
+  auto fits = [&](int V) { return m % V == 0 && p % (V * sizeof(E)) == 0; };
+  if constexpr (sizeof(E) == 2) {
+    if (fits(8) && a.D >= 512) return BWD ? run_bwd<E, 8, K>(a, s) : run_fwd<E, 8, K>(a, s);
+  }
+  if (fits(4)) return BWD ? run_bwd<E, 4, K>(a, s) : run_fwd<E, 4, K>(a, s);
+  return BWD ? run_bwd<E, 1, K>(a, s) : run_fwd<E, 1, K>(a, s);
+}
+template <typename E, bool BWD>
+hipError_t run(const ShortConvArgs& a, hipStream_t s) {
+  if (a.K == 2) return run_k<E, BWD, 2>(a, s);
+  if (a.K == 3) return run_k<E, BWD, 3>(a, s);
+  return run_k<E, BWD, 4>(a, s);
+}
+
+}  // namespace
+
+size_t short_conv_part_bytes(int rows, int D, int K) {
+  return (size_t)parts_of(rows, strip_tokens(rows, D)) * (K + 1) * D * sizeof(float);
+}
+
+template <typename E>
+hipError_t launch_short_conv(const ShortConvArgs& a, hipStream_t s) {
+  return run<E, false>(a, s);
+}
+template <typename E>
+hipError_t launch_short_conv_bwd(const ShortConvArgs& a, hipStream_t s) {
+  return run<E, true>(a, s);
+}
+template hipError_t launch_short_conv<bf16>(const ShortConvArgs&, hipStream_t);
+template hipError_t launch_short_conv<float>(const ShortConvArgs&, hipStream_t);
+template hipError_t launch_short_conv_bwd<bf16>(const ShortConvArgs&, hipStream_t);
+template hipError_t launch_short_conv_bwd<float>(const ShortConvArgs&, hipStream_t);
+
+}  // namespace prism

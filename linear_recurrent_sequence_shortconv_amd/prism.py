@@ -28,7 +28,11 @@ EXPORTS = ("prism_forward_workspace", "prism_backward_workspace",
            "prism_qk_norm", "prism_qk_norm_backward_workspace", "prism_qk_norm_backward",
            "prism_linear_attention_workspace", "prism_linear_attention_packed_workspace",
            "prism_linear_attention",
-           "prism_linear_attention_backward", "prism_linear_attention_step")
+           "prism_linear_attention_backward", "prism_linear_attention_step",
+           "prism_layer_norm", "prism_layer_norm_backward_workspace", "prism_layer_norm_backward",
+           "prism_short_conv", "prism_short_conv_backward_workspace", "prism_short_conv_backward",
+           "prism_gated_recurrence_workspace", "prism_gated_recurrence",
+           "prism_gated_recurrence_backward", "prism_gated_recurrence_step")
 
 
 class Desc(ctypes.Structure):
@@ -58,6 +62,25 @@ class LinearAttentionDesc(ctypes.Structure):
                 ("dtype", ctypes.c_int), ("scale", ctypes.c_float),
                 ("packed_tokens", ctypes.c_int), ("q", Strides), ("k", Strides), ("v", Strides),
                 ("o", Strides), ("g", Strides)]
+
+
+class LayerNormDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int), ("D", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("norm", ctypes.c_int), ("eps", ctypes.c_float),
+                ("x", Strides), ("r", Strides), ("y", Strides), ("h", Strides)]
+
+
+class ShortConvDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("D", ctypes.c_int), ("K", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("activation", ctypes.c_int),
+                ("packed_tokens", ctypes.c_int), ("x", Strides), ("y", Strides), ("dx", Strides)]
+
+
+class GatedRecurrenceDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("D", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("gate", ctypes.c_int), ("packed_tokens", ctypes.c_int),
+                ("x", Strides), ("f", Strides), ("i", Strides), ("h", Strides), ("dh", Strides),
+                ("dx", Strides), ("df", Strides), ("di", Strides)]
 
 
 _lib = None
@@ -109,7 +132,18 @@ def lib():
         L.prism_linear_attention.argtypes = [ld] + [_P] * 9 + [size, _P]
         L.prism_linear_attention_backward.argtypes = [ld] + [_P] * 14 + [size, _P]
         L.prism_linear_attention_step.argtypes = [ld] + [_P] * 8
-        for f in EXPORTS[-8:]:
+        out_size = ctypes.POINTER(size)
+        L.prism_layer_norm.argtypes = [_P] * 8
+        L.prism_layer_norm_backward_workspace.argtypes = [_P, ctypes.c_int, out_size]
+        L.prism_layer_norm_backward.argtypes = [_P] * 9 + [size, _P]
+        L.prism_short_conv.argtypes = [_P] * 9
+        L.prism_short_conv_backward_workspace.argtypes = [_P, ctypes.c_int, out_size]
+        L.prism_short_conv_backward.argtypes = [_P] * 12 + [size, _P]
+        L.prism_gated_recurrence_workspace.argtypes = [_P, ctypes.c_int, ctypes.c_int, out_size]
+        L.prism_gated_recurrence.argtypes = [_P] * 10 + [size, _P]
+        L.prism_gated_recurrence_backward.argtypes = [_P] * 16 + [size, _P]
+        L.prism_gated_recurrence_step.argtypes = [_P] * 9
+        for f in EXPORTS[EXPORTS.index("prism_qk_norm"):]:
             getattr(L, f).restype = ctypes.c_int
         L.prism_status_string.argtypes = [ctypes.c_int]
         L.prism_status_string.restype = ctypes.c_char_p
@@ -755,6 +789,318 @@ def linear_attention_step(q, k, v, g, S, S_out=None, scale=1.0, o=None):
         _LA_DESC.pack(*desc, *_steps(o, "o"), *gs), _addr(q), _addr(k), _addr(v), _addr(g),
         _addr(S), _addr(S if S_out is None else S_out), _addr(o), _stream(q.device)))
     return o
+
+
+# --------------------------------------------------------------------------
+# layer norm, short convolution, gated recurrence
+# --------------------------------------------------------------------------
+LAYER_NORMS = {"rms": 1, "layer": 2}
+CONV_ACTIVATIONS = {"identity": 1, "silu": 2}
+GATES = {"log": 0, "sigmoid": 1, "power": 2}
+
+_LN_DESC = struct.Struct("=6if4x12q")
+_SC_DESC = struct.Struct("=7i4x9q")
+_GR_DESC = struct.Struct("=6i24q")
+assert _LN_DESC.size == ctypes.sizeof(LayerNormDesc)
+assert _SC_DESC.size == ctypes.sizeof(ShortConvDesc)
+assert _GR_DESC.size == ctypes.sizeof(GatedRecurrenceDesc)
+# workspace bytes of the backward passes and of the recurrence by descriptor
+_block_bytes = {}
+
+
+def _block_workspace(query, desc, args, device):
+    key = (query, desc, args)
+    size = _block_bytes.get(key)
+    if size is None:
+        n = ctypes.c_size_t(0)
+        _check(getattr(lib(), query)(desc, *args, ctypes.byref(n)))
+        if len(_block_bytes) >= 4096:
+            _block_bytes.clear()
+        size = _block_bytes[key] = n.value
+    return _workspace(size, device)[1] if size else None
+
+
+def _size(workspace):
+    return 0 if workspace is None else workspace.numel()
+
+
+def _vector(t, name, dtype, device, shape):
+    """A small operand: type, device, shape, and contiguous."""
+    _like(t, name, dtype, device, shape)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _row_steps(t, name):
+    """Steps of rows [D], [N,D], [B,T,D] or [B,T,H,D] as (batch, token, head),
+    dimensions of one entry 0."""
+    n, s = t.shape, t.stride()
+    if s[-1] != 1 and n[-1] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    steps = tuple([a if m > 1 else 0 for a, m in zip(s[:-1], n)])
+    return (0, 0, 0)[len(steps):] + steps
+
+
+def _norm_desc(x, norm, eps):
+    if norm not in LAYER_NORMS:
+        raise ValueError(f"norm must be one of {sorted(LAYER_NORMS)}, got {norm!r}")
+    if not 1 <= x.dim() <= 4:
+        raise ValueError(f"x: expected 1 to 4 dimensions, got shape {tuple(x.shape)}")
+    shape = (1, 1, 1, 1)[x.dim():] + tuple(x.shape)
+    return (*shape, _dtype_code(x), LAYER_NORMS[norm], eps, *_row_steps(x, "x"))
+
+
+def layer_norm(x, w=None, b=None, residual=None, norm="layer", eps=1e-5, y=None, h=None):
+    """Rows normalised over the last dimension, with the residual sum in front
+    (prism_layer_norm): s = x + residual, y = (s - mean) / deviation * w + b
+    (norm "rms": by the root mean square alone).  Returns (y, h), h the sum, or
+    None without a residual.
+
+    x, residual [.., D] of one to four dimensions in bf16 or fp32 (contiguous
+    last dimension, views allowed), w, b [D] or None.  y, h: where the results go
+    (new contiguous tensors by default; each may be x or residual: in place)."""
+    desc = _norm_desc(x, norm, eps)
+    dt, dev = x.dtype, x.get_device()
+    for name, t in (("w", w), ("b", b)):
+        if t is not None:
+            _vector(t, name, dt, dev, x.shape[-1:])
+    _on_gpu(x)
+    rs = hs = _NO_STEPS
+    if residual is not None:
+        _like(residual, "residual", dt, dev, x.shape)
+        rs = _row_steps(residual, "residual")
+        h = _out(x, h, "h")
+        hs = _row_steps(h, "h")
+    elif h is not None:
+        raise ValueError("h without residual")
+    y = _out(x, y, "y")
+    _check(lib().prism_layer_norm(
+        _LN_DESC.pack(*desc, *rs, *_row_steps(y, "y"), *hs), _addr(x), _addr(residual), _addr(w),
+        _addr(b), _addr(y), _addr(h), _stream(x.device)))
+    return y, h
+
+
+def layer_norm_backward(x, dy, w=None, dh=None, norm="layer", eps=1e-5, need_db=False, dx=None,
+                        workspace=None):
+    """Gradients of <dy, y> + <dh, h> of layer_norm, from x, the rows that were
+    normalised (the h that layer_norm returned where there was a residual).
+    Returns a dict: dx (the gradient of x and of the residual alike; into dx when
+    given, which may be dy, dh or x), dw (fp32 [D]) with w, db (fp32 [D]) when
+    need_db."""
+    desc = _norm_desc(x, norm, eps)
+    dt, dev = x.dtype, x.get_device()
+    _like(dy, "dy", dt, dev, x.shape)
+    hs = _NO_STEPS
+    if dh is not None:
+        _like(dh, "dh", dt, dev, x.shape)
+        hs = _row_steps(dh, "dh")
+    if w is not None:
+        _vector(w, "w", dt, dev, x.shape[-1:])
+    _on_gpu(x)
+    out = {"dx": _out(x, dx, "dx")}
+    if w is not None:
+        out["dw"] = x.new_empty(x.shape[-1:], dtype=torch.float32)
+    if need_db:
+        out["db"] = x.new_empty(x.shape[-1:], dtype=torch.float32)
+    packed = _LN_DESC.pack(*desc, *hs, *_row_steps(dy, "dy"), *_row_steps(out["dx"], "dx"))
+    if workspace is None and len(out) > 1:
+        workspace = _block_workspace("prism_layer_norm_backward_workspace", packed, (1,), x.device)
+    _check(lib().prism_layer_norm_backward(
+        packed, _addr(x), _addr(w), _addr(dy), _addr(dh), _addr(out["dx"]), _addr(out.get("dw")),
+        _addr(out.get("db")), _addr(workspace), _size(workspace), _stream(x.device)))
+    return out
+
+
+def _token_steps(t, name):
+    """Steps of [B,T,D] or, packed, [N,D] as (batch, token, 0)."""
+    _, b, s = _row_steps(t, name)
+    return b, s, 0
+
+
+def _batch(x, cu_seqlens):
+    """B, T, D, rows of a packed batch, of x [B,T,D] or [N,D] with cu_seqlens."""
+    if cu_seqlens is None:
+        if x.dim() != 3:
+            raise ValueError(f"x: expected [B, T, D], got shape {tuple(x.shape)}")
+        return (*x.shape, 0)
+    if (cu_seqlens.dtype != torch.int32 or cu_seqlens.device != x.device or cu_seqlens.dim() != 1
+            or cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous()):
+        raise ValueError("cu_seqlens must be a contiguous 1-D int32 tensor of B + 1 entries on x's device")
+    if x.dim() != 2:
+        raise ValueError(f"x: expected [N, D] with cu_seqlens, got shape {tuple(x.shape)}")
+    return cu_seqlens.numel() - 1, 0, x.shape[1], x.shape[0]
+
+
+def _conv_desc(x, w, b, hist, activation, cu_seqlens):
+    if activation not in CONV_ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(CONV_ACTIVATIONS)}, got {activation!r}")
+    B, T, D, N = _batch(x, cu_seqlens)
+    dt, dev = x.dtype, x.get_device()
+    if w.dim() != 2:
+        raise ValueError(f"w: expected [D, K], got shape {tuple(w.shape)}")
+    K = w.shape[1]
+    _vector(w, "w", dt, dev, (D, K))
+    if b is not None:
+        _vector(b, "b", dt, dev, (D,))
+    if hist is not None:
+        _vector(hist, "hist", dt, dev, (B, K - 1, D))
+    return (B, T, D, K, _dtype_code(x), CONV_ACTIVATIONS[activation], N, *_token_steps(x, "x"))
+
+
+def short_conv(x, w, b=None, hist=None, activation="identity", cu_seqlens=None, y=None,
+               hist_out=None):
+    """Depthwise causal convolution over the last K tokens (prism_short_conv):
+    z_t = b + sum_j w[:, j] x_{t-j}, y = z, or z sigmoid(z) with "silu".  Returns
+    y.
+
+    x [B,T,D] in bf16 or fp32 (views of a fused projection allowed), w [D,K], K
+    from 2 to 4, b [D] or None; hist [B,K-1,D], the tokens before the sequence,
+    oldest first (None: zeros); hist_out (same shape, may be hist) receives the
+    last ones for the next call.  cu_seqlens (int32 [B+1]) packs sequences: x is
+    [N,D].  y: where the result goes (a new tensor by default)."""
+    desc = _conv_desc(x, w, b, hist, activation, cu_seqlens)
+    if hist_out is not None:
+        _vector(hist_out, "hist_out", x.dtype, x.get_device(), (desc[0], desc[3] - 1, desc[2]))
+    _on_gpu(x)
+    y = _out(x, y, "y")
+    _check(lib().prism_short_conv(
+        _SC_DESC.pack(*desc, *_token_steps(y, "y"), 0, 0, 0), _addr(x), _addr(w), _addr(b),
+        _addr(hist), _addr(cu_seqlens), _addr(y), _addr(hist_out), _stream(x.device)))
+    return y
+
+
+def short_conv_backward(x, w, dy, b=None, hist=None, activation="identity", cu_seqlens=None,
+                        need_dhist=False, dx=None, workspace=None):
+    """Gradients of <dy, y> of short_conv on the same inputs.  Returns a dict: dx
+    (into dx when given), dw (fp32 [D,K]), db (fp32 [D]) with b, dhist (fp32
+    [B,K-1,D]) when need_dhist."""
+    desc = _conv_desc(x, w, b, hist, activation, cu_seqlens)
+    _like(dy, "dy", x.dtype, x.get_device(), x.shape)
+    _on_gpu(x)
+    B, K, D = desc[0], desc[3], desc[2]
+    f32 = torch.float32
+    out = {"dx": _out(x, dx, "dx"), "dw": x.new_empty((D, K), dtype=f32)}
+    if b is not None:
+        out["db"] = x.new_empty((D,), dtype=f32)
+    if need_dhist:
+        out["dhist"] = x.new_empty((B, K - 1, D), dtype=f32)
+    packed = _SC_DESC.pack(*desc, *_token_steps(dy, "dy"), *_token_steps(out["dx"], "dx"))
+    if workspace is None:
+        workspace = _block_workspace("prism_short_conv_backward_workspace", packed,
+                                     (int(cu_seqlens is not None),), x.device)
+    _check(lib().prism_short_conv_backward(
+        packed, _addr(x), _addr(w), _addr(b), _addr(hist), _addr(cu_seqlens), _addr(dy),
+        _addr(out["dx"]), _addr(out["dw"]), _addr(out.get("db")), _addr(out.get("dhist")),
+        _addr(workspace), _size(workspace), _stream(x.device)))
+    return out
+
+
+def _rec_desc(x, f, i, lam, gate, states, cu_seqlens):
+    """The descriptor's fields up to the steps of i, and the shape of a state."""
+    if gate not in GATES:
+        raise ValueError(f"gate must be one of {sorted(GATES)}, got {gate!r}")
+    B, T, D, N = _batch(x, cu_seqlens)
+    dt, dev = x.dtype, x.get_device()
+    _like(f, "f", dt, dev, x.shape)
+    si = _NO_STEPS
+    if i is not None:
+        _like(i, "i", dt, dev, x.shape)
+        si = _token_steps(i, "i")
+    if (lam is not None) != (gate == "power"):
+        raise ValueError('lam goes with the gate "power", and with it alone')
+    if lam is not None:
+        _vector(lam, "lam", torch.float32, dev, (D,))
+    for name, t in states:
+        if t is not None:
+            _vector(t, name, torch.float32, dev, (B, D))
+    return (B, T, D, _dtype_code(x), GATES[gate], N, *_token_steps(x, "x"), *_token_steps(f, "f"),
+            *si), (B, D)
+
+
+_NO_GRADS = (0,) * 12
+
+
+def gated_recurrence(x, f, i=None, lam=None, h0=None, gate="sigmoid", cu_seqlens=None, h=None,
+                     hT=None, need_state=True, workspace=None):
+    """h_t = a_t h_{t-1} + u_t channel by channel, with its gates
+    (prism_gated_recurrence).  Returns (h, h_T), or (h, None) with need_state
+    false.  With s = sigmoid(i), or 1 without i:
+
+        "log"      a = exp(f),                u = s x
+        "sigmoid"  a = sigmoid(f),            u = (1 - a) s x
+        "power"    a = exp(-lam sigmoid(f)),  u = sqrt(1 - a^2) s x
+
+    x, f, i [B,T,D] in bf16 or fp32 (views of a fused projection allowed), lam
+    fp32 [D] >= 0; h0 fp32 [B,D] or None.  cu_seqlens (int32 [B+1]) packs
+    sequences: token tensors [N,D].  h, hT: where the results go (new tensors by
+    default; hT may be h0)."""
+    if hT is not None and not need_state:
+        raise ValueError("hT given, but need_state is false")
+    desc, state = _rec_desc(x, f, i, lam, gate, (("h0", h0), ("hT", hT)), cu_seqlens)
+    _on_gpu(x)
+    h = _out(x, h, "h")
+    if hT is None and need_state:
+        hT = x.new_empty(state, dtype=torch.float32)
+    packed = _GR_DESC.pack(*desc, *_token_steps(h, "h"), *_NO_GRADS)
+    if workspace is None:
+        workspace = _block_workspace("prism_gated_recurrence_workspace", packed,
+                                     (int(cu_seqlens is not None), 0), x.device)
+    _check(lib().prism_gated_recurrence(
+        packed, _addr(x), _addr(f), _addr(i), _addr(lam), _addr(h0), _addr(cu_seqlens), _addr(h),
+        _addr(hT), _addr(workspace), _size(workspace), _stream(x.device)))
+    return h, hT
+
+
+def gated_recurrence_backward(x, f, h, dh, i=None, lam=None, h0=None, dhT=None, gate="sigmoid",
+                              need_dh0=False, cu_seqlens=None, dx=None, df=None, di=None,
+                              workspace=None):
+    """Gradients of <dh, h> + <dhT, h_T> of gated_recurrence from its inputs and
+    its output h.  Returns a dict: dx, df (input type; into dx, df when given), di
+    with i, dlam (fp32 [D]) with lam, dh0 (fp32 [B,D]) when need_dh0."""
+    desc, state = _rec_desc(x, f, i, lam, gate, (("h0", h0), ("dhT", dhT)), cu_seqlens)
+    dt, dev = x.dtype, x.get_device()
+    _like(h, "h", dt, dev, x.shape)
+    _like(dh, "dh", dt, dev, x.shape)
+    if di is not None and i is None:
+        raise ValueError("di without i")
+    _on_gpu(x)
+    out = {"dx": _out(x, dx, "dx"), "df": _out(x, df, "df")}
+    steps = (*_token_steps(h, "h"), *_token_steps(dh, "dh"), *_token_steps(out["dx"], "dx"),
+             *_token_steps(out["df"], "df"))
+    if i is not None:
+        out["di"] = _out(x, di, "di")
+        steps += _token_steps(out["di"], "di")
+    else:
+        steps += _NO_STEPS
+    if lam is not None:
+        out["dlam"] = torch.empty_like(lam)
+    if need_dh0:
+        out["dh0"] = x.new_empty(state, dtype=torch.float32)
+    packed = _GR_DESC.pack(*desc, *steps)
+    if workspace is None:
+        workspace = _block_workspace("prism_gated_recurrence_workspace", packed,
+                                     (int(cu_seqlens is not None), 1), x.device)
+    _check(lib().prism_gated_recurrence_backward(
+        packed, _addr(x), _addr(f), _addr(i), _addr(lam), _addr(h0), _addr(cu_seqlens), _addr(h),
+        _addr(dh), _addr(dhT), _addr(out["dx"]), _addr(out["df"]), _addr(out.get("di")),
+        _addr(out.get("dlam")), _addr(out.get("dh0")), _addr(workspace), _size(workspace),
+        _stream(x.device)))
+    return out
+
+
+def gated_recurrence_step(x, f, state, i=None, lam=None, gate="sigmoid", state_out=None, h=None):
+    """The T tokens of each sequence, x [B,T,D], one after another from `state`
+    fp32 [B,D] (prism_gated_recurrence_step; T = 1: a decode step).  The state
+    after them goes to state_out, or into state itself when that is None.
+    Returns h."""
+    desc, _ = _rec_desc(x, f, i, lam, gate, (("state", state), ("state_out", state_out)), None)
+    _on_gpu(x)
+    h = _out(x, h, "h")
+    _check(lib().prism_gated_recurrence_step(
+        _GR_DESC.pack(*desc, *_token_steps(h, "h"), *_NO_GRADS), _addr(x), _addr(f), _addr(i),
+        _addr(lam), _addr(state), _addr(state if state_out is None else state_out), _addr(h),
+        _stream(x.device)))
+    return h
 
 
 class KernelTimer:
