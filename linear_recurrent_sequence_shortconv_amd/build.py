@@ -36,7 +36,9 @@ SOURCES = [
     "state.hip",
     "step.hip",
     "refine_bwd.hip",
-    "recurrence.hip",
+    "recurrence_bf16.hip",
+    "recurrence_bf16_single.hip",
+    "recurrence_f32.hip",
     "layer_norm.hip",
     "short_conv.hip",
     "qk_norm.hip",
@@ -45,6 +47,7 @@ SOURCES = [
     "chunk_bwd.hip",
     "prism_api.cpp",
     "operators_api.cpp",
+    "recurrence.hip",
     "block_ops.hip",
     "block_ops_api.cpp",
 ]

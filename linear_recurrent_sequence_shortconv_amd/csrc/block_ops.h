@@ -48,6 +48,7 @@ template <typename E> hipError_t launch_short_conv_bwd(const ShortConvArgs& a, h
 size_t short_conv_part_bytes(int rows, int D, int K);
 
 // --------------------------------------------------------- gated recurrence
+// (part: set by the launch)
 enum Gate { GATE_LOG, GATE_SIGMOID, GATE_POWER };
 struct RecurrenceArgs {
   int B, T, D;
@@ -66,9 +67,9 @@ struct RecurrenceArgs {
   float *dh0, *dlam, *part;
   TokenSteps sdh, sdx, sdf, sdi;
 };
-template <typename E> hipError_t launch_recurrence(const RecurrenceArgs& a, hipStream_t s);
-template <typename E> hipError_t launch_recurrence_bwd(const RecurrenceArgs& a, hipStream_t s);
-size_t recurrence_part_bytes(int B, int D);
+hipError_t launch_recurrence(const RecurrenceArgs& a, bool f32, bool bwd, void* ws, hipStream_t s);
+hipError_t launch_recurrence_step(const RecurrenceArgs& a, bool f32, hipStream_t s);
+size_t recurrence_bytes(const RecurrenceArgs& a, bool packed, bool bwd);   // of the workspace
 
 // ---------------------------------------------------------------- sequences
 // dst[b] = src[b] (nullptr: zeros), n 4- or 2-byte values each, for every

@@ -22,8 +22,7 @@ std::string num(long long x) { return std::to_string(x); }
 Strides strides(const prism_strides& s) { return Strides{(long)s.batch, (long)s.token, (long)s.head}; }
 TokenSteps steps(const prism_strides& s) { return TokenSteps{(long)s.batch, (long)s.token}; }
 
-// Rows of a launch, and values of a token tensor (under 2^32 threads at one for
-// every 32 values, addresses far within 64 bits).
+// Rows of a launch, and values of a token tensor.
 constexpr long long MOST_ROWS = 1LL << 30, MOST_VALUES = 1LL << 37;
 
 prism_status check_elem(const void* p, const char* name, bool required, int size) {
@@ -169,7 +168,8 @@ prism_status check_batch(int B, int T, int D, prism_dtype dtype, int packed_toke
   if (packed && packed_tokens < 0) return fail(PRISM_ERR_SHAPE, "packed_tokens must be >= 0 with cu_seqlens");
   const long long rows = packed ? packed_tokens : (long long)B * T;
   if (rows > MOST_ROWS) return fail(PRISM_ERR_SHAPE, "a batch has at most " + num(MOST_ROWS) + " tokens");
-  if (rows * D > MOST_VALUES || (long long)B * D >= (1LL << 31)) return fail(PRISM_ERR_SHAPE, "problem too large");
+  // (a launch has under 2^32 threads: at most 512 for 64 rows of 64 channels)
+  if (rows * D > MOST_VALUES || (rows + 63) / 64 * ((D + 63) / 64) > (1LL << 22) || (long long)B * D >= (1LL << 31)) return fail(PRISM_ERR_SHAPE, "problem too large");
   return check_dtype(dtype);
 }
 
@@ -349,8 +349,9 @@ prism_status rec_forward(const prism_gated_recurrence_desc* desc, const void* x,
   a.h0 = h0;
   a.h = h;
   a.hT = hT;
-  HIP_TRY("recurrence", stream, d.dtype == PRISM_BF16 ? prism::launch_recurrence<prism::bf16>(a, stream)
-                                                      : prism::launch_recurrence<float>(a, stream));
+  const size_t need = prism::recurrence_bytes(a, packed, false);
+  if (need > 0 && (st = check_buffer(workspace, workspace_bytes, need, "workspace")) != PRISM_OK) return st;
+  HIP_TRY("recurrence", stream, prism::launch_recurrence(a, d.dtype == PRISM_F32, false, workspace, stream));
   return PRISM_OK;
 }
 
@@ -380,7 +381,7 @@ prism_status rec_backward(const prism_gated_recurrence_desc* desc, const void* x
   if ((st = check_token_steps(d.dx, "dx", d.B, d.T, a.rows, packed, true)) != PRISM_OK) return st;
   if ((st = check_token_steps(d.df, "df", d.B, d.T, a.rows, packed, true)) != PRISM_OK) return st;
   if (i && (st = check_token_steps(d.di, "di", d.B, d.T, a.rows, packed, true)) != PRISM_OK) return st;
-  const size_t need = d.gate == PRISM_GATE_POWER ? prism::recurrence_part_bytes(d.B, d.D) : 0;
+  const size_t need = prism::recurrence_bytes(a, packed, true);
   if (need > 0 && (st = check_buffer(workspace, workspace_bytes, need, "workspace")) != PRISM_OK) return st;
   a.cu = cu;
   a.x = x;
@@ -396,9 +397,7 @@ prism_status rec_backward(const prism_gated_recurrence_desc* desc, const void* x
   a.di = i ? di : nullptr;
   a.dlam = dlam;
   a.dh0 = dh0;
-  a.part = static_cast<float*>(workspace);
-  HIP_TRY("recurrence_bwd", stream, d.dtype == PRISM_BF16 ? prism::launch_recurrence_bwd<prism::bf16>(a, stream)
-                                                          : prism::launch_recurrence_bwd<float>(a, stream));
+  HIP_TRY("recurrence_bwd", stream, prism::launch_recurrence(a, d.dtype == PRISM_F32, true, workspace, stream));
   return PRISM_OK;
 }
 
@@ -462,7 +461,7 @@ prism_status prism_gated_recurrence_workspace(const prism_gated_recurrence_desc*
     prism::RecurrenceArgs a;
     const prism_status st = check_rec(desc, packed != 0, &a);
     if (st != PRISM_OK) return st;
-    if (backward && desc->gate == PRISM_GATE_POWER) *bytes = prism::recurrence_part_bytes(desc->B, desc->D);
+    *bytes = prism::recurrence_bytes(a, packed != 0, backward != 0);
     return PRISM_OK;
   });
 }
@@ -505,8 +504,7 @@ prism_status prism_gated_recurrence_step(const prism_gated_recurrence_desc* desc
     a.h0 = state;
     a.h = h;
     a.hT = state_out;
-    HIP_TRY("recurrence_step", stream, d.dtype == PRISM_BF16 ? prism::launch_recurrence<prism::bf16>(a, stream)
-                                                             : prism::launch_recurrence<float>(a, stream));
+    HIP_TRY("recurrence_step", stream, prism::launch_recurrence_step(a, d.dtype == PRISM_F32, stream));
     return PRISM_OK;
   });
 }

@@ -5,8 +5,10 @@
 // dhT added at the last token, dh0 = a_1 g_1.  h_{t-1} is read from the forward
 // pass's output.
 //
-// A lane takes V channels of one sequence and walks its tokens.
-#include "recurrence_kernel.h"
+// Dispatch: whole sequences and the backward pass go through tiles
+// (recurrence_tile.h) after a small kernel that readies their words; sequences of
+// a few tokens, the single-token step among them, token by token.
+#include "recurrence_tile.h"
 
 namespace prism {
 
@@ -23,30 +25,10 @@ __device__ inline void store_v(void* p, long at, const float (&x)[V]) {
   *reinterpret_cast<raw*>(static_cast<E*>(p) + at) = VecIo<E, V>::pack(x);
 }
 
-// First row and tokens of sequence b (packed: the largest clamped offset so far
-// to the next), by every thread of a workgroup.
-__device__ inline void sequence_rows(const RecurrenceArgs& a, int b, int* sm, int& start, int& n) {
-  if (!a.cu) {
-    start = b * a.T;
-    n = a.T;
-    return;
-  }
-  int m = 0;
-  for (int j = threadIdx.x; j <= b; j += 256) m = max(m, min(a.cu[j], a.rows));
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) m = max(m, __shfl_xor(m, o));
-  if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = m;
-  __syncthreads();
-  start = max(max(sm[0], sm[1]), max(sm[2], sm[3]));
-  n = max(min(a.cu[b + 1], a.rows) - start, 0);
-}
-
+// A lane takes V channels of one dense sequence and walks its tokens.
 template <typename E, int V, int G, bool INP>
 __global__ __launch_bounds__(256) void recurrence_walk_kernel(const RecurrenceArgs a, int cb) {
-  __shared__ int sm[4];
   const int b = blockIdx.x / cb, c = ((blockIdx.x % cb) * 256 + threadIdx.x) * V;
-  int start, n;
-  sequence_rows(a, b, sm, start, n);
   if (c >= a.D) return;
   float h[V], lam[V];
 #pragma unroll
@@ -54,8 +36,8 @@ __global__ __launch_bounds__(256) void recurrence_walk_kernel(const RecurrenceAr
     h[v] = a.h0 ? a.h0[(long)b * a.D + c + v] : 0.f;
     lam[v] = G == GATE_POWER ? a.lam[c + v] : 0.f;
   }
-  auto at = [&](const TokenSteps& s, int t) { return (a.cu ? (start + t) * s.t : b * s.b + t * s.t) + c; };
-  for (int t = 0; t < n; ++t) {
+  auto at = [&](const TokenSteps& s, int t) { return b * s.b + t * s.t + c; };
+  for (int t = 0; t < a.T; ++t) {
     float x[V], f[V], i[V];
     load_v<E, V>(a.x, at(a.sx, t), x);
     load_v<E, V>(a.f, at(a.sf, t), f);
@@ -74,76 +56,116 @@ __global__ __launch_bounds__(256) void recurrence_walk_kernel(const RecurrenceAr
   }
 }
 
-template <typename E, int V, int G, bool INP>
-__global__ __launch_bounds__(256) void recurrence_walk_bwd_kernel(const RecurrenceArgs a, int cb) {
+// Readies a pass: no word written yet, no tile taken; a copy of the states to
+// start from where the last states replace them (a tile whose own decays are 0
+// would not wait for the tile that still reads them); the last states of
+// sequences without tokens.
+__global__ __launch_bounds__(256) void recurrence_ready_kernel(uint4* words, long n, unsigned* counter, float* copy,
+                                                               const float* first, long ncopy, const int* cu, int B,
+                                                               int T, int rows, int D, float* last) {
+  const long at = (long)blockIdx.x * 256 + threadIdx.x, all = (long)gridDim.x * 256;
+  if (counter && at == 0) *counter = 0;
+  for (long e = at; e < n; e += all) words[e] = make_uint4(NOT_YET, NOT_YET, NOT_YET, NOT_YET);
+  for (long e = at; e < ncopy; e += all) copy[e] = first[e];
+  if (!last) return;
   __shared__ int sm[4];
-  const int b = blockIdx.x / cb, c = ((blockIdx.x % cb) * 256 + threadIdx.x) * V;
-  int start, n;
-  sequence_rows(a, b, sm, start, n);
-  if (c >= a.D) return;
-  float carry[V], lam[V], dlam[V];
+  for (int b = blockIdx.x; b < B; b += gridDim.x) {
+    bool empty = T == 0;
+    if (cu) {
+      int m = 0;
+      for (int j = threadIdx.x; j <= b; j += 256) m = max(m, min(cu[j], rows));
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    carry[v] = a.dhT ? a.dhT[(long)b * a.D + c + v] : 0.f;
-    lam[v] = G == GATE_POWER ? a.lam[c + v] : 0.f;
-    dlam[v] = 0.f;
-  }
-  auto at = [&](const TokenSteps& s, int t) { return (a.cu ? (start + t) * s.t : b * s.b + t * s.t) + c; };
-  for (int t = n - 1; t >= 0; --t) {
-    float x[V], f[V], i[V], g[V], before[V], dx[V], df[V], di[V];
-    load_v<E, V>(a.x, at(a.sx, t), x);
-    load_v<E, V>(a.f, at(a.sf, t), f);
-    if (INP) load_v<E, V>(a.i, at(a.si, t), i);
-    load_v<E, V>(a.dh, at(a.sdh, t), g);
-    if (t > 0) {
-      load_v<E, V>(a.h, at(a.sh, t - 1), before);
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v) before[v] = a.h0 ? a.h0[(long)b * a.D + c + v] : 0.f;
+      for (int o = 32; o > 0; o >>= 1) m = max(m, __shfl_xor(m, o));
+      __syncthreads();
+      if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = m;
+      __syncthreads();
+      empty = min(cu[b + 1], rows) <= max(max(sm[0], sm[1]), max(sm[2], sm[3]));
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      float av, cv, dl;
-      gate_values<E, G>(f[v], lam[v], av, cv);
-      g[v] += carry[v];
-      carry[v] = av * g[v];
-      gate_gradients<E, G, INP>(x[v], f[v], INP ? i[v] : 0.f, lam[v], before[v], g[v], dx[v], df[v], di[v], dl);
-      dlam[v] += dl;
-    }
-    store_v<E, V>(a.dx, at(a.sdx, t), dx);
-    store_v<E, V>(a.df, at(a.sdf, t), df);
-    if (INP) store_v<E, V>(a.di, at(a.sdi, t), di);
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    if (a.dh0) a.dh0[(long)b * a.D + c + v] = carry[v];
-    if (G == GATE_POWER) a.part[(long)b * a.D + c + v] = dlam[v];
+    if (empty)
+      for (int c = threadIdx.x; c < D; c += 256) last[(long)b * D + c] = first ? first[(long)b * D + c] : 0.f;
   }
 }
 
 template <typename E, int V, int G, bool INP>
 hipError_t run_walk(const RecurrenceArgs& a, hipStream_t s) {
   const int cb = (a.D + 256 * V - 1) / (256 * V);
-  if (a.B == 0) return hipSuccess;
   hipLaunchKernelGGL((recurrence_walk_kernel<E, V, G, INP>), dim3((unsigned)cb * a.B), dim3(256), 0, s, a, cb);
   return hipGetLastError();
 }
-template <typename E, int V, int G, bool INP>
-hipError_t run_walk_bwd(const RecurrenceArgs& a, hipStream_t s) {
-  const int cb = (a.D + 256 * V - 1) / (256 * V);
-  if (a.B > 0) {
-    hipLaunchKernelGGL((recurrence_walk_bwd_kernel<E, V, G, INP>), dim3((unsigned)cb * a.B), dim3(256), 0, s, a, cb);
+template <typename E, int V, int G>
+hipError_t run_walk(const RecurrenceArgs& a, hipStream_t s) {
+  return a.i ? run_walk<E, V, G, true>(a, s) : run_walk<E, V, G, false>(a, s);
+}
+template <typename E, int V>
+hipError_t run_walk(const RecurrenceArgs& a, hipStream_t s) {
+  if (a.gate == GATE_LOG) return run_walk<E, V, GATE_LOG>(a, s);
+  if (a.gate == GATE_SIGMOID) return run_walk<E, V, GATE_SIGMOID>(a, s);
+  return run_walk<E, V, GATE_POWER>(a, s);
+}
+
+// Workspace of a pass by tiles.  Words only where a tile goes on from another.
+struct Plan {
+  int tiles;
+  bool words;
+  size_t first_at, words_at, part_at, bytes;
+};
+Plan plan_of(int B, int T, int D, int rows, bool packed, bool bwd, bool part) {
+  Plan p;
+  const int tile = bwd ? REC_BWD_R * REC_BWD_W : REC_R * REC_W;
+  p.tiles = (rows + tile - 1) / tile;
+  p.words = p.tiles > 1 && (packed || tile % T != 0);
+  const size_t wide = ((size_t)D + 127) / 128 * 128;   // (a slice has 64 or 128 channels)
+  auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
+  p.first_at = p.words ? 256 : 0;
+  p.words_at = p.first_at + (p.words ? up((size_t)B * D * 4) : 0);
+  p.part_at = p.words_at + (p.words ? up(wide * p.tiles * 8) : 0);
+  p.bytes = p.part_at + (part ? up((size_t)p.tiles * D * 4) : 0);
+  return p;
+}
+
+template <typename E, int V>
+hipError_t run_tiles(RecurrenceArgs a, bool bwd, char* ws, hipStream_t s) {
+  const bool part = bwd && a.gate == GATE_POWER;
+  const Plan p = plan_of(a.B, a.T, a.D, a.rows, a.cu != nullptr, bwd, part);
+  const int parts = a.B > 0 ? p.tiles : 0;
+  float* last = bwd ? a.dh0 : a.hT;
+  TileArgs g = {};
+  g.tiles = p.tiles;
+  g.slices = (a.D + WAVE * V - 1) / (WAVE * V);
+  g.first = bwd ? a.dhT : a.h0;
+  auto flat = [&](const TokenSteps& t) { return t.b == a.T * t.t; };
+  g.flat = a.cu || a.B == 1 ||
+           (flat(a.sx) && flat(a.sf) && (!a.i || flat(a.si)) && flat(a.sh) &&
+            (!bwd || (flat(a.sdh) && flat(a.sdx) && flat(a.sdf) && (!a.i || flat(a.sdi)))));
+  a.part = part ? reinterpret_cast<float*>(ws + p.part_at) : nullptr;
+  if (parts > 0 && p.words) {
+    g.counter = reinterpret_cast<unsigned*>(ws);
+    g.words = reinterpret_cast<unsigned long long*>(ws + p.words_at);
+  }
+  const bool copy = g.words && last && last == g.first, empty = last && last != g.first && (a.cu || a.T == 0);
+  if (a.B > 0 && (g.words || empty)) {
+    const long n = g.words ? (long)g.slices * WAVE * V * p.tiles / 2 : 0;
+    long blocks = n / 256 + 1;
+    if (empty && a.B > blocks) blocks = a.B;
+    if (blocks > 1024) blocks = 1024;
+    hipLaunchKernelGGL(recurrence_ready_kernel, dim3((unsigned)blocks), dim3(256), 0, s,
+                       reinterpret_cast<uint4*>(g.words), n, g.counter,
+                       copy ? reinterpret_cast<float*>(ws + p.first_at) : nullptr, g.first, copy ? (long)a.B * a.D : 0L,
+                       a.cu, a.B, a.T, a.rows, a.D, empty ? last : nullptr);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    if (copy) g.first = reinterpret_cast<float*>(ws + p.first_at);
   }
-  if (G == GATE_POWER) return launch_column_sums(a.part, a.B, a.D, a.D, 0, a.dlam, s);
+  if (parts > 0) {
+    const hipError_t e = recurrence_tiles<E, V>(a, g, bwd, s);
+    if (e != hipSuccess) return e;
+  }
+  if (part) return launch_column_sums(a.part, parts, a.D, a.D, 0, a.dlam, s);
   return hipSuccess;
 }
 
 // bf16 channels two a lane where every row starts at a multiple of 4 bytes.
-template <typename E>
 bool pairs(const RecurrenceArgs& a, bool bwd) {
-  if (sizeof(E) == 4) return false;
   long m = a.D | a.sx.b | a.sx.t | a.sf.b | a.sf.t | a.sh.b | a.sh.t;
   uintptr_t p = (uintptr_t)a.x | (uintptr_t)a.f | (uintptr_t)a.i | (uintptr_t)a.h;
   if (a.i) m |= a.si.b | a.si.t;
@@ -155,40 +177,33 @@ bool pairs(const RecurrenceArgs& a, bool bwd) {
   return m % 2 == 0 && p % 4 == 0;
 }
 
-template <typename E, int V, bool BWD, int G>
-hipError_t run_gate(const RecurrenceArgs& a, hipStream_t s) {
-  if (a.i) return BWD ? run_walk_bwd<E, V, G, true>(a, s) : run_walk<E, V, G, true>(a, s);
-  return BWD ? run_walk_bwd<E, V, G, false>(a, s) : run_walk<E, V, G, false>(a, s);
-}
-template <typename E, int V, bool BWD>
-hipError_t run_v(const RecurrenceArgs& a, hipStream_t s) {
-  if (a.gate == GATE_LOG) return run_gate<E, V, BWD, GATE_LOG>(a, s);
-  if (a.gate == GATE_SIGMOID) return run_gate<E, V, BWD, GATE_SIGMOID>(a, s);
-  return run_gate<E, V, BWD, GATE_POWER>(a, s);
-}
-template <typename E, bool BWD>
-hipError_t run(const RecurrenceArgs& a, hipStream_t s) {
-  if constexpr (sizeof(E) == 2) {
-    if (pairs<E>(a, BWD)) return run_v<E, 2, BWD>(a, s);
-  }
-  return run_v<E, 1, BWD>(a, s);
+// Dense sequences of so few tokens are walked: no words to ready, and no strip
+// of which a sequence fills a part.
+constexpr int WALK = 8;
+bool walked(const RecurrenceArgs& a, bool bwd) { return !bwd && !a.cu && a.T > 0 && a.T <= WALK && a.B > 0; }
+
+template <typename E, int V>
+hipError_t run(const RecurrenceArgs& a, bool bwd, void* ws, hipStream_t s) {
+  if (walked(a, bwd)) return run_walk<E, V>(a, s);
+  return run_tiles<E, V>(a, bwd, static_cast<char*>(ws), s);
 }
 
 }  // namespace
 
-size_t recurrence_part_bytes(int B, int D) { return (size_t)B * D * sizeof(float); }
+size_t recurrence_bytes(const RecurrenceArgs& a, bool packed, bool bwd) {
+  if (a.rows == 0 || a.B == 0 || (!packed && !bwd && a.T <= WALK)) return 0;
+  return plan_of(a.B, a.T, a.D, a.rows, packed, bwd, bwd && a.gate == GATE_POWER).bytes;
+}
 
-template <typename E>
-hipError_t launch_recurrence(const RecurrenceArgs& a, hipStream_t s) {
-  return run<E, false>(a, s);
+hipError_t launch_recurrence_step(const RecurrenceArgs& a, bool f32, hipStream_t s) {
+  if (a.B == 0) return hipSuccess;
+  if (f32) return run_walk<float, 1>(a, s);
+  return pairs(a, false) ? run_walk<bf16, 2>(a, s) : run_walk<bf16, 1>(a, s);
 }
-template <typename E>
-hipError_t launch_recurrence_bwd(const RecurrenceArgs& a, hipStream_t s) {
-  return run<E, true>(a, s);
+
+hipError_t launch_recurrence(const RecurrenceArgs& a, bool f32, bool bwd, void* ws, hipStream_t s) {
+  if (f32) return run<float, 1>(a, bwd, ws, s);
+  return pairs(a, bwd) ? run<bf16, 2>(a, bwd, ws, s) : run<bf16, 1>(a, bwd, ws, s);
 }
-template hipError_t launch_recurrence<bf16>(const RecurrenceArgs&, hipStream_t);
-template hipError_t launch_recurrence<float>(const RecurrenceArgs&, hipStream_t);
-template hipError_t launch_recurrence_bwd<bf16>(const RecurrenceArgs&, hipStream_t);
-template hipError_t launch_recurrence_bwd<float>(const RecurrenceArgs&, hipStream_t);
 
 }  // namespace prism

@@ -48,53 +48,61 @@ __device__ inline float one_minus_exp(float z, float aa) {
   return z < 0.25f ? z * s : 1.f - aa;
 }
 
-// a and c.
+// What the gates of a value keep between the two sweeps of a tile: a, and k, from
+// which c follows (sigmoid: c itself; power: e^-f).
+struct GateValue {
+  float a, k;
+};
 template <typename E, int G>
-__device__ inline void gate_values(float f, float lam, float& a, float& c) {
+__device__ inline GateValue gate_value(float f, float lam) {
+  GateValue g;
   if constexpr (G == GATE_LOG) {
-    a = gate_exp<E>(f);
-    c = 1.f;
+    g.a = gate_exp<E>(f);
+    g.k = 1.f;
   } else if constexpr (G == GATE_SIGMOID) {
-    sigmoid_pair<E>(f, a, c);
+    sigmoid_pair<E>(f, g.a, g.k);
   } else {
-    const float y = lam * gate_rcp<E>(1.f + gate_exp<E>(-f));
-    a = gate_exp<E>(-y);
-    c = gate_sqrt<E>(one_minus_exp(2.f * y, a * a));
+    g.k = gate_exp<E>(-f);
+    g.a = gate_exp<E>(-lam * gate_rcp<E>(1.f + g.k));
   }
+  return g;
 }
+
 template <typename E, int G, bool INP>
 __device__ inline void gate_inputs(float x, float f, float i, float lam, float& a, float& u) {
-  float c;
-  gate_values<E, G>(f, lam, a, c);
-  u = G == GATE_LOG ? x : c * x;
+  u = x;
+  if constexpr (G == GATE_POWER) {
+    const float y = lam * gate_rcp<E>(1.f + gate_exp<E>(-f));
+    a = gate_exp<E>(-y);
+    u *= gate_sqrt<E>(one_minus_exp(2.f * y, a * a));
+  } else {
+    const GateValue g = gate_value<E, G>(f, lam);
+    a = g.a;
+    if (G == GATE_SIGMOID) u *= g.k;
+  }
   if (INP) u *= gate_rcp<E>(1.f + gate_exp<E>(-i));
 }
 
-// Gradients of a token's inputs from g, that of h_t, and h_{t-1}; dl: its part
-// of the gradient of lam.  At lam sigma(f) = 0, where the root's slope is
-// infinite, its part is left out.
+// Gradients of a value's inputs from g, that of h_t, and h_{t-1}; dl: its part
+// of the gradient of lam.  Where lam sigma(f) = 0 the root's slope is infinite,
+// and its part is left out.
 template <typename E, int G, bool INP>
-__device__ inline void gate_gradients(float x, float f, float i, float lam, float before, float g, float& dx, float& df,
-                                      float& di, float& dl) {
-  float s = 1.f, t = 0.f;
+__device__ inline void gate_gradients(const GateValue& v, float x, float i, float lam, float before, float g, float& dx,
+                                      float& df, float& di, float& dl) {
+  float s = 1.f, t = 0.f, c = 1.f;
   if (INP) sigmoid_pair<E>(i, s, t);
-  float p, q, a, c;
+  const float xi = INP ? s * x : x;
   dl = 0.f;
   if constexpr (G == GATE_LOG) {
-    a = gate_exp<E>(f);
-    c = 1.f;
-    df = g * a * before;
+    df = g * v.a * before;
   } else if constexpr (G == GATE_SIGMOID) {
-    sigmoid_pair<E>(f, a, c);
-    df = g * (before - s * x) * a * c;
+    c = v.k;
+    df = g * (before - xi) * v.a * c;
   } else {
-    sigmoid_pair<E>(f, p, q);
-    const float y = lam * p;
-    a = gate_exp<E>(-y);
-    c = gate_sqrt<E>(one_minus_exp(2.f * y, a * a));
-    const float slope = c > 0.f ? a * gate_rcp<E>(c) : 0.f;
-    const float d = g * a * (before - slope * s * x);   // of log a
-    dl = -p * d;
+    const float p = gate_rcp<E>(1.f + v.k), q = v.k > 1.f ? 1.f - p : v.k * p, y = lam * p;
+    c = gate_sqrt<E>(one_minus_exp(2.f * y, v.a * v.a));
+    const float slope = c > 0.f ? v.a * gate_rcp<E>(c) : 0.f;
+    dl = -p * (g * v.a * fmaf(-slope, xi, before));   // -p times the gradient of log a
     df = lam * q * dl;
   }
   dx = g * c * s;

@@ -1,0 +1,476 @@
+// Tiles of the gated recurrence and of its backward pass.
+//
+// Memory bound at the copy's rate if every value is read and written once, so
+// the tokens are divided although each needs the state of the one before:
+// a workgroup takes a tile of W strips of R rows and 64 V channels, a strip a
+// wave, V channels a lane.  A strip's effect on the state is h -> A h + U (A the
+// product of its decays, U what it leaves of a state of 0), so a wave sweeps its
+// strip twice, in registers: for (A, U), and, from the state that enters it, for
+// the results.  Between the sweeps the strips of a tile are joined through LDS,
+// and the tiles of a sequence through one 64-bit word (A, U) a channel: a tile
+// writes its own (A, U) there as soon as it has it, and (0, h) once it knows the
+// state h behind it.  A tile reads the words of up to LOOK tiles before it and
+// carries the state on from the nearest word with A = 0, by the same operations
+// in the same order whichever word that is, so that results do not depend on
+// timing.  Workgroups take their tiles in order from a counter: a tile waits for
+// tiles alone whose workgroups run already, down to the first, which waits for
+// none, so every wait ends.
+//
+// Rows of a batch follow one another through the tiles; where a sequence starts,
+// A is 0 and the state h0.  The backward pass goes through rows and tiles in
+// reverse, its state the gradient a_t g_t that a token hands to the one before.
+#pragma once
+
+#include "recurrence_kernel.h"
+
+namespace prism {
+
+// Words of the tiles (nullptr: no tile needs another's), the counter, and the
+// states to start from.
+struct TileArgs {
+  unsigned long long* words;   // [tiles][slices * 64 V]
+  unsigned* counter;
+  int tiles, slices;
+  const float* first;          // h0, or dhT (nullptr: zeros)
+  int flat;                    // the batches' rows follow one another in every tensor
+};
+
+constexpr unsigned NOT_YET = 0xffffffffu;   // of a word's A: nothing written so far
+constexpr int LOOK = 8;
+
+__device__ inline float through(float A, float U, float h) { return A == 0.f ? U : fmaf(A, h, U); }
+
+__device__ inline void publish(unsigned long long* w, float A, float U) {
+  unsigned a = __float_as_uint(A);
+  if (a == NOT_YET) a = 0x7fc00000u;   // (one NaN for another)
+  const unsigned long long v = (unsigned long long)__float_as_uint(U) << 32 | a;
+  __hip_atomic_store(w, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The state behind tile `tile - step` (step 1: forward, -1: backward) for the
+// lane's V channels, by a whole wave; `left` tiles lie before this one.
+template <int V>
+__device__ inline void look_back(const unsigned long long* words, long stride, int tile, int step, int left,
+                                 float (&h)[V]) {
+  unsigned long long w[LOOK][V];
+#pragma unroll
+  for (int k = 0; k < LOOK; ++k)
+#pragma unroll
+    for (int v = 0; v < V; ++v) w[k][v] = k < left ? NOT_YET : 0;
+  while (true) {
+#pragma unroll
+    for (int k = 0; k < LOOK; ++k)
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (k < left && ((unsigned)w[k][v] == NOT_YET || k == LOOK - 1))
+          w[k][v] = __hip_atomic_load(words + (tile - step * (k + 1)) * stride + v, __ATOMIC_RELAXED,
+                                      __HIP_MEMORY_SCOPE_AGENT);
+    bool known = true;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      bool found = false;
+#pragma unroll
+      for (int k = 0; k < LOOK; ++k) {
+        known = known && (found || (unsigned)w[k][v] != NOT_YET);
+        found = found || __uint_as_float((unsigned)w[k][v]) == 0.f;
+      }
+      known = known && found;
+    }
+    if (__all(known)) break;
+    __builtin_amdgcn_s_sleep(1);
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    h[v] = 0.f;
+#pragma unroll
+    for (int k = LOOK - 1; k >= 0; --k)
+      h[v] = through(__uint_as_float((unsigned)w[k][v]), __uint_as_float((unsigned)(w[k][v] >> 32)), h[v]);
+  }
+}
+
+// Rows a strip and waves a tile, forward and backward.
+constexpr int REC_R = 16, REC_W = 8, REC_BWD_R = 8, REC_BWD_W = 8;
+
+// Which rows of a strip start and end a sequence and which belong to one, as
+// bits; place (batch, token) of the first row.
+struct Strip {
+  int row, n;
+  unsigned first, last, in;
+};
+template <int R>
+__device__ inline Strip strip_of(const RecurrenceArgs& a, int row) {
+  Strip s;
+  s.row = min(row, a.rows - 1);
+  s.n = min(max(a.rows - row, 0), R);
+  s.first = s.last = s.in = 0;
+  if (s.n == 0) return s;
+  if (!a.cu) {
+    const int t = row % a.T;
+    for (int k = t ? a.T - t : 0; k < s.n; k += a.T) s.first |= 1u << k;
+    for (int k = a.T - 1 - t; k < s.n; k += a.T) s.last |= 1u << k;
+    s.in = (1u << s.n) - 1;
+  } else {
+    const int end = row + s.n;
+    for (int at = row; at < end;) {
+      const Sequence q = find_sequence(a.cu, a.B, a.T, a.rows, at);
+      const int stop = min(q.end, end);
+      if (q.b >= 0 && q.b < a.B) {
+        s.in |= ((1u << (stop - at)) - 1) << (at - row);
+        if (q.start == at) s.first |= 1u << (at - row);
+        if (q.end == stop) s.last |= 1u << (stop - 1 - row);
+      }
+      at = stop;
+    }
+  }
+  return s;
+}
+
+// Walks a tensor's rows of a strip; rows past its end are its last.
+template <typename E>
+struct RowWalk {
+  const E* p;
+  long step, jump;
+  __device__ inline RowWalk(const void* base, const TokenSteps& s, const RecurrenceArgs& a, const TileArgs& g, int row) {
+    step = s.t;
+    if (g.flat) {
+      p = static_cast<const E*>(base) + row * s.t;
+      jump = 0;
+    } else {
+      const int b = row / a.T;
+      p = static_cast<const E*>(base) + (b * s.b + (row - b * a.T) * s.t);
+      jump = s.b - a.T * s.t;
+    }
+  }
+  __device__ inline void next(const Strip& s, int k) {   // from row k to k + 1
+    if (k + 1 < s.n) {
+      p += step;
+      if (s.first >> (k + 1) & 1) p += jump;
+    }
+  }
+  __device__ inline void back(const Strip& s, int k) {   // from row k to k - 1
+    if (k > 0 && k < s.n) {
+      p -= step;
+      if (s.first >> k & 1) p -= jump;
+    }
+  }
+};
+
+template <typename E, int V>
+__device__ inline typename VecIo<E, V>::raw load_raw(const E* p, int c) {
+  return *reinterpret_cast<const typename VecIo<E, V>::raw*>(p + c);
+}
+
+__device__ inline int batch_of(const RecurrenceArgs& a, int row) {
+  return a.cu ? find_sequence(a.cu, a.B, a.T, a.rows, row).b : row / a.T;
+}
+
+// Values that enter each strip, from the strips' (A, U) in LDS and, where the
+// tile's first row (backward: last) goes on from another tile, from its words.
+// `strip` counts in the direction of the pass.
+template <int V, int W>
+__device__ inline void enter_strip(const TileArgs& g, int tile, int slice, int step, int left, bool open, int strip,
+                                   const float (&A)[V], const float (&U)[V], float (&h)[V]) {
+  __shared__ float sA[W][V][WAVE], sU[W][V][WAVE], s0[V][WAVE];
+  const int lane = threadIdx.x & (WAVE - 1);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    sA[strip][v][lane] = A[v];
+    sU[strip][v][lane] = U[v];
+  }
+  __syncthreads();
+  if (strip == 0) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = 0.f;
+    if (g.words) {
+      float At[V], Ut[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        At[v] = 1.f;
+        Ut[v] = 0.f;
+        for (int k = 0; k < W; ++k) {
+          Ut[v] = through(sA[k][v][lane], sU[k][v][lane], Ut[v]);
+          At[v] = sA[k][v][lane] == 0.f ? 0.f : At[v] * sA[k][v][lane];
+        }
+      }
+      const long stride = (long)g.slices * WAVE * V;
+      unsigned long long* w = g.words + tile * stride + (slice * WAVE + lane) * V;
+#pragma unroll
+      for (int v = 0; v < V; ++v) publish(w + v, open ? At[v] : 0.f, Ut[v]);
+      if (open) {
+        look_back<V>(g.words + (slice * WAVE + lane) * V, stride, tile, step, left, h);
+#pragma unroll
+        for (int v = 0; v < V; ++v) publish(w + v, 0.f, through(At[v], Ut[v], h[v]));
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) s0[v][lane] = h[v];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    h[v] = s0[v][lane];
+    for (int k = 0; k < strip; ++k) h[v] = through(sA[k][v][lane], sU[k][v][lane], h[v]);
+  }
+}
+
+// The workgroup's tile and slice of channels.
+__device__ inline int take_tile(const TileArgs& g) {
+  if (!g.words) return blockIdx.x;
+  __shared__ unsigned taken;
+  if (threadIdx.x == 0)
+    taken = __hip_atomic_fetch_add(g.counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(taken);
+}
+
+template <typename E, int V, int G, bool INP, int R, int W>
+__global__ __launch_bounds__(W * WAVE) void recurrence_tile_kernel(const RecurrenceArgs a, const TileArgs g) {
+  typedef VecIo<E, V> IO;
+  typedef typename IO::raw raw;
+  const int id = take_tile(g), tile = id / g.slices, slice = id - tile * g.slices;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE), lane = threadIdx.x & (WAVE - 1);
+  int c = (slice * WAVE + lane) * V;
+  const bool on = c < a.D;
+  if (!on) c = 0;
+  const Strip s = strip_of<R>(a, tile * (R * W) + wave * R);
+  raw rx[R], rf[R], ri[R];
+  {
+    RowWalk<E> px(a.x, a.sx, a, g, s.row), pf(a.f, a.sf, a, g, s.row), pi(INP ? a.i : a.x, INP ? a.si : a.sx, a, g, s.row);
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      rx[k] = load_raw<E, V>(px.p, c);
+      rf[k] = load_raw<E, V>(pf.p, c);
+      if (INP) ri[k] = load_raw<E, V>(pi.p, c);
+      px.next(s, k);
+      pf.next(s, k);
+      if (INP) pi.next(s, k);
+    }
+  }
+  float lam[V], A[V], U[V], h[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    lam[v] = G == GATE_POWER && on ? a.lam[c + v] : 0.f;
+    A[v] = 1.f;
+    U[v] = 0.f;
+  }
+  float av[R][V], uv[R][V];
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    float x[V], f[V], i[V];
+    IO::unpack(rx[k], x);
+    IO::unpack(rf[k], f);
+    if (INP) IO::unpack(ri[k], i);
+#pragma unroll
+    for (int v = 0; v < V; ++v) gate_inputs<E, G, INP>(x[v], f[v], INP ? i[v] : 0.f, lam[v], av[k][v], uv[k][v]);
+  }
+  constexpr unsigned ALL = R == 32 ? ~0u : (1u << R) - 1;
+  const bool plain = s.in == ALL && !(s.first | s.last);
+  if (plain) {
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        U[v] = fmaf(av[k][v], U[v], uv[k][v]);
+        A[v] *= av[k][v];
+      }
+  } else {
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      if (s.first >> k & 1) {
+        const long at = (long)batch_of(a, s.row + k) * a.D + c;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          uv[k][v] = fmaf(av[k][v], g.first && on ? g.first[at + v] : 0.f, uv[k][v]);
+          A[v] = 0.f;
+          U[v] = uv[k][v];
+        }
+      } else if (s.in >> k & 1) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          U[v] = fmaf(av[k][v], U[v], uv[k][v]);
+          A[v] *= av[k][v];
+        }
+      }
+    }
+  }
+  // (the tile goes on from the one before it unless a sequence starts with it)
+  const Sequence q = find_sequence(a.cu, a.B, a.T, a.rows, tile * (R * W));
+  enter_strip<V, W>(g, tile, slice, 1, tile, q.start != tile * (R * W) && tile > 0, wave, A, U, h);
+  RowWalk<E> ph(a.h, a.sh, a, g, s.row);
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    const bool first = !plain && (s.first >> k & 1), in = plain || (s.in >> k & 1);
+    if (in) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) h[v] = first ? uv[k][v] : fmaf(av[k][v], h[v], uv[k][v]);
+      if (on) *reinterpret_cast<raw*>(const_cast<E*>(ph.p) + c) = IO::pack(h);
+      if (!plain && a.hT && (s.last >> k & 1)) {
+        const long at = (long)batch_of(a, s.row + k) * a.D + c;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (on) a.hT[at + v] = h[v];
+      }
+    }
+    ph.next(s, k);
+  }
+}
+
+// Rows from the last to the first.  before = h_{t-1} is the row of h before, or
+// h0 at a sequence's first token.
+template <typename E, int V, int G, bool INP, int R, int W>
+__global__ __launch_bounds__(W * WAVE) void recurrence_tile_bwd_kernel(const RecurrenceArgs a, const TileArgs g) {
+  typedef VecIo<E, V> IO;
+  typedef typename IO::raw raw;
+  const int id = take_tile(g), turn = id / g.slices, slice = id - turn * g.slices, tile = g.tiles - 1 - turn;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE), lane = threadIdx.x & (WAVE - 1);
+  int c = (slice * WAVE + lane) * V;
+  const bool on = c < a.D;
+  if (!on) c = 0;
+  const Strip s = strip_of<R>(a, tile * (R * W) + wave * R);
+  raw rx[R], ri[R], rb[R], rg[R];
+  GateValue gv[R][V];
+  float lam[V], A[V], U[V], carry[V], dlam[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    lam[v] = G == GATE_POWER && on ? a.lam[c + v] : 0.f;
+    A[v] = 1.f;
+    U[v] = dlam[v] = 0.f;
+  }
+  {
+    raw rf[R];
+    RowWalk<E> px(a.x, a.sx, a, g, s.row), pf(a.f, a.sf, a, g, s.row), pi(INP ? a.i : a.x, INP ? a.si : a.sx, a, g, s.row),
+        pb(a.h, a.sh, a, g, s.row), pg(a.dh, a.sdh, a, g, s.row);
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      rf[k] = load_raw<E, V>(pf.p, c);
+      rg[k] = load_raw<E, V>(pg.p, c);
+      pf.next(s, k);
+      pg.next(s, k);
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      // (a row that starts a sequence, or is of none, has no row before it)
+      const bool inner = (s.in >> k & 1) && !(s.first >> k & 1);
+      rx[k] = load_raw<E, V>(px.p, c);
+      if (INP) ri[k] = load_raw<E, V>(pi.p, c);
+      rb[k] = load_raw<E, V>(pb.p - (inner ? pb.step : 0), c);
+      px.next(s, k);
+      if (INP) pi.next(s, k);
+      pb.next(s, k);
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      float f[V];
+      IO::unpack(rf[k], f);
+#pragma unroll
+      for (int v = 0; v < V; ++v) gv[k][v] = gate_value<E, G>(f[v], lam[v]);
+    }
+  }
+  constexpr unsigned ALL = R == 32 ? ~0u : (1u << R) - 1;
+  const bool plain = s.in == ALL && !(s.first | s.last);
+#pragma unroll
+  for (int k = R - 1; k >= 0; --k) {
+    if (!plain && (s.last >> k & 1)) {
+      const long at = (long)batch_of(a, s.row + k) * a.D + c;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        A[v] = 0.f;
+        U[v] = g.first && on ? g.first[at + v] : 0.f;
+      }
+    }
+    if (plain || (s.in >> k & 1)) {
+      float d[V];
+      IO::unpack(rg[k], d);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        U[v] = gv[k][v].a * (d[v] + U[v]);
+        A[v] = A[v] == 0.f ? 0.f : A[v] * gv[k][v].a;
+      }
+    }
+  }
+  // (the tile goes on from the one behind it unless a sequence ends with it)
+  const int end = min((tile + 1) * (R * W), a.rows);
+  const Sequence q = find_sequence(a.cu, a.B, a.T, a.rows, end - 1);
+  enter_strip<V, W>(g, tile, slice, -1, turn, q.end != end && turn > 0, W - 1 - wave, A, U, carry);
+  const int end_row = s.row + max(s.n - 1, 0);
+  RowWalk<E> px(a.dx, a.sdx, a, g, end_row), pf(a.df, a.sdf, a, g, end_row),
+      pi(INP ? a.di : a.dx, INP ? a.sdi : a.sdx, a, g, end_row);
+#pragma unroll
+  for (int k = R - 1; k >= 0; --k) {
+    if (!plain && (s.last >> k & 1)) {
+      const long at = (long)batch_of(a, s.row + k) * a.D + c;
+#pragma unroll
+      for (int v = 0; v < V; ++v) carry[v] = g.first && on ? g.first[at + v] : 0.f;
+    }
+    if (plain || (s.in >> k & 1)) {
+      float x[V], i[V], b[V], d[V], dx[V], df[V], di[V];
+      IO::unpack(rx[k], x);
+      if (INP) IO::unpack(ri[k], i);
+      IO::unpack(rb[k], b);
+      IO::unpack(rg[k], d);
+      const bool first = !plain && (s.first >> k & 1);
+      const long at = first ? (long)batch_of(a, s.row + k) * a.D + c : 0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (first) b[v] = a.h0 && on ? a.h0[at + v] : 0.f;
+        const float gt = d[v] + carry[v];
+        carry[v] = gv[k][v].a * gt;
+        float dl;
+        gate_gradients<E, G, INP>(gv[k][v], x[v], INP ? i[v] : 0.f, lam[v], b[v], gt, dx[v], df[v], di[v], dl);
+        if (G == GATE_POWER) dlam[v] += dl;
+        if (first && a.dh0 && on) a.dh0[at + v] = carry[v];
+      }
+      if (on) {
+        *reinterpret_cast<raw*>(const_cast<E*>(px.p) + c) = IO::pack(dx);
+        *reinterpret_cast<raw*>(const_cast<E*>(pf.p) + c) = IO::pack(df);
+        if (INP) *reinterpret_cast<raw*>(const_cast<E*>(pi.p) + c) = IO::pack(di);
+      }
+    }
+    px.back(s, k);
+    pf.back(s, k);
+    if (INP) pi.back(s, k);
+  }
+  if constexpr (G == GATE_POWER) {   // the tile's part of dlam, wave after wave
+    __shared__ float sm[W][V][WAVE];
+#pragma unroll
+    for (int v = 0; v < V; ++v) sm[wave][v][lane] = dlam[v];
+    __syncthreads();
+    if (wave == 0 && on) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < W; ++k) sum += sm[k][v][lane];
+        a.part[(long)tile * a.D + c + v] = sum;
+      }
+    }
+  }
+}
+
+template <typename E, int V, int G, bool INP>
+hipError_t launch_tiles(const RecurrenceArgs& a, const TileArgs& g, bool bwd, hipStream_t s) {
+  const dim3 grid((unsigned)g.tiles * g.slices);
+  if (bwd)
+    hipLaunchKernelGGL((recurrence_tile_bwd_kernel<E, V, G, INP, REC_BWD_R, REC_BWD_W>), grid, dim3(REC_BWD_W * WAVE), 0,
+                       s, a, g);
+  else
+    hipLaunchKernelGGL((recurrence_tile_kernel<E, V, G, INP, REC_R, REC_W>), grid, dim3(REC_W * WAVE), 0, s, a, g);
+  return hipGetLastError();
+}
+template <typename E, int V, int G>
+hipError_t launch_tiles(const RecurrenceArgs& a, const TileArgs& g, bool bwd, hipStream_t s) {
+  return a.i ? launch_tiles<E, V, G, true>(a, g, bwd, s) : launch_tiles<E, V, G, false>(a, g, bwd, s);
+}
+// (a storage type and width in a source file each)
+template <typename E, int V>
+hipError_t recurrence_tiles(const RecurrenceArgs& a, const TileArgs& g, bool bwd, hipStream_t s);
+
+#define PRISM_RECURRENCE_TILES(E, V)                                                                           \
+  template <>                                                                                                  \
+  hipError_t recurrence_tiles<E, V>(const RecurrenceArgs& a, const TileArgs& g, bool bwd, hipStream_t s) {     \
+    if (a.gate == GATE_LOG) return launch_tiles<E, V, GATE_LOG>(a, g, bwd, s);                                 \
+    if (a.gate == GATE_SIGMOID) return launch_tiles<E, V, GATE_SIGMOID>(a, g, bwd, s);                         \
+    return launch_tiles<E, V, GATE_POWER>(a, g, bwd, s);                                                       \
+  }
+
+}  // namespace prism
