@@ -76,9 +76,9 @@ size_t recurrence_bytes(const RecurrenceArgs& a, bool packed, bool bwd);   // of
 // sequence without tokens, which no row of the passes belongs to.
 hipError_t launch_empty_sequences(const int* cu, int B, int rows, int T, void* dst, const void* src, int n, int size,
                                   hipStream_t s);
-// out[e] = sum over p of part[p][e], e < n, in a fixed order; with K > 0 the
-// columns are [K][n / K] and go to out[c * K + j].
-hipError_t launch_column_sums(const float* part, int parts, long stride, int n, int K, float* out, hipStream_t s);
+// Sums over partials [K + 1][C] in a fixed order: rows j < K go to out[c * K + j],
+// the last to last[c] (each nullptr: not wanted).
+hipError_t launch_column_sums(const float* part, int parts, int C, int K, float* out, float* last, hipStream_t s);
 
 #ifdef __HIPCC__
 // The sequence that holds row `row` of a batch: rows start .. end - 1 of

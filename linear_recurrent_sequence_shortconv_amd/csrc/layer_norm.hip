@@ -8,8 +8,8 @@
 //
 // Memory bound: every row is read once and written once.  A row stays in the
 // registers of a group of lanes, of a wave, or of a workgroup of up to 16
-// waves, so that mean and deviation are two sums one after the other over
-// exact values (the sum of squares less the squared mean would lose the
+// waves, so that mean and deviation are two sums one after the other over the
+// values themselves (the sum of squares less the squared mean would lose the
 // deviation of rows far from zero).  The backward pass reads no statistics: it
 // forms them again from the row that it holds anyway.
 #include "block_ops.h"
@@ -19,15 +19,15 @@ namespace prism {
 
 namespace {
 
-// Sums over the team of a row: G lanes of a wave (G <= 64), or all waves of the
-// workgroup (G > 64) through LDS, in a fixed order.  `turn` counts the sums: two
-// rows of LDS in turn, so that a wave that is ahead writes where nobody reads.
+// Sums over the team of a row: G lanes of a wave (G <= 64), or G / 64 waves of
+// the workgroup through LDS, in a fixed order.  `turn` counts the sums: two rows
+// of LDS in turn, so that a wave that is ahead writes where nobody reads.
 template <int N>
 __device__ inline void team_sums(float (&v)[N], int G, float (*sm)[16][2], int& turn) {
 #pragma unroll
-  for (int n = 0; n < N; ++n) v[n] = G >= 64 ? wave_sum(v[n]) : group_sum(v[n], G);
-  if (G <= 64) return;
-  const int wave = threadIdx.x / WAVE, nw = G / WAVE;
+  for (int n = 0; n < N; ++n) v[n] = G >= WAVE ? wave_sum(v[n]) : group_sum(v[n], G);
+  if (G <= WAVE) return;
+  const int wave = threadIdx.x / WAVE, nw = G / WAVE, first = wave & -nw;
   float(*s)[2] = sm[turn & 1];
   ++turn;
   if ((threadIdx.x & (WAVE - 1)) == 0) {
@@ -39,8 +39,19 @@ __device__ inline void team_sums(float (&v)[N], int G, float (*sm)[16][2], int& 
   for (int n = 0; n < N; ++n) v[n] = 0.f;
   for (int k = 0; k < nw; ++k) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) v[n] += s[k][n];
+    for (int n = 0; n < N; ++n) v[n] += s[first + k][n];
   }
+}
+
+// A vector of ones or zeros in the place of weights that are not given.
+template <typename E, int V>
+__device__ inline typename VecIo<E, V>::raw weight(const void* p, int at, float other) {
+  typedef typename VecIo<E, V>::raw raw;
+  if (p) return *reinterpret_cast<const raw*>(static_cast<const E*>(p) + at);
+  float x[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) x[i] = other;
+  return VecIo<E, V>::pack(x);
 }
 
 __device__ inline long row_at(const Strides& s, long row, int T, int H) {
@@ -49,9 +60,12 @@ __device__ inline long row_at(const Strides& s, long row, int T, int H) {
   return b * s.b + t * s.t + h * s.h;
 }
 
-// Lane `lane` of the team holds vectors lane + j G, j < NV, of V values.
-template <typename E, int V, int NV>
-__global__ __launch_bounds__(1024) void layer_norm_kernel(const LayerNormArgs a, int G) {
+// Lane `lane` of the team holds vectors lane + j G, j < NV, of V values.  With 8
+// values a lane a row of 2048 is a workgroup's: so few registers that 8 waves a
+// SIMD hide the loads (16 and 32 values a lane, with or without the next row on
+// its way: 50 to 52 us in place of 48 for 8 x 2048 rows of 2048 with a residual).
+template <typename E, int V, int NV, int NT, bool RES>
+__global__ __launch_bounds__(NT) void layer_norm_kernel(const LayerNormArgs a, int G) {
   typedef VecIo<E, V> IO;
   typedef typename IO::raw raw;
   __shared__ float sm[2][16][2];
@@ -60,14 +74,17 @@ __global__ __launch_bounds__(1024) void layer_norm_kernel(const LayerNormArgs a,
   const float inv = 1.f / (float)a.D;
   int at[NV];
   bool on[NV];
-  raw rw[NV], rb[NV];
+  raw rw[NV], rb[NV], rx[NV], rr[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = (lane + j * G) * V;
     on[j] = c < a.D;
     at[j] = on[j] ? c : 0;
-    if (a.w) rw[j] = *reinterpret_cast<const raw*>(static_cast<const E*>(a.w) + at[j]);
-    if (a.b) rb[j] = *reinterpret_cast<const raw*>(static_cast<const E*>(a.b) + at[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    rw[j] = weight<E, V>(a.w, at[j], 1.f);
+    rb[j] = weight<E, V>(a.b, at[j], 0.f);
   }
   // (every team of the workgroup makes every round: the sums have barriers)
   for (long base = (long)blockIdx.x * teams; base < a.rows; base += (long)gridDim.x * teams) {
@@ -75,20 +92,19 @@ __global__ __launch_bounds__(1024) void layer_norm_kernel(const LayerNormArgs a,
     const bool live = want < a.rows;
     const long row = live ? want : a.rows - 1;
     const E* x = static_cast<const E*>(a.x) + row_at(a.sx, row, a.T, a.H);
-    float s[NV][V];
-    float sum[1] = {0.f};
-    raw rx[NV], rr[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) rx[j] = *reinterpret_cast<const raw*>(x + at[j]);
-    if (a.r) {
+    if (RES) {
       const E* r = static_cast<const E*>(a.r) + row_at(a.sr, row, a.T, a.H);
 #pragma unroll
       for (int j = 0; j < NV; ++j) rr[j] = *reinterpret_cast<const raw*>(r + at[j]);
     }
+    float s[NV][V];
+    float sum[1] = {0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       IO::unpack(rx[j], s[j]);
-      if (a.r) {
+      if (RES) {
         float q[V];
         IO::unpack(rr[j], q);
 #pragma unroll
@@ -97,7 +113,7 @@ __global__ __launch_bounds__(1024) void layer_norm_kernel(const LayerNormArgs a,
 #pragma unroll
       for (int i = 0; i < V; ++i) sum[0] += on[j] ? s[j][i] : 0.f;
     }
-    if (a.h && live) {
+    if (RES && a.h && live) {
       E* h = static_cast<E*>(a.h) + row_at(a.sh, row, a.T, a.H);
 #pragma unroll
       for (int j = 0; j < NV; ++j)
@@ -123,15 +139,10 @@ __global__ __launch_bounds__(1024) void layer_norm_kernel(const LayerNormArgs a,
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       float w[V], b[V];
-      if (a.w) IO::unpack(rw[j], w);
-      if (a.b) IO::unpack(rb[j], b);
+      IO::unpack(rw[j], w);
+      IO::unpack(rb[j], b);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float v = s[j][i] * r;
-        if (a.w) v *= w[i];
-        if (a.b) v += b[i];
-        s[j][i] = v;
-      }
+      for (int i = 0; i < V; ++i) s[j][i] = fmaf(s[j][i] * r, w[i], b[i]);
       if (on[j]) *reinterpret_cast<raw*>(y + at[j]) = IO::pack(s[j]);
     }
   }
@@ -139,42 +150,50 @@ __global__ __launch_bounds__(1024) void layer_norm_kernel(const LayerNormArgs a,
 
 // A workgroup's rows are summed for the weights in registers, then over its
 // teams (in the wave, then over the waves through LDS), and written as one
-// partial [2][D] for each workgroup.
-template <typename E, int V, int NV>
-__global__ __launch_bounds__(1024) void layer_norm_bwd_kernel(const LayerNormArgs a, int G) {
+// partial [2][D] for each workgroup.  The next row of a team is on its way while
+// the sums of one are joined (16384 rows of 2048 with dh: 56 us; without, 67).
+template <typename E, int V, int NV, int NT, bool DH>
+__global__ __launch_bounds__(NT) void layer_norm_bwd_kernel(const LayerNormArgs a, int G) {
   typedef VecIo<E, V> IO;
   typedef typename IO::raw raw;
+  constexpr bool PF = NT < 1024;   // (1024 threads have no registers for it)
   __shared__ float sm[2][16][2];
-  __shared__ float cols[NV * V * WAVE];
+  __shared__ float cols[NV * V * (NT < 1024 ? NT / 2 : 1)];   // (of two teams or more; of 1024 threads there is one)
   int turn = 0;
   const int lane = threadIdx.x & (G - 1), teams = blockDim.x / G;
   const float inv = 1.f / (float)a.D;
   int at[NV];
   bool on[NV];
-  raw rw[NV];
+  raw rw[NV], rx[NV], rg[NV], rh[NV];
   float dw[NV][V], db[NV][V];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = (lane + j * G) * V;
     on[j] = c < a.D;
     at[j] = on[j] ? c : 0;
-    if (a.w) rw[j] = *reinterpret_cast<const raw*>(static_cast<const E*>(a.w) + at[j]);
 #pragma unroll
     for (int i = 0; i < V; ++i) dw[j][i] = db[j][i] = 0.f;
   }
-  for (long base = (long)blockIdx.x * teams; base < a.rows; base += (long)gridDim.x * teams) {
-    const long want = base + threadIdx.x / G;
-    const bool live = want < a.rows;
-    const long row = live ? want : a.rows - 1;
+  auto load = [&](long want) {
+    const long row = want < a.rows ? want : a.rows - 1;
     const E* x = static_cast<const E*>(a.x) + row_at(a.sx, row, a.T, a.H);
     const E* dy = static_cast<const E*>(a.dy) + row_at(a.sy, row, a.T, a.H);
-    raw rx[NV], rg[NV], rh[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) rx[j] = *reinterpret_cast<const raw*>(x + at[j]);
 #pragma unroll
     for (int j = 0; j < NV; ++j) rg[j] = *reinterpret_cast<const raw*>(dy + at[j]);
-    if (a.dh) {
-      const E* dh = static_cast<const E*>(a.dh) + row_at(a.sr, row, a.T, a.H);
+  };
+  const long step = (long)gridDim.x * teams;
+  long base = (long)blockIdx.x * teams;
+  if (PF) load(base + threadIdx.x / G);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) rw[j] = weight<E, V>(a.w, at[j], 1.f);
+  for (; base < a.rows; base += step) {
+    const long row = base + threadIdx.x / G;
+    const bool live = row < a.rows;
+    if (!PF) load(row);
+    if (DH) {
+      const E* dh = static_cast<const E*>(a.dh) + row_at(a.sr, live ? row : a.rows - 1, a.T, a.H);
 #pragma unroll
       for (int j = 0; j < NV; ++j) rh[j] = *reinterpret_cast<const raw*>(dh + at[j]);
     }
@@ -185,13 +204,14 @@ __global__ __launch_bounds__(1024) void layer_norm_bwd_kernel(const LayerNormArg
       IO::unpack(rx[j], u[j]);
       IO::unpack(rg[j], g[j]);
       float w[V];
-      if (a.w) IO::unpack(rw[j], w);
+      IO::unpack(rw[j], w);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         one[0] += on[j] ? u[j][i] : 0.f;
-        one[1] += on[j] ? (a.w ? g[j][i] * w[i] : g[j][i]) : 0.f;
+        one[1] += on[j] ? g[j][i] * w[i] : 0.f;
       }
     }
+    if (PF && base + step < a.rows) load(row + step);
     float m = 0.f, mg = 0.f;
     if (a.center) {
       team_sums<2>(one, G, sm, turn);
@@ -202,13 +222,12 @@ __global__ __launch_bounds__(1024) void layer_norm_bwd_kernel(const LayerNormArg
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       float w[V];
-      if (a.w) IO::unpack(rw[j], w);
+      IO::unpack(rw[j], w);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         u[j][i] -= m;
-        const float q = a.w ? g[j][i] * w[i] : g[j][i];
         two[0] += on[j] ? u[j][i] * u[j][i] : 0.f;
-        two[1] += on[j] ? u[j][i] * q : 0.f;
+        two[1] += on[j] ? u[j][i] * (g[j][i] * w[i]) : 0.f;
       }
     }
     team_sums<2>(two, G, sm, turn);
@@ -219,14 +238,13 @@ __global__ __launch_bounds__(1024) void layer_norm_bwd_kernel(const LayerNormArg
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       float w[V], v[V];
-      if (a.w) IO::unpack(rw[j], w);
-      if (a.dh) IO::unpack(rh[j], v);
+      IO::unpack(rw[j], w);
+      if (DH) IO::unpack(rh[j], v);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float un = u[j][i] * r;
-        const float q = a.w ? g[j][i] * w[i] : g[j][i];
-        const float d = r * (q - mg - un * mu);
-        v[i] = a.dh ? d + v[i] : d;
+        const float d = r * (fmaf(g[j][i], w[i], -mg) - un * mu);
+        v[i] = DH ? d + v[i] : d;
         dw[j][i] = fmaf(g[j][i], un, dw[j][i]);
         db[j][i] += g[j][i];
       }
@@ -235,6 +253,7 @@ __global__ __launch_bounds__(1024) void layer_norm_bwd_kernel(const LayerNormArg
   }
   if (!a.part) return;
   float* out = a.part + (long)blockIdx.x * 2 * a.D;
+#pragma unroll
   for (int k = 0; k < 2; ++k) {
     float(&d)[NV][V] = k ? db : dw;
     for (int mask = G; mask < WAVE; mask <<= 1) {
@@ -243,24 +262,24 @@ __global__ __launch_bounds__(1024) void layer_norm_bwd_kernel(const LayerNormArg
 #pragma unroll
         for (int i = 0; i < V; ++i) d[j][i] += __shfl_xor(d[j][i], mask);
     }
-    if (G < (int)blockDim.x) {   // the waves one after the other
-      const int wave = threadIdx.x / WAVE, nw = blockDim.x / WAVE;
-      for (int w = 0; w < nw; ++w) {
+    // the teams, or, where a wave has several, the waves, one after the other
+    const int per = G > WAVE ? G : WAVE, mine = threadIdx.x / per, n = blockDim.x / per;
+    if (n > 1) {
+      for (int w = 0; w < n; ++w) {
         __syncthreads();
-        if (wave == w && (int)(threadIdx.x & (WAVE - 1)) < G) {
+        if (mine == w) {
 #pragma unroll
           for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-              float& c = cols[(j * V + i) * WAVE + lane];
+              float& c = cols[(j * V + i) * per + lane];
               d[j][i] += w ? c : 0.f;
               c = d[j][i];
             }
         }
       }
-      if (wave != nw - 1) continue;
     }
-    if ((int)(threadIdx.x & (WAVE - 1)) < G || G > WAVE) {
+    if (mine == n - 1 && (G >= WAVE || (int)(threadIdx.x & (WAVE - 1)) < G)) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -268,12 +287,6 @@ __global__ __launch_bounds__(1024) void layer_norm_bwd_kernel(const LayerNormArg
           if (on[j]) out[(long)k * a.D + at[j] + i] = d[j][i];
     }
   }
-}
-
-int pow2_at_least(int n) {
-  int p = 1;
-  while (p < n) p *= 2;
-  return p;
 }
 
 // Dimensions whose steps follow from one another in every tensor are taken as
@@ -322,52 +335,92 @@ bool aligned(const LayerNormArgs& a, bool bwd, int V, int size) {
 struct Shape {
   int G, NV, block;
 };
-// Lanes, vectors a lane and workgroup for rows of n vectors, `most` vectors a
-// lane at most.
-Shape shape_of(int n, int most) {
+// Lanes, vectors a lane and threads a workgroup for rows of n vectors, `most`
+// vectors a lane unless a row needs more than 1024 lanes of them.
+Shape shape_of(int n, int most, int block) {
   Shape s;
-  if (n <= WAVE) {
-    s.G = pow2_at_least(n);
-    s.NV = 1;
-    s.block = 256;
-    return s;
+  s.NV = 1;
+  s.G = 1;
+  while (s.G < WAVE && s.G < n) s.G *= 2;
+  while (s.G * s.NV < n) {
+    if (s.NV < most || s.G == 1024)
+      s.NV *= 2;
+    else
+      s.G *= 2;
   }
-  s.NV = pow2_at_least((n + WAVE - 1) / WAVE);
-  s.G = WAVE;
-  while (s.NV > most) {
-    s.NV /= 2;
-    s.G *= 2;
-  }
-  s.block = s.G > WAVE ? s.G : 256;
+  s.block = s.G > block ? s.G : block;
   return s;
 }
 
-constexpr int LN_PARTS = 512;   // workgroups of the backward kernel with weights, at most
+// Values a lane, forward and backward (where the weights' sums want few
+// workgroups with many rows each: 16 values 56 us, 8 values 62 for 16384 rows of
+// 2048, with 256 workgroups of 512 threads).
+constexpr int LN_LANE = 8, LN_LANE_BWD = 16;
+constexpr int LN_PARTS = 512;   // workgroups of the backward kernel, at most
 
-template <typename E, int V, int NV>
+template <typename E, int V, int NV, int NT>
 hipError_t run_fwd(const LayerNormArgs& a, const Shape& p, hipStream_t s) {
   const long teams = p.block / p.G;
   long grid = (a.rows + teams - 1) / teams;
-  if (grid > 4096) grid = 4096;
-  hipLaunchKernelGGL((layer_norm_kernel<E, V, NV>), dim3((unsigned)grid), dim3(p.block), 0, s, a, p.G);
+  if (grid > (1 << 20)) grid = 1 << 20;
+  if (a.r)
+    hipLaunchKernelGGL((layer_norm_kernel<E, V, NV, NT, true>), dim3((unsigned)grid), dim3(p.block), 0, s, a, p.G);
+  else
+    hipLaunchKernelGGL((layer_norm_kernel<E, V, NV, NT, false>), dim3((unsigned)grid), dim3(p.block), 0, s, a, p.G);
   return hipGetLastError();
 }
-template <typename E, int V, int NV>
+template <typename E, int V, int NV, int NT>
 hipError_t run_bwd(const LayerNormArgs& a, const Shape& p, hipStream_t s) {
   const long teams = p.block / p.G;
   long grid = (a.rows + teams - 1) / teams;
-  if (grid > LN_PARTS) grid = LN_PARTS;
+  const long most = p.block > 256 ? LN_PARTS / 2 : LN_PARTS;
+  if (grid > most) grid = most;
   if (grid > 0) {
-    hipLaunchKernelGGL((layer_norm_bwd_kernel<E, V, NV>), dim3((unsigned)grid), dim3(p.block), 0, s, a, p.G);
+    if (a.dh)
+      hipLaunchKernelGGL((layer_norm_bwd_kernel<E, V, NV, NT, true>), dim3((unsigned)grid), dim3(p.block), 0, s, a, p.G);
+    else
+      hipLaunchKernelGGL((layer_norm_bwd_kernel<E, V, NV, NT, false>), dim3((unsigned)grid), dim3(p.block), 0, s, a, p.G);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (a.dw) {
-    const hipError_t e = launch_column_sums(a.part, (int)grid, 2L * a.D, a.D, 0, a.dw, s);
-    if (e != hipSuccess) return e;
-  }
-  if (a.db) return launch_column_sums(a.part + a.D, (int)grid, 2L * a.D, a.D, 0, a.db, s);
+  if (a.part) return launch_column_sums(a.part, (int)grid, a.D, 1, a.dw, a.db, s);
   return hipSuccess;
+}
+
+template <typename E, int V, int NV, bool BWD>
+hipError_t run_nv(const LayerNormArgs& a, const Shape& p, hipStream_t s) {
+  if constexpr (BWD) {
+    if (p.block > 512) return run_bwd<E, V, NV, 1024>(a, p, s);
+    return p.block > 256 ? run_bwd<E, V, NV, 512>(a, p, s) : run_bwd<E, V, NV, 256>(a, p, s);
+  } else {
+    return p.block > 256 ? run_fwd<E, V, NV, 1024>(a, p, s) : run_fwd<E, V, NV, 256>(a, p, s);
+  }
+}
+// (16384 values are at most 16 for each of 1024 lanes)
+template <typename E, int V, bool BWD>
+hipError_t run_v(const LayerNormArgs& a, hipStream_t s) {
+  const int lane = BWD ? LN_LANE_BWD : LN_LANE, n = (a.D + V - 1) / V;
+  Shape p = shape_of(n, lane / V, 256);
+  // (backward, workgroups of 512 threads where 256 of them have four rows each or
+  // more: 16384 rows of 2048 56 us in place of 59; for 4995 rows of 48, 10 to a
+  // wave, 9.0 in place of 7.6, so not below)
+  if (BWD && p.block == 256 && a.rows >= 1024L * (512 / p.G)) p.block = 512;
+  if (p.NV == 1) return run_nv<E, V, 1, BWD>(a, p, s);
+  if (p.NV == 2) return run_nv<E, V, 2, BWD>(a, p, s);
+  if constexpr (V < 8) {
+    if (p.NV == 4) return run_nv<E, V, 4, BWD>(a, p, s);
+  }
+  if constexpr (V == 1) {
+    if (p.NV == 8) return run_nv<E, V, 8, BWD>(a, p, s);
+    if (p.NV == 16) return run_nv<E, V, 16, BWD>(a, p, s);
+  }
+  return hipErrorInvalidValue;
+}
+template <typename E, bool BWD>
+hipError_t run(LayerNormArgs a, hipStream_t s) {
+  merge_rows(a, BWD);
+  constexpr int V = 16 / sizeof(E);
+  return aligned(a, BWD, V, sizeof(E)) ? run_v<E, V, BWD>(a, s) : run_v<E, 1, BWD>(a, s);
 }
 
 }  // namespace
@@ -375,40 +428,13 @@ hipError_t run_bwd(const LayerNormArgs& a, const Shape& p, hipStream_t s) {
 size_t layer_norm_part_bytes(int D) { return (size_t)LN_PARTS * 2 * D * sizeof(float); }
 
 template <typename E>
-hipError_t launch_layer_norm(const LayerNormArgs& in, hipStream_t s) {
-  LayerNormArgs a = in;
-  merge_rows(a, false);
-  constexpr int V = 16 / sizeof(E);
-  if (aligned(a, false, V, sizeof(E))) {
-    const Shape p = shape_of((a.D + V - 1) / V, 32 / V);
-    if (p.NV == 1) return run_fwd<E, V, 1>(a, p, s);
-    if (p.NV == 2) return run_fwd<E, V, 2>(a, p, s);
-    if (p.NV == 4) return run_fwd<E, V, 4>(a, p, s);
-    return run_fwd<E, V, 32 / V>(a, p, s);
-  }
-  const Shape p = shape_of(a.D, 16);
-  if (p.NV == 1) return run_fwd<E, 1, 1>(a, p, s);
-  if (p.NV <= 4) return run_fwd<E, 1, 4>(a, p, s);
-  return run_fwd<E, 1, 16>(a, p, s);
+hipError_t launch_layer_norm(const LayerNormArgs& a, hipStream_t s) {
+  return run<E, false>(a, s);
 }
-
 template <typename E>
-hipError_t launch_layer_norm_bwd(const LayerNormArgs& in, hipStream_t s) {
-  LayerNormArgs a = in;
-  merge_rows(a, true);
-  constexpr int V = 16 / sizeof(E);
-  if (aligned(a, true, V, sizeof(E))) {
-    const Shape p = shape_of((a.D + V - 1) / V, 16 / V);
-    if (p.NV == 1) return run_bwd<E, V, 1>(a, p, s);
-    if (p.NV == 2) return run_bwd<E, V, 2>(a, p, s);
-    return run_bwd<E, V, 16 / V>(a, p, s);
-  }
-  const Shape p = shape_of(a.D, 16);
-  if (p.NV == 1) return run_bwd<E, 1, 1>(a, p, s);
-  if (p.NV <= 4) return run_bwd<E, 1, 4>(a, p, s);
-  return run_bwd<E, 1, 16>(a, p, s);
+hipError_t launch_layer_norm_bwd(const LayerNormArgs& a, hipStream_t s) {
+  return run<E, true>(a, s);
 }
-
 template hipError_t launch_layer_norm<bf16>(const LayerNormArgs&, hipStream_t);
 template hipError_t launch_layer_norm<float>(const LayerNormArgs&, hipStream_t);
 template hipError_t launch_layer_norm_bwd<bf16>(const LayerNormArgs&, hipStream_t);

@@ -160,7 +160,7 @@ hipError_t run_tiles(RecurrenceArgs a, bool bwd, char* ws, hipStream_t s) {
     const hipError_t e = recurrence_tiles<E, V>(a, g, bwd, s);
     if (e != hipSuccess) return e;
   }
-  if (part) return launch_column_sums(a.part, parts, a.D, a.D, 0, a.dlam, s);
+  if (part) return launch_column_sums(a.part, parts, a.D, 0, nullptr, a.dlam, s);
   return hipSuccess;
 }
 

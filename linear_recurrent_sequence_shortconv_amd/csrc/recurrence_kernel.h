@@ -15,7 +15,7 @@ namespace prism {
 // each; the exponential's argument adds 2^-24 of its size), of fp32 inputs by
 // the library's.
 template <typename E> __device__ inline float gate_exp(float x) {
-  if constexpr (sizeof(E) == 2) return __expf(x);
+  if constexpr (sizeof(E) == 2) return __builtin_amdgcn_exp2f(1.44269504f * x);
   return expf(x);
 }
 template <typename E> __device__ inline float gate_rcp(float x) {
@@ -27,25 +27,24 @@ template <typename E> __device__ inline float gate_sqrt(float x) {
   return sqrtf(x);
 }
 
-// sigma(z) and 1 - sigma(z), each to its own size (1 - p of a p near 1 would
-// keep few digits).
+// 1 - sigma(z) from e = e^-z and p = sigma(z) = 1 / (1 + e), to its own size (1 - p
+// of a p near 1 would keep few digits); where e is infinite, 1.
+__device__ inline float other_side(float e, float p) { return p == 0.f ? 1.f : e * p; }
 template <typename E>
 __device__ inline void sigmoid_pair(float z, float& p, float& q) {
   const float e = gate_exp<E>(-z);
   p = gate_rcp<E>(1.f + e);
-  q = e > 1.f ? 1.f - p : e * p;
+  q = other_side(e, p);
 }
 
-// 1 - e^-z for z >= 0: below 1/4 by its series (1 - a^2 of an a near 1 would
-// keep few digits; the first term left out is below 2^-24 of the sum), else from
-// aa = e^-z.
+// 1 - e^-z for z >= 0, aa = e^-z: below 1/8 by its series (1 - aa would be off by
+// 2^-24 / z of itself; the first term left out is 2^-24 of the sum).
 __device__ inline float one_minus_exp(float z, float aa) {
-  float s = fmaf(z, -1.f / 6.f, 1.f);
-  s = fmaf(z * (-1.f / 5.f), s, 1.f);
-  s = fmaf(z * (-1.f / 4.f), s, 1.f);
-  s = fmaf(z * (-1.f / 3.f), s, 1.f);
-  s = fmaf(z * (-1.f / 2.f), s, 1.f);
-  return z < 0.25f ? z * s : 1.f - aa;
+  float s = fmaf(z, 1.f / 120.f, -1.f / 24.f);
+  s = fmaf(z, s, 1.f / 6.f);
+  s = fmaf(z, s, -0.5f);
+  s = fmaf(z, s, 1.f);
+  return z < 0.125f ? z * s : 1.f - aa;
 }
 
 // What the gates of a value keep between the two sweeps of a tile: a, and k, from
@@ -72,9 +71,9 @@ template <typename E, int G, bool INP>
 __device__ inline void gate_inputs(float x, float f, float i, float lam, float& a, float& u) {
   u = x;
   if constexpr (G == GATE_POWER) {
-    const float y = lam * gate_rcp<E>(1.f + gate_exp<E>(-f));
-    a = gate_exp<E>(-y);
-    u *= gate_sqrt<E>(one_minus_exp(2.f * y, a * a));
+    const float p = gate_rcp<E>(1.f + gate_exp<E>(-f));
+    a = gate_exp<E>(-lam * p);
+    u *= gate_sqrt<E>(one_minus_exp(2.f * lam * p, a * a));
   } else {
     const GateValue g = gate_value<E, G>(f, lam);
     a = g.a;
@@ -83,27 +82,35 @@ __device__ inline void gate_inputs(float x, float f, float i, float lam, float& 
   if (INP) u *= gate_rcp<E>(1.f + gate_exp<E>(-i));
 }
 
-// Gradients of a value's inputs from g, that of h_t, and h_{t-1}; dl: its part
-// of the gradient of lam.  Where lam sigma(f) = 0 the root's slope is infinite,
-// and its part is left out.
+// Gradients of a value's inputs from g, that of h_t, ag = a_t g and h_{t-1}; dl: its
+// part of the gradient of lam.  Where lam sigma(f) = 0 the root's slope is
+// infinite, and its part is left out.
 template <typename E, int G, bool INP>
-__device__ inline void gate_gradients(const GateValue& v, float x, float i, float lam, float before, float g, float& dx,
-                                      float& df, float& di, float& dl) {
+__device__ inline void gate_gradients(const GateValue& v, float x, float i, float lam, float before, float g, float ag,
+                                      float& dx, float& df, float& di, float& dl) {
   float s = 1.f, t = 0.f, c = 1.f;
   if (INP) sigmoid_pair<E>(i, s, t);
   const float xi = INP ? s * x : x;
   dl = 0.f;
   if constexpr (G == GATE_LOG) {
-    df = g * v.a * before;
+    df = ag * before;
   } else if constexpr (G == GATE_SIGMOID) {
     c = v.k;
-    df = g * (before - xi) * v.a * c;
+    df = ag * (before - xi) * c;
   } else {
-    const float p = gate_rcp<E>(1.f + v.k), q = v.k > 1.f ? 1.f - p : v.k * p, y = lam * p;
-    c = gate_sqrt<E>(one_minus_exp(2.f * y, v.a * v.a));
-    const float slope = c > 0.f ? v.a * gate_rcp<E>(c) : 0.f;
-    dl = -p * (g * v.a * fmaf(-slope, xi, before));   // -p times the gradient of log a
-    df = lam * q * dl;
+    const float p = gate_rcp<E>(1.f + v.k);
+    const float square = one_minus_exp(2.f * lam * p, v.a * v.a);
+    float slope;
+    if constexpr (sizeof(E) == 2) {
+      const float r = __builtin_amdgcn_rsqf(square);
+      c = square > 0.f ? square * r : square;
+      slope = square > 0.f ? v.a * r : 0.f;
+    } else {
+      c = sqrtf(square);
+      slope = c > 0.f ? v.a / c : 0.f;
+    }
+    dl = -p * (ag * fmaf(-slope, xi, before));   // -p times the gradient of log a
+    df = lam * other_side(v.k, p) * dl;
   }
   dx = g * c * s;
   di = INP ? dx * x * t : 0.f;

@@ -36,7 +36,7 @@ struct TileArgs {
 };
 
 constexpr unsigned NOT_YET = 0xffffffffu;   // of a word's A: nothing written so far
-constexpr int LOOK = 8;
+constexpr int LOOK = 4;
 
 __device__ inline float through(float A, float U, float h) { return A == 0.f ? U : fmaf(A, h, U); }
 
@@ -89,6 +89,7 @@ __device__ inline void look_back(const unsigned long long* words, long stride, i
 }
 
 // Rows a strip and waves a tile, forward and backward.
+
 constexpr int REC_R = 16, REC_W = 8, REC_BWD_R = 8, REC_BWD_W = 8;
 
 // Which rows of a strip start and end a sequence and which belong to one, as
@@ -125,8 +126,9 @@ __device__ inline Strip strip_of(const RecurrenceArgs& a, int row) {
   return s;
 }
 
-// Walks a tensor's rows of a strip; rows past its end are its last.
-template <typename E>
+// Walks a tensor's rows of a strip; rows past its end are its last.  PLAIN: all
+// rows are one sequence's, one step apart.
+template <typename E, bool PLAIN>
 struct RowWalk {
   const E* p;
   long step, jump;
@@ -142,13 +144,17 @@ struct RowWalk {
     }
   }
   __device__ inline void next(const Strip& s, int k) {   // from row k to k + 1
-    if (k + 1 < s.n) {
+    if (PLAIN) {
+      p += step;
+    } else if (k + 1 < s.n) {
       p += step;
       if (s.first >> (k + 1) & 1) p += jump;
     }
   }
   __device__ inline void back(const Strip& s, int k) {   // from row k to k - 1
-    if (k > 0 && k < s.n) {
+    if (PLAIN) {
+      p -= step;
+    } else if (k > 0 && k < s.n) {
       p -= step;
       if (s.first >> k & 1) p -= jump;
     }
@@ -213,7 +219,7 @@ __device__ inline void enter_strip(const TileArgs& g, int tile, int slice, int s
   }
 }
 
-// The workgroup's tile and slice of channels.
+// The workgroup's place in the order of tiles and slices.
 __device__ inline int take_tile(const TileArgs& g) {
   if (!g.words) return blockIdx.x;
   __shared__ unsigned taken;
@@ -223,19 +229,20 @@ __device__ inline int take_tile(const TileArgs& g) {
   return __builtin_amdgcn_readfirstlane(taken);
 }
 
-template <typename E, int V, int G, bool INP, int R, int W>
-__global__ __launch_bounds__(W * WAVE) void recurrence_tile_kernel(const RecurrenceArgs a, const TileArgs g) {
+// A strip's part of a pass: its values in registers, the sweep for (A, U), and the
+// sweep from the state that enters it.
+template <typename E, int V, int G, bool INP, int R>
+struct ForwardStrip {
   typedef VecIo<E, V> IO;
   typedef typename IO::raw raw;
-  const int id = take_tile(g), tile = id / g.slices, slice = id - tile * g.slices;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE), lane = threadIdx.x & (WAVE - 1);
-  int c = (slice * WAVE + lane) * V;
-  const bool on = c < a.D;
-  if (!on) c = 0;
-  const Strip s = strip_of<R>(a, tile * (R * W) + wave * R);
-  raw rx[R], rf[R], ri[R];
-  {
-    RowWalk<E> px(a.x, a.sx, a, g, s.row), pf(a.f, a.sf, a, g, s.row), pi(INP ? a.i : a.x, INP ? a.si : a.sx, a, g, s.row);
+  float lam[V], av[R][V], uv[R][V];
+
+  template <bool PLAIN>
+  __device__ inline void first_sweep(const RecurrenceArgs& a, const TileArgs& g, const Strip& s, int c, bool on,
+                                     float (&A)[V], float (&U)[V]) {
+    raw rx[R], rf[R], ri[R];
+    RowWalk<E, PLAIN> px(a.x, a.sx, a, g, s.row), pf(a.f, a.sf, a, g, s.row),
+        pi(INP ? a.i : a.x, INP ? a.si : a.sx, a, g, s.row);
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       rx[k] = load_raw<E, V>(px.p, c);
@@ -245,38 +252,15 @@ __global__ __launch_bounds__(W * WAVE) void recurrence_tile_kernel(const Recurre
       pf.next(s, k);
       if (INP) pi.next(s, k);
     }
-  }
-  float lam[V], A[V], U[V], h[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    lam[v] = G == GATE_POWER && on ? a.lam[c + v] : 0.f;
-    A[v] = 1.f;
-    U[v] = 0.f;
-  }
-  float av[R][V], uv[R][V];
-#pragma unroll
-  for (int k = 0; k < R; ++k) {
-    float x[V], f[V], i[V];
-    IO::unpack(rx[k], x);
-    IO::unpack(rf[k], f);
-    if (INP) IO::unpack(ri[k], i);
-#pragma unroll
-    for (int v = 0; v < V; ++v) gate_inputs<E, G, INP>(x[v], f[v], INP ? i[v] : 0.f, lam[v], av[k][v], uv[k][v]);
-  }
-  constexpr unsigned ALL = R == 32 ? ~0u : (1u << R) - 1;
-  const bool plain = s.in == ALL && !(s.first | s.last);
-  if (plain) {
-#pragma unroll
-    for (int k = 0; k < R; ++k)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        U[v] = fmaf(av[k][v], U[v], uv[k][v]);
-        A[v] *= av[k][v];
-      }
-  } else {
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-      if (s.first >> k & 1) {
+      float x[V], f[V], i[V];
+      IO::unpack(rx[k], x);
+      IO::unpack(rf[k], f);
+      if (INP) IO::unpack(ri[k], i);
+#pragma unroll
+      for (int v = 0; v < V; ++v) gate_inputs<E, G, INP>(x[v], f[v], INP ? i[v] : 0.f, lam[v], av[k][v], uv[k][v]);
+      if (!PLAIN && (s.first >> k & 1)) {
         const long at = (long)batch_of(a, s.row + k) * a.D + c;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -284,7 +268,7 @@ __global__ __launch_bounds__(W * WAVE) void recurrence_tile_kernel(const Recurre
           A[v] = 0.f;
           U[v] = uv[k][v];
         }
-      } else if (s.in >> k & 1) {
+      } else if (PLAIN || (s.in >> k & 1)) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           U[v] = fmaf(av[k][v], U[v], uv[k][v]);
@@ -293,53 +277,79 @@ __global__ __launch_bounds__(W * WAVE) void recurrence_tile_kernel(const Recurre
       }
     }
   }
-  // (the tile goes on from the one before it unless a sequence starts with it)
-  const Sequence q = find_sequence(a.cu, a.B, a.T, a.rows, tile * (R * W));
-  enter_strip<V, W>(g, tile, slice, 1, tile, q.start != tile * (R * W) && tile > 0, wave, A, U, h);
-  RowWalk<E> ph(a.h, a.sh, a, g, s.row);
-#pragma unroll
-  for (int k = 0; k < R; ++k) {
-    const bool first = !plain && (s.first >> k & 1), in = plain || (s.in >> k & 1);
-    if (in) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) h[v] = first ? uv[k][v] : fmaf(av[k][v], h[v], uv[k][v]);
-      if (on) *reinterpret_cast<raw*>(const_cast<E*>(ph.p) + c) = IO::pack(h);
-      if (!plain && a.hT && (s.last >> k & 1)) {
-        const long at = (long)batch_of(a, s.row + k) * a.D + c;
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-          if (on) a.hT[at + v] = h[v];
-      }
-    }
-    ph.next(s, k);
-  }
-}
 
-// Rows from the last to the first.  before = h_{t-1} is the row of h before, or
-// h0 at a sequence's first token.
+  template <bool PLAIN>
+  __device__ inline void second_sweep(const RecurrenceArgs& a, const TileArgs& g, const Strip& s, int c, bool on,
+                                      float (&h)[V]) const {
+    RowWalk<E, PLAIN> ph(a.h, a.sh, a, g, s.row);
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      if (PLAIN || (s.in >> k & 1)) {
+        const bool first = !PLAIN && (s.first >> k & 1);
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = first ? uv[k][v] : fmaf(av[k][v], h[v], uv[k][v]);
+        if (on) *reinterpret_cast<raw*>(const_cast<E*>(ph.p) + c) = IO::pack(h);
+        if (!PLAIN && a.hT && (s.last >> k & 1)) {
+          const long at = (long)batch_of(a, s.row + k) * a.D + c;
+#pragma unroll
+          for (int v = 0; v < V; ++v)
+            if (on) a.hT[at + v] = h[v];
+        }
+      }
+      ph.next(s, k);
+    }
+  }
+};
+
 template <typename E, int V, int G, bool INP, int R, int W>
-__global__ __launch_bounds__(W * WAVE) void recurrence_tile_bwd_kernel(const RecurrenceArgs a, const TileArgs g) {
-  typedef VecIo<E, V> IO;
-  typedef typename IO::raw raw;
-  const int id = take_tile(g), turn = id / g.slices, slice = id - turn * g.slices, tile = g.tiles - 1 - turn;
+__global__ __launch_bounds__(W * WAVE, 4) void recurrence_tile_kernel(const RecurrenceArgs a, const TileArgs g) {
+  const int id = take_tile(g), tile = id / g.slices, slice = id - tile * g.slices;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE), lane = threadIdx.x & (WAVE - 1);
   int c = (slice * WAVE + lane) * V;
   const bool on = c < a.D;
   if (!on) c = 0;
   const Strip s = strip_of<R>(a, tile * (R * W) + wave * R);
-  raw rx[R], ri[R], rb[R], rg[R];
-  GateValue gv[R][V];
-  float lam[V], A[V], U[V], carry[V], dlam[V];
+  const bool plain = s.in == (1u << R) - 1 && !(s.first | s.last);
+  ForwardStrip<E, V, G, INP, R> strip;
+  float A[V], U[V], h[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    lam[v] = G == GATE_POWER && on ? a.lam[c + v] : 0.f;
+    strip.lam[v] = G == GATE_POWER && on ? a.lam[c + v] : 0.f;
     A[v] = 1.f;
-    U[v] = dlam[v] = 0.f;
+    U[v] = 0.f;
   }
-  {
+  if (plain)
+    strip.template first_sweep<true>(a, g, s, c, on, A, U);
+  else
+    strip.template first_sweep<false>(a, g, s, c, on, A, U);
+  // (the tile goes on from the one before it unless a sequence starts with it; the
+  // first strip knows)
+  bool open = false;
+  if (wave == 0 && tile > 0) open = !(s.first & 1);
+  enter_strip<V, W>(g, tile, slice, 1, tile, open, wave, A, U, h);
+  if (plain)
+    strip.template second_sweep<true>(a, g, s, c, on, h);
+  else
+    strip.template second_sweep<false>(a, g, s, c, on, h);
+}
+
+// Rows from the last to the first.  before = h_{t-1} is the row of h before, or
+// h0 at a sequence's first token.
+template <typename E, int V, int G, bool INP, int R>
+struct BackwardStrip {
+  typedef VecIo<E, V> IO;
+  typedef typename IO::raw raw;
+  raw rx[R], ri[R], rb[R], rg[R];
+  GateValue gv[R][V];
+  float lam[V], dlam[V];
+
+  template <bool PLAIN>
+  __device__ inline void first_sweep(const RecurrenceArgs& a, const TileArgs& g, const Strip& s, int c, bool on,
+                                     float (&A)[V], float (&U)[V]) {
     raw rf[R];
-    RowWalk<E> px(a.x, a.sx, a, g, s.row), pf(a.f, a.sf, a, g, s.row), pi(INP ? a.i : a.x, INP ? a.si : a.sx, a, g, s.row),
-        pb(a.h, a.sh, a, g, s.row), pg(a.dh, a.sdh, a, g, s.row);
+    RowWalk<E, PLAIN> px(a.x, a.sx, a, g, s.row), pf(a.f, a.sf, a, g, s.row),
+        pi(INP ? a.i : a.x, INP ? a.si : a.sx, a, g, s.row), pb(a.h, a.sh, a, g, s.row), pg(a.dh, a.sdh, a, g, s.row);
+    if (PLAIN) pb.p -= pb.step;
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       rf[k] = load_raw<E, V>(pf.p, c);
@@ -350,7 +360,7 @@ __global__ __launch_bounds__(W * WAVE) void recurrence_tile_bwd_kernel(const Rec
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       // (a row that starts a sequence, or is of none, has no row before it)
-      const bool inner = (s.in >> k & 1) && !(s.first >> k & 1);
+      const bool inner = !PLAIN && (s.in >> k & 1) && !(s.first >> k & 1);
       rx[k] = load_raw<E, V>(px.p, c);
       if (INP) ri[k] = load_raw<E, V>(pi.p, c);
       rb[k] = load_raw<E, V>(pb.p - (inner ? pb.step : 0), c);
@@ -359,81 +369,109 @@ __global__ __launch_bounds__(W * WAVE) void recurrence_tile_bwd_kernel(const Rec
       pb.next(s, k);
     }
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
+    for (int k = R - 1; k >= 0; --k) {
       float f[V];
       IO::unpack(rf[k], f);
 #pragma unroll
       for (int v = 0; v < V; ++v) gv[k][v] = gate_value<E, G>(f[v], lam[v]);
-    }
-  }
-  constexpr unsigned ALL = R == 32 ? ~0u : (1u << R) - 1;
-  const bool plain = s.in == ALL && !(s.first | s.last);
+      if (!PLAIN && (s.last >> k & 1)) {
+        const long at = (long)batch_of(a, s.row + k) * a.D + c;
 #pragma unroll
-  for (int k = R - 1; k >= 0; --k) {
-    if (!plain && (s.last >> k & 1)) {
-      const long at = (long)batch_of(a, s.row + k) * a.D + c;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        A[v] = 0.f;
-        U[v] = g.first && on ? g.first[at + v] : 0.f;
+        for (int v = 0; v < V; ++v) {
+          A[v] = 0.f;
+          U[v] = g.first && on ? g.first[at + v] : 0.f;
+        }
       }
-    }
-    if (plain || (s.in >> k & 1)) {
-      float d[V];
-      IO::unpack(rg[k], d);
+      if (PLAIN || (s.in >> k & 1)) {
+        float d[V];
+        IO::unpack(rg[k], d);
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        U[v] = gv[k][v].a * (d[v] + U[v]);
-        A[v] = A[v] == 0.f ? 0.f : A[v] * gv[k][v].a;
+        for (int v = 0; v < V; ++v) {
+          U[v] = gv[k][v].a * (d[v] + U[v]);
+          A[v] *= gv[k][v].a;
+        }
       }
     }
   }
-  // (the tile goes on from the one behind it unless a sequence ends with it)
-  const int end = min((tile + 1) * (R * W), a.rows);
-  const Sequence q = find_sequence(a.cu, a.B, a.T, a.rows, end - 1);
-  enter_strip<V, W>(g, tile, slice, -1, turn, q.end != end && turn > 0, W - 1 - wave, A, U, carry);
-  const int end_row = s.row + max(s.n - 1, 0);
-  RowWalk<E> px(a.dx, a.sdx, a, g, end_row), pf(a.df, a.sdf, a, g, end_row),
-      pi(INP ? a.di : a.dx, INP ? a.sdi : a.sdx, a, g, end_row);
+
+  template <bool PLAIN>
+  __device__ inline void second_sweep(const RecurrenceArgs& a, const TileArgs& g, const Strip& s, int c, bool on,
+                                      float (&carry)[V]) {
+    const int end = s.row + max(s.n - 1, 0);
+    RowWalk<E, PLAIN> px(a.dx, a.sdx, a, g, end), pf(a.df, a.sdf, a, g, end),
+        pi(INP ? a.di : a.dx, INP ? a.sdi : a.sdx, a, g, end);
 #pragma unroll
-  for (int k = R - 1; k >= 0; --k) {
-    if (!plain && (s.last >> k & 1)) {
-      const long at = (long)batch_of(a, s.row + k) * a.D + c;
+    for (int k = R - 1; k >= 0; --k) {
+      if (!PLAIN && (s.last >> k & 1)) {
+        const long at = (long)batch_of(a, s.row + k) * a.D + c;
 #pragma unroll
-      for (int v = 0; v < V; ++v) carry[v] = g.first && on ? g.first[at + v] : 0.f;
-    }
-    if (plain || (s.in >> k & 1)) {
-      float x[V], i[V], b[V], d[V], dx[V], df[V], di[V];
-      IO::unpack(rx[k], x);
-      if (INP) IO::unpack(ri[k], i);
-      IO::unpack(rb[k], b);
-      IO::unpack(rg[k], d);
-      const bool first = !plain && (s.first >> k & 1);
-      const long at = first ? (long)batch_of(a, s.row + k) * a.D + c : 0;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if (first) b[v] = a.h0 && on ? a.h0[at + v] : 0.f;
-        const float gt = d[v] + carry[v];
-        carry[v] = gv[k][v].a * gt;
-        float dl;
-        gate_gradients<E, G, INP>(gv[k][v], x[v], INP ? i[v] : 0.f, lam[v], b[v], gt, dx[v], df[v], di[v], dl);
-        if (G == GATE_POWER) dlam[v] += dl;
-        if (first && a.dh0 && on) a.dh0[at + v] = carry[v];
+        for (int v = 0; v < V; ++v) carry[v] = g.first && on ? g.first[at + v] : 0.f;
       }
-      if (on) {
-        *reinterpret_cast<raw*>(const_cast<E*>(px.p) + c) = IO::pack(dx);
-        *reinterpret_cast<raw*>(const_cast<E*>(pf.p) + c) = IO::pack(df);
-        if (INP) *reinterpret_cast<raw*>(const_cast<E*>(pi.p) + c) = IO::pack(di);
+      if (PLAIN || (s.in >> k & 1)) {
+        float x[V], i[V], b[V], d[V], dx[V], df[V], di[V];
+        IO::unpack(rx[k], x);
+        if (INP) IO::unpack(ri[k], i);
+        IO::unpack(rb[k], b);
+        IO::unpack(rg[k], d);
+        const bool first = !PLAIN && (s.first >> k & 1);
+        const long at = first ? (long)batch_of(a, s.row + k) * a.D + c : 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          if (first) b[v] = a.h0 && on ? a.h0[at + v] : 0.f;
+          const float gt = d[v] + carry[v];
+          carry[v] = gv[k][v].a * gt;
+          float dl;
+          gate_gradients<E, G, INP>(gv[k][v], x[v], INP ? i[v] : 0.f, lam[v], b[v], gt, carry[v], dx[v], df[v], di[v], dl);
+          if (G == GATE_POWER) dlam[v] += dl;
+          if (first && a.dh0 && on) a.dh0[at + v] = carry[v];
+        }
+        if (on) {
+          *reinterpret_cast<raw*>(const_cast<E*>(px.p) + c) = IO::pack(dx);
+          *reinterpret_cast<raw*>(const_cast<E*>(pf.p) + c) = IO::pack(df);
+          if (INP) *reinterpret_cast<raw*>(const_cast<E*>(pi.p) + c) = IO::pack(di);
+        }
       }
+      px.back(s, k);
+      pf.back(s, k);
+      if (INP) pi.back(s, k);
     }
-    px.back(s, k);
-    pf.back(s, k);
-    if (INP) pi.back(s, k);
   }
+};
+
+template <typename E, int V, int G, bool INP, int R, int W>
+__global__ __launch_bounds__(W * WAVE, 4) void recurrence_tile_bwd_kernel(const RecurrenceArgs a, const TileArgs g) {
+  const int id = take_tile(g), turn = id / g.slices, slice = id - turn * g.slices, tile = g.tiles - 1 - turn;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE), lane = threadIdx.x & (WAVE - 1);
+  int c = (slice * WAVE + lane) * V;
+  const bool on = c < a.D;
+  if (!on) c = 0;
+  const Strip s = strip_of<R>(a, tile * (R * W) + wave * R);
+  const bool plain = s.in == (1u << R) - 1 && !(s.first | s.last);
+  BackwardStrip<E, V, G, INP, R> strip;
+  float A[V], U[V], carry[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    strip.lam[v] = G == GATE_POWER && on ? a.lam[c + v] : 0.f;
+    A[v] = 1.f;
+    U[v] = strip.dlam[v] = 0.f;
+  }
+  if (plain)
+    strip.template first_sweep<true>(a, g, s, c, on, A, U);
+  else
+    strip.template first_sweep<false>(a, g, s, c, on, A, U);
+  // (the tile goes on from the one behind it unless a sequence ends with it; only
+  // the last tile of a batch, the first in turn, is not full)
+  bool open = false;
+  if (wave == W - 1 && turn > 0) open = !(s.last >> (R - 1) & 1);
+  enter_strip<V, W>(g, tile, slice, -1, turn, open, W - 1 - wave, A, U, carry);
+  if (plain)
+    strip.template second_sweep<true>(a, g, s, c, on, carry);
+  else
+    strip.template second_sweep<false>(a, g, s, c, on, carry);
   if constexpr (G == GATE_POWER) {   // the tile's part of dlam, wave after wave
     __shared__ float sm[W][V][WAVE];
 #pragma unroll
-    for (int v = 0; v < V; ++v) sm[wave][v][lane] = dlam[v];
+    for (int v = 0; v < V; ++v) sm[wave][v][lane] = strip.dlam[v];
     __syncthreads();
     if (wave == 0 && on) {
 #pragma unroll

@@ -301,10 +301,7 @@ hipError_t run_bwd(const ShortConvArgs& a, hipStream_t s) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const long stride = (long)(K + 1) * a.D;
-  const hipError_t e = launch_column_sums(a.part, parts, stride, K * a.D, K, a.dw, s);
-  if (e != hipSuccess || !a.db) return e;
-  return launch_column_sums(a.part + (long)K * a.D, parts, stride, a.D, 0, a.db, s);
+  return launch_column_sums(a.part, parts, a.D, K, a.dw, a.db, s);
 }
 
 // Channels a lane: 16 bytes of them where every row starts at a multiple of 16
