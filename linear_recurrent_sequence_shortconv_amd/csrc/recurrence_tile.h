@@ -126,8 +126,14 @@ __device__ inline Strip strip_of(const RecurrenceArgs& a, int row) {
   return s;
 }
 
-// Walks a tensor's rows of a strip; rows past its end are its last.  PLAIN: all
-// rows are one sequence's, one step apart.
+// All rows are one sequence's, which may start with the first and end with the last.
+template <int R>
+__device__ inline bool plain_strip(const Strip& s) {
+  return s.in == (1u << R) - 1 && !(s.first >> 1) && !(s.last & ((1u << (R - 1)) - 1));
+}
+
+// Walks a tensor's rows of a strip; rows past its end are its last.  PLAIN: a plain
+// strip, whose rows are one step apart, with channels for all lanes.
 template <typename E, bool PLAIN>
 struct RowWalk {
   const E* p;
@@ -161,9 +167,17 @@ struct RowWalk {
   }
 };
 
+// A lane's values of a row: the row's address is the wave's, the offset of 32 bits
+// the lane's, which one instruction adds by itself.
 template <typename E, int V>
 __device__ inline typename VecIo<E, V>::raw load_raw(const E* p, int c) {
-  return *reinterpret_cast<const typename VecIo<E, V>::raw*>(p + c);
+  return *reinterpret_cast<const typename VecIo<E, V>::raw*>(reinterpret_cast<const char*>(p) +
+                                                             (unsigned)c * (unsigned)sizeof(E));
+}
+template <typename E, int V>
+__device__ inline void store_values(const E* p, int c, const float (&x)[V]) {
+  *reinterpret_cast<typename VecIo<E, V>::raw*>(const_cast<char*>(reinterpret_cast<const char*>(p)) +
+                                                (unsigned)c * (unsigned)sizeof(E)) = VecIo<E, V>::pack(x);
 }
 
 __device__ inline int batch_of(const RecurrenceArgs& a, int row) {
@@ -229,13 +243,25 @@ __device__ inline int take_tile(const TileArgs& g) {
   return __builtin_amdgcn_readfirstlane(taken);
 }
 
+// A lane's values of a state [B, D] (nullptr: zeros).
+template <int V>
+__device__ inline void load_state(const float* p, int b, int D, int c, float (&h)[V]) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) h[v] = p ? p[(long)b * D + c + v] : 0.f;
+}
+template <int V>
+__device__ inline void store_state(float* p, int b, int D, int c, const float (&h)[V]) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) p[(long)b * D + c + v] = h[v];
+}
+
 // A strip's part of a pass: its values in registers, the sweep for (A, U), and the
 // sweep from the state that enters it.
 template <typename E, int V, int G, bool INP, int R>
 struct ForwardStrip {
   typedef VecIo<E, V> IO;
   typedef typename IO::raw raw;
-  float lam[V], av[R][V], uv[R][V];
+  float lam[V], av[R][V], uv[R][V], start[V];   // start: the state before a sequence that starts with the strip
 
   template <bool PLAIN>
   __device__ inline void first_sweep(const RecurrenceArgs& a, const TileArgs& g, const Strip& s, int c, bool on,
@@ -243,6 +269,14 @@ struct ForwardStrip {
     raw rx[R], rf[R], ri[R];
     RowWalk<E, PLAIN> px(a.x, a.sx, a, g, s.row), pf(a.f, a.sf, a, g, s.row),
         pi(INP ? a.i : a.x, INP ? a.si : a.sx, a, g, s.row);
+    if (PLAIN && (s.first & 1)) {
+      load_state<V>(g.first, batch_of(a, s.row), a.D, c, start);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        A[v] = 0.f;
+        U[v] = start[v];
+      }
+    }
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       rx[k] = load_raw<E, V>(px.p, c);
@@ -282,13 +316,17 @@ struct ForwardStrip {
   __device__ inline void second_sweep(const RecurrenceArgs& a, const TileArgs& g, const Strip& s, int c, bool on,
                                       float (&h)[V]) const {
     RowWalk<E, PLAIN> ph(a.h, a.sh, a, g, s.row);
+    if (PLAIN && (s.first & 1)) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) h[v] = start[v];
+    }
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       if (PLAIN || (s.in >> k & 1)) {
         const bool first = !PLAIN && (s.first >> k & 1);
 #pragma unroll
         for (int v = 0; v < V; ++v) h[v] = first ? uv[k][v] : fmaf(av[k][v], h[v], uv[k][v]);
-        if (on) *reinterpret_cast<raw*>(const_cast<E*>(ph.p) + c) = IO::pack(h);
+        if (PLAIN || on) store_values<E, V>(ph.p, c, h);
         if (!PLAIN && a.hT && (s.last >> k & 1)) {
           const long at = (long)batch_of(a, s.row + k) * a.D + c;
 #pragma unroll
@@ -298,6 +336,7 @@ struct ForwardStrip {
       }
       ph.next(s, k);
     }
+    if (PLAIN && a.hT && (s.last >> (R - 1) & 1)) store_state<V>(a.hT, batch_of(a, s.row), a.D, c, h);
   }
 };
 
@@ -309,7 +348,7 @@ __global__ __launch_bounds__(W * WAVE, 4) void recurrence_tile_kernel(const Recu
   const bool on = c < a.D;
   if (!on) c = 0;
   const Strip s = strip_of<R>(a, tile * (R * W) + wave * R);
-  const bool plain = s.in == (1u << R) - 1 && !(s.first | s.last);
+  const bool plain = plain_strip<R>(s) && (slice + 1) * WAVE * V <= a.D;
   ForwardStrip<E, V, G, INP, R> strip;
   float A[V], U[V], h[V];
 #pragma unroll
@@ -341,7 +380,7 @@ struct BackwardStrip {
   typedef typename IO::raw raw;
   raw rx[R], ri[R], rb[R], rg[R];
   GateValue gv[R][V];
-  float lam[V], dlam[V];
+  float lam[V], dlam[V], h0[V], end[V];   // states before and behind the strip, where a sequence starts, ends
 
   template <bool PLAIN>
   __device__ inline void first_sweep(const RecurrenceArgs& a, const TileArgs& g, const Strip& s, int c, bool on,
@@ -349,7 +388,15 @@ struct BackwardStrip {
     raw rf[R];
     RowWalk<E, PLAIN> px(a.x, a.sx, a, g, s.row), pf(a.f, a.sf, a, g, s.row),
         pi(INP ? a.i : a.x, INP ? a.si : a.sx, a, g, s.row), pb(a.h, a.sh, a, g, s.row), pg(a.dh, a.sdh, a, g, s.row);
-    if (PLAIN) pb.p -= pb.step;
+    if (PLAIN && (s.last >> (R - 1) & 1)) {
+      load_state<V>(g.first, batch_of(a, s.row), a.D, c, end);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        A[v] = 0.f;
+        U[v] = end[v];
+      }
+    }
+    if (PLAIN && (s.first & 1)) load_state<V>(a.h0, batch_of(a, s.row), a.D, c, h0);
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       rf[k] = load_raw<E, V>(pf.p, c);
@@ -360,7 +407,7 @@ struct BackwardStrip {
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       // (a row that starts a sequence, or is of none, has no row before it)
-      const bool inner = !PLAIN && (s.in >> k & 1) && !(s.first >> k & 1);
+      const bool inner = PLAIN ? k > 0 || !(s.first & 1) : (s.in >> k & 1) && !(s.first >> k & 1);
       rx[k] = load_raw<E, V>(px.p, c);
       if (INP) ri[k] = load_raw<E, V>(pi.p, c);
       rb[k] = load_raw<E, V>(pb.p - (inner ? pb.step : 0), c);
@@ -397,9 +444,13 @@ struct BackwardStrip {
   template <bool PLAIN>
   __device__ inline void second_sweep(const RecurrenceArgs& a, const TileArgs& g, const Strip& s, int c, bool on,
                                       float (&carry)[V]) {
-    const int end = s.row + max(s.n - 1, 0);
-    RowWalk<E, PLAIN> px(a.dx, a.sdx, a, g, end), pf(a.df, a.sdf, a, g, end),
-        pi(INP ? a.di : a.dx, INP ? a.sdi : a.sdx, a, g, end);
+    const int row = s.row + max(s.n - 1, 0);
+    RowWalk<E, PLAIN> px(a.dx, a.sdx, a, g, row), pf(a.df, a.sdf, a, g, row),
+        pi(INP ? a.di : a.dx, INP ? a.sdi : a.sdx, a, g, row);
+    if (PLAIN && (s.last >> (R - 1) & 1)) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) carry[v] = end[v];
+    }
 #pragma unroll
     for (int k = R - 1; k >= 0; --k) {
       if (!PLAIN && (s.last >> k & 1)) {
@@ -418,6 +469,7 @@ struct BackwardStrip {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           if (first) b[v] = a.h0 && on ? a.h0[at + v] : 0.f;
+          if (PLAIN && k == 0 && (s.first & 1)) b[v] = h0[v];
           const float gt = d[v] + carry[v];
           carry[v] = gv[k][v].a * gt;
           float dl;
@@ -425,16 +477,17 @@ struct BackwardStrip {
           if (G == GATE_POWER) dlam[v] += dl;
           if (first && a.dh0 && on) a.dh0[at + v] = carry[v];
         }
-        if (on) {
-          *reinterpret_cast<raw*>(const_cast<E*>(px.p) + c) = IO::pack(dx);
-          *reinterpret_cast<raw*>(const_cast<E*>(pf.p) + c) = IO::pack(df);
-          if (INP) *reinterpret_cast<raw*>(const_cast<E*>(pi.p) + c) = IO::pack(di);
+        if (PLAIN || on) {
+          store_values<E, V>(px.p, c, dx);
+          store_values<E, V>(pf.p, c, df);
+          if (INP) store_values<E, V>(pi.p, c, di);
         }
       }
       px.back(s, k);
       pf.back(s, k);
       if (INP) pi.back(s, k);
     }
+    if (PLAIN && a.dh0 && (s.first & 1)) store_state<V>(a.dh0, batch_of(a, s.row), a.D, c, carry);
   }
 };
 
@@ -446,7 +499,7 @@ __global__ __launch_bounds__(W * WAVE, 4) void recurrence_tile_bwd_kernel(const 
   const bool on = c < a.D;
   if (!on) c = 0;
   const Strip s = strip_of<R>(a, tile * (R * W) + wave * R);
-  const bool plain = s.in == (1u << R) - 1 && !(s.first | s.last);
+  const bool plain = plain_strip<R>(s) && (slice + 1) * WAVE * V <= a.D;
   BackwardStrip<E, V, G, INP, R> strip;
   float A[V], U[V], carry[V];
 #pragma unroll

@@ -48,10 +48,9 @@ template <> struct VecIo<bf16, 2> {
     x[1] = __uint_as_float(w & 0xffff0000u);
   }
   __device__ static inline raw pack(const float (&x)[2]) {
-    const bf16 b[2] = {(bf16)x[0], (bf16)x[1]};
-    raw w;
-    __builtin_memcpy(&w, b, 4);
-    return w;
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    typedef bf16 b2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(raw, __builtin_convertvector((f2){x[0], x[1]}, b2));
   }
 };
 template <> struct VecIo<bf16, 1> {
