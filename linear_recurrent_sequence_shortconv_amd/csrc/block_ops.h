@@ -88,7 +88,7 @@ hipError_t launch_column_sums(const float* part, int parts, int C, int K, float*
 struct Sequence {
   int b, start, end;
 };
-// Called by whole waves with one row each.
+// Called by whole waves with one row each; 256 offsets in one trip to memory.
 __device__ inline Sequence find_sequence(const int* cu, int B, int T, int rows, int row) {
   Sequence q;
   if (!cu) {
@@ -98,26 +98,37 @@ __device__ inline Sequence find_sequence(const int* cu, int B, int T, int rows, 
     return q;
   }
   const int lane = threadIdx.x & 63;
-  int before = 0;   // largest offset not behind the row
-  for (int j0 = 0; j0 <= B; j0 += 64) {
-    const int j = j0 + lane;
-    const int c = j <= B ? min(max(cu[j], 0), rows) : 0;
-    const unsigned long long behind = __ballot(c > row);
-    const int first = behind ? __builtin_ctzll(behind) : 64;
-    int m = lane < first ? c : 0;
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) m = max(m, __shfl_xor(m, o));
-    before = max(before, m);
-    if (behind) {
-      q.b = __builtin_amdgcn_readfirstlane(j0 + first - 1);
-      q.start = __builtin_amdgcn_readfirstlane(before);
-      q.end = __builtin_amdgcn_readlane(c, first);
-      return q;
-    }
-  }
+  int before = 0;   // largest offset not behind the row, of the lane's
   q.b = B;
-  q.start = __builtin_amdgcn_readfirstlane(before);
   q.end = rows;
+  for (int j0 = 0; j0 <= B; j0 += 256) {
+    int c[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int j = j0 + 64 * u + lane;
+      c[u] = j <= B ? min(max(cu[j], 0), rows) : 0;
+    }
+    bool found = false;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const unsigned long long behind = __ballot(c[u] > row);
+      if (!found && behind) {
+        const int first = __builtin_ctzll(behind);
+        q.b = j0 + 64 * u + first - 1;
+        q.end = __builtin_amdgcn_readlane(c[u], first);
+        if (lane < first) before = max(before, c[u]);
+        found = true;
+      } else if (!found) {
+        before = max(before, c[u]);
+      }
+    }
+    if (found) break;
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) before = max(before, __shfl_xor(before, o));
+  q.b = __builtin_amdgcn_readfirstlane(q.b);
+  q.start = __builtin_amdgcn_readfirstlane(before);
+  q.end = __builtin_amdgcn_readfirstlane(q.end);
   return q;
 }
 #endif

@@ -93,10 +93,12 @@ __device__ inline void look_back(const unsigned long long* words, long stride, i
 constexpr int REC_R = 16, REC_W = 8, REC_BWD_R = 8, REC_BWD_W = 8;
 
 // Which rows of a strip start and end a sequence and which belong to one, as
-// bits; place (batch, token) of the first row.
+// bits, and the sequence of row k in lane k.
 struct Strip {
   int row, n;
   unsigned first, last, in;
+  int b;
+  __device__ inline int batch(int k) const { return __builtin_amdgcn_readlane(b, k); }
 };
 template <int R>
 __device__ inline Strip strip_of(const RecurrenceArgs& a, int row) {
@@ -104,9 +106,13 @@ __device__ inline Strip strip_of(const RecurrenceArgs& a, int row) {
   s.row = min(row, a.rows - 1);
   s.n = min(max(a.rows - row, 0), R);
   s.first = s.last = s.in = 0;
+  s.b = 0;
   if (s.n == 0) return s;
+  const int lane = threadIdx.x & (WAVE - 1);
   if (!a.cu) {
-    const int t = row % a.T;
+    const int b = row / a.T, t = row - b * a.T;
+    s.b = b;
+    for (int k = t ? a.T - t : a.T; k < s.n; k += a.T) s.b += lane >= k;
     for (int k = t ? a.T - t : 0; k < s.n; k += a.T) s.first |= 1u << k;
     for (int k = a.T - 1 - t; k < s.n; k += a.T) s.last |= 1u << k;
     s.in = (1u << s.n) - 1;
@@ -119,6 +125,7 @@ __device__ inline Strip strip_of(const RecurrenceArgs& a, int row) {
         s.in |= ((1u << (stop - at)) - 1) << (at - row);
         if (q.start == at) s.first |= 1u << (at - row);
         if (q.end == stop) s.last |= 1u << (stop - 1 - row);
+        if (lane >= at - row) s.b = q.b;
       }
       at = stop;
     }
@@ -132,9 +139,9 @@ __device__ inline bool plain_strip(const Strip& s) {
   return s.in == (1u << R) - 1 && !(s.first >> 1) && !(s.last & ((1u << (R - 1)) - 1));
 }
 
-// Walks a tensor's rows of a strip; rows past its end are its last.  PLAIN: a plain
-// strip, whose rows are one step apart, with channels for all lanes.
-template <typename E, bool PLAIN>
+// Walks a tensor's rows of a strip; rows past its end are its last.  EVEN: a full
+// strip whose rows are one step apart (a plain one).
+template <typename E, bool EVEN>
 struct RowWalk {
   const E* p;
   long step, jump;
@@ -150,7 +157,7 @@ struct RowWalk {
     }
   }
   __device__ inline void next(const Strip& s, int k) {   // from row k to k + 1
-    if (PLAIN) {
+    if (EVEN) {
       p += step;
     } else if (k + 1 < s.n) {
       p += step;
@@ -158,7 +165,7 @@ struct RowWalk {
     }
   }
   __device__ inline void back(const Strip& s, int k) {   // from row k to k - 1
-    if (PLAIN) {
+    if (EVEN) {
       p -= step;
     } else if (k > 0 && k < s.n) {
       p -= step;
@@ -178,10 +185,6 @@ template <typename E, int V>
 __device__ inline void store_values(const E* p, int c, const float (&x)[V]) {
   *reinterpret_cast<typename VecIo<E, V>::raw*>(const_cast<char*>(reinterpret_cast<const char*>(p)) +
                                                 (unsigned)c * (unsigned)sizeof(E)) = VecIo<E, V>::pack(x);
-}
-
-__device__ inline int batch_of(const RecurrenceArgs& a, int row) {
-  return a.cu ? find_sequence(a.cu, a.B, a.T, a.rows, row).b : row / a.T;
 }
 
 // Values that enter each strip, from the strips' (A, U) in LDS and, where the
@@ -256,27 +259,22 @@ __device__ inline void store_state(float* p, int b, int D, int c, const float (&
 }
 
 // A strip's part of a pass: its values in registers, the sweep for (A, U), and the
-// sweep from the state that enters it.
+// sweep from the state that enters it.  PLAIN: a plain strip with channels for all
+// lanes.
 template <typename E, int V, int G, bool INP, int R>
 struct ForwardStrip {
+  typedef typename VecIo<E, V>::raw raw;
   typedef VecIo<E, V> IO;
-  typedef typename IO::raw raw;
-  float lam[V], av[R][V], uv[R][V], start[V];   // start: the state before a sequence that starts with the strip
+  float lam[V], av[R][V], uv[R][V], start[V];   // start: before the first sequence that starts here
 
   template <bool PLAIN>
-  __device__ inline void first_sweep(const RecurrenceArgs& a, const TileArgs& g, const Strip& s, int c, bool on,
-                                     float (&A)[V], float (&U)[V]) {
+  __device__ inline void first_sweep(const RecurrenceArgs& a, const TileArgs& g, const Strip& s, int c, float (&A)[V],
+                                     float (&U)[V]) {
     raw rx[R], rf[R], ri[R];
+    const int f0 = s.first ? __builtin_ctz(s.first) : 0;
+    if (s.first) load_state<V>(g.first, s.batch(f0), a.D, c, start);
     RowWalk<E, PLAIN> px(a.x, a.sx, a, g, s.row), pf(a.f, a.sf, a, g, s.row),
         pi(INP ? a.i : a.x, INP ? a.si : a.sx, a, g, s.row);
-    if (PLAIN && (s.first & 1)) {
-      load_state<V>(g.first, batch_of(a, s.row), a.D, c, start);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        A[v] = 0.f;
-        U[v] = start[v];
-      }
-    }
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       rx[k] = load_raw<E, V>(px.p, c);
@@ -285,6 +283,13 @@ struct ForwardStrip {
       px.next(s, k);
       pf.next(s, k);
       if (INP) pi.next(s, k);
+    }
+    if (PLAIN && s.first) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        A[v] = 0.f;
+        U[v] = start[v];
+      }
     }
 #pragma unroll
     for (int k = 0; k < R; ++k) {
@@ -295,10 +300,16 @@ struct ForwardStrip {
 #pragma unroll
       for (int v = 0; v < V; ++v) gate_inputs<E, G, INP>(x[v], f[v], INP ? i[v] : 0.f, lam[v], av[k][v], uv[k][v]);
       if (!PLAIN && (s.first >> k & 1)) {
-        const long at = (long)batch_of(a, s.row + k) * a.D + c;
+        float h0[V];
+        if (k == f0) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) h0[v] = start[v];
+        } else {
+          load_state<V>(g.first, s.batch(k), a.D, c, h0);
+        }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          uv[k][v] = fmaf(av[k][v], g.first && on ? g.first[at + v] : 0.f, uv[k][v]);
+          uv[k][v] = fmaf(av[k][v], h0[v], uv[k][v]);
           A[v] = 0.f;
           U[v] = uv[k][v];
         }
@@ -316,7 +327,7 @@ struct ForwardStrip {
   __device__ inline void second_sweep(const RecurrenceArgs& a, const TileArgs& g, const Strip& s, int c, bool on,
                                       float (&h)[V]) const {
     RowWalk<E, PLAIN> ph(a.h, a.sh, a, g, s.row);
-    if (PLAIN && (s.first & 1)) {
+    if (PLAIN && s.first) {
 #pragma unroll
       for (int v = 0; v < V; ++v) h[v] = start[v];
     }
@@ -327,16 +338,11 @@ struct ForwardStrip {
 #pragma unroll
         for (int v = 0; v < V; ++v) h[v] = first ? uv[k][v] : fmaf(av[k][v], h[v], uv[k][v]);
         if (PLAIN || on) store_values<E, V>(ph.p, c, h);
-        if (!PLAIN && a.hT && (s.last >> k & 1)) {
-          const long at = (long)batch_of(a, s.row + k) * a.D + c;
-#pragma unroll
-          for (int v = 0; v < V; ++v)
-            if (on) a.hT[at + v] = h[v];
-        }
+        if (a.hT && (PLAIN ? k == R - 1 && s.last : (s.last >> k & 1)) && (PLAIN || on))
+          store_state<V>(a.hT, s.batch(k), a.D, c, h);
       }
       ph.next(s, k);
     }
-    if (PLAIN && a.hT && (s.last >> (R - 1) & 1)) store_state<V>(a.hT, batch_of(a, s.row), a.D, c, h);
   }
 };
 
@@ -347,20 +353,21 @@ __global__ __launch_bounds__(W * WAVE, 4) void recurrence_tile_kernel(const Recu
   int c = (slice * WAVE + lane) * V;
   const bool on = c < a.D;
   if (!on) c = 0;
+  ForwardStrip<E, V, G, INP, R> strip;
+#pragma unroll
+  for (int v = 0; v < V; ++v) strip.lam[v] = G == GATE_POWER ? a.lam[c + v] : 0.f;   // (loads return in order)
   const Strip s = strip_of<R>(a, tile * (R * W) + wave * R);
   const bool plain = plain_strip<R>(s) && (slice + 1) * WAVE * V <= a.D;
-  ForwardStrip<E, V, G, INP, R> strip;
   float A[V], U[V], h[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    strip.lam[v] = G == GATE_POWER && on ? a.lam[c + v] : 0.f;
     A[v] = 1.f;
     U[v] = 0.f;
   }
   if (plain)
-    strip.template first_sweep<true>(a, g, s, c, on, A, U);
+    strip.template first_sweep<true>(a, g, s, c, A, U);
   else
-    strip.template first_sweep<false>(a, g, s, c, on, A, U);
+    strip.template first_sweep<false>(a, g, s, c, A, U);
   // (the tile goes on from the one before it unless a sequence starts with it; the
   // first strip knows)
   bool open = false;
@@ -376,44 +383,47 @@ __global__ __launch_bounds__(W * WAVE, 4) void recurrence_tile_kernel(const Recu
 // h0 at a sequence's first token.
 template <typename E, int V, int G, bool INP, int R>
 struct BackwardStrip {
+  typedef typename VecIo<E, V>::raw raw;
   typedef VecIo<E, V> IO;
-  typedef typename IO::raw raw;
   raw rx[R], ri[R], rb[R], rg[R];
   GateValue gv[R][V];
-  float lam[V], dlam[V], h0[V], end[V];   // states before and behind the strip, where a sequence starts, ends
+  float lam[V], dlam[V], h0[V], end[V];   // of the last sequence that starts here, of the last that ends
 
   template <bool PLAIN>
-  __device__ inline void first_sweep(const RecurrenceArgs& a, const TileArgs& g, const Strip& s, int c, bool on,
-                                     float (&A)[V], float (&U)[V]) {
+  __device__ inline void first_sweep(const RecurrenceArgs& a, const TileArgs& g, const Strip& s, int c, float (&A)[V],
+                                     float (&U)[V]) {
     raw rf[R];
-    RowWalk<E, PLAIN> px(a.x, a.sx, a, g, s.row), pf(a.f, a.sf, a, g, s.row),
-        pi(INP ? a.i : a.x, INP ? a.si : a.sx, a, g, s.row), pb(a.h, a.sh, a, g, s.row), pg(a.dh, a.sdh, a, g, s.row);
-    if (PLAIN && (s.last >> (R - 1) & 1)) {
-      load_state<V>(g.first, batch_of(a, s.row), a.D, c, end);
+    const int l1 = s.last ? 31 - __builtin_clz(s.last) : 0, f1 = s.first ? 31 - __builtin_clz(s.first) : 0;
+    if (s.last) load_state<V>(g.first, s.batch(l1), a.D, c, end);
+    if (s.first) load_state<V>(a.h0, s.batch(f1), a.D, c, h0);
+    const int row = s.row + max(s.n - 1, 0);
+    RowWalk<E, PLAIN> pf(a.f, a.sf, a, g, row), pg(a.dh, a.sdh, a, g, row);
+#pragma unroll
+    for (int k = R - 1; k >= 0; --k) {
+      rf[k] = load_raw<E, V>(pf.p, c);
+      rg[k] = load_raw<E, V>(pg.p, c);
+      pf.back(s, k);
+      pg.back(s, k);
+    }
+    RowWalk<E, PLAIN> px(a.x, a.sx, a, g, row), pi(INP ? a.i : a.x, INP ? a.si : a.sx, a, g, row),
+        pb(a.h, a.sh, a, g, row);
+#pragma unroll
+    for (int k = R - 1; k >= 0; --k) {
+      rx[k] = load_raw<E, V>(px.p, c);
+      if (INP) ri[k] = load_raw<E, V>(pi.p, c);
+      // (a row that starts a sequence, or is of none, has no row before it)
+      const bool inner = PLAIN ? k > 0 || !s.first : (s.in >> k & 1) && !(s.first >> k & 1);
+      rb[k] = load_raw<E, V>(pb.p - (inner ? pb.step : 0), c);
+      px.back(s, k);
+      if (INP) pi.back(s, k);
+      pb.back(s, k);
+    }
+    if (PLAIN && s.last) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         A[v] = 0.f;
         U[v] = end[v];
       }
-    }
-    if (PLAIN && (s.first & 1)) load_state<V>(a.h0, batch_of(a, s.row), a.D, c, h0);
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-      rf[k] = load_raw<E, V>(pf.p, c);
-      rg[k] = load_raw<E, V>(pg.p, c);
-      pf.next(s, k);
-      pg.next(s, k);
-    }
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-      // (a row that starts a sequence, or is of none, has no row before it)
-      const bool inner = PLAIN ? k > 0 || !(s.first & 1) : (s.in >> k & 1) && !(s.first >> k & 1);
-      rx[k] = load_raw<E, V>(px.p, c);
-      if (INP) ri[k] = load_raw<E, V>(pi.p, c);
-      rb[k] = load_raw<E, V>(pb.p - (inner ? pb.step : 0), c);
-      px.next(s, k);
-      if (INP) pi.next(s, k);
-      pb.next(s, k);
     }
 #pragma unroll
     for (int k = R - 1; k >= 0; --k) {
@@ -422,12 +432,14 @@ struct BackwardStrip {
 #pragma unroll
       for (int v = 0; v < V; ++v) gv[k][v] = gate_value<E, G>(f[v], lam[v]);
       if (!PLAIN && (s.last >> k & 1)) {
-        const long at = (long)batch_of(a, s.row + k) * a.D + c;
+        if (k == l1) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          A[v] = 0.f;
-          U[v] = g.first && on ? g.first[at + v] : 0.f;
+          for (int v = 0; v < V; ++v) U[v] = end[v];
+        } else {
+          load_state<V>(g.first, s.batch(k), a.D, c, U);
         }
+#pragma unroll
+        for (int v = 0; v < V; ++v) A[v] = 0.f;
       }
       if (PLAIN || (s.in >> k & 1)) {
         float d[V];
@@ -447,16 +459,20 @@ struct BackwardStrip {
     const int row = s.row + max(s.n - 1, 0);
     RowWalk<E, PLAIN> px(a.dx, a.sdx, a, g, row), pf(a.df, a.sdf, a, g, row),
         pi(INP ? a.di : a.dx, INP ? a.sdi : a.sdx, a, g, row);
-    if (PLAIN && (s.last >> (R - 1) & 1)) {
+    const int l1 = s.last ? 31 - __builtin_clz(s.last) : 0, f1 = s.first ? 31 - __builtin_clz(s.first) : 0;
+    if (PLAIN && s.last) {
 #pragma unroll
       for (int v = 0; v < V; ++v) carry[v] = end[v];
     }
 #pragma unroll
     for (int k = R - 1; k >= 0; --k) {
       if (!PLAIN && (s.last >> k & 1)) {
-        const long at = (long)batch_of(a, s.row + k) * a.D + c;
+        if (k == l1) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) carry[v] = g.first && on ? g.first[at + v] : 0.f;
+          for (int v = 0; v < V; ++v) carry[v] = end[v];
+        } else {
+          load_state<V>(g.first, s.batch(k), a.D, c, carry);
+        }
       }
       if (PLAIN || (s.in >> k & 1)) {
         float x[V], i[V], b[V], d[V], dx[V], df[V], di[V];
@@ -464,30 +480,34 @@ struct BackwardStrip {
         if (INP) IO::unpack(ri[k], i);
         IO::unpack(rb[k], b);
         IO::unpack(rg[k], d);
-        const bool first = !PLAIN && (s.first >> k & 1);
-        const long at = first ? (long)batch_of(a, s.row + k) * a.D + c : 0;
+        const bool first = PLAIN ? k == 0 && s.first : (s.first >> k & 1);
+        if (first) {
+          if (PLAIN || k == f1) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) b[v] = h0[v];
+          } else {
+            load_state<V>(a.h0, s.batch(k), a.D, c, b);
+          }
+        }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          if (first) b[v] = a.h0 && on ? a.h0[at + v] : 0.f;
-          if (PLAIN && k == 0 && (s.first & 1)) b[v] = h0[v];
           const float gt = d[v] + carry[v];
           carry[v] = gv[k][v].a * gt;
           float dl;
           gate_gradients<E, G, INP>(gv[k][v], x[v], INP ? i[v] : 0.f, lam[v], b[v], gt, carry[v], dx[v], df[v], di[v], dl);
           if (G == GATE_POWER) dlam[v] += dl;
-          if (first && a.dh0 && on) a.dh0[at + v] = carry[v];
         }
         if (PLAIN || on) {
           store_values<E, V>(px.p, c, dx);
           store_values<E, V>(pf.p, c, df);
           if (INP) store_values<E, V>(pi.p, c, di);
+          if (first && a.dh0) store_state<V>(a.dh0, s.batch(k), a.D, c, carry);
         }
       }
       px.back(s, k);
       pf.back(s, k);
       if (INP) pi.back(s, k);
     }
-    if (PLAIN && a.dh0 && (s.first & 1)) store_state<V>(a.dh0, batch_of(a, s.row), a.D, c, carry);
   }
 };
 
@@ -498,20 +518,21 @@ __global__ __launch_bounds__(W * WAVE, 4) void recurrence_tile_bwd_kernel(const 
   int c = (slice * WAVE + lane) * V;
   const bool on = c < a.D;
   if (!on) c = 0;
+  BackwardStrip<E, V, G, INP, R> strip;
+#pragma unroll
+  for (int v = 0; v < V; ++v) strip.lam[v] = G == GATE_POWER ? a.lam[c + v] : 0.f;   // (loads return in order)
   const Strip s = strip_of<R>(a, tile * (R * W) + wave * R);
   const bool plain = plain_strip<R>(s) && (slice + 1) * WAVE * V <= a.D;
-  BackwardStrip<E, V, G, INP, R> strip;
   float A[V], U[V], carry[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    strip.lam[v] = G == GATE_POWER && on ? a.lam[c + v] : 0.f;
     A[v] = 1.f;
     U[v] = strip.dlam[v] = 0.f;
   }
   if (plain)
-    strip.template first_sweep<true>(a, g, s, c, on, A, U);
+    strip.template first_sweep<true>(a, g, s, c, A, U);
   else
-    strip.template first_sweep<false>(a, g, s, c, on, A, U);
+    strip.template first_sweep<false>(a, g, s, c, A, U);
   // (the tile goes on from the one behind it unless a sequence ends with it; only
   // the last tile of a batch, the first in turn, is not full)
   bool open = false;
