@@ -71,11 +71,7 @@ hipError_t launch_recurrence(const RecurrenceArgs& a, bool f32, bool bwd, void* 
 hipError_t launch_recurrence_step(const RecurrenceArgs& a, bool f32, hipStream_t s);
 size_t recurrence_bytes(const RecurrenceArgs& a, bool packed, bool bwd);   // of the workspace
 
-// ---------------------------------------------------------------- sequences
-// dst[b] = src[b] (nullptr: zeros), n 4- or 2-byte values each, for every
-// sequence without tokens, which no row of the passes belongs to.
-hipError_t launch_empty_sequences(const int* cu, int B, int rows, int T, void* dst, const void* src, int n, int size,
-                                  hipStream_t s);
+// ------------------------------------------------- partials and sequences
 // Sums over partials [K + 1][C] in a fixed order: rows j < K go to out[c * K + j],
 // the last to last[c] (each nullptr: not wanted).
 hipError_t launch_column_sums(const float* part, int parts, int C, int K, float* out, float* last, hipStream_t s);
@@ -130,6 +126,20 @@ __device__ inline Sequence find_sequence(const int* cu, int B, int T, int rows, 
   q.start = __builtin_amdgcn_readfirstlane(before);
   q.end = __builtin_amdgcn_readfirstlane(q.end);
   return q;
+}
+
+// Whether sequence b has no tokens, which no row of a pass belongs to; by all 256
+// threads of a workgroup, sm: four ints of LDS.
+__device__ inline bool empty_sequence(const int* cu, int T, int rows, int b, int* sm) {
+  if (!cu) return T == 0;
+  int m = 0;
+  for (int j = threadIdx.x; j <= b; j += 256) m = max(m, min(cu[j], rows));
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = max(m, __shfl_xor(m, o));
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = m;
+  __syncthreads();
+  return min(cu[b + 1], rows) <= max(max(sm[0], sm[1]), max(sm[2], sm[3]));
 }
 #endif
 

@@ -1,5 +1,4 @@
-// What the operators of a recurrent block share: column sums of partials, and
-// the results of sequences without tokens.
+// What the operators of a recurrent block share: column sums of partials.
 #include "block_ops.h"
 #include "prism_common.h"
 
@@ -31,45 +30,11 @@ __global__ __launch_bounds__(1024) void column_sums_kernel(const float* part, in
   }
 }
 
-// A workgroup a sequence: whether it is empty from the largest offset up to its
-// start and to its end.
-template <typename W>
-__global__ __launch_bounds__(256) void empty_sequences_kernel(const int* cu, int rows, int T, W* dst, const W* src,
-                                                              int n) {
-  __shared__ int sm[4];
-  const int b = blockIdx.x;
-  bool empty = T == 0;
-  if (cu) {
-    int m = 0;
-    for (int j = threadIdx.x; j <= b; j += 256) m = max(m, min(cu[j], rows));
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) m = max(m, __shfl_xor(m, o));
-    if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = m;
-    __syncthreads();
-    m = max(max(sm[0], sm[1]), max(sm[2], sm[3]));
-    empty = min(cu[b + 1], rows) <= m;
-  }
-  if (!empty) return;
-  for (int e = threadIdx.x; e < n; e += 256) dst[(long)b * n + e] = src ? src[(long)b * n + e] : W(0);
-}
-
 }  // namespace
 
 hipError_t launch_column_sums(const float* part, int parts, int C, int K, float* out, float* last, hipStream_t s) {
   hipLaunchKernelGGL(column_sums_kernel, dim3((unsigned)(((K + 1L) * C + 31) / 32)), dim3(1024), 0, s, part, parts, C, K,
                      out, last);
-  return hipGetLastError();
-}
-
-hipError_t launch_empty_sequences(const int* cu, int B, int rows, int T, void* dst, const void* src, int n, int size,
-                                  hipStream_t s) {
-  if (B == 0 || n == 0) return hipSuccess;
-  if (size == 2)
-    hipLaunchKernelGGL((empty_sequences_kernel<unsigned short>), dim3(B), dim3(256), 0, s, cu, rows, T,
-                       static_cast<unsigned short*>(dst), static_cast<const unsigned short*>(src), n);
-  else
-    hipLaunchKernelGGL((empty_sequences_kernel<unsigned>), dim3(B), dim3(256), 0, s, cu, rows, T,
-                       static_cast<unsigned*>(dst), static_cast<const unsigned*>(src), n);
   return hipGetLastError();
 }
 

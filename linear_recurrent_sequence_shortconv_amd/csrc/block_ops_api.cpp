@@ -231,12 +231,9 @@ prism_status conv_forward(const prism_short_conv_desc* desc, const void* x, cons
   a.hist = hist;
   a.y = y;
   a.hist_out = hist_out;
-  if (hist_out && hist_out != hist && (packed || d.T == 0))
-    HIP_TRY("empty_sequences", stream,
-            prism::launch_empty_sequences(cu, d.B, a.rows, d.T, hist_out, hist, (d.K - 1) * d.D, size, stream));
-  if (some)
-    HIP_TRY("short_conv", stream, d.dtype == PRISM_BF16 ? prism::launch_short_conv<prism::bf16>(a, stream)
-                                                        : prism::launch_short_conv<float>(a, stream));
+  if (d.B == 0) return PRISM_OK;
+  HIP_TRY("short_conv", stream, d.dtype == PRISM_BF16 ? prism::launch_short_conv<prism::bf16>(a, stream)
+                                                      : prism::launch_short_conv<float>(a, stream));
   return PRISM_OK;
 }
 
@@ -277,9 +274,6 @@ prism_status conv_backward(const prism_short_conv_desc* desc, const void* x, con
   a.db = db;
   a.dhist = dhist;
   a.part = static_cast<float*>(workspace);
-  if (dhist && (packed || d.T == 0))
-    HIP_TRY("empty_sequences", stream,
-            prism::launch_empty_sequences(cu, d.B, a.rows, d.T, dhist, nullptr, (d.K - 1) * d.D, 4, stream));
   HIP_TRY("short_conv_bwd", stream, d.dtype == PRISM_BF16 ? prism::launch_short_conv_bwd<prism::bf16>(a, stream)
                                                           : prism::launch_short_conv_bwd<float>(a, stream));
   return PRISM_OK;

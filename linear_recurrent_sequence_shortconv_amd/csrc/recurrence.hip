@@ -69,21 +69,9 @@ __global__ __launch_bounds__(256) void recurrence_ready_kernel(uint4* words, lon
   for (long e = at; e < ncopy; e += all) copy[e] = first[e];
   if (!last) return;
   __shared__ int sm[4];
-  for (int b = blockIdx.x; b < B; b += gridDim.x) {
-    bool empty = T == 0;
-    if (cu) {
-      int m = 0;
-      for (int j = threadIdx.x; j <= b; j += 256) m = max(m, min(cu[j], rows));
-#pragma unroll
-      for (int o = 32; o > 0; o >>= 1) m = max(m, __shfl_xor(m, o));
-      __syncthreads();
-      if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = m;
-      __syncthreads();
-      empty = min(cu[b + 1], rows) <= max(max(sm[0], sm[1]), max(sm[2], sm[3]));
-    }
-    if (empty)
+  for (int b = blockIdx.x; b < B; b += gridDim.x)
+    if (empty_sequence(cu, T, rows, b, sm))
       for (int c = threadIdx.x; c < D; c += 256) last[(long)b * D + c] = first ? first[(long)b * D + c] : 0.f;
-  }
 }
 
 template <typename E, int V, int G, bool INP>

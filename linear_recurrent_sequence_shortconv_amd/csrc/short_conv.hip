@@ -11,6 +11,8 @@
 // behind it too), which the wave next to it reads at the same time.  The rows
 // before the current one, and in the backward pass the g before it, stay in
 // registers.
+#include <type_traits>
+
 #include "block_ops.h"
 #include "vec_io.h"
 
@@ -19,6 +21,7 @@ namespace prism {
 namespace {
 
 constexpr int SC_WAVES = 4;
+constexpr int SC_STRIP = 32, SC_STRIP_BWD = 64;   // tokens
 
 // sigma, for bf16 results by the hardware's exponential and reciprocal (1 ulp
 // each; the argument's rounding adds 2^-24 of its size).
@@ -65,15 +68,16 @@ __device__ inline void load_taps(const void* w, int c, float (&t)[K][V]) {
 
 // A workgroup's waves take neighbouring strips of the same channels.
 struct Place {
-  int strip, c;
+  int blk, strip, c;
   bool on;
 };
 template <int V>
 __device__ inline Place place_of(int D, int cw) {
   Place p;
-  const int blk = blockIdx.x / cw;
-  p.strip = __builtin_amdgcn_readfirstlane(blk * SC_WAVES + threadIdx.x / WAVE);
-  p.c = ((blockIdx.x % cw) * WAVE + (threadIdx.x & (WAVE - 1))) * V;
+  const int id = blockIdx.x;
+  p.blk = id / cw;
+  p.strip = __builtin_amdgcn_readfirstlane(p.blk * SC_WAVES + threadIdx.x / WAVE);
+  p.c = ((id - p.blk * cw) * WAVE + (threadIdx.x & (WAVE - 1))) * V;
   p.on = p.c < D;
   if (!p.on) p.c = 0;
   return p;
@@ -84,13 +88,26 @@ __device__ inline const E* sequence_base(const void* p, const TokenSteps& s, con
   return static_cast<const E*>(p) + (cu ? q.start * s.t : q.b * s.b);
 }
 
+// Workgroups behind those of the strips take a sequence each: one without tokens
+// leaves its history as it was.
+template <typename W>
+__device__ inline void leave_history(const ShortConvArgs& a, int b, int n, W* dst, const W* src) {
+  __shared__ int sm[4];
+  if (!dst || !empty_sequence(a.cu, a.T, a.rows, b, sm)) return;
+  for (int e = threadIdx.x; e < n; e += SC_WAVES * WAVE) dst[(long)b * n + e] = src ? src[(long)b * n + e] : W(0.f);
+}
+
 // The first K - 1 tokens of a sequence, which read hist, belong to the strip of
 // its first token, whose wave also writes hist_out: hist may be updated in place.
-template <typename E, int V, int K>
-__global__ __launch_bounds__(SC_WAVES * WAVE) void short_conv_kernel(const ShortConvArgs a, int cw, int S) {
+template <typename E, int V, int K, bool SILU>
+__global__ __launch_bounds__(SC_WAVES * WAVE) void short_conv_kernel(const ShortConvArgs a, int cw, int S, int strips) {
   typedef VecIo<E, V> IO;
   typedef typename IO::raw raw;
-  constexpr int U = 8;
+  constexpr int U = 4;
+  if ((int)blockIdx.x >= strips) {
+    leave_history(a, blockIdx.x - strips, (K - 1) * a.D, static_cast<E*>(a.hist_out), static_cast<const E*>(a.hist));
+    return;
+  }
   const Place p = place_of<V>(a.D, cw);
   const int lo = p.strip * S, hi = min(lo + S, a.rows);
   if (lo >= a.rows) return;
@@ -132,11 +149,19 @@ __global__ __launch_bounds__(SC_WAVES * WAVE) void short_conv_kernel(const Short
           *reinterpret_cast<raw*>(static_cast<E*>(a.hist_out) + ((long)q.b * (K - 1) + m) * a.D + p.c) =
               IO::pack(last[m]);
     }
-    for (; row < stop; row += U) {
-      raw in[U];
+    raw in[U], ahead[U];
+    auto load = [&](raw(&r)[U], int row) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        in[u] = *reinterpret_cast<const raw*>(x + (long)(min(row + u, stop - 1) - q.start) * a.sx.t + p.c);
+        r[u] = *reinterpret_cast<const raw*>(x + (long)(min(row + u, stop - 1) - q.start) * a.sx.t + p.c);
+    };
+    const bool all = __all(p.on);
+    load(ahead, row);
+    auto rows = [&](int row, auto inner) {   // INNER: U rows, and channels for all lanes
+      constexpr bool INNER = decltype(inner)::value;
+#pragma unroll
+      for (int u = 0; u < U; ++u) in[u] = ahead[u];
+      if (row + U < stop) load(ahead, row + U);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         float now[V], z[V];
@@ -146,14 +171,20 @@ __global__ __launch_bounds__(SC_WAVES * WAVE) void short_conv_kernel(const Short
           z[i] = fmaf(w[0][i], now[i], bias[i]);
 #pragma unroll
           for (int j = 1; j < K; ++j) z[i] = fmaf(w[j][i], past[j - 1][i], z[i]);
-          if (a.silu) z[i] *= sigma<E>(z[i]);
+          if (SILU) z[i] *= sigma<E>(z[i]);
 #pragma unroll
           for (int j = K - 2; j > 0; --j) past[j][i] = past[j - 1][i];
           past[0][i] = now[i];
         }
-        if (row + u < stop && p.on)
+        if (INNER || (row + u < stop && p.on))
           *reinterpret_cast<raw*>(y + (long)(row + u - q.start) * a.sy.t + p.c) = IO::pack(z);
       }
+    };
+    for (; row < stop; row += U) {
+      if (all && row + U <= stop)
+        rows(row, std::true_type());
+      else
+        rows(row, std::false_type());
     }
     row = stop;
   }
@@ -162,12 +193,16 @@ __global__ __launch_bounds__(SC_WAVES * WAVE) void short_conv_kernel(const Short
 // Rows lo .. hi - 1 of dx come from g up to K - 1 rows further; the sums over
 // tokens take the g of lo .. hi - 1 alone.  The waves' sums are joined through
 // LDS one after the other, and leave as one partial [K + 1][D] a workgroup.
-template <typename E, int V, int K>
-__global__ __launch_bounds__(SC_WAVES * WAVE) void short_conv_bwd_kernel(const ShortConvArgs a, int cw, int S) {
+template <typename E, int V, int K, bool SILU>
+__global__ __launch_bounds__(SC_WAVES * WAVE, V == 4 ? 4 : 8) void short_conv_bwd_kernel(const ShortConvArgs a, int cw, int S, int strips) {
   typedef VecIo<E, V> IO;
   typedef typename IO::raw raw;
   constexpr int U = 4;
   __shared__ float sm[(K + 1) * V][WAVE];
+  if ((int)blockIdx.x >= strips) {
+    leave_history<float>(a, blockIdx.x - strips, (K - 1) * a.D, a.dhist, nullptr);
+    return;
+  }
   const Place p = place_of<V>(a.D, cw);
   const int lo = min(p.strip * S, a.rows), hi = min(lo + S, a.rows);
   float w[K][V], bias[V], dw[K + 1][V];
@@ -200,11 +235,14 @@ __global__ __launch_bounds__(SC_WAVES * WAVE) void short_conv_bwd_kernel(const S
 #pragma unroll
       for (int i = 0; i < V; ++i) gp[j][i] = 0.f;
     }
-    for (int row = at; row < stop; row += U) {
+    // U rows from `row`; INNER: all of them the strip's, behind its first K - 1, and
+    // channels for all lanes
+    auto rows = [&](int row, auto inner) {
+      constexpr bool INNER = decltype(inner)::value;
       raw in[U], gr[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const long t = min(row + u, q.end - 1) - q.start;
+        const long t = (INNER ? row + u : min(row + u, q.end - 1)) - q.start;
         in[u] = *reinterpret_cast<const raw*>(x + t * a.sx.t + p.c);
         gr[u] = *reinterpret_cast<const raw*>(dy + t * a.sy.t + p.c);
       }
@@ -216,15 +254,15 @@ __global__ __launch_bounds__(SC_WAVES * WAVE) void short_conv_bwd_kernel(const S
         IO::unpack(gr[u], g);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          if (a.silu) {
+          if (SILU) {
             float z = fmaf(w[0][i], now[i], bias[i]);
 #pragma unroll
             for (int j = 1; j < K; ++j) z = fmaf(w[j][i], past[j - 1][i], z);
             const float s = sigma<E>(z);
             g[i] *= s * fmaf(z, 1.f - s, 1.f);
           }
-          if (r >= q.end) g[i] = 0.f;
-          if (r < own) {
+          if (!INNER && r >= q.end) g[i] = 0.f;
+          if (INNER || r < own) {
             dw[0][i] = fmaf(g[i], now[i], dw[0][i]);
 #pragma unroll
             for (int j = 1; j < K; ++j) dw[j][i] = fmaf(g[i], past[j - 1][i], dw[j][i]);
@@ -243,8 +281,8 @@ __global__ __launch_bounds__(SC_WAVES * WAVE) void short_conv_bwd_kernel(const S
           gp[0][i] = g[i];
         }
         const int e = r - (K - 1);
-        if (r < stop && p.on) {
-          if (e >= at) {
+        if (INNER || (r < stop && p.on)) {
+          if (INNER || e >= at) {
             *reinterpret_cast<raw*>(dx + (long)(e - q.start) * a.sd.t + p.c) = IO::pack(out);
           } else if (at == q.start && a.dhist) {
             float* d = a.dhist + ((long)q.b * (K - 1) + (r - q.start)) * a.D + p.c;
@@ -253,7 +291,13 @@ __global__ __launch_bounds__(SC_WAVES * WAVE) void short_conv_bwd_kernel(const S
           }
         }
       }
-    }
+    };
+    int row = at;
+    rows(row, std::false_type());
+    row += U;   // (U >= K - 1)
+    if (__all(p.on))
+      for (; row + U <= own; row += U) rows(row, std::true_type());
+    for (; row < stop; row += U) rows(row, std::false_type());
     at = own;
   }
   const int wave = threadIdx.x / WAVE, lane = threadIdx.x & (WAVE - 1);
@@ -266,57 +310,68 @@ __global__ __launch_bounds__(SC_WAVES * WAVE) void short_conv_bwd_kernel(const S
       for (int i = 0; i < V; ++i) {
         float& s = sm[j * V + i][lane];
         s = k ? s + dw[j][i] : dw[j][i];
-        if (k == SC_WAVES - 1 && p.on) a.part[((long)(blockIdx.x / cw) * (K + 1) + j) * a.D + p.c + i] = s;
+        if (k == SC_WAVES - 1 && p.on) a.part[((long)p.blk * (K + 1) + j) * a.D + p.c + i] = s;
       }
   }
 }
 
-// Tokens a strip: 32, fewer (to 4) where that leaves under two waves a SIMD of
-// 4 channels a lane.
-int strip_tokens(int rows, int D) {
+// Tokens a strip, fewer (to 4) where that leaves under two waves a SIMD.  (8 x 2048
+// tokens of 2048 channels, strips of 16, 32 and 64: 31, 28 and 31 us; backward,
+// where a strip also walks K - 1 rows twice on either side, 59, 53 and 51.)
+int strip_tokens(int rows, int D, int S) {
   const long waves = (D + 255) / 256;
-  int S = 32;
   while (S > 4 && (rows + S - 1L) / S * waves < 2048) S /= 2;
   return S;
 }
 int parts_of(int rows, int S) { return (int)((rows + S * SC_WAVES - 1L) / (S * SC_WAVES)); }
+
+// Workgroups for sequences that may be empty and have a result all the same.
+int empties(const ShortConvArgs& a, const void* result) {
+  return result && result != a.hist && (a.cu || a.T == 0) ? a.B : 0;
+}
 
 // (a dense sequence of at most 8 tokens is a strip of its own, with others where
 // a launch would have 2^32 threads)
 template <typename E, int V, int K>
 hipError_t run_fwd(const ShortConvArgs& a, hipStream_t s) {
   const long cw = (a.D + WAVE * V - 1) / (WAVE * V);
-  int S = !a.cu && a.T <= 8 ? a.T : strip_tokens(a.rows, a.D);
+  int S = !a.cu && a.T <= 8 && a.T > 0 ? a.T : strip_tokens(a.rows, a.D, SC_STRIP);
   while (cw * parts_of(a.rows, S) >= (1L << 23)) S *= 2;
-  hipLaunchKernelGGL((short_conv_kernel<E, V, K>), dim3((unsigned)(cw * parts_of(a.rows, S))), dim3(SC_WAVES * WAVE), 0,
-                     s, a, (int)cw, S);
+  const int strips = (int)(cw * parts_of(a.rows, S));
+  const dim3 grid((unsigned)strips + empties(a, a.hist_out));
+  if (grid.x == 0) return hipSuccess;
+  if (a.silu)
+    hipLaunchKernelGGL((short_conv_kernel<E, V, K, true>), grid, dim3(SC_WAVES * WAVE), 0, s, a, (int)cw, S, strips);
+  else
+    hipLaunchKernelGGL((short_conv_kernel<E, V, K, false>), grid, dim3(SC_WAVES * WAVE), 0, s, a, (int)cw, S, strips);
   return hipGetLastError();
 }
 template <typename E, int V, int K>
 hipError_t run_bwd(const ShortConvArgs& a, hipStream_t s) {
-  const int cw = (a.D + WAVE * V - 1) / (WAVE * V), S = strip_tokens(a.rows, a.D), parts = parts_of(a.rows, S);
-  if (parts > 0) {
-    hipLaunchKernelGGL((short_conv_bwd_kernel<E, V, K>), dim3((unsigned)cw * parts), dim3(SC_WAVES * WAVE), 0, s, a, cw,
-                       S);
+  const int cw = (a.D + WAVE * V - 1) / (WAVE * V), S = strip_tokens(a.rows, a.D, SC_STRIP_BWD);
+  const int parts = parts_of(a.rows, S), strips = cw * parts;
+  const dim3 grid((unsigned)strips + empties(a, a.dhist));
+  if (grid.x > 0) {
+    if (a.silu)
+      hipLaunchKernelGGL((short_conv_bwd_kernel<E, V, K, true>), grid, dim3(SC_WAVES * WAVE), 0, s, a, cw, S, strips);
+    else
+      hipLaunchKernelGGL((short_conv_bwd_kernel<E, V, K, false>), grid, dim3(SC_WAVES * WAVE), 0, s, a, cw, S, strips);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return launch_column_sums(a.part, parts, a.D, K, a.dw, a.db, s);
 }
 
-// Channels a lane: 16 bytes of them where every row starts at a multiple of 16
-// bytes and a wave's 64 lanes find enough channels, else 8 bytes, else one.
+// Channels a lane: four where every row starts at a multiple of them, else one.
+// (Eight bf16 take the registers of half the waves: 8 x 2048 tokens of 2048
+// channels 32 us in place of 28, backward 61 in place of 55.)
 template <typename E, bool BWD, int K>
 hipError_t run_k(const ShortConvArgs& a, hipStream_t s) {
   uintptr_t p = (uintptr_t)a.x | (uintptr_t)a.w | (uintptr_t)a.b | (uintptr_t)a.hist | (uintptr_t)a.y |
                 (uintptr_t)a.hist_out | (uintptr_t)a.dy | (uintptr_t)a.dx;
   long m = a.D | a.sx.b | a.sx.t | a.sy.b | a.sy.t;
   if (BWD) m |= a.sd.b | a.sd.t;
-  auto fits = [&](int V) { return m % V == 0 && p % (V * sizeof(E)) == 0; };
-  if constexpr (sizeof(E) == 2) {
-    if (fits(8) && a.D >= 512) return BWD ? run_bwd<E, 8, K>(a, s) : run_fwd<E, 8, K>(a, s);
-  }
-  if (fits(4)) return BWD ? run_bwd<E, 4, K>(a, s) : run_fwd<E, 4, K>(a, s);
+  if (m % 4 == 0 && p % (4 * sizeof(E)) == 0) return BWD ? run_bwd<E, 4, K>(a, s) : run_fwd<E, 4, K>(a, s);
   return BWD ? run_bwd<E, 1, K>(a, s) : run_fwd<E, 1, K>(a, s);
 }
 template <typename E, bool BWD>
@@ -329,7 +384,7 @@ hipError_t run(const ShortConvArgs& a, hipStream_t s) {
 }  // namespace
 
 size_t short_conv_part_bytes(int rows, int D, int K) {
-  return (size_t)parts_of(rows, strip_tokens(rows, D)) * (K + 1) * D * sizeof(float);
+  return (size_t)parts_of(rows, strip_tokens(rows, D, SC_STRIP_BWD)) * (K + 1) * D * sizeof(float);
 }
 
 template <typename E>
