@@ -41,10 +41,11 @@ prism_status check_elem(const void* p, const char* name, bool required, int size
 // result, none that would put several rows in one place.
 prism_status check_steps(const prism_strides& s, const char* name, const long long (&n)[3], bool result) {
   const long long v[3] = {s.batch, s.token, s.head};
+  const bool some = n[0] && n[1] && n[2];
   for (int k = 0; k < 3; ++k) {
     if (v[k] >= (1LL << 40) || v[k] <= -(1LL << 40))
       return fail(PRISM_ERR_SHAPE, std::string("strides of ") + name + " out of range");
-    if (result && n[k] > 1 && v[k] == 0)
+    if (result && some && n[k] > 1 && v[k] == 0)
       return fail(PRISM_ERR_SHAPE, std::string("strides of ") + name + " put several rows in one place");
   }
   return PRISM_OK;

@@ -808,7 +808,7 @@ assert _GR_DESC.size == ctypes.sizeof(GatedRecurrenceDesc)
 _block_bytes = {}
 
 
-def _block_workspace(query, desc, args, device):
+def _block_workspace(query, desc, args, like):
     key = (query, desc, args)
     size = _block_bytes.get(key)
     if size is None:
@@ -817,7 +817,18 @@ def _block_workspace(query, desc, args, device):
         if len(_block_bytes) >= 4096:
             _block_bytes.clear()
         size = _block_bytes[key] = n.value
-    return _workspace(size, device)[1] if size else None
+    if size == 0:
+        return None
+    workspace = like.new_empty(size, dtype=torch.uint8)
+    # (the allocator's blocks start at multiples of 512 bytes)
+    return workspace if workspace.data_ptr() % 256 == 0 else _workspace(size, like.device)[1]
+
+
+# (by device number, without the device object)
+def _stream_of(device):
+    if _raw_stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream(device)
 
 
 def _size(workspace):
@@ -831,9 +842,11 @@ def _vector(t, name, dtype, device, shape):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _row_steps(t, name):
+def _row_steps(t, name, flat):
     """Steps of rows [D], [N,D], [B,T,D] or [B,T,H,D] as (batch, token, head),
-    dimensions of one entry 0."""
+    dimensions of one entry 0; flat: those of a contiguous tensor."""
+    if t.is_contiguous():
+        return flat
     n, s = t.shape, t.stride()
     if s[-1] != 1 and n[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
@@ -842,12 +855,27 @@ def _row_steps(t, name):
 
 
 def _norm_desc(x, norm, eps):
-    if norm not in LAYER_NORMS:
+    """The descriptor's fields up to the steps of x, and the steps of a
+    contiguous tensor of x's shape."""
+    code = LAYER_NORMS.get(norm)
+    if code is None:
         raise ValueError(f"norm must be one of {sorted(LAYER_NORMS)}, got {norm!r}")
-    if not 1 <= x.dim() <= 4:
+    n = x.dim()
+    if n == 3:
+        T, H, D = x.shape
+        B = 1
+    elif 1 <= n <= 4:
+        B, T, H, D = (1, 1, 1, 1)[n:] + tuple(x.shape)
+    else:
         raise ValueError(f"x: expected 1 to 4 dimensions, got shape {tuple(x.shape)}")
-    shape = (1, 1, 1, 1)[x.dim():] + tuple(x.shape)
-    return (*shape, _dtype_code(x), LAYER_NORMS[norm], eps, *_row_steps(x, "x"))
+    flat = (T * H * D, H * D, D)
+    return (B, T, H, D, _dtype_code(x), code, eps, *_row_steps(x, "x", flat)), flat
+
+
+def _weights(w, b, dt, dev, D):
+    for name, t in (("w", w), ("b", b)):
+        if t is not None:
+            _vector(t, name, dt, dev, (D,))
 
 
 def layer_norm(x, w=None, b=None, residual=None, norm="layer", eps=1e-5, y=None, h=None):
@@ -859,24 +887,28 @@ def layer_norm(x, w=None, b=None, residual=None, norm="layer", eps=1e-5, y=None,
     x, residual [.., D] of one to four dimensions in bf16 or fp32 (contiguous
     last dimension, views allowed), w, b [D] or None.  y, h: where the results go
     (new contiguous tensors by default; each may be x or residual: in place)."""
-    desc = _norm_desc(x, norm, eps)
+    desc, flat = _norm_desc(x, norm, eps)
     dt, dev = x.dtype, x.get_device()
-    for name, t in (("w", w), ("b", b)):
-        if t is not None:
-            _vector(t, name, dt, dev, x.shape[-1:])
-    _on_gpu(x)
+    _weights(w, b, dt, dev, desc[3])
+    if dev < 0:
+        _on_gpu(x)
     rs = hs = _NO_STEPS
     if residual is not None:
         _like(residual, "residual", dt, dev, x.shape)
-        rs = _row_steps(residual, "residual")
-        h = _out(x, h, "h")
-        hs = _row_steps(h, "h")
+        rs = _row_steps(residual, "residual", flat)
+        if h is None:
+            h, hs = x.new_empty(x.shape), flat
+        else:
+            hs = _row_steps(_out(x, h, "h"), "h", flat)
     elif h is not None:
         raise ValueError("h without residual")
-    y = _out(x, y, "y")
-    _check(lib().prism_layer_norm(
-        _LN_DESC.pack(*desc, *rs, *_row_steps(y, "y"), *hs), _addr(x), _addr(residual), _addr(w),
-        _addr(b), _addr(y), _addr(h), _stream(x.device)))
+    if y is None:
+        y, ys = x.new_empty(x.shape), flat
+    else:
+        ys = _row_steps(_out(x, y, "y"), "y", flat)
+    _check((_lib or lib()).prism_layer_norm(
+        _LN_DESC.pack(*desc, *rs, *ys, *hs), x.data_ptr(), _addr(residual), _addr(w), _addr(b),
+        y.data_ptr(), _addr(h), _stream_of(dev)))
     return y, h
 
 
@@ -887,54 +919,63 @@ def layer_norm_backward(x, dy, w=None, dh=None, norm="layer", eps=1e-5, need_db=
     Returns a dict: dx (the gradient of x and of the residual alike; into dx when
     given, which may be dy, dh or x), dw (fp32 [D]) with w, db (fp32 [D]) when
     need_db."""
-    desc = _norm_desc(x, norm, eps)
+    desc, flat = _norm_desc(x, norm, eps)
     dt, dev = x.dtype, x.get_device()
     _like(dy, "dy", dt, dev, x.shape)
     hs = _NO_STEPS
     if dh is not None:
         _like(dh, "dh", dt, dev, x.shape)
-        hs = _row_steps(dh, "dh")
-    if w is not None:
-        _vector(w, "w", dt, dev, x.shape[-1:])
-    _on_gpu(x)
+        hs = _row_steps(dh, "dh", flat)
+    _weights(w, None, dt, dev, desc[3])
+    if dev < 0:
+        _on_gpu(x)
     out = {"dx": _out(x, dx, "dx")}
     if w is not None:
         out["dw"] = x.new_empty(x.shape[-1:], dtype=torch.float32)
     if need_db:
         out["db"] = x.new_empty(x.shape[-1:], dtype=torch.float32)
-    packed = _LN_DESC.pack(*desc, *hs, *_row_steps(dy, "dy"), *_row_steps(out["dx"], "dx"))
+    packed = _LN_DESC.pack(*desc, *hs, *_row_steps(dy, "dy", flat),
+                           *_row_steps(out["dx"], "dx", flat))
     if workspace is None and len(out) > 1:
-        workspace = _block_workspace("prism_layer_norm_backward_workspace", packed, (1,), x.device)
-    _check(lib().prism_layer_norm_backward(
+        workspace = _block_workspace("prism_layer_norm_backward_workspace", packed, (1,), x)
+    _check((_lib or lib()).prism_layer_norm_backward(
         packed, _addr(x), _addr(w), _addr(dy), _addr(dh), _addr(out["dx"]), _addr(out.get("dw")),
-        _addr(out.get("db")), _addr(workspace), _size(workspace), _stream(x.device)))
+        _addr(out.get("db")), _addr(workspace), _size(workspace), _stream_of(dev)))
     return out
 
 
-def _token_steps(t, name):
-    """Steps of [B,T,D] or, packed, [N,D] as (batch, token, 0)."""
-    _, b, s = _row_steps(t, name)
+def _token_steps(t, name, flat):
+    """Steps of [B,T,D] or, packed, [N,D] as (batch, token, 0); flat: those of a
+    contiguous tensor."""
+    if t.is_contiguous():
+        return flat
+    _, b, s = _row_steps(t, name, flat)
     return b, s, 0
 
 
 def _batch(x, cu_seqlens):
-    """B, T, D, rows of a packed batch, of x [B,T,D] or [N,D] with cu_seqlens."""
+    """B, T, D, rows of a packed batch, of x [B,T,D] or [N,D] with cu_seqlens, and
+    the steps of a contiguous tensor of x's shape."""
     if cu_seqlens is None:
         if x.dim() != 3:
             raise ValueError(f"x: expected [B, T, D], got shape {tuple(x.shape)}")
-        return (*x.shape, 0)
+        B, T, D = x.shape
+        return B, T, D, 0, (T * D, D, 0)
     if (cu_seqlens.dtype != torch.int32 or cu_seqlens.device != x.device or cu_seqlens.dim() != 1
             or cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous()):
         raise ValueError("cu_seqlens must be a contiguous 1-D int32 tensor of B + 1 entries on x's device")
     if x.dim() != 2:
         raise ValueError(f"x: expected [N, D] with cu_seqlens, got shape {tuple(x.shape)}")
-    return cu_seqlens.numel() - 1, 0, x.shape[1], x.shape[0]
+    return cu_seqlens.numel() - 1, 0, x.shape[1], x.shape[0], (0, x.shape[1], 0)
 
 
 def _conv_desc(x, w, b, hist, activation, cu_seqlens):
-    if activation not in CONV_ACTIVATIONS:
+    """The descriptor's fields up to the steps of x, and the steps of a
+    contiguous tensor of x's shape."""
+    code = CONV_ACTIVATIONS.get(activation)
+    if code is None:
         raise ValueError(f"activation must be one of {sorted(CONV_ACTIVATIONS)}, got {activation!r}")
-    B, T, D, N = _batch(x, cu_seqlens)
+    B, T, D, N, flat = _batch(x, cu_seqlens)
     dt, dev = x.dtype, x.get_device()
     if w.dim() != 2:
         raise ValueError(f"w: expected [D, K], got shape {tuple(w.shape)}")
@@ -944,7 +985,7 @@ def _conv_desc(x, w, b, hist, activation, cu_seqlens):
         _vector(b, "b", dt, dev, (D,))
     if hist is not None:
         _vector(hist, "hist", dt, dev, (B, K - 1, D))
-    return (B, T, D, K, _dtype_code(x), CONV_ACTIVATIONS[activation], N, *_token_steps(x, "x"))
+    return (B, T, D, K, _dtype_code(x), code, N, *_token_steps(x, "x", flat)), flat
 
 
 def short_conv(x, w, b=None, hist=None, activation="identity", cu_seqlens=None, y=None,
@@ -958,14 +999,19 @@ def short_conv(x, w, b=None, hist=None, activation="identity", cu_seqlens=None, 
     oldest first (None: zeros); hist_out (same shape, may be hist) receives the
     last ones for the next call.  cu_seqlens (int32 [B+1]) packs sequences: x is
     [N,D].  y: where the result goes (a new tensor by default)."""
-    desc = _conv_desc(x, w, b, hist, activation, cu_seqlens)
+    desc, flat = _conv_desc(x, w, b, hist, activation, cu_seqlens)
+    dev = x.get_device()
     if hist_out is not None:
-        _vector(hist_out, "hist_out", x.dtype, x.get_device(), (desc[0], desc[3] - 1, desc[2]))
-    _on_gpu(x)
-    y = _out(x, y, "y")
-    _check(lib().prism_short_conv(
-        _SC_DESC.pack(*desc, *_token_steps(y, "y"), 0, 0, 0), _addr(x), _addr(w), _addr(b),
-        _addr(hist), _addr(cu_seqlens), _addr(y), _addr(hist_out), _stream(x.device)))
+        _vector(hist_out, "hist_out", x.dtype, dev, (desc[0], desc[3] - 1, desc[2]))
+    if dev < 0:
+        _on_gpu(x)
+    if y is None:
+        y, ys = x.new_empty(x.shape), flat
+    else:
+        ys = _token_steps(_out(x, y, "y"), "y", flat)
+    _check((_lib or lib()).prism_short_conv(
+        _SC_DESC.pack(*desc, *ys, 0, 0, 0), x.data_ptr(), w.data_ptr(), _addr(b), _addr(hist),
+        _addr(cu_seqlens), y.data_ptr(), _addr(hist_out), _stream_of(dev)))
     return y
 
 
@@ -974,9 +1020,11 @@ def short_conv_backward(x, w, dy, b=None, hist=None, activation="identity", cu_s
     """Gradients of <dy, y> of short_conv on the same inputs.  Returns a dict: dx
     (into dx when given), dw (fp32 [D,K]), db (fp32 [D]) with b, dhist (fp32
     [B,K-1,D]) when need_dhist."""
-    desc = _conv_desc(x, w, b, hist, activation, cu_seqlens)
-    _like(dy, "dy", x.dtype, x.get_device(), x.shape)
-    _on_gpu(x)
+    desc, flat = _conv_desc(x, w, b, hist, activation, cu_seqlens)
+    dev = x.get_device()
+    _like(dy, "dy", x.dtype, dev, x.shape)
+    if dev < 0:
+        _on_gpu(x)
     B, K, D = desc[0], desc[3], desc[2]
     f32 = torch.float32
     out = {"dx": _out(x, dx, "dx"), "dw": x.new_empty((D, K), dtype=f32)}
@@ -984,28 +1032,31 @@ def short_conv_backward(x, w, dy, b=None, hist=None, activation="identity", cu_s
         out["db"] = x.new_empty((D,), dtype=f32)
     if need_dhist:
         out["dhist"] = x.new_empty((B, K - 1, D), dtype=f32)
-    packed = _SC_DESC.pack(*desc, *_token_steps(dy, "dy"), *_token_steps(out["dx"], "dx"))
+    packed = _SC_DESC.pack(*desc, *_token_steps(dy, "dy", flat),
+                           *_token_steps(out["dx"], "dx", flat))
     if workspace is None:
         workspace = _block_workspace("prism_short_conv_backward_workspace", packed,
-                                     (int(cu_seqlens is not None),), x.device)
-    _check(lib().prism_short_conv_backward(
+                                     (int(cu_seqlens is not None),), x)
+    _check((_lib or lib()).prism_short_conv_backward(
         packed, _addr(x), _addr(w), _addr(b), _addr(hist), _addr(cu_seqlens), _addr(dy),
         _addr(out["dx"]), _addr(out["dw"]), _addr(out.get("db")), _addr(out.get("dhist")),
-        _addr(workspace), _size(workspace), _stream(x.device)))
+        _addr(workspace), _size(workspace), _stream_of(dev)))
     return out
 
 
 def _rec_desc(x, f, i, lam, gate, states, cu_seqlens):
-    """The descriptor's fields up to the steps of i, and the shape of a state."""
-    if gate not in GATES:
+    """The descriptor's fields up to the steps of i, the shape of a state, and the
+    steps of a contiguous tensor of x's shape."""
+    code = GATES.get(gate)
+    if code is None:
         raise ValueError(f"gate must be one of {sorted(GATES)}, got {gate!r}")
-    B, T, D, N = _batch(x, cu_seqlens)
+    B, T, D, N, flat = _batch(x, cu_seqlens)
     dt, dev = x.dtype, x.get_device()
     _like(f, "f", dt, dev, x.shape)
     si = _NO_STEPS
     if i is not None:
         _like(i, "i", dt, dev, x.shape)
-        si = _token_steps(i, "i")
+        si = _token_steps(i, "i", flat)
     if (lam is not None) != (gate == "power"):
         raise ValueError('lam goes with the gate "power", and with it alone')
     if lam is not None:
@@ -1013,8 +1064,8 @@ def _rec_desc(x, f, i, lam, gate, states, cu_seqlens):
     for name, t in states:
         if t is not None:
             _vector(t, name, torch.float32, dev, (B, D))
-    return (B, T, D, _dtype_code(x), GATES[gate], N, *_token_steps(x, "x"), *_token_steps(f, "f"),
-            *si), (B, D)
+    return (B, T, D, _dtype_code(x), code, N, *_token_steps(x, "x", flat),
+            *_token_steps(f, "f", flat), *si), (B, D), flat
 
 
 _NO_GRADS = (0,) * 12
@@ -1036,18 +1087,20 @@ def gated_recurrence(x, f, i=None, lam=None, h0=None, gate="sigmoid", cu_seqlens
     default; hT may be h0)."""
     if hT is not None and not need_state:
         raise ValueError("hT given, but need_state is false")
-    desc, state = _rec_desc(x, f, i, lam, gate, (("h0", h0), ("hT", hT)), cu_seqlens)
-    _on_gpu(x)
+    desc, state, flat = _rec_desc(x, f, i, lam, gate, (("h0", h0), ("hT", hT)), cu_seqlens)
+    dev = x.get_device()
+    if dev < 0:
+        _on_gpu(x)
     h = _out(x, h, "h")
     if hT is None and need_state:
         hT = x.new_empty(state, dtype=torch.float32)
-    packed = _GR_DESC.pack(*desc, *_token_steps(h, "h"), *_NO_GRADS)
+    packed = _GR_DESC.pack(*desc, *_token_steps(h, "h", flat), *_NO_GRADS)
     if workspace is None:
         workspace = _block_workspace("prism_gated_recurrence_workspace", packed,
-                                     (int(cu_seqlens is not None), 0), x.device)
-    _check(lib().prism_gated_recurrence(
+                                     (int(cu_seqlens is not None), 0), x)
+    _check((_lib or lib()).prism_gated_recurrence(
         packed, _addr(x), _addr(f), _addr(i), _addr(lam), _addr(h0), _addr(cu_seqlens), _addr(h),
-        _addr(hT), _addr(workspace), _size(workspace), _stream(x.device)))
+        _addr(hT), _addr(workspace), _size(workspace), _stream_of(dev)))
     return h, hT
 
 
@@ -1057,19 +1110,20 @@ def gated_recurrence_backward(x, f, h, dh, i=None, lam=None, h0=None, dhT=None, 
     """Gradients of <dh, h> + <dhT, h_T> of gated_recurrence from its inputs and
     its output h.  Returns a dict: dx, df (input type; into dx, df when given), di
     with i, dlam (fp32 [D]) with lam, dh0 (fp32 [B,D]) when need_dh0."""
-    desc, state = _rec_desc(x, f, i, lam, gate, (("h0", h0), ("dhT", dhT)), cu_seqlens)
+    desc, state, flat = _rec_desc(x, f, i, lam, gate, (("h0", h0), ("dhT", dhT)), cu_seqlens)
     dt, dev = x.dtype, x.get_device()
     _like(h, "h", dt, dev, x.shape)
     _like(dh, "dh", dt, dev, x.shape)
     if di is not None and i is None:
         raise ValueError("di without i")
-    _on_gpu(x)
+    if dev < 0:
+        _on_gpu(x)
     out = {"dx": _out(x, dx, "dx"), "df": _out(x, df, "df")}
-    steps = (*_token_steps(h, "h"), *_token_steps(dh, "dh"), *_token_steps(out["dx"], "dx"),
-             *_token_steps(out["df"], "df"))
+    steps = (*_token_steps(h, "h", flat), *_token_steps(dh, "dh", flat),
+             *_token_steps(out["dx"], "dx", flat), *_token_steps(out["df"], "df", flat))
     if i is not None:
         out["di"] = _out(x, di, "di")
-        steps += _token_steps(out["di"], "di")
+        steps += _token_steps(out["di"], "di", flat)
     else:
         steps += _NO_STEPS
     if lam is not None:
@@ -1079,12 +1133,12 @@ def gated_recurrence_backward(x, f, h, dh, i=None, lam=None, h0=None, dhT=None, 
     packed = _GR_DESC.pack(*desc, *steps)
     if workspace is None:
         workspace = _block_workspace("prism_gated_recurrence_workspace", packed,
-                                     (int(cu_seqlens is not None), 1), x.device)
-    _check(lib().prism_gated_recurrence_backward(
+                                     (int(cu_seqlens is not None), 1), x)
+    _check((_lib or lib()).prism_gated_recurrence_backward(
         packed, _addr(x), _addr(f), _addr(i), _addr(lam), _addr(h0), _addr(cu_seqlens), _addr(h),
         _addr(dh), _addr(dhT), _addr(out["dx"]), _addr(out["df"]), _addr(out.get("di")),
         _addr(out.get("dlam")), _addr(out.get("dh0")), _addr(workspace), _size(workspace),
-        _stream(x.device)))
+        _stream_of(dev)))
     return out
 
 
@@ -1093,13 +1147,18 @@ def gated_recurrence_step(x, f, state, i=None, lam=None, gate="sigmoid", state_o
     fp32 [B,D] (prism_gated_recurrence_step; T = 1: a decode step).  The state
     after them goes to state_out, or into state itself when that is None.
     Returns h."""
-    desc, _ = _rec_desc(x, f, i, lam, gate, (("state", state), ("state_out", state_out)), None)
-    _on_gpu(x)
-    h = _out(x, h, "h")
-    _check(lib().prism_gated_recurrence_step(
-        _GR_DESC.pack(*desc, *_token_steps(h, "h"), *_NO_GRADS), _addr(x), _addr(f), _addr(i),
-        _addr(lam), _addr(state), _addr(state if state_out is None else state_out), _addr(h),
-        _stream(x.device)))
+    desc, _, flat = _rec_desc(x, f, i, lam, gate, (("state", state), ("state_out", state_out)), None)
+    dev = x.get_device()
+    if dev < 0:
+        _on_gpu(x)
+    if h is None:
+        h, hs = x.new_empty(x.shape), flat
+    else:
+        hs = _token_steps(_out(x, h, "h"), "h", flat)
+    _check((_lib or lib()).prism_gated_recurrence_step(
+        _GR_DESC.pack(*desc, *hs, *_NO_GRADS), x.data_ptr(), f.data_ptr(), _addr(i), _addr(lam),
+        state.data_ptr(), (state if state_out is None else state_out).data_ptr(), h.data_ptr(),
+        _stream_of(dev)))
     return h
 
 
