@@ -158,7 +158,7 @@ __global__ __launch_bounds__(NT) void layer_norm_bwd_kernel(const LayerNormArgs 
   typedef typename IO::raw raw;
   constexpr bool PF = NT < 1024;   // (1024 threads have no registers for it)
   __shared__ float sm[2][16][2];
-  __shared__ float cols[NV * V * (NT < 1024 ? NT / 2 : 1)];   // (of two teams or more; of 1024 threads there is one)
+  __shared__ float cols[2 * NV * V * (NT < 1024 ? NT / 2 : 1)];   // (of two teams or more; of 1024 threads there is one)
   int turn = 0;
   const int lane = threadIdx.x & (G - 1), teams = blockDim.x / G;
   const float inv = 1.f / (float)a.D;
@@ -253,39 +253,32 @@ __global__ __launch_bounds__(NT) void layer_norm_bwd_kernel(const LayerNormArgs 
   }
   if (!a.part) return;
   float* out = a.part + (long)blockIdx.x * 2 * a.D;
+  auto each = [&](auto f) {
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    float(&d)[NV][V] = k ? db : dw;
-    for (int mask = G; mask < WAVE; mask <<= 1) {
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
+      for (int i = 0; i < V; ++i) f(dw[j][i], j, i, 0), f(db[j][i], j, i, 1);
+  };
+  for (int mask = G; mask < WAVE; mask <<= 1) each([&](float& d, int, int, int) { d += __shfl_xor(d, mask); });
+  // the teams, or, where a wave has several, the waves, one after the other
+  const int per = G > WAVE ? G : WAVE, mine = threadIdx.x / per, n = blockDim.x / per;
+  for (int w = 0; w < n; ++w) {
+    if (w) __syncthreads();
+    if (mine == w)
+      each([&](float& d, int j, int i, int k) {
+        float& c = cols[((j * V + i) * 2 + k) * per + lane];
+        if (w) d += c;
+        if (w < n - 1) c = d;
+      });
+  }
+  if (mine != n - 1 || (G < WAVE && (int)(threadIdx.x & (WAVE - 1)) >= G)) return;
 #pragma unroll
-        for (int i = 0; i < V; ++i) d[j][i] += __shfl_xor(d[j][i], mask);
-    }
-    // the teams, or, where a wave has several, the waves, one after the other
-    const int per = G > WAVE ? G : WAVE, mine = threadIdx.x / per, n = blockDim.x / per;
-    if (n > 1) {
-      for (int w = 0; w < n; ++w) {
-        __syncthreads();
-        if (mine == w) {
+  for (int j = 0; j < NV; ++j) {
+    if (!on[j]) continue;
 #pragma unroll
-          for (int j = 0; j < NV; ++j)
+    for (int i = 0; i < V; ++i) out[at[j] + i] = dw[j][i];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-              float& c = cols[(j * V + i) * per + lane];
-              d[j][i] += w ? c : 0.f;
-              c = d[j][i];
-            }
-        }
-      }
-    }
-    if (mine == n - 1 && (G >= WAVE || (int)(threadIdx.x & (WAVE - 1)) < G)) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (on[j]) out[(long)k * a.D + at[j] + i] = d[j][i];
-    }
+    for (int i = 0; i < V; ++i) out[a.D + at[j] + i] = db[j][i];
   }
 }
 
@@ -356,7 +349,10 @@ Shape shape_of(int n, int most, int block) {
 // workgroups with many rows each: 16 values 56 us, 8 values 62 for 16384 rows of
 // 2048, with 256 workgroups of 512 threads).
 constexpr int LN_LANE = 8, LN_LANE_BWD = 16;
-constexpr int LN_PARTS = 512;   // workgroups of the backward kernel, at most
+// Workgroups of the backward kernel, at most: one a CU where their partials are
+// wide (16384 rows of 2048, 512 of them: 62 us in place of 56), four where rows are
+// short and a wave has few bytes on their way.
+int parts_of(int D) { return D >= 2048 ? 256 : D >= 1024 ? 512 : 1024; }
 
 template <typename E, int V, int NV, int NT>
 hipError_t run_fwd(const LayerNormArgs& a, const Shape& p, hipStream_t s) {
@@ -373,8 +369,7 @@ template <typename E, int V, int NV, int NT>
 hipError_t run_bwd(const LayerNormArgs& a, const Shape& p, hipStream_t s) {
   const long teams = p.block / p.G;
   long grid = (a.rows + teams - 1) / teams;
-  const long most = p.block > 256 ? LN_PARTS / 2 : LN_PARTS;
-  if (grid > most) grid = most;
+  if (grid > parts_of(a.D)) grid = parts_of(a.D);
   if (grid > 0) {
     if (a.dh)
       hipLaunchKernelGGL((layer_norm_bwd_kernel<E, V, NV, NT, true>), dim3((unsigned)grid), dim3(p.block), 0, s, a, p.G);
@@ -401,10 +396,10 @@ template <typename E, int V, bool BWD>
 hipError_t run_v(const LayerNormArgs& a, hipStream_t s) {
   const int lane = BWD ? LN_LANE_BWD : LN_LANE, n = (a.D + V - 1) / V;
   Shape p = shape_of(n, lane / V, 256);
-  // (backward, workgroups of 512 threads where 256 of them have four rows each or
-  // more: 16384 rows of 2048 56 us in place of 59; for 4995 rows of 48, 10 to a
-  // wave, 9.0 in place of 7.6, so not below)
-  if (BWD && p.block == 256 && a.rows >= 1024L * (512 / p.G)) p.block = 512;
+  // (backward, workgroups of 512 threads where there are rows for two of 256
+  // threads a CU: half the partials; for 4995 rows of 48, 16 to a workgroup, 9.0 us
+  // in place of 7.6, so not below)
+  if (BWD && V > 1 && p.block == 256 && a.rows > 512L * (256 / p.G)) p.block = 512;
   if (p.NV == 1) return run_nv<E, V, 1, BWD>(a, p, s);
   if (p.NV == 2) return run_nv<E, V, 2, BWD>(a, p, s);
   if constexpr (V < 8) {
@@ -425,7 +420,7 @@ hipError_t run(LayerNormArgs a, hipStream_t s) {
 
 }  // namespace
 
-size_t layer_norm_part_bytes(int D) { return (size_t)LN_PARTS * 2 * D * sizeof(float); }
+size_t layer_norm_part_bytes(int D) { return (size_t)parts_of(D) * 2 * D * sizeof(float); }
 
 template <typename E>
 hipError_t launch_layer_norm(const LayerNormArgs& a, hipStream_t s) {
