@@ -350,8 +350,9 @@ Shape shape_of(int n, int most, int block) {
 // 2048, with 256 workgroups of 512 threads).
 constexpr int LN_LANE = 8, LN_LANE_BWD = 16;
 // Workgroups of the backward kernel, at most: one a CU where their partials are
-// wide (16384 rows of 2048, 512 of them: 62 us in place of 56), four where rows are
-// short and a wave has few bytes on their way.
+// wide (16384 rows of 2048: 56 us; with 512 of them 62), four of half the size where
+// rows are short and a wave has few bytes on their way (65536 rows of 256: with 512
+// of them 35 us, 1024 28, 2048 34).
 int parts_of(int D) { return D >= 2048 ? 256 : D >= 1024 ? 512 : 1024; }
 
 template <typename E, int V, int NV, int NT>
@@ -369,6 +370,9 @@ template <typename E, int V, int NV, int NT>
 hipError_t run_bwd(const LayerNormArgs& a, const Shape& p, hipStream_t s) {
   const long teams = p.block / p.G;
   long grid = (a.rows + teams - 1) / teams;
+  // (two rows a team before there are more than one a CU: 4096 rows of 512 12 us in
+  // place of 13.5)
+  if (grid > 256) grid = grid > 512 ? grid / 2 : 256;
   if (grid > parts_of(a.D)) grid = parts_of(a.D);
   if (grid > 0) {
     if (a.dh)
@@ -396,10 +400,9 @@ template <typename E, int V, bool BWD>
 hipError_t run_v(const LayerNormArgs& a, hipStream_t s) {
   const int lane = BWD ? LN_LANE_BWD : LN_LANE, n = (a.D + V - 1) / V;
   Shape p = shape_of(n, lane / V, 256);
-  // (backward, workgroups of 512 threads where there are rows for two of 256
-  // threads a CU: half the partials; for 4995 rows of 48, 16 to a workgroup, 9.0 us
-  // in place of 7.6, so not below)
-  if (BWD && V > 1 && p.block == 256 && a.rows > 512L * (256 / p.G)) p.block = 512;
+  // (backward, workgroups of 512 threads for wide rows, of which there are enough for
+  // two of 256 threads a CU: half the partials)
+  if (BWD && V > 1 && a.D >= 1024 && p.block == 256 && a.rows > 512L * (256 / p.G)) p.block = 512;
   if (p.NV == 1) return run_nv<E, V, 1, BWD>(a, p, s);
   if (p.NV == 2) return run_nv<E, V, 2, BWD>(a, p, s);
   if constexpr (V < 8) {
