@@ -523,9 +523,11 @@ prism_status prism_short_conv_backward(const prism_short_conv_desc* desc, const 
  *   PRISM_GATE_LOG      a = exp(f),                  u = s x
  *   PRISM_GATE_SIGMOID  a = sigmoid(f),              u = (1 - a) s x
  *   PRISM_GATE_POWER    a = exp(-lam sigmoid(f)),    u = sqrt(1 - a^2) s x
- * lam [D] f32, >= 0.  Gates, state and sums are fp32 (1 - a and 1 - a^2 to their
- * own size); h is rounded once.  A value that is not finite may reach every later
- * token of its sequence and channel, never another's.
+ * lam [D] f32, >= 0.  f of PRISM_GATE_LOG is at most 0 in earnest; above it, the
+ * product of the decays of any 128 tokens in a row has to stay within fp32.
+ * Gates, state and sums are fp32 (1 - a and 1 - a^2 to their own size); h is
+ * rounded once.  A value that is not finite may reach every later token of its
+ * sequence and channel, never another's.
  *
  *   B, T, D    as in prism_short_conv_desc
  *   gate       a prism_gate value
@@ -564,9 +566,9 @@ prism_status prism_gated_recurrence(const prism_gated_recurrence_desc* desc, con
  * which is read as h_{t-1} (in bf16 as rounded: df and dlam then carry its
  * rounding, of at most 2^-9 of each h_{t-1}).  dhT [B,D] f32 may be NULL (zero).
  * dx, df, di dt, strided (di: NULL without i); dlam [D] f32, NULL but with
- * PRISM_GATE_POWER, summed in a fixed order; dh0 [B,D] f32 or NULL (may be dhT).
- * Where lam sigmoid(f) = 0 the root's infinite slope is taken as 0.  Written, not
- * accumulated. */
+ * PRISM_GATE_POWER, summed in a fixed order; dh0 [B,D] f32 or NULL (not the buffer
+ * of dhT or h0).  Where lam sigmoid(f) = 0 the root's infinite slope is taken as 0.
+ * Written, not accumulated. */
 prism_status prism_gated_recurrence_backward(const prism_gated_recurrence_desc* desc,
                                              const void* x, const void* f, const void* i,
                                              const float* lam, const float* h0,

@@ -169,8 +169,10 @@ prism_status check_batch(int B, int T, int D, prism_dtype dtype, int packed_toke
   if (packed && packed_tokens < 0) return fail(PRISM_ERR_SHAPE, "packed_tokens must be >= 0 with cu_seqlens");
   const long long rows = packed ? packed_tokens : (long long)B * T;
   if (rows > MOST_ROWS) return fail(PRISM_ERR_SHAPE, "a batch has at most " + num(MOST_ROWS) + " tokens");
-  // (a launch has under 2^32 threads: at most 512 for 64 rows of 64 channels)
-  if (rows * D > MOST_VALUES || (rows + 63) / 64 * ((D + 63) / 64) > (1LL << 22) || (long long)B * D >= (1LL << 31)) return fail(PRISM_ERR_SHAPE, "problem too large");
+  // (a launch has under 2^32 threads: at most 512 for 64 rows of 64 channels, 256 for
+  // 256 channels of a sequence)
+  if (rows * D > MOST_VALUES || (rows + 63) / 64 * ((D + 63) / 64) > (1LL << 22) || (long long)B * D >= (1LL << 31) ||
+      B * ((D + 255LL) / 256) >= (1LL << 23)) return fail(PRISM_ERR_SHAPE, "problem too large");
   return check_dtype(dtype);
 }
 
@@ -376,6 +378,7 @@ prism_status rec_backward(const prism_gated_recurrence_desc* desc, const void* x
   if ((st = check_token_steps(d.dx, "dx", d.B, d.T, a.rows, packed, true)) != PRISM_OK) return st;
   if ((st = check_token_steps(d.df, "df", d.B, d.T, a.rows, packed, true)) != PRISM_OK) return st;
   if (i && (st = check_token_steps(d.di, "di", d.B, d.T, a.rows, packed, true)) != PRISM_OK) return st;
+  if (dh0 && (dh0 == dhT || dh0 == h0)) return fail(PRISM_ERR_UNSUPPORTED, "dh0 is the buffer of dhT or h0");
   const size_t need = prism::recurrence_bytes(a, packed, true);
   if (need > 0 && (st = check_buffer(workspace, workspace_bytes, need, "workspace")) != PRISM_OK) return st;
   a.cu = cu;

@@ -386,14 +386,24 @@ hipError_t run_bwd(const LayerNormArgs& a, const Shape& p, hipStream_t s) {
   return hipSuccess;
 }
 
+// (a row of more than a wave has as many vectors a lane as a lane may have, or, of
+// more than 1024 lanes, more)
 template <typename E, int V, int NV, bool BWD>
 hipError_t run_nv(const LayerNormArgs& a, const Shape& p, hipStream_t s) {
-  if constexpr (BWD) {
-    if (p.block > 512) return run_bwd<E, V, NV, 1024>(a, p, s);
-    return p.block > 256 ? run_bwd<E, V, NV, 512>(a, p, s) : run_bwd<E, V, NV, 256>(a, p, s);
-  } else {
-    return p.block > 256 ? run_fwd<E, V, NV, 1024>(a, p, s) : run_fwd<E, V, NV, 256>(a, p, s);
+  constexpr int most = BWD ? LN_LANE_BWD : LN_LANE;
+  if constexpr (NV * V >= most) {
+    if constexpr (BWD) {
+      if (p.block > 512) return run_bwd<E, V, NV, 1024>(a, p, s);
+      if (p.block > 256) return run_bwd<E, V, NV, 512>(a, p, s);
+    } else {
+      if (p.block > 256) return run_fwd<E, V, NV, 1024>(a, p, s);
+    }
   }
+  if constexpr (NV * V <= most) {
+    if constexpr (BWD) return run_bwd<E, V, NV, 256>(a, p, s);
+    return run_fwd<E, V, NV, 256>(a, p, s);
+  }
+  return hipErrorInvalidValue;
 }
 // (16384 values are at most 16 for each of 1024 lanes)
 template <typename E, int V, bool BWD>

@@ -36,6 +36,12 @@ struct TileArgs {
 };
 
 constexpr unsigned NOT_YET = 0xffffffffu;   // of a word's A: nothing written so far
+// Looks at the words before a wait ends by itself, with a state that is not a
+// number: about a second, where waits of a correct call end within milliseconds.
+// (Two calls at the same time on one workspace, which is an error, could otherwise
+// wait for ever.)
+constexpr int MOST_LOOKS = 1 << 20;
+constexpr unsigned long long NO_STATE = 0x7fc00000ull << 32;   // (0, not a number)
 // Words a tile reads at once, and waves of a workgroup that share a SIMD's
 // registers: with few tiles in all, the state goes from tile to tile faster if
 // they look further; with many, their registers and reads cost more.
@@ -64,7 +70,7 @@ __device__ inline void look_back(const unsigned long long* words, long stride, i
   for (int k = 0; k < L; ++k)
 #pragma unroll
     for (int v = 0; v < V; ++v) w[k][v] = k < left ? load(k, v) : 0;
-  while (true) {
+  for (int looks = 0;; ++looks) {
     // whether all are written, and whether those between the tile and a state are
     bool written = true, known = true, found[V];
 #pragma unroll
@@ -85,7 +91,7 @@ __device__ inline void look_back(const unsigned long long* words, long stride, i
         bool state = true;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          w[L - 1][v] = load(L - 1, v);
+          w[L - 1][v] = ++looks < MOST_LOOKS ? load(L - 1, v) : NO_STATE;
           state = state && (found[v] || __uint_as_float((unsigned)w[L - 1][v]) == 0.f);
         }
         if (__all(state)) break;
@@ -97,7 +103,7 @@ __device__ inline void look_back(const unsigned long long* words, long stride, i
     for (int k = 0; k < L; ++k)
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        if ((unsigned)w[k][v] == NOT_YET) w[k][v] = load(k, v);
+        if ((unsigned)w[k][v] == NOT_YET) w[k][v] = looks < MOST_LOOKS ? load(k, v) : NO_STATE;
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -369,6 +375,7 @@ struct ForwardStrip {
 template <typename E, int V, int G, bool INP, int R, int W, bool FAR>
 __global__ __launch_bounds__(W * WAVE, FAR ? WAVES_FAR : WAVES) void recurrence_tile_kernel(const RecurrenceArgs a, const TileArgs g) {
   const int id = take_tile(g), tile = id / g.slices, slice = id - tile * g.slices;
+  if (tile >= g.tiles) return;   // (a counter that another call counts on too)
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE), lane = threadIdx.x & (WAVE - 1);
   int c = (slice * WAVE + lane) * V;
   const bool on = c < a.D;
@@ -539,6 +546,7 @@ struct BackwardStrip {
 template <typename E, int V, int G, bool INP, int R, int W, bool FAR>
 __global__ __launch_bounds__(W * WAVE, FAR ? WAVES_FAR : WAVES) void recurrence_tile_bwd_kernel(const RecurrenceArgs a, const TileArgs g) {
   const int id = take_tile(g), turn = id / g.slices, slice = id - turn * g.slices, tile = g.tiles - 1 - turn;
+  if (tile < 0) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE), lane = threadIdx.x & (WAVE - 1);
   int c = (slice * WAVE + lane) * V;
   const bool on = c < a.D;

@@ -108,7 +108,7 @@ def _sc_bwd(D, ws=FAKE, nbytes=1 << 30, **kw):
 
 
 BATCH = [("B", -1, E_SHAPE), ("T", -1, E_SHAPE), ("D", 0, E_SHAPE), ("D", (1 << 22) + 1, E_SHAPE), ("B", 1 << 28, E_SHAPE),
-         ("T", 1 << 30, E_SHAPE), ("dtype", 7, E_UNSUP)]
+         ("T", 1 << 30, E_SHAPE), ("B", 1 << 23, E_SHAPE), ("dtype", 7, E_UNSUP)]
 
 
 @no_gpu
@@ -162,7 +162,8 @@ def _gr(D, ws=FAKE, nbytes=1 << 30, **kw):
 
 def _gr_bwd(D, ws=FAKE, nbytes=1 << 30, **kw):
     names = ("x", "f", "i", "lam", "h0", "cu_seqlens", "h", "dh", "dhT", "dx", "df", "di", "dlam", "dh0")
-    p = [kw.get(n, None if n == "cu_seqlens" else FAKE) for n in names]
+    own = {"cu_seqlens": None, "dh0": ctypes.c_void_p(0x30000)}
+    p = [kw.get(n, own.get(n, FAKE)) for n in names]
     return P.lib().prism_gated_recurrence_backward(ctypes.byref(D), *p, ws, nbytes, None)
 
 
@@ -202,6 +203,8 @@ def test_gated_recurrence_pointers_strides_workspace():
         assert _gr_bwd(gr(**{"s" + n: _st(0, 64)})) == E_SHAPE and n in _err()
     for n in ("dhT", "dlam", "dh0"):
         assert _gr_bwd(gr(), **{n: ctypes.c_void_p(0x10002)}) == E_ALIGN and n in _err()
+    for n in ("dhT", "h0"):
+        assert _gr_bwd(gr(), **{n: FAKE, "dh0": FAKE}) == E_UNSUP and "dh0" in _err()
     for n in ("x", "f", "lam", "state", "state_out", "h"):
         assert _gr_step(gr(), **{n: None}) == E_NULL and n in _err()
     assert _gr_step(gr(sh=_st(0, 64))) == E_SHAPE
