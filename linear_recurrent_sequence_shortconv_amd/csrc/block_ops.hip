@@ -7,7 +7,8 @@ namespace prism {
 namespace {
 
 // 32 columns a workgroup, 32 threads on each column taking every 32nd partial,
-// joined through LDS in a fixed order.
+// joined through LDS in a fixed order: latency bound, 8 loads on their way (256
+// partials of 2 x 2048 values, 4 MB, 4 us).
 __global__ __launch_bounds__(1024) void column_sums_kernel(const float* part, int parts, int C, int K, float* out,
                                                            float* last) {
   __shared__ float sm[32][33];
@@ -33,8 +34,8 @@ __global__ __launch_bounds__(1024) void column_sums_kernel(const float* part, in
 }  // namespace
 
 hipError_t launch_column_sums(const float* part, int parts, int C, int K, float* out, float* last, hipStream_t s) {
-  hipLaunchKernelGGL(column_sums_kernel, dim3((unsigned)(((K + 1L) * C + 31) / 32)), dim3(1024), 0, s, part, parts, C, K,
-                     out, last);
+  hipLaunchKernelGGL(column_sums_kernel, dim3((unsigned)(((K + 1L) * C + 31) / 32)), dim3(1024), 0, s, part, parts, C,
+                     K, out, last);
   return hipGetLastError();
 }
 

@@ -295,7 +295,9 @@ prism_status check_rec(const prism_gated_recurrence_desc* desc, bool packed, pri
   a->T = d.T;
   a->D = d.D;
   a->rows = packed ? d.packed_tokens : d.B * d.T;
-  a->gate = d.gate == PRISM_GATE_LOG ? prism::GATE_LOG : d.gate == PRISM_GATE_SIGMOID ? prism::GATE_SIGMOID : prism::GATE_POWER;
+  a->gate = d.gate == PRISM_GATE_LOG       ? prism::GATE_LOG
+            : d.gate == PRISM_GATE_SIGMOID ? prism::GATE_SIGMOID
+                                           : prism::GATE_POWER;
   a->sx = steps(d.x);
   a->sf = steps(d.f);
   a->si = steps(d.i);

