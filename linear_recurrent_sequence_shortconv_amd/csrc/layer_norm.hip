@@ -51,8 +51,7 @@ __device__ inline void team_sums(float (&v)[N], int G, float (*sm)[16][2], int& 
 // A vector of ones or zeros in the place of weights that are not given.
 template <typename E, int V>
 __device__ inline typename VecIo<E, V>::raw weight(const void* p, int at, float other) {
-  typedef typename VecIo<E, V>::raw raw;
-  if (p) return *reinterpret_cast<const raw*>(static_cast<const E*>(p) + at);
+  if (p) return load_vec<E, V>(static_cast<const E*>(p) + at);
   float x[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) x[i] = other;
@@ -69,7 +68,8 @@ __device__ inline long row_at(const Strides& s, long row, int T, int H) {
 // values a lane a row of 2048 is a workgroup's: so few registers that 8 waves a
 // SIMD hide the loads (16 and 32 values a lane, with or without the next row on
 // its way: 50 to 52 us in place of 48 for 8 x 2048 rows of 2048 with a residual).
-template <typename E, int V, int NV, int NT, bool RES>
+// ODD: the row's last vector is no whole one, and begins before its place.
+template <typename E, int V, int NV, int NT, bool ODD, bool RES>
 __global__ __launch_bounds__(NT) void layer_norm_kernel(const LayerNormArgs a, int G) {
   typedef VecIo<E, V> IO;
   typedef typename IO::raw raw;
@@ -77,20 +77,20 @@ __global__ __launch_bounds__(NT) void layer_norm_kernel(const LayerNormArgs a, i
   int turn = 0;
   const int lane = threadIdx.x & (G - 1), teams = blockDim.x / G;
   const float inv = 1.f / (float)a.D;
-  int at[NV];
-  bool on[NV];
+  int at[NV], skip[NV];   // values at + skip .. at + V - 1 are the lane's (skip = V: none)
   raw rw[NV], rb[NV], rx[NV], rr[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = (lane + j * G) * V;
-    on[j] = c < a.D;
-    at[j] = on[j] ? c : 0;
+    at[j] = c >= a.D ? 0 : ODD ? min(c, a.D - V) : c;
+    skip[j] = c >= a.D ? V : ODD ? c - at[j] : 0;
   }
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     rw[j] = weight<E, V>(a.w, at[j], 1.f);
     rb[j] = weight<E, V>(a.b, at[j], 0.f);
   }
+  auto mine = [&](int j, int i) { return ODD ? i >= skip[j] : skip[j] == 0; };
   // (every team of the workgroup makes every round: the sums have barriers)
   for (long base = (long)blockIdx.x * teams; base < a.rows; base += (long)gridDim.x * teams) {
     const long want = base + threadIdx.x / G;
@@ -98,11 +98,11 @@ __global__ __launch_bounds__(NT) void layer_norm_kernel(const LayerNormArgs a, i
     const long row = live ? want : a.rows - 1;
     const E* x = static_cast<const E*>(a.x) + row_at(a.sx, row, a.T, a.H);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) rx[j] = *reinterpret_cast<const raw*>(x + at[j]);
+    for (int j = 0; j < NV; ++j) rx[j] = load_vec<E, V>(x + at[j]);
     if (RES) {
       const E* r = static_cast<const E*>(a.r) + row_at(a.sr, row, a.T, a.H);
 #pragma unroll
-      for (int j = 0; j < NV; ++j) rr[j] = *reinterpret_cast<const raw*>(r + at[j]);
+      for (int j = 0; j < NV; ++j) rr[j] = load_vec<E, V>(r + at[j]);
     }
     float s[NV][V];
     float sum[1] = {0.f};
@@ -116,13 +116,13 @@ __global__ __launch_bounds__(NT) void layer_norm_kernel(const LayerNormArgs a, i
         for (int i = 0; i < V; ++i) s[j][i] += q[i];
       }
 #pragma unroll
-      for (int i = 0; i < V; ++i) sum[0] += on[j] ? s[j][i] : 0.f;
+      for (int i = 0; i < V; ++i) sum[0] += mine(j, i) ? s[j][i] : 0.f;
     }
     if (RES && a.h && live) {
       E* h = static_cast<E*>(a.h) + row_at(a.sh, row, a.T, a.H);
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        if (on[j]) *reinterpret_cast<raw*>(h + at[j]) = IO::pack(s[j]);
+        store_vec<E, V>(h + at[j], s[j], skip[j]);
     }
     float m = 0.f;
     if (a.center) {
@@ -135,7 +135,7 @@ __global__ __launch_bounds__(NT) void layer_norm_kernel(const LayerNormArgs a, i
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         s[j][i] -= m;
-        sq[0] += on[j] ? s[j][i] * s[j][i] : 0.f;
+        sq[0] += mine(j, i) ? s[j][i] * s[j][i] : 0.f;
       }
     team_sums<1>(sq, G, sm, turn);
     const float r = rsqrtf(fmaf(sq[0], inv, a.eps));
@@ -148,7 +148,7 @@ __global__ __launch_bounds__(NT) void layer_norm_kernel(const LayerNormArgs a, i
       IO::unpack(rb[j], b);
 #pragma unroll
       for (int i = 0; i < V; ++i) s[j][i] = fmaf(s[j][i] * r, w[i], b[i]);
-      if (on[j]) *reinterpret_cast<raw*>(y + at[j]) = IO::pack(s[j]);
+      store_vec<E, V>(y + at[j], s[j], skip[j]);
     }
   }
 }
@@ -157,7 +157,7 @@ __global__ __launch_bounds__(NT) void layer_norm_kernel(const LayerNormArgs a, i
 // teams (in the wave, then over the waves through LDS), and written as one
 // partial [2][D] for each workgroup.  The next row of a team is on its way while
 // the sums of one are joined (16384 rows of 2048 with dh: 56 us; without, 67).
-template <typename E, int V, int NV, int NT, bool DH>
+template <typename E, int V, int NV, int NT, bool ODD, bool DH>
 __global__ __launch_bounds__(NT) void layer_norm_bwd_kernel(const LayerNormArgs a, int G) {
   typedef VecIo<E, V> IO;
   typedef typename IO::raw raw;
@@ -167,26 +167,26 @@ __global__ __launch_bounds__(NT) void layer_norm_bwd_kernel(const LayerNormArgs 
   int turn = 0;
   const int lane = threadIdx.x & (G - 1), teams = blockDim.x / G;
   const float inv = 1.f / (float)a.D;
-  int at[NV];
-  bool on[NV];
+  int at[NV], skip[NV];   // values at + skip .. at + V - 1 are the lane's (skip = V: none)
   raw rw[NV], rx[NV], rg[NV], rh[NV];
   float dw[NV][V], db[NV][V];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = (lane + j * G) * V;
-    on[j] = c < a.D;
-    at[j] = on[j] ? c : 0;
+    at[j] = c >= a.D ? 0 : ODD ? min(c, a.D - V) : c;
+    skip[j] = c >= a.D ? V : ODD ? c - at[j] : 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) dw[j][i] = db[j][i] = 0.f;
   }
+  auto mine = [&](int j, int i) { return ODD ? i >= skip[j] : skip[j] == 0; };
   auto load = [&](long want) {
     const long row = want < a.rows ? want : a.rows - 1;
     const E* x = static_cast<const E*>(a.x) + row_at(a.sx, row, a.T, a.H);
     const E* dy = static_cast<const E*>(a.dy) + row_at(a.sy, row, a.T, a.H);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) rx[j] = *reinterpret_cast<const raw*>(x + at[j]);
+    for (int j = 0; j < NV; ++j) rx[j] = load_vec<E, V>(x + at[j]);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) rg[j] = *reinterpret_cast<const raw*>(dy + at[j]);
+    for (int j = 0; j < NV; ++j) rg[j] = load_vec<E, V>(dy + at[j]);
   };
   const long step = (long)gridDim.x * teams;
   long base = (long)blockIdx.x * teams;
@@ -200,7 +200,7 @@ __global__ __launch_bounds__(NT) void layer_norm_bwd_kernel(const LayerNormArgs 
     if (DH) {
       const E* dh = static_cast<const E*>(a.dh) + row_at(a.sr, live ? row : a.rows - 1, a.T, a.H);
 #pragma unroll
-      for (int j = 0; j < NV; ++j) rh[j] = *reinterpret_cast<const raw*>(dh + at[j]);
+      for (int j = 0; j < NV; ++j) rh[j] = load_vec<E, V>(dh + at[j]);
     }
     float u[NV][V], g[NV][V];
     float one[2] = {0.f, 0.f};
@@ -212,8 +212,8 @@ __global__ __launch_bounds__(NT) void layer_norm_bwd_kernel(const LayerNormArgs 
       IO::unpack(rw[j], w);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        one[0] += on[j] ? u[j][i] : 0.f;
-        one[1] += on[j] ? g[j][i] * w[i] : 0.f;
+        one[0] += mine(j, i) ? u[j][i] : 0.f;
+        one[1] += mine(j, i) ? g[j][i] * w[i] : 0.f;
       }
     }
     if (PF && base + step < a.rows) load(row + step);
@@ -231,8 +231,8 @@ __global__ __launch_bounds__(NT) void layer_norm_bwd_kernel(const LayerNormArgs 
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         u[j][i] -= m;
-        two[0] += on[j] ? u[j][i] * u[j][i] : 0.f;
-        two[1] += on[j] ? u[j][i] * (g[j][i] * w[i]) : 0.f;
+        two[0] += mine(j, i) ? u[j][i] * u[j][i] : 0.f;
+        two[1] += mine(j, i) ? u[j][i] * (g[j][i] * w[i]) : 0.f;
       }
     }
     team_sums<2>(two, G, sm, turn);
@@ -253,7 +253,7 @@ __global__ __launch_bounds__(NT) void layer_norm_bwd_kernel(const LayerNormArgs 
         dw[j][i] = fmaf(g[j][i], un, dw[j][i]);
         db[j][i] += g[j][i];
       }
-      if (on[j]) *reinterpret_cast<raw*>(dx + at[j]) = IO::pack(v);
+      store_vec<E, V>(dx + at[j], v, skip[j]);
     }
   }
   if (!a.part) return;
@@ -266,24 +266,26 @@ __global__ __launch_bounds__(NT) void layer_norm_bwd_kernel(const LayerNormArgs 
   };
   for (int mask = G; mask < WAVE; mask <<= 1) each([&](float& d, int, int, int) { d += __shfl_xor(d, mask); });
   // the teams, or, where a wave has several, the waves, one after the other
-  const int per = G > WAVE ? G : WAVE, mine = threadIdx.x / per, n = blockDim.x / per;
+  const int per = G > WAVE ? G : WAVE, part = threadIdx.x / per, n = blockDim.x / per;
   for (int w = 0; w < n; ++w) {
     if (w) __syncthreads();
-    if (mine == w)
+    if (part == w)
       each([&](float& d, int j, int i, int k) {
         float& c = cols[((j * V + i) * 2 + k) * per + lane];
         if (w) d += c;
         if (w < n - 1) c = d;
       });
   }
-  if (mine != n - 1 || (G < WAVE && (int)(threadIdx.x & (WAVE - 1)) >= G)) return;
+  if (part != n - 1 || (G < WAVE && (int)(threadIdx.x & (WAVE - 1)) >= G)) return;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    if (!on[j]) continue;
+    if (skip[j] == V) continue;
 #pragma unroll
-    for (int i = 0; i < V; ++i) out[at[j] + i] = dw[j][i];
+    for (int i = 0; i < V; ++i)
+      if (!ODD || i >= skip[j]) out[at[j] + i] = dw[j][i];
 #pragma unroll
-    for (int i = 0; i < V; ++i) out[a.D + at[j] + i] = db[j][i];
+    for (int i = 0; i < V; ++i)
+      if (!ODD || i >= skip[j]) out[a.D + at[j] + i] = db[j][i];
   }
 }
 
@@ -320,18 +322,6 @@ void merge_rows(LayerNormArgs& a, bool bwd) {
     if (all[k]) *all[k] = Strides{step[k][0], step[k][1], step[k][2]};
 }
 
-// Vectors of 16 bytes where every row starts at a multiple of them and has a
-// whole number of them, else single values (8 x 2048 rows of 2048 in bf16 48 us by
-// vectors, 86 by values; backward 56 and 95).
-bool aligned(const LayerNormArgs& a, bool bwd, int V, int size) {
-  long m = a.D | a.sx.b | a.sx.t | a.sx.h | a.sy.b | a.sy.t | a.sy.h;
-  uintptr_t p = (uintptr_t)a.x | (uintptr_t)a.w | (uintptr_t)a.b;
-  if (a.r || a.dh) m |= a.sr.b | a.sr.t | a.sr.h;
-  if (bwd || a.h) m |= a.sh.b | a.sh.t | a.sh.h;
-  p |= (uintptr_t)a.r | (uintptr_t)a.y | (uintptr_t)a.h | (uintptr_t)a.dy | (uintptr_t)a.dh | (uintptr_t)a.dx;
-  return m % V == 0 && p % (V * size) == 0;
-}
-
 struct Shape {
   int G, NV, block;
 };
@@ -363,18 +353,18 @@ constexpr int LN_LANE = 8, LN_LANE_BWD = 16;
 // (65536 rows of 256: with 512 workgroups 35 us, 1024 28, 2048 34).
 int parts_of(int D) { return D >= 2048 ? 256 : D >= 1024 ? 512 : 1024; }
 
-template <typename E, int V, int NV, int NT>
+template <typename E, int V, int NV, int NT, bool ODD>
 hipError_t run_fwd(const LayerNormArgs& a, const Shape& p, hipStream_t s) {
   const long teams = p.block / p.G;
   long grid = (a.rows + teams - 1) / teams;
   if (grid > (1 << 20)) grid = 1 << 20;
   if (a.r)
-    hipLaunchKernelGGL((layer_norm_kernel<E, V, NV, NT, true>), dim3((unsigned)grid), dim3(p.block), 0, s, a, p.G);
+    hipLaunchKernelGGL((layer_norm_kernel<E, V, NV, NT, ODD, true>), dim3((unsigned)grid), dim3(p.block), 0, s, a, p.G);
   else
-    hipLaunchKernelGGL((layer_norm_kernel<E, V, NV, NT, false>), dim3((unsigned)grid), dim3(p.block), 0, s, a, p.G);
+    hipLaunchKernelGGL((layer_norm_kernel<E, V, NV, NT, ODD, false>), dim3((unsigned)grid), dim3(p.block), 0, s, a, p.G);
   return hipGetLastError();
 }
-template <typename E, int V, int NV, int NT>
+template <typename E, int V, int NV, int NT, bool ODD>
 hipError_t run_bwd(const LayerNormArgs& a, const Shape& p, hipStream_t s) {
   const long teams = p.block / p.G;
   long grid = (a.rows + teams - 1) / teams;
@@ -385,9 +375,9 @@ hipError_t run_bwd(const LayerNormArgs& a, const Shape& p, hipStream_t s) {
   if (grid > 0) {
     const dim3 blocks((unsigned)grid), threads(p.block);
     if (a.dh)
-      hipLaunchKernelGGL((layer_norm_bwd_kernel<E, V, NV, NT, true>), blocks, threads, 0, s, a, p.G);
+      hipLaunchKernelGGL((layer_norm_bwd_kernel<E, V, NV, NT, ODD, true>), blocks, threads, 0, s, a, p.G);
     else
-      hipLaunchKernelGGL((layer_norm_bwd_kernel<E, V, NV, NT, false>), blocks, threads, 0, s, a, p.G);
+      hipLaunchKernelGGL((layer_norm_bwd_kernel<E, V, NV, NT, ODD, false>), blocks, threads, 0, s, a, p.G);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -397,47 +387,49 @@ hipError_t run_bwd(const LayerNormArgs& a, const Shape& p, hipStream_t s) {
 
 // (a row of more than a wave has as many vectors a lane as a lane may have, or, of
 // more than 1024 lanes, more)
-template <typename E, int V, int NV, bool BWD>
+template <typename E, int V, int NV, bool ODD, bool BWD>
 hipError_t run_nv(const LayerNormArgs& a, const Shape& p, hipStream_t s) {
   constexpr int most = BWD ? LN_LANE_BWD : LN_LANE;
   if constexpr (NV * V >= most) {
     if constexpr (BWD) {
-      if (p.block > 512) return run_bwd<E, V, NV, 1024>(a, p, s);
-      if (p.block > 256) return run_bwd<E, V, NV, 512>(a, p, s);
+      if (p.block > 512) return run_bwd<E, V, NV, 1024, ODD>(a, p, s);
+      if (p.block > 256) return run_bwd<E, V, NV, 512, ODD>(a, p, s);
     } else {
-      if (p.block > 256) return run_fwd<E, V, NV, 1024>(a, p, s);
+      if (p.block > 256) return run_fwd<E, V, NV, 1024, ODD>(a, p, s);
     }
   }
   if constexpr (NV * V <= most) {
-    if constexpr (BWD) return run_bwd<E, V, NV, 256>(a, p, s);
-    return run_fwd<E, V, NV, 256>(a, p, s);
+    if constexpr (BWD) return run_bwd<E, V, NV, 256, ODD>(a, p, s);
+    return run_fwd<E, V, NV, 256, ODD>(a, p, s);
   }
   return hipErrorInvalidValue;
 }
 // (16384 values are at most 16 for each of 1024 lanes)
-template <typename E, int V, bool BWD>
+template <typename E, int V, bool ODD, bool BWD>
 hipError_t run_v(const LayerNormArgs& a, hipStream_t s) {
   const int lane = BWD ? LN_LANE_BWD : LN_LANE, n = (a.D + V - 1) / V;
   Shape p = shape_of(n, lane / V, 256);
   // (backward, workgroups of 512 threads for wide rows, where these leave more than two
   // rows a team: 4096 rows of 2048 21 us in place of 22, 16384 56 in place of 70)
-  if (BWD && V > 1 && a.D >= 2048 && p.block == 256 && a.rows > 512L * (256 / p.G)) p.block = 512;
-  if (p.NV == 1) return run_nv<E, V, 1, BWD>(a, p, s);
-  if (p.NV == 2) return run_nv<E, V, 2, BWD>(a, p, s);
-  if constexpr (V < 8) {
-    if (p.NV == 4) return run_nv<E, V, 4, BWD>(a, p, s);
+  if (BWD && a.D >= 2048 && p.block == 256 && a.rows > 512L * (256 / p.G)) p.block = 512;
+  if (p.NV == 1) return run_nv<E, V, 1, ODD, BWD>(a, p, s);
+  if constexpr (V > 1) {
+    if (p.NV == 2) return run_nv<E, V, 2, ODD, BWD>(a, p, s);
   }
-  if constexpr (V == 1) {
-    if (p.NV == 8) return run_nv<E, V, 8, BWD>(a, p, s);
-    if (p.NV == 16) return run_nv<E, V, 16, BWD>(a, p, s);
+  if constexpr (V == 4) {
+    if (p.NV == 4) return run_nv<E, V, 4, ODD, BWD>(a, p, s);
   }
   return hipErrorInvalidValue;
 }
+// Vectors of 16 bytes, or single values of rows narrower than that (8 x 2048 rows of
+// 2048 in bf16 48 us by vectors, 86 by values, backward 56 and 95; 16384 rows of 1001
+// 17.5 and 27, backward 38 and 47).
 template <typename E, bool BWD>
 hipError_t run(LayerNormArgs a, hipStream_t s) {
   merge_rows(a, BWD);
   constexpr int V = 16 / sizeof(E);
-  return aligned(a, BWD, V, sizeof(E)) ? run_v<E, V, BWD>(a, s) : run_v<E, 1, BWD>(a, s);
+  if (a.D % V == 0) return run_v<E, V, false, BWD>(a, s);
+  return a.D > V ? run_v<E, V, true, BWD>(a, s) : run_v<E, 1, false, BWD>(a, s);
 }
 
 }  // namespace

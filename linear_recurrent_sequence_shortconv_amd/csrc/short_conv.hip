@@ -36,8 +36,7 @@ __device__ inline float sigma(float z) {
 
 template <typename E, int V>
 __device__ inline void load_row(const E* p, float (&x)[V]) {
-  typedef typename VecIo<E, V>::raw raw;
-  VecIo<E, V>::unpack(*reinterpret_cast<const raw*>(p), x);
+  VecIo<E, V>::unpack(load_vec<E, V>(p), x);
 }
 
 // Row e - start of a sequence, or of the rows before it.
@@ -60,7 +59,7 @@ __device__ inline void load_taps(const void* w, int c, float (&t)[K][V]) {
   E e[V * K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const raw r = *reinterpret_cast<const raw*>(static_cast<const E*>(w) + (long)c * K + k * V);
+    const raw r = load_vec<E, V>(static_cast<const E*>(w) + (long)c * K + k * V);
     __builtin_memcpy(e + k * V, &r, sizeof(raw));
   }
 #pragma unroll
@@ -69,10 +68,11 @@ __device__ inline void load_taps(const void* w, int c, float (&t)[K][V]) {
     for (int i = 0; i < V; ++i) t[j][i] = to_f(e[i * K + j]);
 }
 
-// A workgroup's waves take neighbouring strips of the same channels.
+// A workgroup's waves take neighbouring strips of the same channels.  The lane's
+// channels are c + skip .. c + V - 1 (skip = V: none).
 struct Place {
-  int blk, strip, c;
-  bool on;
+  int blk, strip, c, skip;
+  bool whole;   // no lane of the wave skips any
 };
 template <int V>
 __device__ inline Place place_of(int D, int cw) {
@@ -80,9 +80,10 @@ __device__ inline Place place_of(int D, int cw) {
   const int id = blockIdx.x;
   p.blk = id / cw;
   p.strip = __builtin_amdgcn_readfirstlane(p.blk * SC_WAVES + threadIdx.x / WAVE);
-  p.c = ((id - p.blk * cw) * WAVE + (threadIdx.x & (WAVE - 1))) * V;
-  p.on = p.c < D;
-  if (!p.on) p.c = 0;
+  const int c = ((id - p.blk * cw) * WAVE + (threadIdx.x & (WAVE - 1))) * V;
+  p.c = c < D ? min(c, D - V) : 0;
+  p.skip = c < D ? c - p.c : V;
+  p.whole = __all(p.skip == 0);
   return p;
 }
 
@@ -148,19 +149,16 @@ __global__ __launch_bounds__(SC_WAVES * WAVE) void short_conv_kernel(const Short
       for (int m = 0; m < K - 1; ++m) load_past<E, V, K>(a, x, q.b, n - (K - 1) + m, p.c, last[m]);
 #pragma unroll
       for (int m = 0; m < K - 1; ++m)
-        if (p.on)
-          *reinterpret_cast<raw*>(static_cast<E*>(a.hist_out) + ((long)q.b * (K - 1) + m) * a.D + p.c) =
-              IO::pack(last[m]);
+        store_vec<E, V>(static_cast<E*>(a.hist_out) + ((long)q.b * (K - 1) + m) * a.D + p.c, last[m], p.skip, p.whole);
     }
     raw in[U], ahead[U];
     auto load = [&](raw(&r)[U], int row) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        r[u] = *reinterpret_cast<const raw*>(x + (long)(min(row + u, stop - 1) - q.start) * a.sx.t + p.c);
+        r[u] = load_vec<E, V>(x + (long)(min(row + u, stop - 1) - q.start) * a.sx.t + p.c);
     };
-    const bool all = __all(p.on);
     load(ahead, row);
-    auto rows = [&](int row, auto inner) {   // INNER: U rows, and channels for all lanes
+    auto rows = [&](int row, auto inner) {   // INNER: U rows, and a whole wave
       constexpr bool INNER = decltype(inner)::value;
 #pragma unroll
       for (int u = 0; u < U; ++u) in[u] = ahead[u];
@@ -179,12 +177,12 @@ __global__ __launch_bounds__(SC_WAVES * WAVE) void short_conv_kernel(const Short
           for (int j = K - 2; j > 0; --j) past[j][i] = past[j - 1][i];
           past[0][i] = now[i];
         }
-        if (INNER || (row + u < stop && p.on))
-          *reinterpret_cast<raw*>(y + (long)(row + u - q.start) * a.sy.t + p.c) = IO::pack(z);
+        if (INNER || row + u < stop)
+          store_vec<E, V>(y + (long)(row + u - q.start) * a.sy.t + p.c, z, INNER ? 0 : p.skip, INNER || p.whole);
       }
     };
     for (; row < stop; row += U) {
-      if (all && row + U <= stop)
+      if (p.whole && row + U <= stop)
         rows(row, std::true_type());
       else
         rows(row, std::false_type());
@@ -240,15 +238,15 @@ __global__ __launch_bounds__(SC_WAVES * WAVE, V == 4 ? 4 : 8) void short_conv_bw
       for (int i = 0; i < V; ++i) gp[j][i] = 0.f;
     }
     // U rows from `row`; INNER: all of them the strip's, behind its first K - 1, and
-    // channels for all lanes
+    // the wave whole
     auto rows = [&](int row, auto inner) {
       constexpr bool INNER = decltype(inner)::value;
       raw in[U], gr[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const long t = (INNER ? row + u : min(row + u, q.end - 1)) - q.start;
-        in[u] = *reinterpret_cast<const raw*>(x + t * a.sx.t + p.c);
-        gr[u] = *reinterpret_cast<const raw*>(dy + t * a.sy.t + p.c);
+        in[u] = load_vec<E, V>(x + t * a.sx.t + p.c);
+        gr[u] = load_vec<E, V>(dy + t * a.sy.t + p.c);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -285,13 +283,14 @@ __global__ __launch_bounds__(SC_WAVES * WAVE, V == 4 ? 4 : 8) void short_conv_bw
           gp[0][i] = g[i];
         }
         const int e = r - (K - 1);
-        if (INNER || (r < stop && p.on)) {
+        if (INNER || r < stop) {
           if (INNER || e >= at) {
-            *reinterpret_cast<raw*>(dx + (long)(e - q.start) * a.sd.t + p.c) = IO::pack(out);
+            store_vec<E, V>(dx + (long)(e - q.start) * a.sd.t + p.c, out, INNER ? 0 : p.skip, INNER || p.whole);
           } else if (at == q.start && a.dhist) {
             float* d = a.dhist + ((long)q.b * (K - 1) + (r - q.start)) * a.D + p.c;
 #pragma unroll
-            for (int i = 0; i < V; ++i) d[i] = out[i];
+            for (int i = 0; i < V; ++i)
+              if (i >= p.skip) d[i] = out[i];
           }
         }
       }
@@ -299,7 +298,7 @@ __global__ __launch_bounds__(SC_WAVES * WAVE, V == 4 ? 4 : 8) void short_conv_bw
     int row = at;
     rows(row, std::false_type());
     row += U;   // (U >= K - 1)
-    if (__all(p.on))
+    if (p.whole)
       for (; row + U <= own; row += U) rows(row, std::true_type());
     for (; row < stop; row += U) rows(row, std::false_type());
     at = own;
@@ -314,7 +313,7 @@ __global__ __launch_bounds__(SC_WAVES * WAVE, V == 4 ? 4 : 8) void short_conv_bw
       for (int i = 0; i < V; ++i) {
         float& s = sm[j * V + i][lane];
         s = k ? s + dw[j][i] : dw[j][i];
-        if (k == SC_WAVES - 1 && p.on) a.part[((long)p.blk * (K + 1) + j) * a.D + p.c + i] = s;
+        if (k == SC_WAVES - 1 && i >= p.skip) a.part[((long)p.blk * (K + 1) + j) * a.D + p.c + i] = s;
       }
   }
 }
@@ -366,16 +365,13 @@ hipError_t run_bwd(const ShortConvArgs& a, hipStream_t s) {
   return launch_column_sums(a.part, parts, a.D, K, a.dw, a.db, s);
 }
 
-// Channels a lane: four where every row starts at a multiple of them, else one (8 x
-// 2048 tokens of 2048 channels 28 us with four, 36 with one, backward 51 and 57; eight
-// bf16 take the registers of half the waves: 32 us, backward 61).
+// Channels a lane: four, or one of rows narrower than that.  (8 x 2048 tokens of 2048
+// channels 28 us with four, 36 with one, backward 51 and 57, of 1001 channels 18 and
+// 23, backward 39 and 42; eight bf16 take the registers of half the waves: 32 us,
+// backward 61.)
 template <typename E, bool BWD, int K>
 hipError_t run_k(const ShortConvArgs& a, hipStream_t s) {
-  uintptr_t p = (uintptr_t)a.x | (uintptr_t)a.w | (uintptr_t)a.b | (uintptr_t)a.hist | (uintptr_t)a.y |
-                (uintptr_t)a.hist_out | (uintptr_t)a.dy | (uintptr_t)a.dx;
-  long m = a.D | a.sx.b | a.sx.t | a.sy.b | a.sy.t;
-  if (BWD) m |= a.sd.b | a.sd.t;
-  if (m % 4 == 0 && p % (4 * sizeof(E)) == 0) return BWD ? run_bwd<E, 4, K>(a, s) : run_fwd<E, 4, K>(a, s);
+  if (a.D >= 4) return BWD ? run_bwd<E, 4, K>(a, s) : run_fwd<E, 4, K>(a, s);
   return BWD ? run_bwd<E, 1, K>(a, s) : run_fwd<E, 1, K>(a, s);
 }
 template <typename E, bool BWD>

@@ -77,6 +77,40 @@ template <> struct VecIo<float, 4> {
   __device__ static inline raw pack(const float (&x)[4]) { return raw{x[0], x[1], x[2], x[3]}; }
 };
 
+// V values from an address of any alignment (the memory unit takes 16 bytes from
+// any), and those behind the first `skip` of them to one: lanes of a row whose width
+// is no multiple of V take V values each all the same, the last with values of the
+// lane before it in front, which it neither counts nor writes.
+template <typename E, int V>
+__device__ inline typename VecIo<E, V>::raw load_vec(const E* p) {
+  typename VecIo<E, V>::raw w;
+  __builtin_memcpy(&w, p, sizeof(w));
+  return w;
+}
+template <typename E, int V>
+__device__ inline void store_vec(E* p, const float (&x)[V]) {
+  const typename VecIo<E, V>::raw w = VecIo<E, V>::pack(x);
+  __builtin_memcpy(p, &w, sizeof(w));
+}
+template <typename E, int V>
+__device__ inline void store_vec(E* p, const float (&x)[V], int skip) {
+  if (skip == 0) {
+    store_vec<E, V>(p, x);
+  } else {
+#pragma unroll
+    for (int i = 1; i < V; ++i)
+      if (i >= skip) p[i] = (E)x[i];
+  }
+}
+// (whole: no lane of the wave skips any)
+template <typename E, int V>
+__device__ inline void store_vec(E* p, const float (&x)[V], int skip, bool whole) {
+  if (whole)
+    store_vec<E, V>(p, x);
+  else
+    store_vec<E, V>(p, x, skip);
+}
+
 // Sum over each group of G = 1, 2, .., 32 consecutive lanes, in every lane of
 // the group: quad permutations, then mirrors of half rows and rows (whose
 // quads already hold equal values), then one exchange between rows.

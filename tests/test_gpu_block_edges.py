@@ -270,3 +270,46 @@ def test_neighbours_of_results_stay(D):
     torch.cuda.synchronize()
     for b, _ in bufs + [hist, state]:
         check(b)
+
+
+def _np(t):
+    return t.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("dt,D", [(BF, 2), (BF, 9), (BF, 15), (BF, 515), (BF, 2051), (F, 3), (F, 7), (F, 257), (F, 4099)])
+def test_last_values_of_odd_rows(dt, D):
+    """Rows that no whole number of vectors makes, whose last lane may be another
+    wave's than the one before it (515 of eights, 257 of fours): against the oracle,
+    and in place bitwise as into new tensors."""
+    gen = _gen(D)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    B, T, tol = 3, 70, 2.0 ** -8 + 1e-5 if dt == BF else 1e-5
+    x, res, dy, dh = (r(B, T, D).to(dt) for _ in range(4))
+    w, b = (1 + 0.2 * r(D)).to(dt), r(D).to(dt)
+    y, h = P().layer_norm(x, w, b, residual=res)
+    g = P().layer_norm_backward(h, dy, w, dh=dh, need_db=True)
+    want, s = O.layer_norm(_np(x), _np(w), _np(b), _np(res))
+    assert O.rel2(_np(h), s) < tol
+    if D > 3:          # (of two or three values the deviation may be far below the values)
+        assert O.rel2(_np(y), want) < tol
+    x2, res2 = x.clone(), res.clone()
+    P().layer_norm(x2, w, b, residual=res2, y=x2, h=res2)
+    assert torch.equal(x2, y) and torch.equal(res2, h)
+    for into in range(3):
+        args = [h.clone(), dy.clone(), dh.clone()]
+        gi = P().layer_norm_backward(args[0], args[1], w, dh=args[2], need_db=True, dx=args[into])
+        assert torch.equal(args[into], g["dx"]) and torch.equal(gi["dw"], g["dw"]) and torch.equal(gi["db"], g["db"])
+    taps, hist = r(D, 4).to(dt), r(B, 3, D).to(dt)
+    u = P().short_conv(x, taps, hist=hist, activation="silu", hist_out=(last := torch.empty_like(hist)))
+    gc = P().short_conv_backward(x, taps, dy, hist=hist, activation="silu", need_dhist=True)
+    for k in range(B):
+        want, tail = O.short_conv(_np(x[k]), _np(taps), None, _np(hist[k]), "silu")
+        wc = O.short_conv_backward(_np(x[k]), _np(taps), _np(dy[k]), None, _np(hist[k]), "silu")
+        assert O.rel2(_np(u[k]), want) < tol and O.rel2(_np(last[k]), tail) == 0.0
+        assert O.rel2(_np(gc["dx"][k]), wc["dx"]) < tol and O.rel2(_np(gc["dhist"][k]), wc["dhist"]) < 1e-5
+    hist2 = hist.clone()
+    assert torch.equal(P().short_conv(x, taps, hist=hist2, activation="silu", hist_out=hist2), u)
+    assert torch.equal(hist2, last)
+    one = hist.clone()          # a token a call
+    steps = [P().short_conv(x[:, t:t + 1], taps, hist=one, activation="silu", hist_out=one) for t in range(5)]
+    assert torch.equal(torch.cat(steps, 1), u[:, :5])
