@@ -831,6 +831,18 @@ def _stream_of(device):
     return _raw_stream(device)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _launch(entry, device, *args):
+    """Calls a C entry with the device's stream, the tensors' device current (a
+    default stream is the current device's)."""
+    if device == _current_device():
+        return _check(entry(*args, _stream_of(device)))
+    with torch.cuda.device(device):
+        return _check(entry(*args, _stream_of(device)))
+
+
 def _size(workspace):
     return 0 if workspace is None else workspace.numel()
 
@@ -906,9 +918,9 @@ def layer_norm(x, w=None, b=None, residual=None, norm="layer", eps=1e-5, y=None,
         y, ys = x.new_empty(x.shape), flat
     else:
         ys = _row_steps(_out(x, y, "y"), "y", flat)
-    _check((_lib or lib()).prism_layer_norm(
+    _launch((_lib or lib()).prism_layer_norm, dev,
         _LN_DESC.pack(*desc, *rs, *ys, *hs), x.data_ptr(), _addr(residual), _addr(w), _addr(b),
-        y.data_ptr(), _addr(h), _stream_of(dev)))
+        y.data_ptr(), _addr(h))
     return y, h
 
 
@@ -938,9 +950,9 @@ def layer_norm_backward(x, dy, w=None, dh=None, norm="layer", eps=1e-5, need_db=
                            *_row_steps(out["dx"], "dx", flat))
     if workspace is None and len(out) > 1:
         workspace = _block_workspace("prism_layer_norm_backward_workspace", packed, (1,), x)
-    _check((_lib or lib()).prism_layer_norm_backward(
+    _launch((_lib or lib()).prism_layer_norm_backward, dev,
         packed, _addr(x), _addr(w), _addr(dy), _addr(dh), _addr(out["dx"]), _addr(out.get("dw")),
-        _addr(out.get("db")), _addr(workspace), _size(workspace), _stream_of(dev)))
+        _addr(out.get("db")), _addr(workspace), _size(workspace))
     return out
 
 
@@ -1009,9 +1021,9 @@ def short_conv(x, w, b=None, hist=None, activation="identity", cu_seqlens=None, 
         y, ys = x.new_empty(x.shape), flat
     else:
         ys = _token_steps(_out(x, y, "y"), "y", flat)
-    _check((_lib or lib()).prism_short_conv(
+    _launch((_lib or lib()).prism_short_conv, dev,
         _SC_DESC.pack(*desc, *ys, 0, 0, 0), x.data_ptr(), w.data_ptr(), _addr(b), _addr(hist),
-        _addr(cu_seqlens), y.data_ptr(), _addr(hist_out), _stream_of(dev)))
+        _addr(cu_seqlens), y.data_ptr(), _addr(hist_out))
     return y
 
 
@@ -1037,10 +1049,10 @@ def short_conv_backward(x, w, dy, b=None, hist=None, activation="identity", cu_s
     if workspace is None:
         workspace = _block_workspace("prism_short_conv_backward_workspace", packed,
                                      (int(cu_seqlens is not None),), x)
-    _check((_lib or lib()).prism_short_conv_backward(
+    _launch((_lib or lib()).prism_short_conv_backward, dev,
         packed, _addr(x), _addr(w), _addr(b), _addr(hist), _addr(cu_seqlens), _addr(dy),
         _addr(out["dx"]), _addr(out["dw"]), _addr(out.get("db")), _addr(out.get("dhist")),
-        _addr(workspace), _size(workspace), _stream_of(dev)))
+        _addr(workspace), _size(workspace))
     return out
 
 
@@ -1098,9 +1110,9 @@ def gated_recurrence(x, f, i=None, lam=None, h0=None, gate="sigmoid", cu_seqlens
     if workspace is None:
         workspace = _block_workspace("prism_gated_recurrence_workspace", packed,
                                      (int(cu_seqlens is not None), 0), x)
-    _check((_lib or lib()).prism_gated_recurrence(
+    _launch((_lib or lib()).prism_gated_recurrence, dev,
         packed, _addr(x), _addr(f), _addr(i), _addr(lam), _addr(h0), _addr(cu_seqlens), _addr(h),
-        _addr(hT), _addr(workspace), _size(workspace), _stream_of(dev)))
+        _addr(hT), _addr(workspace), _size(workspace))
     return h, hT
 
 
@@ -1134,11 +1146,10 @@ def gated_recurrence_backward(x, f, h, dh, i=None, lam=None, h0=None, dhT=None, 
     if workspace is None:
         workspace = _block_workspace("prism_gated_recurrence_workspace", packed,
                                      (int(cu_seqlens is not None), 1), x)
-    _check((_lib or lib()).prism_gated_recurrence_backward(
+    _launch((_lib or lib()).prism_gated_recurrence_backward, dev,
         packed, _addr(x), _addr(f), _addr(i), _addr(lam), _addr(h0), _addr(cu_seqlens), _addr(h),
         _addr(dh), _addr(dhT), _addr(out["dx"]), _addr(out["df"]), _addr(out.get("di")),
-        _addr(out.get("dlam")), _addr(out.get("dh0")), _addr(workspace), _size(workspace),
-        _stream_of(dev)))
+        _addr(out.get("dlam")), _addr(out.get("dh0")), _addr(workspace), _size(workspace))
     return out
 
 
@@ -1155,10 +1166,9 @@ def gated_recurrence_step(x, f, state, i=None, lam=None, gate="sigmoid", state_o
         h, hs = x.new_empty(x.shape), flat
     else:
         hs = _token_steps(_out(x, h, "h"), "h", flat)
-    _check((_lib or lib()).prism_gated_recurrence_step(
+    _launch((_lib or lib()).prism_gated_recurrence_step, dev,
         _GR_DESC.pack(*desc, *hs, *_NO_GRADS), x.data_ptr(), f.data_ptr(), _addr(i), _addr(lam),
-        state.data_ptr(), (state if state_out is None else state_out).data_ptr(), h.data_ptr(),
-        _stream_of(dev)))
+        state.data_ptr(), (state if state_out is None else state_out).data_ptr(), h.data_ptr())
     return h
 
 

@@ -313,3 +313,22 @@ def test_last_values_of_odd_rows(dt, D):
     one = hist.clone()          # a token a call
     steps = [P().short_conv(x[:, t:t + 1], taps, hist=one, activation="silu", hist_out=one) for t in range(5)]
     assert torch.equal(torch.cat(steps, 1), u[:, :5])
+
+
+def test_tensors_of_another_device_than_the_current(monkeypatch):
+    """The tensors' device is current around the launch, and the other one after it
+    (with one device here: the current one is said to be another)."""
+    entered = []
+
+    class device(torch.cuda.device):
+        def __init__(self, index):
+            entered.append(index)
+            super().__init__(index)
+
+    _, run = _block(BF, 2, 20, 64, 5)
+    want = run()
+    assert not entered
+    monkeypatch.setattr(P(), "_current_device", lambda: 1)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    _same(run(), want)
+    assert entered == [0] * 10          # (norm, convolution, three gates, forward and backward)
