@@ -444,7 +444,8 @@ typedef struct {
 
 /* Forward.  x, residual, y, h [B,T,H,D] dt, strided; w, b [D] dt or NULL (ones,
  * zeros).  residual may be NULL (s = x; h is then NULL too); h may be NULL (the
- * sum is not wanted).  y and h may each be x or residual, with its strides. */
+ * sum is not wanted).  y and h may each be x or residual, with its strides, but
+ * not each other. */
 prism_status prism_layer_norm(const prism_layer_norm_desc* desc, const void* x,
                               const void* residual, const void* w, const void* b, void* y, void* h,
                               hipStream_t stream);
@@ -556,7 +557,7 @@ prism_status prism_gated_recurrence_workspace(const prism_gated_recurrence_desc*
 /* Whole sequences.  x, f, i, h [B,T,D] ([N,D] with cu_seqlens) dt, strided; i may
  * be NULL; lam is NULL but with PRISM_GATE_POWER.  h0 [B,D] f32, the state before
  * the sequence, may be NULL (zeros); hT [B,D] f32, the state after it, may be NULL,
- * or h0 itself.  A sequence of no tokens gives hT = h0. */
+ * or h0 itself.  A sequence of no tokens gives hT = h0.  h overlaps no input. */
 prism_status prism_gated_recurrence(const prism_gated_recurrence_desc* desc, const void* x,
                                     const void* f, const void* i, const float* lam,
                                     const float* h0, const int* cu_seqlens, void* h, float* hT,
@@ -564,11 +565,11 @@ prism_status prism_gated_recurrence(const prism_gated_recurrence_desc* desc, con
 
 /* Gradients of <dh, h> + <dhT, hT> from the forward's inputs and its output h,
  * which is read as h_{t-1} (in bf16 as rounded: df and dlam then carry its
- * rounding, of at most 2^-9 of each h_{t-1}).  dhT [B,D] f32 may be NULL (zero).
+ * rounding, of at most 2^-8 of each h_{t-1}).  dhT [B,D] f32 may be NULL (zero).
  * dx, df, di dt, strided (di: NULL without i); dlam [D] f32, NULL but with
  * PRISM_GATE_POWER, summed in a fixed order; dh0 [B,D] f32 or NULL (not the buffer
  * of dhT or h0).  Where lam sigmoid(f) = 0 the root's infinite slope is taken as 0.
- * Written, not accumulated. */
+ * Written, not accumulated; no result overlaps an input or another result. */
 prism_status prism_gated_recurrence_backward(const prism_gated_recurrence_desc* desc,
                                              const void* x, const void* f, const void* i,
                                              const float* lam, const float* h0,

@@ -847,6 +847,13 @@ def _size(workspace):
     return 0 if workspace is None else workspace.numel()
 
 
+def _apart(out, name, *others):
+    """A result's buffer is none of the others'."""
+    for t in others:
+        if t is not None and t.data_ptr() == out.data_ptr() and out.numel() > 0:
+            raise ValueError(f"{name} must not share a buffer with another operand")
+
+
 def _vector(t, name, dtype, device, shape):
     """A small operand: type, device, shape, and contiguous."""
     _like(t, name, dtype, device, shape)
@@ -902,6 +909,8 @@ def layer_norm(x, w=None, b=None, residual=None, norm="layer", eps=1e-5, y=None,
     desc, flat = _norm_desc(x, norm, eps)
     dt, dev = x.dtype, x.get_device()
     _weights(w, b, dt, dev, desc[3])
+    if y is not None and h is not None:
+        _apart(y, "y", h)
     if dev < 0:
         _on_gpu(x)
     rs = hs = _NO_STEPS
@@ -1015,6 +1024,8 @@ def short_conv(x, w, b=None, hist=None, activation="identity", cu_seqlens=None, 
     dev = x.get_device()
     if hist_out is not None:
         _vector(hist_out, "hist_out", x.dtype, dev, (desc[0], desc[3] - 1, desc[2]))
+    if y is not None:
+        _apart(y, "y", x, hist, hist_out)
     if dev < 0:
         _on_gpu(x)
     if y is None:
@@ -1035,6 +1046,8 @@ def short_conv_backward(x, w, dy, b=None, hist=None, activation="identity", cu_s
     desc, flat = _conv_desc(x, w, b, hist, activation, cu_seqlens)
     dev = x.get_device()
     _like(dy, "dy", x.dtype, dev, x.shape)
+    if dx is not None:
+        _apart(dx, "dx", x, dy)
     if dev < 0:
         _on_gpu(x)
     B, K, D = desc[0], desc[3], desc[2]
@@ -1101,6 +1114,8 @@ def gated_recurrence(x, f, i=None, lam=None, h0=None, gate="sigmoid", cu_seqlens
         raise ValueError("hT given, but need_state is false")
     desc, state, flat = _rec_desc(x, f, i, lam, gate, (("h0", h0), ("hT", hT)), cu_seqlens)
     dev = x.get_device()
+    if h is not None:
+        _apart(h, "h", x, f, i)
     if dev < 0:
         _on_gpu(x)
     h = _out(x, h, "h")
@@ -1128,6 +1143,9 @@ def gated_recurrence_backward(x, f, h, dh, i=None, lam=None, h0=None, dhT=None, 
     _like(dh, "dh", dt, dev, x.shape)
     if di is not None and i is None:
         raise ValueError("di without i")
+    for name, t, others in (("dx", dx, (df, di)), ("df", df, (di,)), ("di", di, ())):
+        if t is not None:
+            _apart(t, name, x, f, i, h, dh, *others)
     if dev < 0:
         _on_gpu(x)
     out = {"dx": _out(x, dx, "dx"), "df": _out(x, df, "df")}
@@ -1160,6 +1178,8 @@ def gated_recurrence_step(x, f, state, i=None, lam=None, gate="sigmoid", state_o
     Returns h."""
     desc, _, flat = _rec_desc(x, f, i, lam, gate, (("state", state), ("state_out", state_out)), None)
     dev = x.get_device()
+    if h is not None:
+        _apart(h, "h", x, f, i)
     if dev < 0:
         _on_gpu(x)
     if h is None:

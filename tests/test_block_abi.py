@@ -276,3 +276,29 @@ def test_binding_gated_recurrence():
     _refused(ValueError, "dhT: expected shape", P.gated_recurrence_backward, x, x, x, x, dhT=h0[:1])
     _refused(ValueError, "state: expected shape", P.gated_recurrence_step, x, x, h0[:1])
     _refused(ValueError, "state_out: expected shape", P.gated_recurrence_step, x, x, h0, state_out=h0[:1])
+
+
+def test_binding_results_apart():
+    """A result in the place of an operand that is still read is refused by name."""
+    t = lambda *n: torch.zeros(*n, dtype=torch.bfloat16)
+    x, f, i, dh, h = (t(2, 3, 8) for _ in range(5))
+    w, hist = t(8, 4), t(2, 3, 8)
+
+    def refused(name, call, *a, **kw):
+        with pytest.raises(ValueError, match=f"{name} must not share"):
+            call(*a, **kw)
+
+    out = t(2, 3, 8)
+    refused("y", P.layer_norm, x, residual=f, y=out, h=out)
+    refused("y", P.short_conv, x, w, y=x)
+    refused("y", P.short_conv, x, w, hist=hist, y=hist)
+    for other in (x, f):
+        refused("dx", P.short_conv_backward, x, w, f, dx=other)
+        refused("h", P.gated_recurrence, x, f, h=other)
+    refused("h", P.gated_recurrence, x, f, i=i, h=i)
+    refused("h", P.gated_recurrence_step, x, f, torch.zeros(2, 8), h=x)
+    for other in (x, f, i, h, dh):
+        for name in ("dx", "df", "di"):
+            refused(name, P.gated_recurrence_backward, x, f, h, dh, i=i, **{name: other})
+    refused("dx", P.gated_recurrence_backward, x, f, h, dh, i=i, dx=out, df=out)
+    refused("df", P.gated_recurrence_backward, x, f, h, dh, i=i, df=out, di=out)
