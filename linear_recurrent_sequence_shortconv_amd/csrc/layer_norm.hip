@@ -13,10 +13,11 @@
 // deviation of rows far from zero).  The backward pass reads no statistics: it
 // forms them again from the row that it holds anyway.
 //
-// bf16, 2048 channels: 8 x 2048 rows with a residual and the sum 48 us, 5.6 TB/s;
-// backward, 16384 rows with dh 56 us with the sums of partials (4), 4.8 TB/s.  What is
-// left there: two workgroups' sums a row wait for one another, and registers for 16
-// values of three rows and of dw and db let 2 waves a SIMD hide them.
+// bf16, 2048 channels: 8 x 2048 rows with a residual and the sum 48 us, 5.6 TB/s,
+// without 26 us, 5.1 TB/s; backward, 16384 rows with dh 56 us with the sums of
+// partials (4), 4.8 TB/s.  What is left there: a row's two sums wait for its waves,
+// and registers for 16 values of three rows and of dw and db leave 2 waves a SIMD to
+// hide that.
 #include "block_ops.h"
 #include "vec_io.h"
 
@@ -64,10 +65,8 @@ __device__ inline long row_at(const Strides& s, long row, int T, int H) {
   return b * s.b + t * s.t + h * s.h;
 }
 
-// Lane `lane` of the team holds vectors lane + j G, j < NV, of V values.  With 8
-// values a lane a row of 2048 is a workgroup's: so few registers that 8 waves a
-// SIMD hide the loads (16 and 32 values a lane, with or without the next row on
-// its way: 50 to 52 us in place of 48 for 8 x 2048 rows of 2048 with a residual).
+// Lane `lane` of the team holds vectors lane + j G, j < NV, of V values; 8 waves a
+// SIMD hide the loads (the next row on its way as well gained nothing).
 // ODD: the row's last vector is no whole one, and begins before its place.
 template <typename E, int V, int NV, int NT, bool ODD, bool RES>
 __global__ __launch_bounds__(NT) void layer_norm_kernel(const LayerNormArgs a, int G) {
@@ -342,10 +341,20 @@ Shape shape_of(int n, int most, int block) {
   return s;
 }
 
-// Values a lane, forward and backward (where the weights' sums want few
-// workgroups with many rows each: 16 values 56 us, 8 values 62 for 16384 rows of
-// 2048, with 256 workgroups of 512 threads).
-constexpr int LN_LANE = 8, LN_LANE_BWD = 16;
+// Values a lane, forward: 16, for fewer waves that a row's sums wait for (bf16 rows
+// of 2048 without a residual, 8 x 2048 of them, 26 us in place of 31 with 8; 2048 of
+// 8192 14 in place of 17.5, with a residual 26 in place of 33), or 8, for more of them
+// on a SIMD, where a lane would hold twice the bytes and a row has few waves anyway
+// (bf16 with a residual below 4096, fp32 below 8192 values: 8 x 2048 rows of 2048 with
+// a residual 48 us, with 16 values 49.5; fp32 4096 rows of 2048 23.7 and 24.9).
+// Backward, where the weights' sums want few workgroups with many rows each, 16 (56 us,
+// 8 values 62 for 16384 rows of 2048, with 256 workgroups of 512 threads).
+constexpr int LN_LANE = 8, LN_LANE_WIDE = 16, LN_LANE_BWD = 16;
+template <typename E>
+int lane_of(const LayerNormArgs& a, bool bwd) {
+  if (bwd) return LN_LANE_BWD;
+  return a.D >= 8192 || (sizeof(E) == 2 && (!a.r || a.D >= 4096)) ? LN_LANE_WIDE : LN_LANE;
+}
 // Workgroups of the backward kernel, at most: one a CU, of 512 threads, where their
 // partials are wide (16384 rows of 2048: 56 us; two of 256 threads 58, 1024 rows of
 // 4096 18 and 21), two of 256 threads from 1024 channels (16384 rows of 1536 43 us; one
@@ -389,8 +398,8 @@ hipError_t run_bwd(const LayerNormArgs& a, const Shape& p, hipStream_t s) {
 // more than 1024 lanes, more)
 template <typename E, int V, int NV, bool ODD, bool BWD>
 hipError_t run_nv(const LayerNormArgs& a, const Shape& p, hipStream_t s) {
-  constexpr int most = BWD ? LN_LANE_BWD : LN_LANE;
-  if constexpr (NV * V >= most) {
+  constexpr int least = BWD ? LN_LANE_BWD : LN_LANE, most = BWD ? LN_LANE_BWD : LN_LANE_WIDE;
+  if constexpr (NV * V >= least) {
     if constexpr (BWD) {
       if (p.block > 512) return run_bwd<E, V, NV, 1024, ODD>(a, p, s);
       if (p.block > 256) return run_bwd<E, V, NV, 512, ODD>(a, p, s);
@@ -407,8 +416,7 @@ hipError_t run_nv(const LayerNormArgs& a, const Shape& p, hipStream_t s) {
 // (16384 values are at most 16 for each of 1024 lanes)
 template <typename E, int V, bool ODD, bool BWD>
 hipError_t run_v(const LayerNormArgs& a, hipStream_t s) {
-  const int lane = BWD ? LN_LANE_BWD : LN_LANE, n = (a.D + V - 1) / V;
-  Shape p = shape_of(n, lane / V, 256);
+  Shape p = shape_of((a.D + V - 1) / V, lane_of<E>(a, BWD) / V, 256);
   // (backward, workgroups of 512 threads for wide rows, where these leave more than two
   // rows a team: 4096 rows of 2048 21 us in place of 22, 16384 56 in place of 70)
   if (BWD && a.D >= 2048 && p.block == 256 && a.rows > 512L * (256 / p.G)) p.block = 512;
@@ -423,7 +431,7 @@ hipError_t run_v(const LayerNormArgs& a, hipStream_t s) {
 }
 // Vectors of 16 bytes, or single values of rows narrower than that (8 x 2048 rows of
 // 2048 in bf16 48 us by vectors, 86 by values, backward 56 and 95; 16384 rows of 1001
-// 17.5 and 27, backward 38 and 47).
+// 14 and 27, backward 38 and 47).
 template <typename E, bool BWD>
 hipError_t run(LayerNormArgs a, hipStream_t s) {
   merge_rows(a, BWD);
