@@ -950,18 +950,21 @@ def layer_norm_backward(x, dy, w=None, dh=None, norm="layer", eps=1e-5, need_db=
     _weights(w, None, dt, dev, desc[3])
     if dev < 0:
         _on_gpu(x)
-    out = {"dx": _out(x, dx, "dx")}
+    if dx is None:
+        dx, xs = x.new_empty(x.shape), flat
+    else:
+        xs = _row_steps(_out(x, dx, "dx"), "dx", flat)
+    out, dw, db = {"dx": dx}, None, None
     if w is not None:
-        out["dw"] = x.new_empty(x.shape[-1:], dtype=torch.float32)
+        dw = out["dw"] = x.new_empty(x.shape[-1:], dtype=torch.float32)
     if need_db:
-        out["db"] = x.new_empty(x.shape[-1:], dtype=torch.float32)
-    packed = _LN_DESC.pack(*desc, *hs, *_row_steps(dy, "dy", flat),
-                           *_row_steps(out["dx"], "dx", flat))
+        db = out["db"] = x.new_empty(x.shape[-1:], dtype=torch.float32)
+    packed = _LN_DESC.pack(*desc, *hs, *_row_steps(dy, "dy", flat), *xs)
     if workspace is None and len(out) > 1:
         workspace = _block_workspace("prism_layer_norm_backward_workspace", packed, (1,), x)
     _launch((_lib or lib()).prism_layer_norm_backward, dev,
-        packed, _addr(x), _addr(w), _addr(dy), _addr(dh), _addr(out["dx"]), _addr(out.get("dw")),
-        _addr(out.get("db")), _addr(workspace), _size(workspace))
+        packed, x.data_ptr(), _addr(w), dy.data_ptr(), _addr(dh), dx.data_ptr(), _addr(dw),
+        _addr(db), _addr(workspace), _size(workspace))
     return out
 
 
@@ -1052,20 +1055,24 @@ def short_conv_backward(x, w, dy, b=None, hist=None, activation="identity", cu_s
         _on_gpu(x)
     B, K, D = desc[0], desc[3], desc[2]
     f32 = torch.float32
-    out = {"dx": _out(x, dx, "dx"), "dw": x.new_empty((D, K), dtype=f32)}
+    if dx is None:
+        dx, xs = x.new_empty(x.shape), flat
+    else:
+        xs = _token_steps(_out(x, dx, "dx"), "dx", flat)
+    dw, db, dhist = x.new_empty((D, K), dtype=f32), None, None
+    out = {"dx": dx, "dw": dw}
     if b is not None:
-        out["db"] = x.new_empty((D,), dtype=f32)
+        db = out["db"] = x.new_empty((D,), dtype=f32)
     if need_dhist:
-        out["dhist"] = x.new_empty((B, K - 1, D), dtype=f32)
-    packed = _SC_DESC.pack(*desc, *_token_steps(dy, "dy", flat),
-                           *_token_steps(out["dx"], "dx", flat))
+        dhist = out["dhist"] = x.new_empty((B, K - 1, D), dtype=f32)
+    packed = _SC_DESC.pack(*desc, *_token_steps(dy, "dy", flat), *xs)
     if workspace is None:
         workspace = _block_workspace("prism_short_conv_backward_workspace", packed,
                                      (int(cu_seqlens is not None),), x)
     _launch((_lib or lib()).prism_short_conv_backward, dev,
-        packed, _addr(x), _addr(w), _addr(b), _addr(hist), _addr(cu_seqlens), _addr(dy),
-        _addr(out["dx"]), _addr(out["dw"]), _addr(out.get("db")), _addr(out.get("dhist")),
-        _addr(workspace), _size(workspace))
+        packed, x.data_ptr(), w.data_ptr(), _addr(b), _addr(hist), _addr(cu_seqlens),
+        dy.data_ptr(), dx.data_ptr(), dw.data_ptr(), _addr(db), _addr(dhist), _addr(workspace),
+        _size(workspace))
     return out
 
 
@@ -1118,16 +1125,19 @@ def gated_recurrence(x, f, i=None, lam=None, h0=None, gate="sigmoid", cu_seqlens
         _apart(h, "h", x, f, i)
     if dev < 0:
         _on_gpu(x)
-    h = _out(x, h, "h")
+    if h is None:
+        h, hs = x.new_empty(x.shape), flat
+    else:
+        hs = _token_steps(_out(x, h, "h"), "h", flat)
     if hT is None and need_state:
         hT = x.new_empty(state, dtype=torch.float32)
-    packed = _GR_DESC.pack(*desc, *_token_steps(h, "h", flat), *_NO_GRADS)
+    packed = _GR_DESC.pack(*desc, *hs, *_NO_GRADS)
     if workspace is None:
         workspace = _block_workspace("prism_gated_recurrence_workspace", packed,
                                      (int(cu_seqlens is not None), 0), x)
     _launch((_lib or lib()).prism_gated_recurrence, dev,
-        packed, _addr(x), _addr(f), _addr(i), _addr(lam), _addr(h0), _addr(cu_seqlens), _addr(h),
-        _addr(hT), _addr(workspace), _size(workspace))
+        packed, x.data_ptr(), f.data_ptr(), _addr(i), _addr(lam), _addr(h0), _addr(cu_seqlens),
+        h.data_ptr(), _addr(hT), _addr(workspace), _size(workspace))
     return h, hT
 
 
@@ -1148,26 +1158,30 @@ def gated_recurrence_backward(x, f, h, dh, i=None, lam=None, h0=None, dhT=None, 
             _apart(t, name, x, f, i, h, dh, *others)
     if dev < 0:
         _on_gpu(x)
-    out = {"dx": _out(x, dx, "dx"), "df": _out(x, df, "df")}
-    steps = (*_token_steps(h, "h", flat), *_token_steps(dh, "dh", flat),
-             *_token_steps(out["dx"], "dx", flat), *_token_steps(out["df"], "df", flat))
+    def result(t, name):
+        if t is None:
+            return x.new_empty(x.shape), flat
+        return t, _token_steps(_out(x, t, name), name, flat)
+
+    dx, xs = result(dx, "dx")
+    df, fs = result(df, "df")
+    out, dis, dlam, dh0 = {"dx": dx, "df": df}, _NO_STEPS, None, None
     if i is not None:
-        out["di"] = _out(x, di, "di")
-        steps += _token_steps(out["di"], "di", flat)
-    else:
-        steps += _NO_STEPS
+        di, dis = result(di, "di")
+        out["di"] = di
     if lam is not None:
-        out["dlam"] = torch.empty_like(lam)
+        dlam = out["dlam"] = torch.empty_like(lam)
     if need_dh0:
-        out["dh0"] = x.new_empty(state, dtype=torch.float32)
-    packed = _GR_DESC.pack(*desc, *steps)
+        dh0 = out["dh0"] = x.new_empty(state, dtype=torch.float32)
+    packed = _GR_DESC.pack(*desc, *_token_steps(h, "h", flat), *_token_steps(dh, "dh", flat), *xs,
+                           *fs, *dis)
     if workspace is None:
         workspace = _block_workspace("prism_gated_recurrence_workspace", packed,
                                      (int(cu_seqlens is not None), 1), x)
     _launch((_lib or lib()).prism_gated_recurrence_backward, dev,
-        packed, _addr(x), _addr(f), _addr(i), _addr(lam), _addr(h0), _addr(cu_seqlens), _addr(h),
-        _addr(dh), _addr(dhT), _addr(out["dx"]), _addr(out["df"]), _addr(out.get("di")),
-        _addr(out.get("dlam")), _addr(out.get("dh0")), _addr(workspace), _size(workspace))
+        packed, x.data_ptr(), f.data_ptr(), _addr(i), _addr(lam), _addr(h0), _addr(cu_seqlens),
+        h.data_ptr(), dh.data_ptr(), _addr(dhT), dx.data_ptr(), df.data_ptr(), _addr(di),
+        _addr(dlam), _addr(dh0), _addr(workspace), _size(workspace))
     return out
 
 
