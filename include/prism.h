@@ -526,9 +526,10 @@ prism_status prism_short_conv_backward(const prism_short_conv_desc* desc, const 
  *   PRISM_GATE_POWER    a = exp(-lam sigmoid(f)),    u = sqrt(1 - a^2) s x
  * lam [D] f32, >= 0.  f of PRISM_GATE_LOG is at most 0 in earnest; above it, the
  * product of the decays of any 128 tokens in a row has to stay within fp32.
- * Gates, state and sums are fp32 (1 - a and 1 - a^2 to their own size); h is
- * rounded once.  A value that is not finite may reach every later token of its
- * sequence and channel, never another's.
+ * Gates, state and sums are fp32 (1 - a and 1 - a^2 to their own size; of numbers
+ * below 2^-126, the forward pass may take 1 - a^2 and both may take sigmoid(f) as
+ * 0); h is rounded once.  A value that is not finite may reach every later token of
+ * its sequence and channel, never another's.
  *
  *   B, T, D    as in prism_short_conv_desc
  *   gate       a prism_gate value
@@ -568,7 +569,7 @@ prism_status prism_gated_recurrence(const prism_gated_recurrence_desc* desc, con
  * rounding, of at most 2^-8 of each h_{t-1}).  dhT [B,D] f32 may be NULL (zero).
  * dx, df, di dt, strided (di: NULL without i); dlam [D] f32, NULL but with
  * PRISM_GATE_POWER, summed in a fixed order; dh0 [B,D] f32 or NULL (not the buffer
- * of dhT or h0).  Where lam sigmoid(f) = 0 the root's infinite slope is taken as 0.
+ * of dhT or h0).  Where lam or sigmoid(f) is 0 the root's infinite slope is taken as 0.
  * Written, not accumulated; no result overlaps an input or another result. */
 prism_status prism_gated_recurrence_backward(const prism_gated_recurrence_desc* desc,
                                              const void* x, const void* f, const void* i,

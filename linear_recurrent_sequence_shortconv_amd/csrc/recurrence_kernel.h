@@ -82,9 +82,12 @@ __device__ inline void gate_inputs(float x, float f, float i, float lam, float& 
   if (INP) u *= gate_rcp<E>(1.f + gate_exp<E>(-i));
 }
 
+constexpr float NORMAL = 0x1p-126f;   // the smallest normal number
+
 // Gradients of a value's inputs from g, that of h_t, ag = a_t g and h_{t-1}; dl: its
-// part of the gradient of lam.  Where lam sigma(f) = 0 the root's slope is
-// infinite, and its part is left out.
+// part of the gradient of lam.  Where 1 - a^2 is below fp32's normal range (the
+// hardware takes no root of such numbers) the root's part is left out: it is
+// shut_gradients'.
 template <typename E, int G, bool INP>
 __device__ inline void gate_gradients(const GateValue& v, float x, float i, float lam, float before, float g, float ag,
                                       float& dx, float& df, float& di, float& dl) {
@@ -103,11 +106,11 @@ __device__ inline void gate_gradients(const GateValue& v, float x, float i, floa
     float slope;
     if constexpr (sizeof(E) == 2) {
       const float r = __builtin_amdgcn_rsqf(square);
-      c = square > 0.f ? square * r : square;
-      slope = square > 0.f ? v.a * r : 0.f;
+      c = square >= NORMAL ? square * r : square;
+      slope = square >= NORMAL ? v.a * r : 0.f;
     } else {
       c = sqrtf(square);
-      slope = c > 0.f ? v.a / c : 0.f;
+      slope = square >= NORMAL ? v.a / c : 0.f;
     }
     dl = -p * (ag * fmaf(-slope, xi, before));   // -p times the gradient of log a
     df = lam * other_side(v.k, p) * dl;
@@ -115,5 +118,28 @@ __device__ inline void gate_gradients(const GateValue& v, float x, float i, floa
   dx = g * c * s;
   di = INP ? dx * x * t : 0.f;
 }
+
+// Power gates that are nearly shut: 1 - a^2 = 2 lam sigma(f) below fp32's normal
+// range, though neither factor is 0.  Both are scaled by 2^64 by themselves, and the
+// root's slope, which can leave the range, meets its sigma(f) first.  dl: the root's
+// part alone.  Where a factor is 0 the slope is infinite, and its part is left out.
+template <typename E, bool INP>
+__device__ inline bool shut_gradients(const GateValue& v, float x, float i, float lam, float before, float g, float ag,
+                                      float& dx, float& df, float& di, float& dl) {
+  const float p = gate_rcp<E>(1.f + v.k);
+  if (!(2.f * lam * p < NORMAL && lam > 0.f && p > 0.f)) return false;
+  float s = 1.f, t = 0.f;
+  if (INP) sigmoid_pair<E>(i, s, t);
+  const float q = 0x1p64f * p, zs = 2.f * (0x1p64f * lam) * q;   // 2^128 (1 - a^2)
+  const float r = rsqrtf(zs);
+  dx = g * (0x1p-64f * (zs * r)) * s;
+  di = INP ? dx * x * t : 0.f;
+  dl = ag * (q * r * (INP ? s * x : x));                         // (a = 1)
+  df = lam * other_side(v.k, p) * (dl - p * (ag * before));
+  return true;
+}
+// Whether a channel may have such values, from the largest e^-f of its values that
+// is finite (with a factor of 2 to spare for roundings).
+__device__ inline bool nearly_shut(float lam, float k) { return lam > 0.f && 1.f + k >= lam / NORMAL; }
 
 }  // namespace prism

@@ -428,6 +428,20 @@ struct BackwardStrip {
   raw rx[R], ri[R], rb[R], rg[R];
   GateValue gv[R][V];
   float lam[V], dlam[V], h0[V], end[V];   // of the last sequence that starts here, of the last that ends
+  // (power gates) of the finite e^-f the largest, as bits with the exponent one
+  // higher, which puts infinities below all
+  int top[V];
+  static constexpr int ONE_UP = 1 << 23;
+
+  // Whether any value may be of a nearly shut gate.
+  __device__ inline bool shut() const {
+    bool any = false;
+    if constexpr (G == GATE_POWER) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) any = any || nearly_shut(lam[v], __int_as_float(top[v] - ONE_UP));
+    }
+    return __any(any);
+  }
 
   template <bool PLAIN, bool EVEN>
   __device__ inline void first_sweep(const RecurrenceArgs& a, const TileArgs& g, const Strip& s, int c, float (&A)[V],
@@ -466,11 +480,16 @@ struct BackwardStrip {
       }
     }
 #pragma unroll
+    for (int v = 0; v < V; ++v) top[v] = ONE_UP;
+#pragma unroll
     for (int k = R - 1; k >= 0; --k) {
       float f[V];
       IO::unpack(rf[k], f);
 #pragma unroll
-      for (int v = 0; v < V; ++v) gv[k][v] = gate_value<E, G>(f[v], lam[v]);
+      for (int v = 0; v < V; ++v) {
+        gv[k][v] = gate_value<E, G>(f[v], lam[v]);
+        if (G == GATE_POWER) top[v] = max(top[v], (int)(__float_as_uint(gv[k][v].k) + ONE_UP));
+      }
       if (!PLAIN && (s.last >> k & 1)) {
         if (k == l1) {
 #pragma unroll
@@ -493,7 +512,9 @@ struct BackwardStrip {
     }
   }
 
-  template <bool PLAIN, bool EVEN>
+  // SHUT: once more, for the values of nearly shut gates alone (apart from the
+  // sweep that all take, which keeps its registers, its time and its other results).
+  template <bool PLAIN, bool EVEN, bool SHUT>
   __device__ inline void second_sweep(const RecurrenceArgs& a, const TileArgs& g, const Strip& s, int c, bool on,
                                       float (&carry)[V]) {
     const int row = s.row + max(s.n - 1, 0);
@@ -534,10 +555,20 @@ struct BackwardStrip {
           const float gt = d[v] + carry[v];
           carry[v] = gv[k][v].a * gt;
           float dl;
+          if constexpr (SHUT) {
+            if (on && shut_gradients<E, INP>(gv[k][v], x[v], INP ? i[v] : 0.f, lam[v], b[v], gt, carry[v], dx[v], df[v],
+                                             di[v], dl)) {
+              dlam[v] += dl;
+              const_cast<E*>(px.p)[c + v] = (E)dx[v];
+              const_cast<E*>(pf.p)[c + v] = (E)df[v];
+              if (INP) const_cast<E*>(pi.p)[c + v] = (E)di[v];
+            }
+            continue;
+          }
           gate_gradients<E, G, INP>(gv[k][v], x[v], INP ? i[v] : 0.f, lam[v], b[v], gt, carry[v], dx[v], df[v], di[v], dl);
           if (G == GATE_POWER) dlam[v] += dl;
         }
-        if (PLAIN || on) {
+        if (!SHUT && (PLAIN || on)) {
           store_values<E, V>(px.p, c, dx);
           store_values<E, V>(pf.p, c, df);
           if (INP) store_values<E, V>(pi.p, c, di);
@@ -583,12 +614,17 @@ __global__ __launch_bounds__(W * WAVE, FAR ? WAVES_FAR : WAVES) void recurrence_
   bool open = false;
   if (wave == W - 1 && turn > 0) open = !(s.last >> (R - 1) & 1);
   enter_strip<V, W, FAR ? LOOK_FAR : LOOK>(g, tile, slice, -1, turn, open, W - 1 - wave, A, U, carry);
+  float again[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) again[v] = carry[v];
   if (plain)
-    strip.template second_sweep<true, true>(a, g, s, c, on, carry);
+    strip.template second_sweep<true, true, false>(a, g, s, c, on, carry);
   else if (even)
-    strip.template second_sweep<false, true>(a, g, s, c, on, carry);
+    strip.template second_sweep<false, true, false>(a, g, s, c, on, carry);
   else
-    strip.template second_sweep<false, false>(a, g, s, c, on, carry);
+    strip.template second_sweep<false, false, false>(a, g, s, c, on, carry);
+  if constexpr (G == GATE_POWER)
+    if (strip.shut()) strip.template second_sweep<false, false, true>(a, g, s, c, on, again);
   if constexpr (G == GATE_POWER) {   // the tile's part of dlam, wave after wave
     __shared__ float sm[W][V][WAVE];
 #pragma unroll
