@@ -94,7 +94,8 @@ hipError_t run_walk(const RecurrenceArgs& a, hipStream_t s) {
   return run_walk<E, V, GATE_POWER>(a, s);
 }
 
-// Workspace of a pass by tiles.  Words only where a tile goes on from another.
+// Workspace of a pass by tiles.  Words only where a tile goes on from another; the
+// counter's place is kept in any case, so that no pass writes anything else there.
 struct Plan {
   int tiles;
   bool words;
@@ -107,7 +108,7 @@ Plan plan_of(int B, int T, int D, int rows, bool packed, bool bwd, bool part) {
   p.words = p.tiles > 1 && (packed || tile % T != 0);
   const size_t wide = ((size_t)D + 127) / 128 * 128;   // (a slice has 64 or 128 channels)
   auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
-  p.first_at = p.words ? 256 : 0;
+  p.first_at = p.words || part ? 256 : 0;
   p.words_at = p.first_at + (p.words ? up((size_t)B * D * 4) : 0);
   p.part_at = p.words_at + (p.words ? up(wide * p.tiles * 8) : 0);
   p.bytes = p.part_at + (part ? up((size_t)p.tiles * D * 4) : 0);

@@ -27,6 +27,7 @@
 #pragma once
 
 #include "recurrence_kernel.h"
+#include "tile_place.h"
 
 namespace prism {
 
@@ -270,13 +271,13 @@ __device__ inline void enter_strip(const TileArgs& g, int tile, int slice, int s
 }
 
 // The workgroup's place in the order of tiles and slices.
-__device__ inline int take_tile(const TileArgs& g) {
-  if (!g.words) return blockIdx.x;
+__device__ inline TilePlace take_tile(const TileArgs& g) {
+  if (!g.words) return tile_place(blockIdx.x, g.tiles, g.slices);
   __shared__ unsigned taken;
   if (threadIdx.x == 0)
     taken = __hip_atomic_fetch_add(g.counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   __syncthreads();
-  return __builtin_amdgcn_readfirstlane(taken);
+  return tile_place(__builtin_amdgcn_readfirstlane(taken), g.tiles, g.slices);
 }
 
 // A lane's values of a state [B, D] (nullptr: zeros).
@@ -382,8 +383,9 @@ struct ForwardStrip {
 template <typename E, int V, int G, bool INP, int R, int W, bool FAR>
 __global__ __launch_bounds__(W * WAVE, FAR ? WAVES_FAR : WAVES) void recurrence_tile_kernel(const RecurrenceArgs a,
                                                                                            const TileArgs g) {
-  const int id = take_tile(g), tile = id / g.slices, slice = id - tile * g.slices;
-  if (tile >= g.tiles) return;   // (a counter that another call counts on too)
+  const TilePlace place = take_tile(g);
+  if (place.turn < 0) return;
+  const int tile = place.turn, slice = place.slice;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE), lane = threadIdx.x & (WAVE - 1);
   int c = (slice * WAVE + lane) * V;
   const bool on = c < a.D;
@@ -585,8 +587,9 @@ struct BackwardStrip {
 template <typename E, int V, int G, bool INP, int R, int W, bool FAR>
 __global__ __launch_bounds__(W * WAVE, FAR ? WAVES_FAR : WAVES) void recurrence_tile_bwd_kernel(
     const RecurrenceArgs a, const TileArgs g) {
-  const int id = take_tile(g), turn = id / g.slices, slice = id - turn * g.slices, tile = g.tiles - 1 - turn;
-  if (tile < 0) return;
+  const TilePlace place = take_tile(g);
+  if (place.turn < 0) return;
+  const int turn = place.turn, slice = place.slice, tile = g.tiles - 1 - turn;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE), lane = threadIdx.x & (WAVE - 1);
   int c = (slice * WAVE + lane) * V;
   const bool on = c < a.D;
