@@ -493,6 +493,7 @@ prism_status prism_gated_recurrence_step(const prism_gated_recurrence_desc* desc
     if (st != PRISM_OK) return st;
     const prism_gated_recurrence_desc& d = *desc;
     if ((st = check_rec_inputs(d, false, a.rows, x, f, i, lam, nullptr)) != PRISM_OK) return st;
+    CHECK_ELEM(lam, d.B > 0 && d.gate == PRISM_GATE_POWER, 4);   // (read without tokens too)
     CHECK_ELEM(state, d.B > 0, 4);
     CHECK_ELEM(state_out, d.B > 0, 4);
     CHECK_ELEM(h, a.rows > 0, size_of(d.dtype));
