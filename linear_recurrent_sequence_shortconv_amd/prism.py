@@ -259,6 +259,15 @@ def _workspace(nbytes, device):
     return ws, ws[off:]
 
 
+def _given(t, name, like):
+    """A buffer of the caller's, which the kernels write by its address and size:
+    on the tensors' device and without gaps or repeats."""
+    if t.device != like.device:
+        raise ValueError(f"{name}: expected device {like.device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
 def forward_workspace_bytes(desc):
     n = ctypes.c_size_t(0)
     _check(lib().prism_forward_workspace(ctypes.byref(desc), ctypes.byref(n)))
@@ -343,9 +352,12 @@ def forward(q, k, v, alpha, beta, Wk=None, Wp=None, wbeta=None, conv=None, S0=No
     o = torch.empty_like(v)
     ST = torch.empty((B, H, dv, dk), dtype=torch.float32, device=q.device)
     need = forward_workspace_bytes(desc) if saved is None else forward_train_workspace_bytes(desc)
+    if saved is not None:
+        _given(saved, "saved", q)
     if workspace is None:
         _, ws = _workspace(need, q.device)
     else:
+        _given(workspace, "workspace", q)
         ws = workspace
     stream = torch.cuda.current_stream(q.device).cuda_stream
     if saved is None:
@@ -412,9 +424,12 @@ def backward(q, k, v, alpha, beta, Wk=None, Wp=None, wbeta=None, conv=None, S0=N
     if need_dconv_hist:
         g["dconv_hist"] = torch.empty((B, 4, H, dv_), dtype=torch.float32, device=dev)
     need = backward_workspace_bytes(desc) if saved is None else backward_train_workspace_bytes(desc)
+    if saved is not None:
+        _given(saved, "saved", q)
     if workspace is None:
         _, ws = _workspace(need, dev)
     else:
+        _given(workspace, "workspace", q)
         ws = workspace
     stream = torch.cuda.current_stream(dev).cuda_stream
     grads = (_ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]), _ptr(g["dalpha"]), _ptr(g["dbeta"]),
@@ -465,6 +480,8 @@ def step(q, k, v, alpha, beta, Wk=None, Wp=None, wbeta=None, conv=None, S=None, 
         return o
     if workspace is None:
         _, workspace = _workspace(step_workspace_bytes(desc), q.device)
+    else:
+        _given(workspace, "workspace", q)
     _check(lib().prism_step(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(alpha),
                             _ptr(beta), _ptr(Wk), _ptr(Wp), _ptr(wbeta), _ptr(conv), _ptr(S),
                             _ptr(conv_state), _ptr(o), _ptr(workspace),
@@ -646,6 +663,8 @@ def qk_norm_backward(q, k, dq_out, dk_out, wq=None, wk=None, positions=None, tur
                 _qk_bytes.clear()
             size = _qk_bytes[packed] = n.value
         workspace = _workspace(size, q.device)[1]
+    elif workspace is not None:
+        _given(workspace, "workspace", q)
     _check(lib().prism_qk_norm_backward(
         packed, _addr(q), _addr(k), _addr(wq), _addr(wk), _addr(positions), _addr(turns),
         _addr(dq_out), _addr(dk_out), _addr(out["dq"]), _addr(out.get("dk")),
@@ -741,6 +760,8 @@ def linear_attention(q, k, v, g, S0=None, scale=1.0, cu_seqlens=None, max_seqlen
     packed = _LA_DESC.pack(*desc, *_steps(o, "o"), *gs)
     if workspace is None:
         workspace = _la_workspace(packed, cu_seqlens is not None, 0, 0, q.device)
+    else:
+        _given(workspace, "workspace", q)
     _check(lib().prism_linear_attention(
         packed, _addr(q), _addr(k), _addr(v), _addr(g), _addr(S0), _addr(cu_seqlens), _addr(o),
         _addr(ST), _addr(workspace), 0 if workspace is None else workspace.numel(),
@@ -766,6 +787,8 @@ def linear_attention_backward(q, k, v, g, dO, S0=None, dST=None, scale=1.0, need
         out["dS0"] = g.new_empty(state)
     if workspace is None:
         workspace = _la_workspace(packed, cu_seqlens is not None, 1, int(need_dg), q.device)
+    else:
+        _given(workspace, "workspace", q)
     _check(lib().prism_linear_attention_backward(
         packed, _addr(q), _addr(k), _addr(v), _addr(g), _addr(S0), _addr(cu_seqlens), _addr(dO),
         _addr(dST), _addr(out["dq"]), _addr(out["dk"]), _addr(out["dv"]), _addr(out.get("dg")),
@@ -948,6 +971,8 @@ def layer_norm_backward(x, dy, w=None, dh=None, norm="layer", eps=1e-5, need_db=
         _like(dh, "dh", dt, dev, x.shape)
         hs = _row_steps(dh, "dh", flat)
     _weights(w, None, dt, dev, desc[3])
+    if workspace is not None:
+        _given(workspace, "workspace", x)
     if dev < 0:
         _on_gpu(x)
     if dx is None:
@@ -1051,6 +1076,8 @@ def short_conv_backward(x, w, dy, b=None, hist=None, activation="identity", cu_s
     _like(dy, "dy", x.dtype, dev, x.shape)
     if dx is not None:
         _apart(dx, "dx", x, dy)
+    if workspace is not None:
+        _given(workspace, "workspace", x)
     if dev < 0:
         _on_gpu(x)
     B, K, D = desc[0], desc[3], desc[2]
@@ -1123,6 +1150,8 @@ def gated_recurrence(x, f, i=None, lam=None, h0=None, gate="sigmoid", cu_seqlens
     dev = x.get_device()
     if h is not None:
         _apart(h, "h", x, f, i)
+    if workspace is not None:
+        _given(workspace, "workspace", x)
     if dev < 0:
         _on_gpu(x)
     if h is None:
@@ -1156,6 +1185,8 @@ def gated_recurrence_backward(x, f, h, dh, i=None, lam=None, h0=None, dhT=None, 
     for name, t, others in (("dx", dx, (df, di)), ("df", df, (di,)), ("di", di, ())):
         if t is not None:
             _apart(t, name, x, f, i, h, dh, *others)
+    if workspace is not None:
+        _given(workspace, "workspace", x)
     if dev < 0:
         _on_gpu(x)
     def result(t, name):
