@@ -497,7 +497,8 @@ typedef struct {
  * multiplying x_{t-j}; b [D] dt or NULL; hist [B,K-1,D] dt, the tokens before the
  * sequence, oldest first, or NULL (zeros); hist_out (may be NULL) receives the
  * last K - 1 tokens for the next call, from hist or zeros where the sequence is
- * shorter, and may be hist itself.  y overlaps no input. */
+ * shorter, and may be hist itself.  Apart from that no result overlaps an input or
+ * the other result. */
 prism_status prism_short_conv(const prism_short_conv_desc* desc, const void* x, const void* w,
                               const void* b, const void* hist, const int* cu_seqlens, void* y,
                               void* hist_out, hipStream_t stream);
@@ -558,7 +559,8 @@ prism_status prism_gated_recurrence_workspace(const prism_gated_recurrence_desc*
 /* Whole sequences.  x, f, i, h [B,T,D] ([N,D] with cu_seqlens) dt, strided; i may
  * be NULL; lam is NULL but with PRISM_GATE_POWER.  h0 [B,D] f32, the state before
  * the sequence, may be NULL (zeros); hT [B,D] f32, the state after it, may be NULL,
- * or h0 itself.  A sequence of no tokens gives hT = h0.  h overlaps no input. */
+ * or h0 itself.  A sequence of no tokens gives hT = h0.  Apart from that no result
+ * overlaps an input or the other result. */
 prism_status prism_gated_recurrence(const prism_gated_recurrence_desc* desc, const void* x,
                                     const void* f, const void* i, const float* lam,
                                     const float* h0, const int* cu_seqlens, void* h, float* hT,
@@ -581,7 +583,7 @@ prism_status prism_gated_recurrence_backward(const prism_gated_recurrence_desc* 
 
 /* Token by token for the T tokens of each dense sequence (T = 1: a decode step):
  * state [B,D] f32 is read, the state after the tokens goes to state_out (state
- * itself: in place). */
+ * itself: in place).  Apart from that no result overlaps an input. */
 prism_status prism_gated_recurrence_step(const prism_gated_recurrence_desc* desc, const void* x,
                                          const void* f, const void* i, const float* lam,
                                          const float* state, float* state_out, void* h,

@@ -870,11 +870,55 @@ def _size(workspace):
     return 0 if workspace is None else workspace.numel()
 
 
+def _reach(t):
+    """A tensor's first address and the one behind its last."""
+    lo, size = t.data_ptr(), t.element_size()
+    if t.is_contiguous():
+        return lo, lo + size * t.numel()
+    return lo, lo + size * (1 + sum([(n - 1) * s for n, s in zip(t.shape, t.stride())]))
+
+
+class _Layout:
+    """A tensor's addresses as numpy looks at them (which reads none of them)."""
+
+    def __init__(self, t):
+        size = t.element_size()
+        self.__array_interface__ = {"version": 3, "shape": tuple(t.shape), "typestr": f"|V{size}",
+                                    "strides": tuple([s * size for s in t.stride()]),
+                                    "data": (t.data_ptr(), False)}
+
+
+def _overlap(a, b):
+    """Whether two tensors have an address in common (columns of one fused row, or
+    parts of a longer sequence, have none though they lie between one another)."""
+    (a0, a1), (b0, b1) = _reach(a), _reach(b)
+    if a1 <= b0 or b1 <= a0:
+        return False
+    import numpy
+    try:
+        return numpy.shares_memory(numpy.asarray(_Layout(a)), numpy.asarray(_Layout(b)), max_work=1 << 20)
+    except RuntimeError:       # (too many strides to tell)
+        return True
+
+
 def _apart(out, name, *others):
-    """A result's buffer is none of the others'."""
+    """A result has no address in common with the others."""
+    lo, hi = _reach(out)
     for t in others:
-        if t is not None and t.data_ptr() == out.data_ptr() and out.numel() > 0:
+        if t is not None and lo < hi and t.data_ptr() < hi and _overlap(out, t):
             raise ValueError(f"{name} must not share a buffer with another operand")
+
+
+def _in_place(out, name, *others):
+    """A result is in the very place of an operand, row by row, or apart from it."""
+    for t in others:
+        if t is None or t is out:
+            continue
+        if t.data_ptr() == out.data_ptr() and t.shape == out.shape and (
+                t.stride() == out.stride()
+                or all([n == 1 or a == b for n, a, b in zip(t.shape, t.stride(), out.stride())])):
+            continue
+        _apart(out, name, t)
 
 
 def _vector(t, name, dtype, device, shape):
@@ -932,8 +976,12 @@ def layer_norm(x, w=None, b=None, residual=None, norm="layer", eps=1e-5, y=None,
     desc, flat = _norm_desc(x, norm, eps)
     dt, dev = x.dtype, x.get_device()
     _weights(w, b, dt, dev, desc[3])
-    if y is not None and h is not None:
-        _apart(y, "y", h)
+    if y is not None:
+        _in_place(y, "y", x, residual)
+        _apart(y, "y", h, w, b)
+    if h is not None:
+        _in_place(h, "h", x, residual)
+        _apart(h, "h", w, b)
     if dev < 0:
         _on_gpu(x)
     rs = hs = _NO_STEPS
@@ -971,6 +1019,9 @@ def layer_norm_backward(x, dy, w=None, dh=None, norm="layer", eps=1e-5, need_db=
         _like(dh, "dh", dt, dev, x.shape)
         hs = _row_steps(dh, "dh", flat)
     _weights(w, None, dt, dev, desc[3])
+    if dx is not None:
+        _in_place(dx, "dx", x, dy, dh)
+        _apart(dx, "dx", w)
     if workspace is not None:
         _given(workspace, "workspace", x)
     if dev < 0:
@@ -1049,11 +1100,22 @@ def short_conv(x, w, b=None, hist=None, activation="identity", cu_seqlens=None, 
     last ones for the next call.  cu_seqlens (int32 [B+1]) packs sequences: x is
     [N,D].  y: where the result goes (a new tensor by default)."""
     desc, flat = _conv_desc(x, w, b, hist, activation, cu_seqlens)
-    dev = x.get_device()
+    dev, at, old, last = x.get_device(), x.data_ptr(), None, None
+    if hist is not None:
+        old = hist.data_ptr()
     if hist_out is not None:
-        _vector(hist_out, "hist_out", x.dtype, dev, (desc[0], desc[3] - 1, desc[2]))
+        B, T, D, K, code, _, N, sb, st, _ = desc
+        _vector(hist_out, "hist_out", x.dtype, dev, (B, K - 1, D))
+        value, last = 2 if code == PRISM_BF16 else 4, hist_out.data_ptr()
+        end = last + value * B * (K - 1) * D
+        # (by the addresses that either reaches at most: what a call for single tokens
+        # has time for)
+        if old is not None and old != last and 2 * last - end < old < end:
+            _apart(hist_out, "hist_out", hist)
+        if at < end and last < at + value * ((B - 1) * sb + ((N or T) - 1) * st + D):
+            _apart(hist_out, "hist_out", x)
     if y is not None:
-        _apart(y, "y", x, hist, hist_out)
+        _apart(y, "y", x, w, b, hist, hist_out, cu_seqlens)
     if dev < 0:
         _on_gpu(x)
     if y is None:
@@ -1061,8 +1123,8 @@ def short_conv(x, w, b=None, hist=None, activation="identity", cu_seqlens=None, 
     else:
         ys = _token_steps(_out(x, y, "y"), "y", flat)
     _launch((_lib or lib()).prism_short_conv, dev,
-        _SC_DESC.pack(*desc, *ys, 0, 0, 0), x.data_ptr(), w.data_ptr(), _addr(b), _addr(hist),
-        _addr(cu_seqlens), y.data_ptr(), _addr(hist_out))
+        _SC_DESC.pack(*desc, *ys, 0, 0, 0), at, w.data_ptr(), _addr(b), old,
+        _addr(cu_seqlens), y.data_ptr(), last)
     return y
 
 
@@ -1075,7 +1137,7 @@ def short_conv_backward(x, w, dy, b=None, hist=None, activation="identity", cu_s
     dev = x.get_device()
     _like(dy, "dy", x.dtype, dev, x.shape)
     if dx is not None:
-        _apart(dx, "dx", x, dy)
+        _apart(dx, "dx", x, dy, w, b, hist, cu_seqlens)
     if workspace is not None:
         _given(workspace, "workspace", x)
     if dev < 0:
@@ -1149,7 +1211,10 @@ def gated_recurrence(x, f, i=None, lam=None, h0=None, gate="sigmoid", cu_seqlens
     desc, state, flat = _rec_desc(x, f, i, lam, gate, (("h0", h0), ("hT", hT)), cu_seqlens)
     dev = x.get_device()
     if h is not None:
-        _apart(h, "h", x, f, i)
+        _apart(h, "h", x, f, i, lam, h0, hT, cu_seqlens)
+    if hT is not None:
+        _in_place(hT, "hT", h0)
+        _apart(hT, "hT", x, f, i, lam, cu_seqlens)
     if workspace is not None:
         _given(workspace, "workspace", x)
     if dev < 0:
@@ -1184,7 +1249,7 @@ def gated_recurrence_backward(x, f, h, dh, i=None, lam=None, h0=None, dhT=None, 
         raise ValueError("di without i")
     for name, t, others in (("dx", dx, (df, di)), ("df", df, (di,)), ("di", di, ())):
         if t is not None:
-            _apart(t, name, x, f, i, h, dh, *others)
+            _apart(t, name, x, f, i, h, dh, lam, h0, dhT, cu_seqlens, *others)
     if workspace is not None:
         _given(workspace, "workspace", x)
     if dev < 0:
@@ -1224,7 +1289,21 @@ def gated_recurrence_step(x, f, state, i=None, lam=None, gate="sigmoid", state_o
     desc, _, flat = _rec_desc(x, f, i, lam, gate, (("state", state), ("state_out", state_out)), None)
     dev = x.get_device()
     if h is not None:
-        _apart(h, "h", x, f, i)
+        _like(h, "h", x.dtype, dev, x.shape)
+        _apart(h, "h", x, f, i, lam)
+        # (one fp32 token's h is the state after it)
+        _in_place(h[:, 0] if h.shape[1] == 1 else h, "h", state, state_out)
+    B, T, D, code = desc[:4]
+    at = to = state.data_ptr()
+    if state_out is not None:
+        to = state_out.data_ptr()
+        if 0 < abs(to - at) < 4 * B * D:
+            _apart(state_out, "state_out", state)
+    if code != PRISM_BF16:             # (a state in the place of bf16 tokens is none)
+        for t, k in ((x, 6), (f, 9), (i, 12)):
+            if (t is not None and t.data_ptr() < to + 4 * B * D
+                    and to < t.data_ptr() + 4 * ((B - 1) * desc[k] + (T - 1) * desc[k + 1] + D)):
+                _apart(state if state_out is None else state_out, "the state", t)
     if dev < 0:
         _on_gpu(x)
     if h is None:
@@ -1233,7 +1312,7 @@ def gated_recurrence_step(x, f, state, i=None, lam=None, gate="sigmoid", state_o
         hs = _token_steps(_out(x, h, "h"), "h", flat)
     _launch((_lib or lib()).prism_gated_recurrence_step, dev,
         _GR_DESC.pack(*desc, *hs, *_NO_GRADS), x.data_ptr(), f.data_ptr(), _addr(i), _addr(lam),
-        state.data_ptr(), (state if state_out is None else state_out).data_ptr(), h.data_ptr())
+        at, to, h.data_ptr())
     return h
 
 
