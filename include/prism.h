@@ -432,8 +432,9 @@ prism_status prism_linear_attention_step(const prism_linear_attention_desc* desc
  *   norm       PRISM_NORM_LAYER or PRISM_NORM_RMS
  *   eps        finite and >= 0
  *   x, r, y, h strides; r: of the residual (backward: of dh), y: of y (backward:
- *              of dy), h: of h (backward: of dx).  Magnitude < 2^40; a result's
- *              are not 0 where there is more than one entry.                 */
+ *              of dy), h: of h (backward: of dx).  Magnitude < 2^40; of a
+ *              result's dimensions of more than one entry each steps over all
+ *              rows of those with smaller steps.                             */
 typedef struct {
   int B, T, H, D;
   prism_dtype dtype;

@@ -4,6 +4,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 #include <string>
 
 #include "api_common.h"
@@ -37,18 +38,29 @@ prism_status check_elem(const void* p, const char* name, bool required, int size
     if (st_ != PRISM_OK) return st_;                           \
   } while (0)
 
-// Steps of a tensor whose dimensions (batch, token, head) have n entries; of a
-// result, none that would put several rows in one place.
-prism_status check_steps(const prism_strides& s, const char* name, const long long (&n)[3], bool result) {
+// Steps of a tensor of rows of D values whose dimensions (batch, token, head) have n
+// entries; of a result, none that would put values of several rows in one place:
+// from the smallest to the largest, each step leaves the rows inside it behind.
+prism_status check_steps(const prism_strides& s, const char* name, const long long (&n)[3], int D, bool result) {
   const long long v[3] = {s.batch, s.token, s.head};
-  const bool some = n[0] && n[1] && n[2];
-  for (int k = 0; k < 3; ++k) {
-    if (v[k] >= (1LL << 40) || v[k] <= -(1LL << 40))
+  constexpr long long MOST = 1LL << 40;
+  for (int k = 0; k < 3; ++k)
+    if (v[k] >= MOST || v[k] <= -MOST)
       return fail(PRISM_ERR_SHAPE, std::string("strides of ") + name + " out of range");
-    if (result && some && n[k] > 1 && v[k] == 0)
+  if (!result || !n[0] || !n[1] || !n[2]) return PRISM_OK;
+  long long reach = D;   // of the rows inside a dimension (no step is beyond MOST)
+  bool taken[3] = {n[0] == 1, n[1] == 1, n[2] == 1};
+  while (true) {
+    int k = -1;
+    for (int m = 0; m < 3; ++m)
+      if (!taken[m] && (k < 0 || std::llabs(v[m]) < std::llabs(v[k]))) k = m;
+    if (k < 0) return PRISM_OK;
+    const long long step = std::llabs(v[k]);
+    if (step < reach)
       return fail(PRISM_ERR_SHAPE, std::string("strides of ") + name + " put several rows in one place");
+    reach = (n[k] - 1) >= MOST / step ? MOST : reach + step * (n[k] - 1);
+    taken[k] = true;
   }
-  return PRISM_OK;
 }
 
 prism_status check_dtype(prism_dtype t) {
@@ -110,10 +122,10 @@ prism_status ln_forward(const prism_layer_norm_desc* desc, const void* x, const 
   CHECK_ELEM(y, true, size);
   CHECK_ELEM(h, false, size);
   if (h && !residual) return fail(PRISM_ERR_NULL, "h without residual");
-  if ((st = check_steps(d.x, "x", n, false)) != PRISM_OK) return st;
-  if (residual && (st = check_steps(d.r, "residual", n, false)) != PRISM_OK) return st;
-  if ((st = check_steps(d.y, "y", n, true)) != PRISM_OK) return st;
-  if (h && (st = check_steps(d.h, "h", n, true)) != PRISM_OK) return st;
+  if ((st = check_steps(d.x, "x", n, d.D, false)) != PRISM_OK) return st;
+  if (residual && (st = check_steps(d.r, "residual", n, d.D, false)) != PRISM_OK) return st;
+  if ((st = check_steps(d.y, "y", n, d.D, true)) != PRISM_OK) return st;
+  if (h && (st = check_steps(d.h, "h", n, d.D, true)) != PRISM_OK) return st;
   prism::LayerNormArgs a = ln_args(d, x, w);
   a.r = residual;
   a.b = b;
@@ -139,10 +151,10 @@ prism_status ln_backward(const prism_layer_norm_desc* desc, const void* x, const
   CHECK_ELEM(dx, some, size);
   CHECK_ELEM(dw, false, 4);
   CHECK_ELEM(db, false, 4);
-  if ((st = check_steps(d.x, "x", n, false)) != PRISM_OK) return st;
-  if ((st = check_steps(d.y, "dy", n, false)) != PRISM_OK) return st;
-  if (dh && (st = check_steps(d.r, "dh", n, false)) != PRISM_OK) return st;
-  if ((st = check_steps(d.h, "dx", n, true)) != PRISM_OK) return st;
+  if ((st = check_steps(d.x, "x", n, d.D, false)) != PRISM_OK) return st;
+  if ((st = check_steps(d.y, "dy", n, d.D, false)) != PRISM_OK) return st;
+  if (dh && (st = check_steps(d.r, "dh", n, d.D, false)) != PRISM_OK) return st;
+  if ((st = check_steps(d.h, "dx", n, d.D, true)) != PRISM_OK) return st;
   if (!some && !dw && !db) return PRISM_OK;
   prism::LayerNormArgs a = ln_args(d, x, w);
   a.dy = dy;
@@ -176,10 +188,10 @@ prism_status check_batch(int B, int T, int D, prism_dtype dtype, int packed_toke
   return check_dtype(dtype);
 }
 
-prism_status check_token_steps(const prism_strides& s, const char* name, int B, int T, int rows, bool packed,
+prism_status check_token_steps(const prism_strides& s, const char* name, int B, int T, int D, int rows, bool packed,
                                bool result) {
   const long long n[3] = {packed ? 1 : B, packed ? rows : T, 1};
-  return check_steps(prism_strides{s.batch, s.token, 0}, name, n, result);
+  return check_steps(prism_strides{s.batch, s.token, 0}, name, n, D, result);
 }
 
 prism_status check_cu(const int* cu) {
@@ -225,8 +237,8 @@ prism_status conv_forward(const prism_short_conv_desc* desc, const void* x, cons
   CHECK_ELEM(y, some, size);
   CHECK_ELEM(hist_out, false, size);
   if ((st = check_cu(cu)) != PRISM_OK) return st;
-  if ((st = check_token_steps(d.x, "x", d.B, d.T, a.rows, packed, false)) != PRISM_OK) return st;
-  if ((st = check_token_steps(d.y, "y", d.B, d.T, a.rows, packed, true)) != PRISM_OK) return st;
+  if ((st = check_token_steps(d.x, "x", d.B, d.T, d.D, a.rows, packed, false)) != PRISM_OK) return st;
+  if ((st = check_token_steps(d.y, "y", d.B, d.T, d.D, a.rows, packed, true)) != PRISM_OK) return st;
   a.cu = cu;
   a.x = x;
   a.w = w;
@@ -261,9 +273,9 @@ prism_status conv_backward(const prism_short_conv_desc* desc, const void* x, con
   CHECK_ELEM(db, false, 4);
   CHECK_ELEM(dhist, false, 4);
   if ((st = check_cu(cu)) != PRISM_OK) return st;
-  if ((st = check_token_steps(d.x, "x", d.B, d.T, a.rows, packed, false)) != PRISM_OK) return st;
-  if ((st = check_token_steps(d.y, "dy", d.B, d.T, a.rows, packed, false)) != PRISM_OK) return st;
-  if ((st = check_token_steps(d.dx, "dx", d.B, d.T, a.rows, packed, true)) != PRISM_OK) return st;
+  if ((st = check_token_steps(d.x, "x", d.B, d.T, d.D, a.rows, packed, false)) != PRISM_OK) return st;
+  if ((st = check_token_steps(d.y, "dy", d.B, d.T, d.D, a.rows, packed, false)) != PRISM_OK) return st;
+  if ((st = check_token_steps(d.dx, "dx", d.B, d.T, d.D, a.rows, packed, true)) != PRISM_OK) return st;
   const size_t need = prism::short_conv_part_bytes(a.rows, d.D, d.K);
   if (need > 0 && (st = check_buffer(workspace, workspace_bytes, need, "workspace")) != PRISM_OK) return st;
   a.cu = cu;
@@ -321,9 +333,9 @@ prism_status check_rec_inputs(const prism_gated_recurrence_desc& d, bool packed,
   if (lam && d.gate != PRISM_GATE_POWER) return fail(PRISM_ERR_UNSUPPORTED, "lam goes with PRISM_GATE_POWER alone");
   CHECK_ELEM(h0, false, 4);
   prism_status st;
-  if ((st = check_token_steps(d.x, "x", d.B, d.T, rows, packed, false)) != PRISM_OK) return st;
-  if ((st = check_token_steps(d.f, "f", d.B, d.T, rows, packed, false)) != PRISM_OK) return st;
-  if (i && (st = check_token_steps(d.i, "i", d.B, d.T, rows, packed, false)) != PRISM_OK) return st;
+  if ((st = check_token_steps(d.x, "x", d.B, d.T, d.D, rows, packed, false)) != PRISM_OK) return st;
+  if ((st = check_token_steps(d.f, "f", d.B, d.T, d.D, rows, packed, false)) != PRISM_OK) return st;
+  if (i && (st = check_token_steps(d.i, "i", d.B, d.T, d.D, rows, packed, false)) != PRISM_OK) return st;
   return PRISM_OK;
 }
 
@@ -339,7 +351,7 @@ prism_status rec_forward(const prism_gated_recurrence_desc* desc, const void* x,
   CHECK_ELEM(h, a.rows > 0 && d.B > 0, size_of(d.dtype));
   CHECK_ELEM(hT, false, 4);
   if ((st = check_cu(cu)) != PRISM_OK) return st;
-  if ((st = check_token_steps(d.h, "h", d.B, d.T, a.rows, packed, true)) != PRISM_OK) return st;
+  if ((st = check_token_steps(d.h, "h", d.B, d.T, d.D, a.rows, packed, true)) != PRISM_OK) return st;
   a.cu = cu;
   a.x = x;
   a.f = f;
@@ -375,11 +387,11 @@ prism_status rec_backward(const prism_gated_recurrence_desc* desc, const void* x
   CHECK_ELEM(dlam, d.gate == PRISM_GATE_POWER, 4);
   CHECK_ELEM(dh0, false, 4);
   if ((st = check_cu(cu)) != PRISM_OK) return st;
-  if ((st = check_token_steps(d.h, "h", d.B, d.T, a.rows, packed, false)) != PRISM_OK) return st;
-  if ((st = check_token_steps(d.dh, "dh", d.B, d.T, a.rows, packed, false)) != PRISM_OK) return st;
-  if ((st = check_token_steps(d.dx, "dx", d.B, d.T, a.rows, packed, true)) != PRISM_OK) return st;
-  if ((st = check_token_steps(d.df, "df", d.B, d.T, a.rows, packed, true)) != PRISM_OK) return st;
-  if (i && (st = check_token_steps(d.di, "di", d.B, d.T, a.rows, packed, true)) != PRISM_OK) return st;
+  if ((st = check_token_steps(d.h, "h", d.B, d.T, d.D, a.rows, packed, false)) != PRISM_OK) return st;
+  if ((st = check_token_steps(d.dh, "dh", d.B, d.T, d.D, a.rows, packed, false)) != PRISM_OK) return st;
+  if ((st = check_token_steps(d.dx, "dx", d.B, d.T, d.D, a.rows, packed, true)) != PRISM_OK) return st;
+  if ((st = check_token_steps(d.df, "df", d.B, d.T, d.D, a.rows, packed, true)) != PRISM_OK) return st;
+  if (i && (st = check_token_steps(d.di, "di", d.B, d.T, d.D, a.rows, packed, true)) != PRISM_OK) return st;
   if (dh0 && (dh0 == dhT || dh0 == h0)) return fail(PRISM_ERR_UNSUPPORTED, "dh0 is the buffer of dhT or h0");
   const size_t need = prism::recurrence_bytes(a, packed, true);
   if (need > 0 && (st = check_buffer(workspace, workspace_bytes, need, "workspace")) != PRISM_OK) return st;
@@ -497,7 +509,7 @@ prism_status prism_gated_recurrence_step(const prism_gated_recurrence_desc* desc
     CHECK_ELEM(state, d.B > 0, 4);
     CHECK_ELEM(state_out, d.B > 0, 4);
     CHECK_ELEM(h, a.rows > 0, size_of(d.dtype));
-    if ((st = check_token_steps(d.h, "h", d.B, d.T, a.rows, false, true)) != PRISM_OK) return st;
+    if ((st = check_token_steps(d.h, "h", d.B, d.T, d.D, a.rows, false, true)) != PRISM_OK) return st;
     a.x = x;
     a.f = f;
     a.i = i;
