@@ -476,8 +476,8 @@ prism_status prism_layer_norm_backward(const prism_layer_norm_desc* desc, const 
  *   z_t sigmoid(z_t) (PRISM_ACT_SILU),
  * x_{-1}, x_{-2}, .. from hist.  The arithmetic is fp32, y rounded once.
  *
- *   B, T, D    sequences, tokens (each >= 0, B * T <= 2^30), channels (1 ..
- *              4194304; B * D < 2^31)
+ *   B, T, D    sequences, tokens (each >= 0, at most 2^30 tokens in all), channels
+ *              (1 .. 4194304); B * D < 2^31 and B * ceil(D / 256) < 2^23
  *   K          taps, 2 .. 4
  *   activation PRISM_ACT_IDENTITY or PRISM_ACT_SILU
  *   packed_tokens  with cu_seqlens: rows N of the token tensors (T is then not
@@ -533,7 +533,8 @@ prism_status prism_short_conv_backward(const prism_short_conv_desc* desc, const 
  * 0); h is rounded once.  A value that is not finite may reach every later token of
  * its sequence and channel, never another's.
  *
- *   B, T, D    as in prism_short_conv_desc
+ *   B, T, D    as in prism_short_conv_desc, and, of N tokens in all,
+ *              ceil(N / 64) * ceil(D / 64) <= 2^22
  *   gate       a prism_gate value
  *   packed_tokens  as in prism_short_conv_desc
  *   x, f, i, h strides (batch and token) of the inputs and of h; dh, dx, df, di:

@@ -23,8 +23,8 @@ std::string num(long long x) { return std::to_string(x); }
 Strides strides(const prism_strides& s) { return Strides{(long)s.batch, (long)s.token, (long)s.head}; }
 TokenSteps steps(const prism_strides& s) { return TokenSteps{(long)s.batch, (long)s.token}; }
 
-// Rows of a launch, and values of a token tensor.
-constexpr long long MOST_ROWS = 1LL << 30, MOST_VALUES = 1LL << 37;
+// Rows of a launch.
+constexpr long long MOST_ROWS = 1LL << 30;
 
 prism_status check_elem(const void* p, const char* name, bool required, int size) {
   if (!p) return required ? fail(PRISM_ERR_NULL, std::string(name) + " is NULL") : PRISM_OK;
@@ -181,10 +181,9 @@ prism_status check_batch(int B, int T, int D, prism_dtype dtype, int packed_toke
   if (packed && packed_tokens < 0) return fail(PRISM_ERR_SHAPE, "packed_tokens must be >= 0 with cu_seqlens");
   const long long rows = packed ? packed_tokens : (long long)B * T;
   if (rows > MOST_ROWS) return fail(PRISM_ERR_SHAPE, "a batch has at most " + num(MOST_ROWS) + " tokens");
-  // (a launch has under 2^32 threads: at most 512 for 64 rows of 64 channels, 256 for
-  // 256 channels of a sequence)
-  if (rows * D > MOST_VALUES || (rows + 63) / 64 * ((D + 63) / 64) > (1LL << 22) || (long long)B * D >= (1LL << 31) ||
-      B * ((D + 255LL) / 256) >= (1LL << 23)) return fail(PRISM_ERR_SHAPE, "problem too large");
+  // (a launch has under 2^32 threads, 256 for 256 channels of a sequence)
+  if ((long long)B * D >= (1LL << 31) || B * ((D + 255LL) / 256) >= (1LL << 23))
+    return fail(PRISM_ERR_SHAPE, "problem too large: B * D has to be below 2^31, B * ceil(D / 256) below 2^23");
   return check_dtype(dtype);
 }
 
@@ -302,6 +301,10 @@ prism_status check_rec(const prism_gated_recurrence_desc* desc, bool packed, pri
   if (st != PRISM_OK) return st;
   if (d.gate != PRISM_GATE_LOG && d.gate != PRISM_GATE_SIGMOID && d.gate != PRISM_GATE_POWER)
     return fail(PRISM_ERR_UNSUPPORTED, "gate must be PRISM_GATE_LOG, PRISM_GATE_SIGMOID or PRISM_GATE_POWER");
+  // (a tile of at least 64 rows and 64 channels is 512 threads)
+  const long long rows = packed ? d.packed_tokens : (long long)d.B * d.T;
+  if ((rows + 63) / 64 * ((d.D + 63) / 64) > (1LL << 22))
+    return fail(PRISM_ERR_SHAPE, "problem too large: ceil(tokens / 64) * ceil(D / 64) has to be at most 2^22");
   *a = prism::RecurrenceArgs{};
   a->B = d.B;
   a->T = d.T;

@@ -321,32 +321,35 @@ __global__ __launch_bounds__(SC_WAVES * WAVE, V == 4 ? 4 : 8) void short_conv_bw
 // Tokens a strip, fewer (to 4) where that leaves under two waves a SIMD.  (8 x 2048
 // tokens of 2048 channels, strips of 16, 32 and 64: 31, 28 and 31 us; backward,
 // where a strip also walks K - 1 rows twice on either side, 59, 53 and 51.)
+int parts_of(int rows, int S) { return (int)((rows + S * SC_WAVES - 1L) / (S * SC_WAVES)); }
+// (longer strips where a launch would have 2^32 threads)
+int launchable(int rows, int D, int S) {
+  while ((D + 255L) / 256 * parts_of(rows, S) >= (1L << 23)) S *= 2;
+  return S;
+}
 int strip_tokens(int rows, int D, int S) {
   const long waves = (D + 255) / 256;
   while (S > 4 && (rows + S - 1L) / S * waves < 2048) S /= 2;
-  return S;
+  return launchable(rows, D, S);
 }
-int parts_of(int rows, int S) { return (int)((rows + S * SC_WAVES - 1L) / (S * SC_WAVES)); }
 
 // Workgroups for sequences that may be empty and have a result all the same.
 int empties(const ShortConvArgs& a, const void* result) {
   return result && result != a.hist && (a.cu || a.T == 0) ? a.B : 0;
 }
 
-// (a dense sequence of at most 8 tokens is a strip of its own, with others where
-// a launch would have 2^32 threads)
+// (a dense sequence of at most 8 tokens is a strip of its own)
 template <typename E, int V, int K>
 hipError_t run_fwd(const ShortConvArgs& a, hipStream_t s) {
-  const long cw = (a.D + WAVE * V - 1) / (WAVE * V);
-  int S = !a.cu && a.T <= 8 && a.T > 0 ? a.T : strip_tokens(a.rows, a.D, SC_STRIP);
-  while (cw * parts_of(a.rows, S) >= (1L << 23)) S *= 2;
-  const int strips = (int)(cw * parts_of(a.rows, S));
+  const int cw = (a.D + WAVE * V - 1) / (WAVE * V);
+  const int S = !a.cu && a.T <= 8 && a.T > 0 ? launchable(a.rows, a.D, a.T) : strip_tokens(a.rows, a.D, SC_STRIP);
+  const int strips = cw * parts_of(a.rows, S);
   const dim3 grid((unsigned)strips + empties(a, a.hist_out));
   if (grid.x == 0) return hipSuccess;
   if (a.silu)
-    hipLaunchKernelGGL((short_conv_kernel<E, V, K, true>), grid, dim3(SC_WAVES * WAVE), 0, s, a, (int)cw, S, strips);
+    hipLaunchKernelGGL((short_conv_kernel<E, V, K, true>), grid, dim3(SC_WAVES * WAVE), 0, s, a, cw, S, strips);
   else
-    hipLaunchKernelGGL((short_conv_kernel<E, V, K, false>), grid, dim3(SC_WAVES * WAVE), 0, s, a, (int)cw, S, strips);
+    hipLaunchKernelGGL((short_conv_kernel<E, V, K, false>), grid, dim3(SC_WAVES * WAVE), 0, s, a, cw, S, strips);
   return hipGetLastError();
 }
 template <typename E, int V, int K>
