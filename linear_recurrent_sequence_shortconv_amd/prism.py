@@ -1286,23 +1286,22 @@ def gated_recurrence_step(x, f, state, i=None, lam=None, gate="sigmoid", state_o
     fp32 [B,D] (prism_gated_recurrence_step; T = 1: a decode step).  The state
     after them goes to state_out, or into state itself when that is None.
     Returns h."""
-    desc, _, flat = _rec_desc(x, f, i, lam, gate, (("state", state), ("state_out", state_out)), None)
+    desc, (B, D), flat = _rec_desc(x, f, i, lam, gate, (("state", state), ("state_out", state_out)), None)
     dev = x.get_device()
     if h is not None:
         _like(h, "h", x.dtype, dev, x.shape)
         _apart(h, "h", x, f, i, lam)
         # (one fp32 token's h is the state after it)
         _in_place(h[:, 0] if h.shape[1] == 1 else h, "h", state, state_out)
-    B, T, D, code = desc[:4]
     at = to = state.data_ptr()
     if state_out is not None:
         to = state_out.data_ptr()
-        if 0 < abs(to - at) < 4 * B * D:
+        if at != to and at - 4 * B * D < to < at + 4 * B * D:
             _apart(state_out, "state_out", state)
-    if code != PRISM_BF16:             # (a state in the place of bf16 tokens is none)
+    if desc[3] != PRISM_BF16:          # (a state in the place of bf16 tokens is none)
         for t, k in ((x, 6), (f, 9), (i, 12)):
             if (t is not None and t.data_ptr() < to + 4 * B * D
-                    and to < t.data_ptr() + 4 * ((B - 1) * desc[k] + (T - 1) * desc[k + 1] + D)):
+                    and to < t.data_ptr() + 4 * ((B - 1) * desc[k] + (desc[1] - 1) * desc[k + 1] + D)):
                 _apart(state if state_out is None else state_out, "the state", t)
     if dev < 0:
         _on_gpu(x)
