@@ -421,8 +421,9 @@ prism_status prism_linear_attention_step(const prism_linear_attention_desc* desc
  *   s = x + residual,  m = mean(s)           (PRISM_NORM_RMS: m = 0)
  *   r = (mean((s - m)^2) + eps)^(-1/2),  y = (s - m) r w + b,  h = s.
  * The arithmetic is fp32; y is formed from the sum before it is rounded to the
- * storage type, which h then is.  Squares of deviations have to be within
- * fp32's range (deviations below about 2^60).
+ * storage type, which h then is.  The sum of a row's squared deviations has to be
+ * within fp32's normal range: deviations below about 2^62 / sqrt(D), and, where eps
+ * does not cover them, above about 2^-62.
  *
  * In this section and the following two, token tensors start at any multiple of
  * their element's size, and so do their rows; 16-byte rows are read faster.
