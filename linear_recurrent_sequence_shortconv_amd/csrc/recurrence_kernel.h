@@ -87,10 +87,10 @@ constexpr float NORMAL = 0x1p-126f;   // the smallest normal number
 // Gradients of a value's inputs from g, that of h_t, ag = a_t g and h_{t-1}; dl: its
 // part of the gradient of lam.  Where 1 - a^2 is below fp32's normal range (the
 // hardware takes no root of such numbers) the root's part is left out: it is
-// shut_gradients'.
+// shut_gradients'; `low` then becomes true.
 template <typename E, int G, bool INP>
 __device__ inline void gate_gradients(const GateValue& v, float x, float i, float lam, float before, float g, float ag,
-                                      float& dx, float& df, float& di, float& dl) {
+                                      float& dx, float& df, float& di, float& dl, bool& low) {
   float s = 1.f, t = 0.f, c = 1.f;
   if (INP) sigmoid_pair<E>(i, s, t);
   const float xi = INP ? s * x : x;
@@ -103,14 +103,16 @@ __device__ inline void gate_gradients(const GateValue& v, float x, float i, floa
   } else {
     const float p = gate_rcp<E>(1.f + v.k);
     const float square = one_minus_exp(2.f * lam * p, v.a * v.a);
+    const bool normal = square >= NORMAL;
+    low = low || !normal;
     float slope;
     if constexpr (sizeof(E) == 2) {
       const float r = __builtin_amdgcn_rsqf(square);
-      c = square >= NORMAL ? square * r : square;
-      slope = square >= NORMAL ? v.a * r : 0.f;
+      c = normal ? square * r : square;
+      slope = normal ? v.a * r : 0.f;
     } else {
       c = sqrtf(square);
-      slope = square >= NORMAL ? v.a / c : 0.f;
+      slope = normal ? v.a / c : 0.f;
     }
     dl = -p * (ag * fmaf(-slope, xi, before));   // -p times the gradient of log a
     df = lam * other_side(v.k, p) * dl;
@@ -120,14 +122,16 @@ __device__ inline void gate_gradients(const GateValue& v, float x, float i, floa
 }
 
 // Power gates that are nearly shut: 1 - a^2 = 2 lam sigma(f) below fp32's normal
-// range, though neither factor is 0.  Both are scaled by 2^64 by themselves, and the
-// root's slope, which can leave the range, meets its sigma(f) first.  dl: the root's
+// range, though neither factor is 0.
+__device__ inline bool nearly_shut(float lam, float p) { return 2.f * lam * p < NORMAL && lam > 0.f && p > 0.f; }
+// Their gradients.  Both factors are scaled by 2^64 by themselves, and the root's slope,
+// which can leave the range, meets its sigma(f) first.  dl: the root's
 // part alone.  Where a factor is 0 the slope is infinite, and its part is left out.
 template <typename E, bool INP>
 __device__ inline bool shut_gradients(const GateValue& v, float x, float i, float lam, float before, float g, float ag,
                                       float& dx, float& df, float& di, float& dl) {
   const float p = gate_rcp<E>(1.f + v.k);
-  if (!(2.f * lam * p < NORMAL && lam > 0.f && p > 0.f)) return false;
+  if (!nearly_shut(lam, p)) return false;
   float s = 1.f, t = 0.f;
   if (INP) sigmoid_pair<E>(i, s, t);
   const float q = 0x1p64f * p, zs = 2.f * (0x1p64f * lam) * q;   // 2^128 (1 - a^2)
@@ -138,8 +142,4 @@ __device__ inline bool shut_gradients(const GateValue& v, float x, float i, floa
   df = lam * other_side(v.k, p) * (dl - p * (ag * before));
   return true;
 }
-// Whether a channel may have such values, from the largest e^-f of its values that
-// is finite (with a factor of 2 to spare for roundings).
-__device__ inline bool nearly_shut(float lam, float k) { return lam > 0.f && 1.f + k >= lam / NORMAL; }
-
 }  // namespace prism

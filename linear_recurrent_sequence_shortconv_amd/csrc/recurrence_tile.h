@@ -430,18 +430,17 @@ struct BackwardStrip {
   raw rx[R], ri[R], rb[R], rg[R];
   GateValue gv[R][V];
   float lam[V], dlam[V], h0[V], end[V];   // of the last sequence that starts here, of the last that ends
-  // (power gates) of the finite e^-f the largest, as bits with the exponent one
-  // higher, which puts infinities below all
-  int top[V];
-  static constexpr int ONE_UP = 1 << 23;
+  bool low;   // (power gates) whether 1 - a^2 of a value is below the normal numbers
 
-  // Whether any value may be of a nearly shut gate.
+  // Whether one of them is of a nearly shut gate: neither shut altogether, as gates of
+  // padding may be, nor of a rate of 0.
   __device__ inline bool shut() const {
+    if (!__any(low)) return false;
     bool any = false;
-    if constexpr (G == GATE_POWER) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) any = any || nearly_shut(lam[v], __int_as_float(top[v] - ONE_UP));
-    }
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+      for (int v = 0; v < V; ++v) any = any || nearly_shut(lam[v], gate_rcp<E>(1.f + gv[k][v].k));
     return __any(any);
   }
 
@@ -482,16 +481,11 @@ struct BackwardStrip {
       }
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) top[v] = ONE_UP;
-#pragma unroll
     for (int k = R - 1; k >= 0; --k) {
       float f[V];
       IO::unpack(rf[k], f);
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        gv[k][v] = gate_value<E, G>(f[v], lam[v]);
-        if (G == GATE_POWER) top[v] = max(top[v], (int)(__float_as_uint(gv[k][v].k) + ONE_UP));
-      }
+      for (int v = 0; v < V; ++v) gv[k][v] = gate_value<E, G>(f[v], lam[v]);
       if (!PLAIN && (s.last >> k & 1)) {
         if (k == l1) {
 #pragma unroll
@@ -567,7 +561,8 @@ struct BackwardStrip {
             }
             continue;
           }
-          gate_gradients<E, G, INP>(gv[k][v], x[v], INP ? i[v] : 0.f, lam[v], b[v], gt, carry[v], dx[v], df[v], di[v], dl);
+          gate_gradients<E, G, INP>(gv[k][v], x[v], INP ? i[v] : 0.f, lam[v], b[v], gt, carry[v], dx[v], df[v], di[v], dl,
+                                    low);
           if (G == GATE_POWER) dlam[v] += dl;
         }
         if (!SHUT && (PLAIN || on)) {
@@ -595,6 +590,7 @@ __global__ __launch_bounds__(W * WAVE, FAR ? WAVES_FAR : WAVES) void recurrence_
   const bool on = c < a.D;
   if (!on) c = 0;
   BackwardStrip<E, V, G, INP, R> strip;
+  strip.low = false;
 #pragma unroll
   for (int v = 0; v < V; ++v) strip.lam[v] = G == GATE_POWER ? a.lam[c + v] : 0.f;   // (loads return in order)
   const Strip s = strip_of<R>(a, tile * (R * W) + wave * R);
