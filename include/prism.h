@@ -23,8 +23,9 @@
  * Conventions common to every entry point
  * ---------------------------------------
  * - All tensor pointers are DEVICE pointers, contiguous, row-major, 16-byte
- *   aligned (the later sections name what they take beside that).  The caller owns every buffer, including the workspace.  The
- *   library allocates no device memory and keeps no pointer after a call.
+ *   aligned (the later sections name what they take beside that).  The caller
+ *   owns every buffer, including the workspace.  The library allocates no
+ *   device memory and keeps no pointer after a call.
  * - Work is enqueued asynchronously on `stream`; nothing synchronises the
  *   host.  Buffers must stay alive until the stream has finished the work.
  * - Every argument is validated on the host before any HIP call; a failed
@@ -32,7 +33,9 @@
  *   prism_last_error() then returns a message naming the argument.
  * - NaN / Inf inputs are not checked; they propagate.
  * - Results are deterministic: the same inputs and descriptor give bitwise
- *   identical outputs (no atomics; all reductions in a fixed order).
+ *   identical outputs (all reductions in a fixed order; atomics only where
+ *   the gated recurrence's tiles take their places and pass their states on,
+ *   which changes no order of operations).
  * - Functions are thread-safe except while kernel timing is enabled
  *   (prism_timing_begin .. prism_timing_end).
  */
@@ -532,7 +535,8 @@ prism_status prism_short_conv_backward(const prism_short_conv_desc* desc, const 
  * Gates, state and sums are fp32 (1 - a and 1 - a^2 to their own size; of numbers
  * below 2^-126, the forward pass may take 1 - a^2 and both may take sigmoid(f) as
  * 0); h is rounded once.  A value that is not finite may reach every later token of
- * its sequence and channel, never another's.
+ * its sequence and channel, never another's, or be forgotten where the decays since
+ * then multiply to 0 in fp32.
  *
  *   B, T, D    as in prism_short_conv_desc, and, of N tokens in all,
  *              ceil(N / 64) * ceil(D / 64) <= 2^22

@@ -3,7 +3,8 @@
 ``forward`` and ``backward`` are thin bindings over ``libprism.so``, as are
 ``qk_norm`` (queries and keys normalised and rotated) and ``linear_attention``
 (with a decay for each head), and ``layer_norm``, ``short_conv`` and
-``gated_recurrence``, with their backward passes and decode steps; the submodule ``workloads`` draws seeded synthetic inputs.  The binding is loaded
+``gated_recurrence``, with their backward passes and decode steps; the
+submodule ``workloads`` draws seeded synthetic inputs.  The binding is loaded
 lazily so that ``workloads`` imports without touching the GPU runtime.
 """
 

@@ -8,7 +8,8 @@
 //
 // Memory bound: every row is read once and written once.  A row stays in the
 // registers of a group of lanes, of a wave, or of a workgroup of up to 16
-// waves, so that mean and deviation are two sums one after the other over the
+// waves (but for 8 to 9 of 128 registers a lane in bf16, with dh, and 5 to 23 in
+// fp32, which the backward pass of more than 8192 values spills), so that mean and deviation are two sums one after the other over the
 // values themselves (the sum of squares less the squared mean would lose the
 // deviation of rows far from zero).  The backward pass reads no statistics: it
 // forms them again from the row that it holds anyway.
@@ -17,7 +18,12 @@
 // without 26 us, 5.1 TB/s; backward, 16384 rows with dh 56 us with the sums of
 // partials (4), 4.8 TB/s.  What is left there: a row's two sums wait for its waves,
 // and registers for 16 values of three rows and of dw and db leave 2 waves a SIMD to
-// hide that.
+// hide that.  fp32, 8192 rows of 2048 with dh: backward 52 us, 5.2 TB/s.
+//
+// Errors of fp32 results against 64 bits (2-norms): y 5e-8 to 6e-8 and dx 6e-8 to 7e-8,
+// as elementary operations in fp32 have them; dw and db, where a lane adds a
+// workgroup's rows one after the other, 1.4e-7 to 1.7e-7 (elementary sums: 0.9e-7 of
+// 4995 rows of 48, 1.5e-7 and 1.9e-7 of 4096 and 16384 rows of 2048 and 1000).
 #include "block_ops.h"
 #include "vec_io.h"
 

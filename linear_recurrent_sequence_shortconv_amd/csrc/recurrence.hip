@@ -157,8 +157,8 @@ hipError_t run_tiles(RecurrenceArgs a, bool bwd, char* ws, hipStream_t s) {
 }
 
 // bf16 channels two a lane where every row starts at a multiple of 4 bytes (one
-// sequence of 16384 tokens of 2048 channels 69 us with two, 76 with one; backward of
-// 8 x 2048 tokens 134 and 138).
+// sequence of 16384 tokens of 2048 channels 68 us with two, 77 with one; backward of
+// 8 x 2048 tokens 129 and 144).
 bool pairs(const RecurrenceArgs& a, bool bwd) {
   long m = a.D | a.sx.b | a.sx.t | a.sf.b | a.sf.t | a.sh.b | a.sh.t;
   uintptr_t p = (uintptr_t)a.x | (uintptr_t)a.f | (uintptr_t)a.i | (uintptr_t)a.h;

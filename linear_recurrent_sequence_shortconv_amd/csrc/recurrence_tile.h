@@ -21,7 +21,9 @@
 // reverse, its state the gradient a_t g_t that a token hands to the one before.
 //
 // bf16, gates by power with an input gate, 2048 channels: one sequence of 16384 tokens
-// 69 us, 3.9 TB/s, backward of 8 x 2048 tokens 134 us, 4.0 TB/s.  In the middle of a
+// 66 us, 4.0 TB/s, backward of 8 x 2048 tokens 129 us, 4.2 TB/s.  fp32, 8 x 1024 tokens:
+// 72 us, 3.7 TB/s, bound by the vector units (99 instructions a value for the bf16
+// kernel's 33, in three quarters of the cycles).  In the middle of a
 // launch tiles move 4.7 to 4.9 TB/s; the rest is the kernel that readies the words
 // (5 us), the first workgroups, which load before any computes, and the last.
 #pragma once
@@ -643,7 +645,9 @@ __global__ __launch_bounds__(W * WAVE, FAR ? WAVES_FAR : WAVES) void recurrence_
 
 // (16384 tokens of 256 channels 35 us without looking far, 22 with, backward 66 and
 // 38; of 2048 channels 71 without, 88 with; 64 sequences of up to 200 tokens,
-// backward, 408 tiles, 19 without, 22 with)
+// backward, 408 tiles, 19 without, 22 with.  A packed batch goes by the average of its
+// sequences, since the host does not read the offsets: one long sequence among many
+// short ones looks near.)
 template <typename E, int V, int G, bool INP, bool FAR>
 hipError_t launch_tiles(const RecurrenceArgs& a, const TileArgs& g, bool bwd, hipStream_t s) {
   const dim3 grid((unsigned)g.tiles * g.slices);

@@ -10,8 +10,8 @@
 // each value is read once but for the K - 1 rows in front of a strip (backward:
 // behind it too), which the wave next to it reads at the same time.  The rows
 // before the current one, and in the backward pass the g before it, stay in
-// registers.  bf16, K = 4, silu, 8 x 2048 tokens of 2048 channels: 28 us, 4.7 TB/s;
-// backward 51 us with the sums of partials, 4.0 TB/s.  What is left: the start of a
+// registers.  bf16, K = 4, silu, 8 x 2048 tokens of 2048 channels: 26 us, 5.2 TB/s;
+// backward 49 us with the sums of partials, 4.1 TB/s.  What is left: the start of a
 // strip, whose first rows nothing hides, and backward the arithmetic (the vector
 // units' issue of sigma, its slope and 8 products a value).
 #include <type_traits>
