@@ -84,3 +84,30 @@ def test_other_channels_stay_as_they_were(dt, packed):
     a, b = _backward(x, h, **kw), _backward(y, h, **kw)
     for n in a:
         assert torch.equal(a[n][..., ordinary], b[n][..., ordinary]), n
+
+
+@pytest.mark.parametrize("dt", [BF, F])
+def test_views_and_odd_widths(dt):
+    """Batch entries that do not follow one another, results into columns of one row,
+    and a width of single channels: as contiguous tensors within a rounding each (strips
+    take other paths), and what lies beside the results stays."""
+    x = _case(dt, True, -100.0, -40.0, 7)
+    B, T, D = x["x"].shape
+    h = P().gated_recurrence(x["x"], x["f"], i=x["i"], lam=x["lam"], h0=x["h0"], gate="power")[0]
+    want = _backward(x, h)
+    tol = 2.0 ** -8 if dt == BF else 1e-6      # (fp32: 150 roundings of 2^-24 of a carried gradient at most)
+    tol += 150 * 2.0 ** -24
+    far = {n: torch.zeros(B, T + 3, D, device="cuda", dtype=dt) for n in ("x", "f", "i", "dh")}
+    for n, t in far.items():
+        t[:, :T] = x[n]
+    into = torch.full((B, T + 3, 4, D), 7.0, device="cuda", dtype=dt)
+    part = [into[:, :T, k] for k in range(3)]
+    g = _backward({**x, **{n: t[:, :T] for n, t in far.items()}}, h, dx=part[0], df=part[1], di=part[2])
+    assert bool((into[:, :, 3] == 7).all()) and bool((into[:, T:] == 7).all())
+    odd = {n: None if t is None else t[..., :D - 1].contiguous() for n, t in x.items()}
+    o = _backward(odd, h[..., :D - 1].contiguous())
+    for n, t in want.items():
+        for k in range(len(RATES)):
+            at = slice(k * EACH, (k + 1) * EACH - 1)
+            assert O.rel2(_np(g[n][..., at]), _np(t[..., at])) < tol or not bool(t[..., at].any()), (n, k)
+            assert O.rel2(_np(o[n][..., at]), _np(t[..., at])) < tol or not bool(t[..., at].any()), (n, k)
